@@ -407,3 +407,159 @@ gdr_status gdr_chunk_fwd_noalloc(const gdr_problem* p, int32_t chunk_size, const
 }
 
 }  // extern "C"
+
+// ---- gated linear recurrence and beam search -----------------------------------------------------
+namespace {
+
+gdr_status check_linear(const gdr_linear_problem* p) {
+    if (!p) return GDR_ERROR_INVALID_VALUE;
+    if (p->total_tokens < 0 || p->num_seqs < 0 || p->num_channels <= 0) return GDR_ERROR_INVALID_VALUE;
+    if (p->gate != GDR_LINEAR_LOG_DECAY && p->gate != GDR_LINEAR_SIGMOID) return GDR_ERROR_INVALID_VALUE;
+    if (!dtype_ok(p->io_dtype)) return GDR_ERROR_INVALID_VALUE;
+    if (p->num_seqs > 65535) return GDR_ERROR_NOT_SUPPORTED;  // grid y limit
+    // the launch grid counts tiles of 64 tokens by 64 channels in 32 bits
+    const int64_t tiles = (p->total_tokens + 63) / 64, across = ((int64_t)p->num_channels + 63) / 64;
+    if (tiles > 0x7FFFFFFF / across) return GDR_ERROR_NOT_SUPPORTED;
+    return GDR_SUCCESS;
+}
+
+// Checks that both directions of the scan share.
+gdr_status check_linear_scan(const gdr_linear_problem* p, const int32_t* cu_seqlens, const void* workspace,
+                             size_t workspace_bytes) {
+    if (p->num_seqs > 1 && !cu_seqlens) return GDR_ERROR_INVALID_VALUE;
+    if (p->num_seqs == 0 && p->total_tokens > 0) return GDR_ERROR_INVALID_VALUE;
+    const size_t need = gdr::linear_workspace(p->total_tokens, p->num_channels);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return GDR_ERROR_INVALID_VALUE;
+    if (reinterpret_cast<uintptr_t>(workspace) % 256 != 0) return GDR_ERROR_INVALID_VALUE;
+    return GDR_SUCCESS;
+}
+
+gdr_status check_beam(const gdr_beam_problem* p) {
+    if (!p) return GDR_ERROR_INVALID_VALUE;
+    if (p->batch < 0 || p->beams <= 0 || p->vocab <= 0 || p->num_out <= 0) return GDR_ERROR_INVALID_VALUE;
+    if (p->num_out > p->vocab || p->row_stride < p->vocab) return GDR_ERROR_INVALID_VALUE;
+    if (!dtype_ok(p->io_dtype)) return GDR_ERROR_INVALID_VALUE;
+    if (p->beams > gdr::kBeamMaxBeams || p->num_out > gdr::kBeamMaxOut || p->vocab > gdr::kBeamMaxVocab)
+        return GDR_ERROR_NOT_SUPPORTED;
+    if ((int64_t)p->batch * p->beams > 65535) return GDR_ERROR_NOT_SUPPORTED;  // grid y limit
+    return GDR_SUCCESS;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t gdr_linear_workspace_size(const gdr_linear_problem* p) {
+    if (check_linear(p) != GDR_SUCCESS) return 0;
+    return gdr::linear_workspace(p->total_tokens, p->num_channels);
+}
+
+gdr_status gdr_linear_scan_fwd(const gdr_linear_problem* p, const void* x, const void* gate, const int32_t* cu_seqlens,
+                               const float* initial_state, void* y, float* final_state, float* block_states,
+                               void* workspace, size_t workspace_bytes, void* hip_stream) {
+    gdr_status st = check_linear(p);
+    if (st != GDR_SUCCESS) return st;
+    if (p->total_tokens > 0 && !(x && gate && y)) return GDR_ERROR_INVALID_VALUE;
+    if ((st = check_linear_scan(p, cu_seqlens, workspace, workspace_bytes)) != GDR_SUCCESS) return st;
+    if (p->num_seqs == 0 || (p->total_tokens == 0 && !final_state)) return GDR_SUCCESS;
+    if ((st = check_device()) != GDR_SUCCESS) return st;
+    const hipStream_t stream = static_cast<hipStream_t>(hip_stream);
+    if (p->total_tokens == 0)
+        return status_of(gdr::launch_linear_empty(nullptr, initial_state, final_state, p->num_seqs, p->num_channels, stream));
+    gdr::LinearArgs a{};
+    a.x = x; a.gate = gate; a.cu = cu_seqlens; a.h0 = initial_state; a.y = y; a.ht = final_state;
+    a.block_states = block_states;
+    a.runs = static_cast<float2*>(workspace);
+    a.T = p->total_tokens; a.D = p->num_channels; a.N = p->num_seqs;
+    return status_of(gdr::launch_linear_scan(a, p->gate, p->io_dtype, false, stream));
+}
+
+gdr_status gdr_linear_scan_bwd(const gdr_linear_problem* p, const void* x, const void* gate, const int32_t* cu_seqlens,
+                               const float* initial_state, const float* block_states, const void* dy,
+                               const float* d_final_state, void* dx, void* dgate, float* d_initial_state,
+                               void* workspace, size_t workspace_bytes, void* hip_stream) {
+    gdr_status st = check_linear(p);
+    if (st != GDR_SUCCESS) return st;
+    if (p->total_tokens > 0 && !(x && gate && block_states && dy && dx && dgate)) return GDR_ERROR_INVALID_VALUE;
+    if ((st = check_linear_scan(p, cu_seqlens, workspace, workspace_bytes)) != GDR_SUCCESS) return st;
+    if (p->num_seqs == 0 || (p->total_tokens == 0 && !d_initial_state)) return GDR_SUCCESS;
+    if ((st = check_device()) != GDR_SUCCESS) return st;
+    const hipStream_t stream = static_cast<hipStream_t>(hip_stream);
+    if (p->total_tokens == 0)
+        return status_of(gdr::launch_linear_empty(nullptr, d_final_state, d_initial_state, p->num_seqs, p->num_channels, stream));
+    gdr::LinearArgs a{};
+    a.x = x; a.gate = gate; a.cu = cu_seqlens; a.h0 = initial_state;
+    a.block_states = const_cast<float*>(block_states);
+    a.runs = static_cast<float2*>(workspace);
+    a.dy = dy; a.dht = d_final_state; a.dx = dx; a.dgate = dgate; a.dh0 = d_initial_state;
+    a.T = p->total_tokens; a.D = p->num_channels; a.N = p->num_seqs;
+    return status_of(gdr::launch_linear_scan(a, p->gate, p->io_dtype, true, stream));
+}
+
+gdr_status gdr_linear_decode_paged(const gdr_linear_problem* p, int32_t max_q_len, const void* x, const void* gate,
+                                   const int32_t* cu_seqlens, void* pool, gdr_dtype pool_dtype, int32_t num_slots,
+                                   const int32_t* state_indices, int32_t commit, void* y, void* hip_stream) {
+    gdr_status st = check_linear(p);
+    if (st != GDR_SUCCESS) return st;
+    if (max_q_len < 1 || max_q_len > 12) return GDR_ERROR_INVALID_VALUE;
+    if (!pool || num_slots <= 0 || !state_indices) return GDR_ERROR_INVALID_VALUE;
+    if (!dtype_ok(pool_dtype)) return GDR_ERROR_INVALID_VALUE;
+    if (commit != 0 && commit != 1) return GDR_ERROR_INVALID_VALUE;
+    if (p->total_tokens > 0 && !(x && gate && y)) return GDR_ERROR_INVALID_VALUE;
+    if (!cu_seqlens && p->total_tokens != p->num_seqs) return GDR_ERROR_INVALID_VALUE;
+    if (p->total_tokens > (int64_t)p->num_seqs * max_q_len) return GDR_ERROR_INVALID_VALUE;
+    if (p->num_seqs == 0 || p->total_tokens == 0) return GDR_SUCCESS;
+    if ((st = check_device()) != GDR_SUCCESS) return st;
+    gdr::LinearArgs a{};
+    a.x = x; a.gate = gate; a.cu = cu_seqlens; a.y = y;
+    a.pool = pool; a.slots = state_indices; a.num_slots = num_slots; a.commit = commit;
+    a.T = p->total_tokens; a.D = p->num_channels; a.N = p->num_seqs;
+    return status_of(gdr::launch_linear_decode(a, p->gate, p->io_dtype, pool_dtype, static_cast<hipStream_t>(hip_stream)));
+}
+
+size_t gdr_beam_workspace_size(const gdr_beam_problem* p) {
+    if (check_beam(p) != GDR_SUCCESS || p->batch == 0) return 0;
+    return gdr::beam_plan(p->batch, p->beams, p->vocab, p->num_out).total;
+}
+
+gdr_status gdr_beam_select(const gdr_beam_problem* p, const void* logits, const float* scores, const uint8_t* finished,
+                           float* out_scores, int32_t* out_parents, int32_t* out_tokens, void* workspace,
+                           size_t workspace_bytes, void* hip_stream) {
+    gdr_status st = check_beam(p);
+    if (st != GDR_SUCCESS) return st;
+    if (finished && (p->eos_token < 0 || p->eos_token >= p->vocab)) return GDR_ERROR_INVALID_VALUE;
+    if (p->batch == 0) return GDR_SUCCESS;
+    if (!(logits && scores && out_scores && out_parents && out_tokens)) return GDR_ERROR_INVALID_VALUE;
+    const gdr::BeamPlan pl = gdr::beam_plan(p->batch, p->beams, p->vocab, p->num_out);
+    if (!workspace || workspace_bytes < pl.total) return GDR_ERROR_INVALID_VALUE;
+    if (reinterpret_cast<uintptr_t>(workspace) % 256 != 0) return GDR_ERROR_INVALID_VALUE;
+    if ((st = check_device()) != GDR_SUCCESS) return st;
+    gdr::BeamArgs a{};
+    a.logits = logits; a.stride = p->row_stride; a.scores = scores; a.finished = finished;
+    a.out_scores = out_scores; a.out_parents = out_parents; a.out_tokens = out_tokens;
+    a.batch = p->batch; a.beams = p->beams; a.vocab = p->vocab; a.out = p->num_out; a.eos = p->eos_token;
+    return status_of(gdr::launch_beam_select(a, pl, static_cast<char*>(workspace), p->io_dtype,
+                                             static_cast<hipStream_t>(hip_stream)));
+}
+
+gdr_status gdr_beam_reorder(int32_t batch, int32_t beams, const int32_t* parents, const int32_t* state_indices,
+                            int32_t* state_indices_out, void* pool, int32_t num_layers, int32_t num_slots,
+                            int64_t slot_bytes, void* hip_stream) {
+    if (batch < 0 || beams <= 0 || num_layers < 0 || num_slots <= 0 || slot_bytes <= 0) return GDR_ERROR_INVALID_VALUE;
+    if (slot_bytes % 2 != 0 || reinterpret_cast<uintptr_t>(pool) % 2 != 0) return GDR_ERROR_INVALID_VALUE;
+    if (beams > gdr::kBeamMaxBeams) return GDR_ERROR_NOT_SUPPORTED;
+    if ((int64_t)batch * beams > 65535 || num_layers > 65535) return GDR_ERROR_NOT_SUPPORTED;  // grid y/z limits
+    if (batch == 0 || num_layers == 0) return GDR_SUCCESS;
+    if (!(parents && state_indices && state_indices_out && pool)) return GDR_ERROR_INVALID_VALUE;
+    if (state_indices_out == state_indices || state_indices_out == parents) return GDR_ERROR_INVALID_VALUE;
+    gdr_status st = check_device();
+    if (st != GDR_SUCCESS) return st;
+    gdr::ReorderArgs a{};
+    a.pool = static_cast<char*>(pool);
+    a.slot_bytes = slot_bytes; a.layer_bytes = slot_bytes * num_slots;
+    a.layers = num_layers; a.num_slots = num_slots; a.batch = batch; a.beams = beams;
+    a.slots = state_indices; a.parents = parents; a.slots_out = state_indices_out;
+    return status_of(gdr::launch_beam_reorder(a, static_cast<hipStream_t>(hip_stream)));
+}
+
+}  // extern "C"

@@ -1,0 +1,536 @@
+// Beam search for gfx950: the best candidates over beams and vocabulary, and the paged states moved to
+// where the chosen beams expect them.
+//
+// Selection: s[w, v] = score[w] + logit[w, v] - log sum_v e^logit[w, v]; the best of the W V candidates
+// of a batch row in descending order, equal ones by the lower w V + v.
+//   rows   one workgroup per (row, part of the vocabulary), its logits in registers, read once: maximum,
+//          sum of exponentials, and the part's best `out` entries by (logit, lower token).  Within a beam
+//          the order of the candidates is the order of their logits, so these lists are exact.
+//   merge  one workgroup per batch row: log-sum-exp per beam from the parts in 64 bits, scores of the
+//          listed entries in 64 bits, the best `out` of them.  The sums come from 32-bit exponentials, so
+//          scores of different beams closer than kNear could stand in the wrong order: where two
+//          neighbours of the result are that close, their beams' sums are formed again in 64 bits.
+//
+// Reordering: a parent's first child keeps its slot; the other children take, in order, the slots of
+// parents without children, and only these are copied.  What is read (slots of parents with children) and
+// what is written (slots of parents without) never meet, so all copies of all layers run at once.
+#include "gdr_device.h"
+#include "gdr_internal.h"
+
+namespace gdr {
+
+namespace {
+
+constexpr int kRowThreads = 256;
+constexpr int kRowWaves = kRowThreads / 64;
+constexpr int kWaveCap = 256;                      // entries above the threshold that a wave may list
+constexpr int kRowList = 2048;                     // >= kRowWaves * (kWaveCap + kBeamMaxOut), a power of two
+constexpr int kMergeThreads = 256;
+constexpr int kMaxSplits = 64;
+
+// Bound of the difference between the 32-bit sums' log and the true one: every exponential carries the
+// hardware's 2^-23 and its argument's rounding, at most |d| 2^-23 for a distance d to the maximum; what
+// lies beyond |d| = 20 is below 2^20 e^-20 = 2e-3 of the sum.  (1 + 20) 2^-23 = 2.5e-6, plus 3 additions
+// in 32 bits (2e-7); two beams' scores are in the right order if they differ by more than twice this.
+constexpr double kNear = 6e-6;
+
+// Keys in ascending order of the float they stand for.  -0 counts as 0, NaN as -inf.
+__device__ __forceinline__ uint32_t key_of(float x) {
+    const uint32_t b = __float_as_uint(x);
+    return b ^ ((uint32_t)((int)b >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float of_key(uint32_t k) { return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k); }
+__device__ __forceinline__ float clean(float x) { return x == x ? x + 0.0f : -__builtin_inff(); }
+
+__device__ __forceinline__ uint64_t entry_of(float x, uint32_t token) { return ((uint64_t)key_of(x) << 32) | ~token; }
+
+__device__ __forceinline__ float wave_max(float x) {
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) x = fmaxf(x, __shfl_xor(x, m));
+    return x;
+}
+__device__ __forceinline__ double wave_sum(double x) {
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) x += __shfl_xor(x, m);
+    return x;
+}
+
+__device__ __forceinline__ int lanes_below(uint64_t mask) {
+    return __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0));
+}
+
+// Sorts n (a power of two) items of LDS, the first in order first; all threads of the workgroup call it.
+template <int THREADS, typename Swap> __device__ __forceinline__ void bitonic_sort(int n, Swap swap_if_wrong) {
+    for (int k = 2; k <= n; k <<= 1)
+        for (int j = k >> 1; j > 0; j >>= 1) {
+            __syncthreads();
+            for (int i = threadIdx.x; i < n / 2; i += THREADS) {
+                const int lo = ((i & ~(j - 1)) << 1) | (i & (j - 1));
+                swap_if_wrong(lo, lo | j, (lo & k) == 0);
+            }
+        }
+    __syncthreads();
+}
+
+__device__ __forceinline__ int pow2_at_least(int n) { return n <= 2 ? 2 : 1 << (32 - __builtin_clz(n - 1)); }
+
+// PER logits per thread.  VECW of them at a time are neighbours (one aligned 16-byte load), or 1.
+template <typename IO, int PER, int VECW>
+__global__ __launch_bounds__(kRowThreads) void beam_rows_kernel(const BeamArgs a) {
+    const int row = blockIdx.y, split = blockIdx.x;
+    const float score = a.scores[row];
+    // ended beams and beams without probability list nothing
+    if ((a.finished && a.finished[row]) || !(score > -__builtin_inff() && score < __builtin_inff())) return;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int base = split * a.chunk;
+    const int64_t row_at = (int64_t)row * a.stride;
+
+    float x[PER];
+#pragma unroll
+    for (int j = 0; j < PER / VECW; ++j) {
+        const int v = base + (j * kRowThreads + tid) * VECW;
+        if constexpr (VECW == 1) {
+            x[j] = v < a.vocab ? Elem<IO>::load(a.logits, row_at + v) : -__builtin_inff();
+        } else {
+            if (v + VECW <= a.vocab) {
+                Vec<IO, VECW>::load(a.logits, row_at + v, &x[j * VECW]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < VECW; ++e)
+                    x[j * VECW + e] = v + e < a.vocab ? Elem<IO>::load(a.logits, row_at + v + e) : -__builtin_inff();
+            }
+        }
+    }
+    float top = -__builtin_inff();
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        x[i] = clean(x[i]);
+        top = fmaxf(top, x[i]);
+    }
+
+    __shared__ uint64_t list[kRowList];
+    __shared__ double sh_sum[kRowWaves];
+    __shared__ float sh_top[kRowWaves];
+    __shared__ uint32_t sh_tau[kRowWaves];
+    __shared__ int count;
+    if (tid == 0) count = 0;
+
+    // sum of exponentials about the thread's own maximum, eight at a time in 32 bits
+    const bool some = top > -__builtin_inff();
+    const float about = some ? top : 0.0f;
+    double sum = 0.0;
+#pragma unroll
+    for (int i = 0; i < PER; i += 8) {
+        float p[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) p[e] = exp_f32(x[i + e] - about);
+        sum += (double)(((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7])));
+    }
+    const float wtop = wave_max(top);
+    sum = wave_sum(some ? sum * (double)exp_f32(top - wtop) : 0.0);
+
+    // tau: a logit that at least `out` of this wave's reach or pass (the out-th best of the lanes' maxima)
+    const uint32_t mine = key_of(top);
+    uint32_t tau = 0;
+    constexpr int kLowBit = Elem<IO>::bytes == 2 ? 16 : 0;
+#pragma unroll
+    for (int bit = 31; bit >= kLowBit; --bit) {
+        const uint32_t t = tau | (1u << bit);
+        if (__popcll(__ballot(mine >= t)) >= a.out) tau = t;
+    }
+    if (!(tau >> 31)) tau |= (1u << kLowBit) - 1;  // the keys of negative bf16 values end in ones
+    if (lane == 0) {
+        sh_sum[tid >> 6] = sum;
+        sh_top[tid >> 6] = wtop;
+        sh_tau[tid >> 6] = tau;
+    }
+    __syncthreads();
+    float btop = sh_top[0];
+#pragma unroll
+    for (int i = 1; i < kRowWaves; ++i) btop = fmaxf(btop, sh_top[i]);
+    tau = sh_tau[0];
+#pragma unroll
+    for (int i = 1; i < kRowWaves; ++i) tau = max(tau, sh_tau[i]);
+    if (tid == 0) {
+        double s = 0.0;
+        for (int i = 0; i < kRowWaves; ++i)
+            if (sh_top[i] > -__builtin_inff()) s += sh_sum[i] * (double)exp_f32(sh_top[i] - btop);
+        a.sums[(int64_t)row * a.splits + split] = s;
+        a.tops[(int64_t)row * a.splits + split] = btop;
+    }
+
+    // logits above tau, unless a few lanes hold very many of them: then tau becomes the wave's out-th best
+    const uint32_t none = key_of(-__builtin_inff());
+    tau = max(tau, none);
+    int above = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) above += __popcll(__ballot(key_of(x[i]) > tau));
+    if (above > kWaveCap) {
+        uint32_t t = 0;
+        for (int bit = 31; bit >= 0; --bit) {
+            const uint32_t u = t | (1u << bit);
+            int c = 0;
+#pragma unroll
+            for (int i = 0; i < PER; ++i) c += __popcll(__ballot(key_of(x[i]) >= u));
+            if (c >= a.out) t = u;
+        }
+        tau = max(tau, t);
+    }
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const bool take = key_of(x[i]) > tau;
+        const uint64_t m = __ballot(take);
+        if (!m) continue;
+        int at = 0;
+        if (lane == 0) at = atomicAdd(&count, __popcll(m));
+        at = __builtin_amdgcn_readfirstlane(at);
+        if (take) list[at + lanes_below(m)] = entry_of(x[i], base + ((i / VECW) * kRowThreads + tid) * VECW + i % VECW);
+    }
+    // logits equal to tau: the wave's first `out` in the order of the tokens (-inf is never listed)
+    if (tau > none) {
+        int found = 0;
+#pragma unroll
+        for (int j = 0; j < PER / VECW; ++j) {
+            uint64_t any = 0;
+            int n = 0;
+#pragma unroll
+            for (int e = 0; e < VECW; ++e) {
+                const bool eq = key_of(x[j * VECW + e]) == tau;
+                any |= __ballot(eq);
+                n += eq;
+            }
+            if (!any || found >= a.out) continue;
+            // equal ones in lower lanes come first, then this lane's in order
+            const int incl = (int)wave_inclusive_sum((float)n);
+            int rank = found + incl - n;
+            const int total = __builtin_amdgcn_readlane(incl, 63);
+            const int take = min(total, a.out - found);
+            int at = 0;
+            if (lane == 0) at = atomicAdd(&count, take);
+            at = __builtin_amdgcn_readfirstlane(at);
+#pragma unroll
+            for (int e = 0; e < VECW; ++e)
+                if (key_of(x[j * VECW + e]) == tau) {
+                    if (rank < a.out)
+                        list[at + rank - found] = entry_of(x[j * VECW + e], base + (j * kRowThreads + tid) * VECW + e);
+                    ++rank;
+                }
+            found += total;
+        }
+    }
+    __syncthreads();
+    const int n = count, np = pow2_at_least(n);
+    for (int i = n + tid; i < np; i += kRowThreads) list[i] = 0;
+    bitonic_sort<kRowThreads>(np, [&](int i, int j, bool down) {
+        const uint64_t p = list[i], q = list[j];
+        if ((p < q) == down && p != q) {
+            list[i] = q;
+            list[j] = p;
+        }
+    });
+    uint64_t* out = a.entries + ((int64_t)row * a.splits + split) * a.out;
+    for (int i = tid; i < a.out; i += kRowThreads) out[i] = i < n ? list[i] : 0;
+}
+
+__device__ __forceinline__ uint64_t key_of64(double x) {
+    const uint64_t b = (uint64_t)__double_as_longlong(x + 0.0);
+    return b ^ ((uint64_t)((int64_t)b >> 63) | 0x8000000000000000ull);
+}
+__device__ __forceinline__ double of_key64(uint64_t k) {
+    return __longlong_as_double((int64_t)(k >> 63 ? k ^ 0x8000000000000000ull : ~k));
+}
+
+template <typename IO> __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(const BeamArgs a) {
+    const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    constexpr int kWavesM = kMergeThreads / 64;
+    const int W = a.beams, S = a.splits, K = a.out;
+    extern __shared__ __align__(16) char smem[];
+    uint64_t* keys = reinterpret_cast<uint64_t*>(smem);                       // [kMergeList]
+    uint32_t* flat = reinterpret_cast<uint32_t*>(keys + a.merge_list);        // [kMergeList]
+    __shared__ double lse[kBeamMaxBeams], red[kWavesM];
+    __shared__ int state[kBeamMaxBeams];                                      // 0: listed, 1: ended, 2: no candidates
+    __shared__ int count, near_mask;
+    __shared__ uint64_t tau_key;
+    __shared__ uint32_t tau_flat;
+
+    for (int w = wave; w < W; w += kWavesM) {
+        const int64_t row = (int64_t)b * W + w;
+        const float score = a.scores[row];
+        const bool real = score > -__builtin_inff() && score < __builtin_inff();
+        int st = !real ? 2 : (a.finished && a.finished[row]) ? 1 : 0;
+        double l = 0.0;
+        if (st == 0) {
+            const float m = lane < S ? a.tops[row * S + lane] : -__builtin_inff();
+            const float top = wave_max(m);
+            if (!(top > -__builtin_inff() && top < __builtin_inff())) {
+                st = 2;
+            } else {
+                // a part without a finite logit has the sum of nothing
+                const double part = lane < S && m > -__builtin_inff() ? a.sums[row * S + lane] * exp((double)m - (double)top) : 0.0;
+                l = (double)top + log(wave_sum(part));
+            }
+        }
+        if (lane == 0) {
+            lse[w] = l;
+            state[w] = st;
+        }
+    }
+    __syncthreads();
+
+    const int lists = W * S, total = lists * K;
+    int n = 0;
+    for (int pass = 0; pass < 2; ++pass) {
+        // score and flat index of entry i; false: none
+        auto candidate = [&](int i, uint64_t& key, uint32_t& at) {
+            const int w = i / (S * K);
+            if (state[w] == 1) {
+                if (i % (S * K) != 0 || a.eos < 0) return false;
+                key = key_of64((double)a.scores[(int64_t)b * W + w]);
+                at = (uint32_t)w * a.vocab + a.eos;
+                return true;
+            }
+            if (state[w] == 2) return false;
+            const uint64_t e = a.entries[((int64_t)b * W * S * K) + i];
+            if (!e) return false;
+            const double s = (double)a.scores[(int64_t)b * W + w] + ((double)of_key((uint32_t)(e >> 32)) - lse[w]);
+            key = key_of64(s);
+            at = (uint32_t)w * a.vocab + ~(uint32_t)e;
+            return true;
+        };
+        if (tid == 0) {
+            count = 0;
+            near_mask = 0;
+            tau_key = 0;
+            tau_flat = 0xFFFFFFFFu;
+        }
+        __syncthreads();
+        // with more lists than results, no result and not the one behind them comes after the (K+1)-th best of
+        // the lists' first entries, and at most K lists hold better ones
+        if (lists > K) {
+            for (int i = tid; i < lists; i += kMergeThreads) {
+                uint64_t key = 0;
+                uint32_t at = 0xFFFFFFFFu;
+                candidate(i * K, key, at);
+                keys[i] = key;
+                flat[i] = at;
+            }
+            __syncthreads();
+            for (int i = tid; i < lists; i += kMergeThreads) {
+                const uint64_t key = keys[i];
+                const uint32_t at = flat[i];
+                int rank = 0;
+                for (int j = 0; j < lists; ++j) rank += keys[j] > key || (keys[j] == key && flat[j] < at);
+                if (rank == K && key) {
+                    tau_key = key;
+                    tau_flat = at;
+                }
+            }
+            __syncthreads();
+        }
+        for (int i = tid; i < total; i += kMergeThreads) {
+            uint64_t key;
+            uint32_t at;
+            if (!candidate(i, key, at)) continue;
+            if (key > tau_key || (key == tau_key && at < tau_flat)) {
+                const int p = atomicAdd(&count, 1);
+                keys[p] = key;
+                flat[p] = at;
+            }
+        }
+        __syncthreads();
+        if (tid == 0 && tau_key && count <= K) {
+            keys[count] = tau_key;
+            flat[count] = tau_flat;
+            ++count;
+        }
+        __syncthreads();
+        n = count;
+        const int np = pow2_at_least(n);
+        for (int i = n + tid; i < np; i += kMergeThreads) {
+            keys[i] = 0;
+            flat[i] = 0xFFFFFFFFu;
+        }
+        bitonic_sort<kMergeThreads>(np, [&](int i, int j, bool down) {
+            const uint64_t p = keys[i], q = keys[j];
+            const bool behind = p < q || (p == q && flat[i] > flat[j]);
+            if (behind == down) {
+                const uint32_t f = flat[i];
+                keys[i] = q;
+                flat[i] = flat[j];
+                keys[j] = p;
+                flat[j] = f;
+            }
+        });
+        if (pass == 1) break;
+        for (int i = tid; i + 1 < n && i < K; i += kMergeThreads) {
+            const int w0 = flat[i] / a.vocab, w1 = flat[i + 1] / a.vocab;
+            if (w0 != w1 && of_key64(keys[i]) - of_key64(keys[i + 1]) < kNear) atomicOr(&near_mask, (1 << w0) | (1 << w1));
+        }
+        __syncthreads();
+        const uint32_t near = (uint32_t)near_mask;
+        if (!near) break;
+        for (int w = 0; w < W; ++w) {
+            if (!((near >> w) & 1) || state[w] != 0) continue;
+            const int64_t at = ((int64_t)b * W + w) * a.stride;
+            float top = -__builtin_inff();
+            for (int s = 0; s < S; ++s) top = fmaxf(top, a.tops[((int64_t)b * W + w) * S + s]);
+            double sum = 0.0;
+            for (int v = tid; v < a.vocab; v += kMergeThreads)
+                sum += exp((double)clean(Elem<IO>::load(a.logits, at + v)) - (double)top);
+            sum = wave_sum(sum);
+            if (lane == 0) red[wave] = sum;
+            __syncthreads();
+            if (tid == 0) {
+                double s = 0.0;
+                for (int i = 0; i < kWavesM; ++i) s += red[i];
+                lse[w] = (double)top + log(s);
+            }
+            __syncthreads();
+        }
+    }
+    const int have = min(n, K);
+    for (int i = tid; i < have; i += kMergeThreads) {
+        a.out_scores[(int64_t)b * K + i] = (float)of_key64(keys[i]);
+        a.out_parents[(int64_t)b * K + i] = flat[i] / a.vocab;
+        a.out_tokens[(int64_t)b * K + i] = flat[i] % a.vocab;
+    }
+    // fewer candidates than asked for: those of probability zero follow, by the lower index
+    if (have == K || wave != 0) return;
+    int at = have;
+    for (int w = 0; w < W && at < K; ++w) {
+        const int64_t row = ((int64_t)b * W + w) * a.stride;
+        for (int v0 = 0; v0 < a.vocab && at < K; v0 += 64) {
+            const int v = v0 + lane;
+            bool none = v < a.vocab;
+            if (none && state[w] == 1) none = v != a.eos;
+            if (none && state[w] == 0) none = clean(Elem<IO>::load(a.logits, row + v)) == -__builtin_inff();
+            const uint64_t m = __ballot(none);
+            const int p = at + lanes_below(m);
+            if (none && p < K) {
+                a.out_scores[(int64_t)b * K + p] = -__builtin_inff();
+                a.out_parents[(int64_t)b * K + p] = w;
+                a.out_tokens[(int64_t)b * K + p] = v;
+            }
+            at += __popcll(m);
+        }
+    }
+}
+
+// ---- reordering ----
+constexpr int kCopyThreads = 256;
+constexpr int kCopyUnroll = 8;
+
+// One workgroup per (part of a slot, child, layer); every wave works out the child's slot for itself.
+template <typename T> __global__ __launch_bounds__(kCopyThreads) void beam_reorder_kernel(const ReorderArgs a) {
+    const int child = blockIdx.y % a.beams, b = blockIdx.y / a.beams;
+    const int lane = threadIdx.x & 63;
+    const bool in = lane < a.beams;
+    const int parent = in ? a.parents[b * a.beams + lane] : -1;
+    const int slot = in ? a.slots[b * a.beams + lane] : -1;
+    const bool wrong = in && ((unsigned)parent >= (unsigned)a.beams || (unsigned)slot >= (unsigned)a.num_slots);
+    const int my_parent = __builtin_amdgcn_readlane(parent, child);
+    const bool head = blockIdx.x == 0 && blockIdx.z == 0 && threadIdx.x == 0;
+    if (__ballot(wrong)) {  // a padded row: its slots stay
+        if (head) a.slots_out[b * a.beams + child] = __builtin_amdgcn_readlane(slot, child);
+        return;
+    }
+    uint64_t childless = 0, first = 0;
+    for (int p = 0; p < a.beams; ++p) {
+        const uint64_t m = __ballot(parent == p);
+        if (m) first |= m & -m; else childless |= 1ull << p;
+    }
+    const int src = __builtin_amdgcn_readlane(slot, my_parent);
+    int dst = src;
+    if (!((first >> child) & 1)) {
+        int rank = __popcll(~first & ((1ull << child) - 1));
+        while (rank-- > 0) childless &= childless - 1;
+        dst = __builtin_amdgcn_readlane(slot, __builtin_ctzll(childless));
+    }
+    if (head) a.slots_out[b * a.beams + child] = dst;
+    if (dst == src) return;
+    const int64_t units = a.slot_bytes / sizeof(T);
+    char* layer = a.pool + (int64_t)blockIdx.z * a.layer_bytes;
+    const T* from = reinterpret_cast<const T*>(layer + (int64_t)src * a.slot_bytes);
+    T* to = reinterpret_cast<T*>(layer + (int64_t)dst * a.slot_bytes);
+    const int64_t i0 = (int64_t)blockIdx.x * (kCopyThreads * kCopyUnroll) + threadIdx.x;
+    T r[kCopyUnroll];
+#pragma unroll
+    for (int u = 0; u < kCopyUnroll; ++u)
+        if (i0 + u * kCopyThreads < units) r[u] = from[i0 + u * kCopyThreads];
+#pragma unroll
+    for (int u = 0; u < kCopyUnroll; ++u)
+        if (i0 + u * kCopyThreads < units) to[i0 + u * kCopyThreads] = r[u];
+}
+
+template <typename T> hipError_t reorder(const ReorderArgs& a, hipStream_t s) {
+    const int64_t units = a.slot_bytes / sizeof(T), per = kCopyThreads * kCopyUnroll;
+    const int64_t parts = (units + per - 1) / per;
+    if (parts > 0x7FFFFFFF) return hipErrorInvalidValue;
+    beam_reorder_kernel<T><<<dim3((unsigned)parts, (unsigned)(a.batch * a.beams), (unsigned)a.layers), kCopyThreads, 0, s>>>(a);
+    return hipGetLastError();
+}
+
+size_t up256(size_t n) { return (n + 255) / 256 * 256; }
+
+template <typename IO, int PER> hipError_t rows(const BeamArgs& a, hipStream_t s) {
+    constexpr int VECW = 16 / Elem<IO>::bytes;
+    const dim3 grid(a.splits, a.batch * a.beams);
+    if (a.stride % VECW == 0 && reinterpret_cast<uintptr_t>(a.logits) % 16 == 0)
+        beam_rows_kernel<IO, PER, VECW><<<grid, kRowThreads, 0, s>>>(a);
+    else
+        beam_rows_kernel<IO, PER, 1><<<grid, kRowThreads, 0, s>>>(a);
+    return hipGetLastError();
+}
+
+template <typename IO> hipError_t select(BeamArgs a, const BeamPlan& pl, hipStream_t s) {
+    hipError_t e = pl.per_thread == 16 ? rows<IO, 16>(a, s) : pl.per_thread == 32 ? rows<IO, 32>(a, s) : rows<IO, 64>(a, s);
+    if (e != hipSuccess) return e;
+    // the merge keeps the entries of at most `out` lists and one more where these are fewer than out + 1;
+    // the lists' first entries stand there before
+    int most = a.out * a.out;
+    const int lists = a.beams * a.splits;
+    if (most < lists) most = lists;
+    if (most < a.out + 1) most = a.out + 1;
+    a.merge_list = 2;
+    while (a.merge_list < most) a.merge_list *= 2;
+    beam_merge_kernel<IO><<<a.batch, kMergeThreads, (size_t)a.merge_list * 12, s>>>(a);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+// Parts of 4096, 8192 or 16384 logits: the largest that still gives the part two workgroups per CU, and
+// at most kMaxSplits of them per row.
+BeamPlan beam_plan(int32_t batch, int32_t beams, int32_t vocab, int32_t out) {
+    BeamPlan pl{};
+    const int64_t rows = (int64_t)batch * beams;
+    pl.per_thread = 64;
+    auto splits = [&](int per) { return (vocab + per * kRowThreads - 1) / (per * kRowThreads); };
+    while (pl.per_thread > 16 && rows * splits(pl.per_thread) < 512 && splits(pl.per_thread / 2) <= kMaxSplits) pl.per_thread /= 2;
+    pl.splits = splits(pl.per_thread);
+    pl.chunk = pl.per_thread * kRowThreads;
+    pl.sums = 0;
+    pl.tops = up256((size_t)rows * pl.splits * sizeof(double));
+    pl.entries = pl.tops + up256((size_t)rows * pl.splits * sizeof(float));
+    pl.total = pl.entries + up256((size_t)rows * pl.splits * out * sizeof(uint64_t));
+    return pl;
+}
+
+hipError_t launch_beam_select(const BeamArgs& args, const BeamPlan& pl, char* ws, int io_dtype, hipStream_t stream) {
+    BeamArgs a = args;
+    a.splits = pl.splits;
+    a.chunk = pl.chunk;
+    a.sums = reinterpret_cast<double*>(ws + pl.sums);
+    a.tops = reinterpret_cast<float*>(ws + pl.tops);
+    a.entries = reinterpret_cast<uint64_t*>(ws + pl.entries);
+    return io_dtype == 0 ? select<float>(a, pl, stream) : select<bf16_t>(a, pl, stream);
+}
+
+hipError_t launch_beam_reorder(const ReorderArgs& a, hipStream_t s) {
+    const uintptr_t both = reinterpret_cast<uintptr_t>(a.pool) | (uintptr_t)a.slot_bytes;
+    if (both % 16 == 0) return reorder<uint4>(a, s);
+    if (both % 4 == 0) return reorder<uint32_t>(a, s);
+    return reorder<uint16_t>(a, s);
+}
+
+}  // namespace gdr

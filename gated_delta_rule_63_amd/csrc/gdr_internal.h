@@ -144,4 +144,79 @@ hipError_t launch_cp_scan(const CpPlan& pl, char* ws, const float* h0, int32_t H
 hipError_t launch_cp_final(const CpPlan& pl, const char* ws, float* out, int32_t HV, int32_t K, int32_t V,
                            hipStream_t stream);
 
+// Gated linear recurrence (gdr_linear.hip).
+constexpr int kLinearBlock = 64;     // tokens per row of block_states (GDR_LINEAR_BLOCK)
+
+struct LinearArgs {
+    const void* x;               // [T, D] io dtype
+    const void* gate;            // [T, D] fp32 log-decay, or io dtype before the sigmoid
+    const int32_t* cu;           // [N + 1]; NULL: one sequence (scan), one token per sequence (decode)
+    const float* h0;             // [N, D] or NULL (zeros)
+    void* y;                     // [T, D] io dtype
+    float* ht;                   // [N, D] or NULL
+    float* block_states;         // [ceil(T / kLinearBlock), D]: the state entering each block, or NULL
+    float2* runs;                // workspace: a word per (tile, channel)
+    // backward
+    const void* dy;              // [T, D] io dtype
+    const float* dht;            // [N, D] or NULL (zeros)
+    void* dx;                    // [T, D] io dtype
+    void* dgate;                 // [T, D] the gate's dtype
+    float* dh0;                  // [N, D] or NULL
+    // decode
+    void* pool;                  // [num_slots, D] state dtype
+    const int32_t* slots;        // [N]; negative = padded sequence
+    int32_t num_slots, commit;
+    int64_t T, D;
+    int32_t N;
+    int32_t nch;                 // set by the launcher: workgroups across the channels, tiles along the tokens
+    int64_t tiles;
+};
+
+size_t linear_workspace(int64_t T, int64_t D);
+// kind 0: log-decay, 1: sigmoid.  Requires a.T >= 1 and a workspace of linear_workspace bytes.
+hipError_t launch_linear_scan(const LinearArgs& a, int kind, int io_dtype, bool backward, hipStream_t stream);
+hipError_t launch_linear_decode(const LinearArgs& a, int kind, int io_dtype, int st_dtype, hipStream_t stream);
+// dst[n] = src[n] (zeros without src) for empty sequences, or for all when cu is NULL.
+hipError_t launch_linear_empty(const int32_t* cu, const float* src, float* dst, int32_t N, int64_t D, hipStream_t stream);
+
+// Beam search (gdr_beam.hip).
+constexpr int kBeamMaxBeams = 32, kBeamMaxOut = 64, kBeamMaxVocab = 1 << 20;
+
+struct BeamArgs {
+    const void* logits;          // [batch, beams, >= vocab] io dtype, rows `stride` elements apart
+    int64_t stride;
+    const float* scores;         // [batch, beams]
+    const uint8_t* finished;     // [batch, beams] or NULL
+    float* out_scores;           // [batch, out]
+    int32_t* out_parents;
+    int32_t* out_tokens;
+    int32_t batch, beams, vocab, out, eos;
+    // workspace, per (row, split)
+    double* sums;
+    float* tops;
+    uint64_t* entries;           // [row, split, out]
+    int32_t splits, chunk;       // set by the plan
+    int32_t merge_list;          // set by the launcher: candidates the merge may hold
+};
+
+struct BeamPlan {
+    int per_thread;              // logits per thread of a row kernel's workgroup
+    int splits, chunk;
+    size_t sums, tops, entries, total;   // workspace offsets (256-byte aligned) and size
+};
+
+BeamPlan beam_plan(int32_t batch, int32_t beams, int32_t vocab, int32_t out);
+hipError_t launch_beam_select(const BeamArgs& a, const BeamPlan& pl, char* ws, int io_dtype, hipStream_t stream);
+
+struct ReorderArgs {
+    char* pool;                  // [layers, num_slots, slot_bytes]
+    int64_t slot_bytes, layer_bytes;
+    int32_t layers, num_slots, batch, beams;
+    const int32_t* slots;        // [batch, beams]
+    const int32_t* parents;      // [batch, beams]
+    int32_t* slots_out;          // [batch, beams]
+};
+
+hipError_t launch_beam_reorder(const ReorderArgs& a, hipStream_t stream);
+
 }  // namespace gdr

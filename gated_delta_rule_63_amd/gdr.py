@@ -8,7 +8,9 @@ HIP kernels.  If the library has not been built, loading it raises immediately.
 
 Names follow the C entry points: ``gdr_recurrent_fwd``, ``gdr_chunk_fwd``,
 ``gdr_chunk_fwd_noalloc``, ``gdr_chunk_workspace_size``, ``gdr_decode_paged``,
-``gdr_gating_prepass``, ``gdr_decode_paged_gated``, ``gdr_kda_decode_fused``, ``gdr_status_string``.
+``gdr_gating_prepass``, ``gdr_decode_paged_gated``, ``gdr_kda_decode_fused``, ``gdr_linear_scan_fwd``,
+``gdr_linear_scan_bwd``, ``gdr_linear_decode_paged``, ``gdr_linear_workspace_size``, ``gdr_beam_select``,
+``gdr_beam_workspace_size``, ``gdr_beam_reorder``, ``gdr_status_string``.
 """
 from __future__ import annotations
 
@@ -28,6 +30,8 @@ GDR_ERROR_SCRATCH_LIMIT = 4
 GDR_NOALLOC_SCRATCH_BYTES = 64 << 20
 GDR_F32, GDR_BF16 = 0, 1
 GDR_GATE_SCALAR, GDR_GATE_PER_K = 0, 1
+GDR_LINEAR_LOG_DECAY, GDR_LINEAR_SIGMOID = 0, 1
+GDR_LINEAR_BLOCK = 64
 
 
 class GdrError(RuntimeError):
@@ -64,6 +68,28 @@ class KdaFront(ctypes.Structure):
         ("norm_weight", ctypes.c_void_p),
         ("norm_gate", ctypes.c_void_p),
         ("norm_eps", ctypes.c_float),
+    ]
+
+
+class LinearProblem(ctypes.Structure):
+    _fields_ = [
+        ("total_tokens", ctypes.c_int64),
+        ("num_seqs", ctypes.c_int32),
+        ("num_channels", ctypes.c_int32),
+        ("gate", ctypes.c_int),
+        ("io_dtype", ctypes.c_int),
+    ]
+
+
+class BeamProblem(ctypes.Structure):
+    _fields_ = [
+        ("batch", ctypes.c_int32),
+        ("beams", ctypes.c_int32),
+        ("vocab", ctypes.c_int32),
+        ("num_out", ctypes.c_int32),
+        ("row_stride", ctypes.c_int64),
+        ("eos_token", ctypes.c_int32),
+        ("io_dtype", ctypes.c_int),
     ]
 
 
@@ -125,6 +151,22 @@ def lib():
         L.gdr_kda_decode_fused.restype = ctypes.c_int
         L.gdr_kda_decode_fused.argtypes = [P, i32, vp, vp, vp, ctypes.POINTER(KdaFront), vp, vp, ctypes.c_int, i32, vp,
                                            i32, vp, vp]
+        LP, sz = ctypes.POINTER(LinearProblem), ctypes.c_size_t
+        L.gdr_linear_workspace_size.restype = sz
+        L.gdr_linear_workspace_size.argtypes = [LP]
+        L.gdr_linear_scan_fwd.restype = ctypes.c_int
+        L.gdr_linear_scan_fwd.argtypes = [LP, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.gdr_linear_scan_bwd.restype = ctypes.c_int
+        L.gdr_linear_scan_bwd.argtypes = [LP, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.gdr_linear_decode_paged.restype = ctypes.c_int
+        L.gdr_linear_decode_paged.argtypes = [LP, i32, vp, vp, vp, vp, ctypes.c_int, i32, vp, i32, vp, vp]
+        BP = ctypes.POINTER(BeamProblem)
+        L.gdr_beam_workspace_size.restype = sz
+        L.gdr_beam_workspace_size.argtypes = [BP]
+        L.gdr_beam_select.restype = ctypes.c_int
+        L.gdr_beam_select.argtypes = [BP, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.gdr_beam_reorder.restype = ctypes.c_int
+        L.gdr_beam_reorder.argtypes = [i32, i32, vp, vp, vp, vp, i32, i32, i64, vp]
         _lib = L
     return _lib
 
@@ -443,3 +485,225 @@ def gdr_kda_decode_fused(q, k, v, conv_weight, conv_state, gate_in, gate_weight,
                                     _ptr(state_indices), int(bool(commit)), _ptr(o), _stream(stream))
     _raise(st, "gdr_kda_decode_fused")
     return o
+
+
+# ---------------------------------------------------------------------------
+class _On:
+    """The device and stream of a call: outputs and workspaces that the binding makes are allocated on the
+    stream that uses them, and the launch goes to the tensors' device whatever the current one is."""
+
+    def __init__(self, device: torch.device, stream):
+        self.stream = torch.cuda.current_stream(device) if stream is None else stream
+        if self.stream.device != device:
+            raise ValueError(f"stream of {self.stream.device}, tensors on {device}")
+        self.ptr = ctypes.c_void_p(self.stream.cuda_stream)
+        # entering a stream's context costs a few microseconds: only where it is not current already
+        self.ctx = None
+        if torch.cuda.current_device() != device.index or stream is not None:
+            self.ctx = torch.cuda.stream(self.stream)
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+        return self.ptr
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+
+
+def _same_device(device: torch.device, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
+def _linear_problem(x, gate, gate_kind: int, num_seqs: int) -> LinearProblem:
+    if x.dim() != 2:
+        raise ValueError("x is [T, D]")
+    _check(x, "x")
+    io = _dtype_code(x.dtype)
+    if gate_kind not in (GDR_LINEAR_LOG_DECAY, GDR_LINEAR_SIGMOID):
+        raise ValueError("gate_kind is GDR_LINEAR_LOG_DECAY or GDR_LINEAR_SIGMOID")
+    _check(gate, "gate", x.shape, torch.float32 if gate_kind == GDR_LINEAR_LOG_DECAY else x.dtype)
+    return LinearProblem(x.shape[0], num_seqs, x.shape[1], gate_kind, io)
+
+
+def _linear_blocks(T: int) -> int:
+    return -(-T // GDR_LINEAR_BLOCK)
+
+
+def gdr_linear_workspace_size(x, gate, gate_kind: int, num_seqs: int) -> int:
+    p = _linear_problem(x, gate, gate_kind, num_seqs)
+    return int(lib().gdr_linear_workspace_size(ctypes.byref(p)))
+
+
+def _workspace(workspace, need: int, device):
+    if workspace is None:
+        return torch.empty(need, dtype=torch.uint8, device=device) if need else None
+    _check(workspace, "workspace", dtype=torch.uint8)
+    return workspace
+
+
+def gdr_linear_scan_fwd(x, gate, gate_kind: int, cu_seqlens=None, initial_state=None, y=None, final_state=None,
+                        output_final_state: bool = True, block_states=None, output_block_states: bool = False,
+                        workspace=None, stream=None):
+    """Gated linear recurrence over a packed batch: x [T, D], gate [T, D] (fp32 log-decay, or x's dtype
+    before the sigmoid), initial_state [N, D] fp32.  Returns (y, final_state or None), and block_states
+    [ceil(T / GDR_LINEAR_BLOCK), D] for gdr_linear_scan_bwd as a third where it is asked for or given.
+    ``workspace`` is a uint8 device tensor of at least gdr_linear_workspace_size bytes (allocated here if
+    absent)."""
+    N = _num_seqs(cu_seqlens, 1)
+    p = _linear_problem(x, gate, gate_kind, N)
+    T, D = x.shape
+    with _On(x.device, stream) as sp:
+        if y is None:
+            y = torch.empty_like(x)
+        if final_state is None and output_final_state:
+            final_state = torch.empty((N, D), dtype=torch.float32, device=x.device)
+        want_blocks = output_block_states or block_states is not None
+        if block_states is None and want_blocks:
+            block_states = torch.empty((_linear_blocks(T), D), dtype=torch.float32, device=x.device)
+        _check(y, "y", (T, D), x.dtype)
+        _check(initial_state, "initial_state", (N, D), torch.float32, optional=True)
+        _check(final_state, "final_state", (N, D), torch.float32, optional=True)
+        _check(block_states, "block_states", (_linear_blocks(T), D), torch.float32, optional=True)
+        ws = _workspace(workspace, int(lib().gdr_linear_workspace_size(ctypes.byref(p))), x.device)
+        _same_device(x.device, gate=gate, cu_seqlens=cu_seqlens, initial_state=initial_state, y=y,
+                     final_state=final_state, block_states=block_states, workspace=ws)
+        st = lib().gdr_linear_scan_fwd(ctypes.byref(p), _ptr(x), _ptr(gate), _ptr(cu_seqlens), _ptr(initial_state),
+                                       _ptr(y), _ptr(final_state), _ptr(block_states), _ptr(ws),
+                                       0 if ws is None else ws.numel(), sp)
+    _raise(st, "gdr_linear_scan_fwd")
+    return (y, final_state, block_states) if want_blocks else (y, final_state)
+
+
+def gdr_linear_scan_bwd(x, gate, gate_kind: int, dy, block_states, cu_seqlens=None, initial_state=None,
+                        d_final_state=None, dx=None, dgate=None, d_initial_state=None,
+                        output_d_initial_state: bool = True, workspace=None, stream=None):
+    """Gradients of gdr_linear_scan_fwd: dy [T, D] (x's dtype), block_states as the forward call wrote
+    them, d_final_state [N, D] fp32 or None.  Returns (dx, dgate, d_initial_state or None)."""
+    N = _num_seqs(cu_seqlens, 1)
+    p = _linear_problem(x, gate, gate_kind, N)
+    T, D = x.shape
+    _check(dy, "dy", (T, D), x.dtype)
+    _check(block_states, "block_states", (_linear_blocks(T), D), torch.float32)
+    with _On(x.device, stream) as sp:
+        dx = torch.empty_like(x) if dx is None else dx
+        dgate = torch.empty_like(gate) if dgate is None else dgate
+        if d_initial_state is None and output_d_initial_state:
+            d_initial_state = torch.empty((N, D), dtype=torch.float32, device=x.device)
+        _check(dx, "dx", (T, D), x.dtype)
+        _check(dgate, "dgate", (T, D), gate.dtype)
+        _check(initial_state, "initial_state", (N, D), torch.float32, optional=True)
+        _check(d_final_state, "d_final_state", (N, D), torch.float32, optional=True)
+        _check(d_initial_state, "d_initial_state", (N, D), torch.float32, optional=True)
+        ws = _workspace(workspace, int(lib().gdr_linear_workspace_size(ctypes.byref(p))), x.device)
+        _same_device(x.device, gate=gate, dy=dy, block_states=block_states, cu_seqlens=cu_seqlens,
+                     initial_state=initial_state, d_final_state=d_final_state, dx=dx, dgate=dgate,
+                     d_initial_state=d_initial_state, workspace=ws)
+        st = lib().gdr_linear_scan_bwd(ctypes.byref(p), _ptr(x), _ptr(gate), _ptr(cu_seqlens), _ptr(initial_state),
+                                       _ptr(block_states), _ptr(dy), _ptr(d_final_state), _ptr(dx), _ptr(dgate),
+                                       _ptr(d_initial_state), _ptr(ws), 0 if ws is None else ws.numel(), sp)
+    _raise(st, "gdr_linear_scan_bwd")
+    return dx, dgate, d_initial_state
+
+
+def gdr_linear_decode_paged(x, gate, gate_kind: int, pool, state_indices, cu_seqlens=None, max_q_len: int = 1,
+                            commit: bool = True, y=None, stream=None):
+    """Paged decode of the gated linear recurrence: pool [num_slots, D] (float32 or bfloat16),
+    state_indices int32 [N] (negative = padded).  Returns y (rows of padded sequences are left as they
+    were)."""
+    _check(state_indices, "state_indices", dtype=torch.int32)
+    N = state_indices.shape[0]
+    p = _linear_problem(x, gate, gate_kind, N)
+    T, D = x.shape
+    if cu_seqlens is not None:
+        _check(cu_seqlens, "cu_seqlens", (N + 1,), torch.int32)
+    if pool.dim() != 2:
+        raise ValueError("pool is [num_slots, D]")
+    _check(pool, "pool", (pool.shape[0], D))
+    with _On(x.device, stream) as sp:
+        y = torch.empty_like(x) if y is None else y
+        _check(y, "y", (T, D), x.dtype)
+        _same_device(x.device, gate=gate, pool=pool, state_indices=state_indices, cu_seqlens=cu_seqlens, y=y)
+        st = lib().gdr_linear_decode_paged(ctypes.byref(p), int(max_q_len), _ptr(x), _ptr(gate), _ptr(cu_seqlens),
+                                           _ptr(pool), _dtype_code(pool.dtype), pool.shape[0], _ptr(state_indices),
+                                           1 if commit else 0, _ptr(y), sp)
+    _raise(st, "gdr_linear_decode_paged")
+    return y
+
+
+# ---------------------------------------------------------------------------
+def _beam_problem(logits, num_out: int, eos_token: int) -> BeamProblem:
+    if logits.dim() != 3:
+        raise ValueError("logits is [batch, beams, vocab]")
+    if not logits.is_cuda:
+        raise ValueError("logits must be a device tensor")
+    B, W, V = logits.shape
+    sb, sw, sv = logits.stride()
+    # axes of one entry may have any stride
+    if (sv != 1 and V > 1) or (B > 1 and W > 1 and sb != W * sw):
+        raise ValueError("logits: the rows must be contiguous and evenly spaced")
+    row = sw if W > 1 else sb if B > 1 else V
+    return BeamProblem(B, W, V, int(num_out), row, int(eos_token), _dtype_code(logits.dtype))
+
+
+def gdr_beam_workspace_size(logits, num_out: int) -> int:
+    p = _beam_problem(logits, num_out, 0)
+    return int(lib().gdr_beam_workspace_size(ctypes.byref(p)))
+
+
+def gdr_beam_select(logits, scores, num_out: int, finished=None, eos_token: int = -1, out_scores=None,
+                    out_parents=None, out_tokens=None, workspace=None, stream=None):
+    """The num_out best candidates of each batch row: logits [batch, beams, vocab] (rows may be padded:
+    a view of wider rows is taken as it is), scores [batch, beams] fp32, finished [batch, beams] uint8 or
+    bool or None.  Returns (scores fp32, parents int32, tokens int32), each [batch, num_out]."""
+    p = _beam_problem(logits, num_out, eos_token)
+    B, W, _ = logits.shape
+    dev = logits.device
+    _check(scores, "scores", (B, W), torch.float32)
+    if finished is not None and finished.dtype == torch.bool:
+        finished = finished.view(torch.uint8)
+    _check(finished, "finished", (B, W), torch.uint8, optional=True)
+    with _On(dev, stream) as sp:
+        shape = (B, max(0, int(num_out)))
+        out_scores = torch.empty(shape, dtype=torch.float32, device=dev) if out_scores is None else out_scores
+        out_parents = torch.empty(shape, dtype=torch.int32, device=dev) if out_parents is None else out_parents
+        out_tokens = torch.empty(shape, dtype=torch.int32, device=dev) if out_tokens is None else out_tokens
+        _check(out_scores, "out_scores", shape, torch.float32)
+        _check(out_parents, "out_parents", shape, torch.int32)
+        _check(out_tokens, "out_tokens", shape, torch.int32)
+        ws = _workspace(workspace, int(lib().gdr_beam_workspace_size(ctypes.byref(p))), dev)
+        _same_device(dev, scores=scores, finished=finished, out_scores=out_scores, out_parents=out_parents,
+                     out_tokens=out_tokens, workspace=ws)
+        st = lib().gdr_beam_select(ctypes.byref(p), _ptr(logits), _ptr(scores), _ptr(finished), _ptr(out_scores),
+                                   _ptr(out_parents), _ptr(out_tokens), _ptr(ws), 0 if ws is None else ws.numel(), sp)
+    _raise(st, "gdr_beam_select")
+    return out_scores, out_parents, out_tokens
+
+
+def gdr_beam_reorder(pool, state_indices, parents, slot_dim: int = 0, state_indices_out=None, stream=None):
+    """Moves the parents' states to their children: pool [num_slots, ...] (slot_dim 0, as the decode entry
+    points take it) or [layers, num_slots, ...] (slot_dim 1), state_indices and parents int32 [batch,
+    beams].  Returns the new beams' slots, int32 [batch, beams]; give the old ones to the calls for all
+    pools of a model."""
+    if slot_dim not in (0, 1) or pool.dim() < slot_dim + 1:
+        raise ValueError("pool is [num_slots, ...] with slot_dim 0 or [layers, num_slots, ...] with slot_dim 1")
+    if state_indices.dim() != 2:
+        raise ValueError("state_indices is [batch, beams]")
+    B, W = state_indices.shape
+    _check(pool, "pool")
+    _check(state_indices, "state_indices", dtype=torch.int32)
+    _check(parents, "parents", (B, W), torch.int32)
+    layers = pool.shape[0] if slot_dim else 1
+    slots = pool.shape[slot_dim]
+    slot_bytes = pool.element_size() * math.prod(pool.shape[slot_dim + 1:])
+    with _On(pool.device, stream) as sp:
+        out = torch.empty_like(state_indices) if state_indices_out is None else state_indices_out
+        _check(out, "state_indices_out", (B, W), torch.int32)
+        _same_device(pool.device, state_indices=state_indices, parents=parents, state_indices_out=out)
+        st = lib().gdr_beam_reorder(B, W, _ptr(parents), _ptr(state_indices), _ptr(out), _ptr(pool), layers, slots,
+                                    slot_bytes, sp)
+    _raise(st, "gdr_beam_reorder")
+    return out

@@ -339,6 +339,145 @@ GDR_API gdr_status gdr_kda_decode_fused(const gdr_problem* p, int32_t max_q_len,
                                 const int32_t* state_indices, int32_t commit,
                                 void* o, void* hip_stream);
 
+/*
+ * Gated linear recurrence: one state value per channel, without keys or values (the diagonal
+ * recurrence that hybrid stacks put beside delta-rule layers).  Per channel d of sequence n:
+ *
+ *     h[t] = a[t] h[t-1] + b[t]      y[t] = h[t]      h before the first token: initial_state or 0
+ *     GDR_LINEAR_LOG_DECAY   gate = g [T, D] fp32, natural log, g <= 0 (-inf: a = 0):  a = e^g, b = x
+ *     GDR_LINEAR_SIGMOID     gate = z [T, D] io_dtype:  a = sigmoid(z), b = (1 - a) x
+ *
+ * and its gradients, with D[t] the gradient of h[t]:
+ *
+ *     D[t] = dy[t] + a[t+1] D[t+1]   (+ d_final_state at a sequence's last token)
+ *     LOG_DECAY  dx = D, dg = D a h[t-1]      SIGMOID  dx = (1 - a) D, dz = D a (1 - a) (h[t-1] - x)
+ *     d_initial_state = a[first] D[first]
+ *
+ * Layouts: x, y, dy, dx [T, D] io_dtype; gate, dgate [T, D]; states [N, D] fp32; cu_seqlens as above,
+ * except that cu_seqlens[N] may be less than T: rows behind the last sequence are neither read nor
+ * written.  States are held in fp32 throughout; every channel count >= 1 is accepted.  An infinity or a
+ * NaN stays within its sequence and channel.
+ */
+typedef enum gdr_linear_gate {
+    GDR_LINEAR_LOG_DECAY = 0,
+    GDR_LINEAR_SIGMOID = 1
+} gdr_linear_gate;
+
+#define GDR_LINEAR_BLOCK 64  /* tokens per row of block_states */
+
+typedef struct gdr_linear_problem {
+    int64_t total_tokens;   /* T                                                         */
+    int32_t num_seqs;       /* N <= 65535                                                */
+    int32_t num_channels;   /* D >= 1                                                    */
+    gdr_linear_gate gate;
+    gdr_dtype io_dtype;
+} gdr_linear_problem;
+
+/* Bytes of device workspace either scan needs (0 where one block of tokens covers the batch, and for
+ * invalid metadata). */
+GDR_API size_t gdr_linear_workspace_size(const gdr_linear_problem* p);
+
+/*
+ * gdr_linear_scan_fwd -- the recurrence over a packed varlen batch, parallel over tokens and channels.
+ *
+ *   cu_seqlens     int32 [N+1]; may be NULL only when N == 1 (one sequence of T tokens)
+ *   initial_state  fp32 [N, D] or NULL (zeros)
+ *   final_state    fp32 [N, D] or NULL.  An empty sequence's is its initial state
+ *   block_states   fp32 [ceil(T / GDR_LINEAR_BLOCK), D] or NULL: the state behind the tokens before
+ *                  each block, which gdr_linear_scan_bwd takes
+ *   workspace      gdr_linear_workspace_size(p) bytes, 256-byte aligned, contents need not be
+ *                  initialised; calls that may overlap need one each
+ */
+GDR_API gdr_status gdr_linear_scan_fwd(const gdr_linear_problem* p,
+                               const void* x, const void* gate,
+                               const int32_t* cu_seqlens, const float* initial_state,
+                               void* y, float* final_state, float* block_states,
+                               void* workspace, size_t workspace_bytes, void* hip_stream);
+
+/*
+ * gdr_linear_scan_bwd -- the gradients.  x, gate, cu_seqlens and initial_state are the forward call's,
+ * block_states is what it wrote.
+ *
+ *   d_final_state    fp32 [N, D] or NULL (zeros)
+ *   dx, dgate        [T, D] (written)
+ *   d_initial_state  fp32 [N, D] or NULL (not written)
+ */
+GDR_API gdr_status gdr_linear_scan_bwd(const gdr_linear_problem* p,
+                               const void* x, const void* gate,
+                               const int32_t* cu_seqlens, const float* initial_state,
+                               const float* block_states, const void* dy, const float* d_final_state,
+                               void* dx, void* dgate, float* d_initial_state,
+                               void* workspace, size_t workspace_bytes, void* hip_stream);
+
+/*
+ * gdr_linear_decode_paged -- 1..12 tokens of each sequence against a paged pool [num_slots, D] of
+ * pool_dtype.  max_q_len, cu_seqlens, num_slots, state_indices (negative: the sequence is skipped, its
+ * y rows untouched), commit as in gdr_decode_paged.
+ */
+GDR_API gdr_status gdr_linear_decode_paged(const gdr_linear_problem* p, int32_t max_q_len,
+                                   const void* x, const void* gate, const int32_t* cu_seqlens,
+                                   void* pool, gdr_dtype pool_dtype, int32_t num_slots,
+                                   const int32_t* state_indices, int32_t commit,
+                                   void* y, void* hip_stream);
+
+/*
+ * Beam search over paged states: gdr_beam_select picks the next candidates from a step's logits,
+ * gdr_beam_reorder moves the chosen parents' states (any pool of the decode entry points).
+ *
+ * Candidate (w, v) of a batch row scores  scores[w] + logits[w, v] - log sum_u e^logits[w, u].
+ * The num_out best are written in descending order, equal ones by the lower w * vocab + v; the order
+ * is that of the scores in 64 bits, whatever io_dtype.
+ *   - a -inf or NaN logit has probability zero; a row without a finite logit, or with a +inf one, and a
+ *     beam whose score is not finite have no candidate above -inf
+ *   - an ended beam (finished[w] != 0) has one candidate, (w, eos_token) with its score unchanged
+ *   - where fewer than num_out candidates score above -inf, those at -inf follow by the lower index
+ */
+typedef struct gdr_beam_problem {
+    int32_t batch;          /* batch * beams <= 65535                                     */
+    int32_t beams;          /* 1..32                                                      */
+    int32_t vocab;          /* 1..2^20                                                    */
+    int32_t num_out;        /* 1..64, at most vocab                                       */
+    int64_t row_stride;     /* elements from one row of logits to the next, >= vocab      */
+    int32_t eos_token;      /* read with `finished` only: 0..vocab-1                      */
+    gdr_dtype io_dtype;     /* of the logits                                              */
+} gdr_beam_problem;
+
+/* Bytes of device workspace gdr_beam_select needs; 0 for invalid metadata and for an empty batch. */
+GDR_API size_t gdr_beam_workspace_size(const gdr_beam_problem* p);
+
+/*
+ * gdr_beam_select
+ *   logits       [batch, beams, vocab] io_dtype, rows row_stride elements apart
+ *   scores       [batch, beams] fp32: each beam's log-probability so far
+ *   finished     [batch, beams] bytes, or NULL (none has ended)
+ *   out_scores, out_parents, out_tokens   [batch, num_out] fp32, int32 (beam w), int32 (token v)
+ *   workspace    gdr_beam_workspace_size(p) bytes, 256-byte aligned, need not be initialised; calls
+ *                that may overlap need one each
+ */
+GDR_API gdr_status gdr_beam_select(const gdr_beam_problem* p, const void* logits, const float* scores,
+                           const uint8_t* finished, float* out_scores, int32_t* out_parents,
+                           int32_t* out_tokens, void* workspace, size_t workspace_bytes,
+                           void* hip_stream);
+
+/*
+ * gdr_beam_reorder -- beam j of batch row b goes on from the state of beam parents[b, j].  A parent's
+ * first child keeps the parent's slot; every other child gets, in order, the slot of a parent without
+ * children, and the state is copied there in every layer.  Nothing else of the pool is written.
+ *
+ *   parents            int32 [batch, beams], values 0..beams-1
+ *   state_indices      int32 [batch, beams]: each beam's slot, distinct and < num_slots
+ *   state_indices_out  int32 [batch, beams] (written): the slots of the new beams; must not be
+ *                      state_indices or parents.  The same call for another pool that is indexed by
+ *                      the same slots takes the same state_indices
+ *   pool               [num_layers, num_slots] slots of slot_bytes bytes (a multiple of 2) each
+ * A batch row that holds a negative slot is padded: its slots stay and nothing is copied (so for a row
+ * with a slot or a parent outside its range).  beams is 1..32, batch * beams and num_layers <= 65535.
+ */
+GDR_API gdr_status gdr_beam_reorder(int32_t batch, int32_t beams, const int32_t* parents,
+                            const int32_t* state_indices, int32_t* state_indices_out,
+                            void* pool, int32_t num_layers, int32_t num_slots, int64_t slot_bytes,
+                            void* hip_stream);
+
 /* Human-readable name of a status code (static string, never NULL; unknown codes map to
  * "GDR_ERROR_UNKNOWN").  The codes stand for the loud contract checks of the pages' entry
  * points: a device-capability check (cuLA PR #113, review thread on SM90 availability) and a

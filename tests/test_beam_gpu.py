@@ -1,0 +1,264 @@
+"""Beam search on the GPU: selection against the fp64 oracle (parents and tokens equal, scores to the
+rounding of an fp32 value: the sums behind a score are good to 3e-6 absolutely, half the distance below
+which the kernel forms them again in 64 bits), state reordering bit for bit, and both in a decode loop."""
+import numpy as np
+import pytest
+import torch
+
+from _dev import f64, to_dev, to_host
+from gated_delta_rule_63_amd import gdr, inputs
+from oracle import beam
+
+pytestmark = pytest.mark.gpu
+
+
+def _dev_logits(lg, io, pad):
+    t = to_dev(lg.astype(np.float32))
+    wide = torch.full(lg.shape[:2] + (lg.shape[2] + pad,), 50.0, device="cuda")
+    wide[:, :, :lg.shape[2]] = t
+    return wide.to(torch.bfloat16 if io == "bf16" else torch.float32)[:, :, :lg.shape[2]]
+
+
+def _compare(lg, sc, K, io, pad=0, finished=None, eos=-1):
+    d = _dev_logits(lg, io, pad)
+    fin = None if finished is None else to_dev(finished.astype(np.uint8))
+    s, p, t = gdr.gdr_beam_select(d, to_dev(sc), K, finished=fin, eos_token=eos)
+    torch.cuda.synchronize()
+    want = beam.select(f64(d), sc.astype(np.float64), K, finished, eos)
+    assert np.array_equal(to_host(p), want[1]), "parents"
+    assert np.array_equal(to_host(t), want[2]), "tokens"
+    got = f64(s)
+    assert np.array_equal(np.isneginf(got), np.isneginf(want[0]))
+    fine = np.isfinite(want[0])
+    assert np.all(np.abs(got - want[0])[fine] <= 3e-6 + 2.0 ** -24 * np.abs(want[0])[fine])
+
+
+def _logits(seed, B, W, V, sd=2.5):
+    return np.random.default_rng(seed).normal(size=(B, W, V)) * sd
+
+
+def _scores(seed, B, W):
+    return (-10 - np.cumsum(np.random.default_rng(seed).uniform(0, 1.5, (B, W)), 1)).astype(np.float32)
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("B,W,V,K,pad", [(1, 1, 1, 1, 0), (1, 1, 64, 64, 0), (3, 4, 1000, 8, 0), (2, 5, 4097, 5, 3),
+                                         (2, 32, 777, 64, 1), (1, 4, 32000, 8, 0), (2, 3, 50257, 6, 47),
+                                         (1, 16, 20001, 1, 7), (1, 2, 262147, 17, 0), (2, 1, 70000, 64, 8)])
+def test_sizes(B, W, V, K, pad, io):
+    _compare(_logits(V, B, W, V), _scores(K, B, W), K, io, pad)
+
+
+def test_largest_vocabulary_and_many_rows():
+    _compare(_logits(1, 1, 1, 1 << 20), _scores(1, 1, 1), 64, "bf16")
+    _compare(_logits(2, 150, 7, 600), _scores(2, 150, 7), 14, "f32")
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_ties_go_to_the_lower_index(io):
+    for sd in (0.0, 0.25):  # all equal; a handful of distinct values
+        lg = np.round(_logits(3, 2, 4, 9000, sd) * 4) / 4
+        _compare(lg, np.zeros((2, 4), np.float32), 33, io)
+        _compare(lg[:, :1], np.zeros((2, 1), np.float32), 64, io)
+    # equal beams: the same logits and scores
+    lg = np.repeat(_logits(4, 1, 1, 5000), 6, axis=1)
+    _compare(lg, np.full((1, 6), -3.0, np.float32), 12, io)
+    lg = np.zeros((1, 2, 3000))
+    lg[..., ::2] = -0.0
+    _compare(lg, np.zeros((1, 2), np.float32), 20, io)
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_concentrated_logits(io):
+    """Every large logit in few lanes' hands (neighbours, or a fixed distance apart), and sorted rows."""
+    V = 40000
+    for step in (1, 8, 256, 2048):
+        lg = _logits(5, 1, 2, V, 0.5)
+        at = (np.arange(300) * step) % V
+        lg[:, :, np.unique(at)] += 10 + np.random.default_rng(6).normal(size=(1, 2, len(np.unique(at))))
+        _compare(lg, _scores(7, 1, 2), 64, io)
+    up = np.sort(_logits(8, 1, 2, V), axis=2)
+    _compare(up, _scores(9, 1, 2), 50, io)
+    _compare(up[:, :, ::-1].copy(), _scores(9, 1, 2), 50, io)
+
+
+@pytest.mark.parametrize("fill", [-np.inf, np.nan, -3.3e38])
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_masked_tokens(fill, io):
+    r = np.random.default_rng(10)
+    for kept in (0, 1, 3, 100):  # tokens that the mask leaves of each row
+        lg = np.full((2, 3, 6001), fill)
+        for b in range(2):
+            for w in range(3):
+                at = r.permutation(6001)[:kept]
+                lg[b, w, at] = r.normal(size=kept) * 3
+        if np.isfinite(fill):
+            lg = lg.astype(np.float32).astype(np.float64)
+        _compare(lg, _scores(11, 2, 3), 16, io)
+    lg = _logits(12, 2, 3, 6001)
+    lg[0, 1] = fill                       # one row with nothing left
+    lg[1, :2] = fill
+    _compare(lg, _scores(13, 2, 3), 20, io)
+
+
+def test_rows_and_scores_without_candidates():
+    lg = _logits(14, 3, 4, 900)
+    sc = _scores(15, 3, 4)
+    sc[0, 1:] = -np.inf                   # the first step of a search: one live beam
+    sc[1] = [-np.inf, np.nan, np.inf, -np.inf]
+    lg[2, 0, 5] = np.inf
+    _compare(lg, sc, 30, "f32")
+    _compare(lg, sc, 30, "bf16")
+    _compare(lg[:, :, :3], sc, 3, "f32")
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_ended_beams(io):
+    r = np.random.default_rng(16)
+    lg, sc = _logits(17, 4, 5, 3000), _scores(18, 4, 5)
+    fin = (r.uniform(size=(4, 5)) < 0.5).astype(np.uint8)
+    fin[2], fin[3] = 1, 0
+    sc[2, 1] = -np.inf
+    for eos in (0, 2, 2999):
+        _compare(lg, sc, 10, io, finished=fin, eos=eos)
+
+
+def test_near_ties_between_beams_are_settled_in_64_bits():
+    """Beams whose candidates differ by 1e-8 to 1e-6, below what 32-bit sums resolve."""
+    r = np.random.default_rng(19)
+    for trial in range(6):
+        V = 5000 + trial
+        base = r.normal(size=V) * 2
+        lg = np.stack([r.permutation(base) for _ in range(6)])[None].astype(np.float32).astype(np.float64)
+        # every row has the same sum; scores that differ by one fp32 step (5e-7 at 5) or not at all
+        sc = np.full((1, 6), -5.0, np.float32)
+        for w in range(1, 6):
+            sc[0, w] = np.nextafter(sc[0, w - 1], np.float32(0)) if trial % 2 else sc[0, 0]
+        lg[0, :, :] += (np.arange(6) * 1e-7)[:, None]
+        lg = lg.astype(np.float32).astype(np.float64)
+        d = _dev_logits(lg, "f32", 0)
+        s, p, t = gdr.gdr_beam_select(d, to_dev(sc), 12)
+        p, t = to_host(p)[0], to_host(t)[0]
+        x = f64(d)[0]
+        val = lambda w, v: sc[0, w].astype(np.float64) + (x[w, v] - (x[w].max() + np.log(np.exp(x[w] - x[w].max()).sum())))  # noqa: E731
+        got = [val(w, v) for w, v in zip(p, t)]
+        every = np.sort(np.concatenate([sc[0, w].astype(np.float64) + (x[w] - (x[w].max() + np.log(np.exp(x[w] - x[w].max()).sum()))) for w in range(6)]))[::-1]
+        # in descending order and the best ones, to the rounding of 64-bit sums over V terms
+        assert np.allclose(got, every[:12], rtol=0, atol=1e-12)
+
+
+def test_select_captured_and_on_another_stream():
+    lg, sc = _logits(20, 3, 4, 20000), _scores(21, 3, 4)
+    d, dsc = _dev_logits(lg, "bf16", 0), to_dev(sc)
+    want = gdr.gdr_beam_select(d, dsc, 8)
+    ws = torch.full((gdr.gdr_beam_workspace_size(d, 8),), 0x5A, dtype=torch.uint8, device="cuda")
+    out = [torch.empty_like(t) for t in want]
+    args = dict(out_scores=out[0], out_parents=out[1], out_tokens=out[2], workspace=ws)
+    gdr.gdr_beam_select(d, dsc, 8, **args)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        gdr.gdr_beam_select(d, dsc, 8, **args)
+    for _ in range(3):
+        for t in out:
+            t.zero_()
+        g.replay()
+        gdr.gdr_beam_select(d, dsc, 8)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, want))
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    other = gdr.gdr_beam_select(d, dsc, 8, stream=s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(other, want))
+
+
+# ---------------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("B,W,layers,shape", [(1, 1, 1, (8,)), (3, 4, 1, (2, 128, 64)), (2, 32, 3, (77,)), (5, 7, 2, (1, 1)),
+                                              (1, 8, 24, (4096,)), (4, 5, 1, (32, 65, 64))])
+def test_reorder(B, W, layers, shape, dt):
+    r = np.random.default_rng(B * W)
+    slots = B * W + 5
+    for trial in range(3):
+        pool = torch.randn(layers, slots, *shape, device="cuda").to(dt)
+        idx = r.permutation(slots)[:B * W].reshape(B, W).astype(np.int32)
+        par = r.integers(0, W, (B, W)).astype(np.int32)
+        if trial == 1:
+            par[:] = 0
+        if trial == 2:
+            par = np.tile(np.arange(W, dtype=np.int32)[::-1], (B, 1)).copy()
+        want, moves = beam.reorder(idx, par, slots)
+        after = pool.clone()
+        for s, dst in moves:
+            after[:, dst] = pool[:, s]
+        new = gdr.gdr_beam_reorder(pool, to_dev(idx), to_dev(par), slot_dim=1)
+        torch.cuda.synchronize()
+        assert np.array_equal(to_host(new), want)
+        assert torch.equal(pool, after)
+        assert trial != 2 or not moves
+
+
+def test_reorder_leaves_padded_and_invalid_rows():
+    idx = np.array([[0, 1, 2], [3, -1, 5], [6, 7, 8], [9, 10, 12], [-1, -1, -1]], np.int32)
+    par = np.array([[0, 0, 0], [0, 0, 0], [2, 2, 3], [1, 1, 1], [0, 0, 0]], np.int32)
+    pool = torch.randn(12, 40, device="cuda")
+    before = pool.clone()
+    new = gdr.gdr_beam_reorder(pool, to_dev(idx), to_dev(par))
+    want = idx.copy()
+    before[1] = before[2] = before[0]
+    torch.cuda.synchronize()
+    assert np.array_equal(to_host(new), want) and torch.equal(pool, before)
+
+
+def test_reorder_unaligned_slots():
+    for n in (1, 3, 6, 10):                   # slots of 2, 6, 12, 20 bytes
+        pool = torch.randn(2, 8, n, device="cuda").bfloat16()
+        after = pool.clone()
+        idx, par = np.array([[7, 2, 5]], np.int32), np.array([[1, 1, 1]], np.int32)
+        new = gdr.gdr_beam_reorder(pool, to_dev(idx), to_dev(par), slot_dim=1)
+        after[:, 7] = after[:, 5] = after[:, 2]
+        torch.cuda.synchronize()
+        assert to_host(new).tolist() == [[2, 7, 5]] and torch.equal(pool, after)
+
+
+# ---------------------------------------------------------------------------------------------------
+def test_beam_search_over_paged_states():
+    """Decode, selection and reordering together: a small model of one delta-rule layer and one linear
+    layer, 2 searches of 3 beams for 6 steps.  The states in the slots of each beam, after every step, equal
+    the states of running that beam's whole token history from scratch."""
+    torch.manual_seed(5)
+    dev, B, W, H, K, D, V = "cuda", 2, 3, 2, 64, 128, 50
+    emb = {n: torch.randn(V, *s, device=dev) for n, s in dict(q=(H, K), k=(H, K), v=(H, K), x=(D,), g=(D,)).items()}
+    emb["q"], emb["k"] = (torch.nn.functional.normalize(emb[n], dim=-1) for n in "qk")
+    emb["g"] = -emb["g"].abs()
+    decay, beta = -torch.rand(V, H, device=dev), torch.rand(V, H, device=dev)
+    head = torch.randn(H * K + D, V, device=dev) * 0.7
+    pool_m = torch.zeros(B * W + 2, H, K, K, device=dev)
+    pool_c = torch.zeros(B * W + 2, D, device=dev)
+    idx = torch.randperm(B * W + 2, device=dev)[:B * W].view(B, W).int()
+    scores = torch.tensor([[0.0] + [-np.inf] * (W - 1)] * B, device=dev)
+    tokens = torch.zeros(B, W, dtype=torch.int32, device=dev)
+    hist = [[[0] for _ in range(W)] for _ in range(B)]
+
+    def step(tok, pm, pc, slots):
+        t = tok.flatten().long()
+        o = gdr.gdr_decode_paged(emb["q"][t], emb["k"][t], emb["v"][t], decay[t], beta[t], pm, slots, scale=1.0)
+        y = gdr.gdr_linear_decode_paged(emb["x"][t], emb["g"][t], gdr.GDR_LINEAR_LOG_DECAY, pc, slots)
+        return torch.cat([o.flatten(1), y], 1) @ head
+
+    for _ in range(6):
+        logits = step(tokens, pool_m, pool_c, idx.flatten()).view(B, W, V)
+        scores, parents, tokens = gdr.gdr_beam_select(logits, scores, W)
+        new = gdr.gdr_beam_reorder(pool_m, idx, parents)
+        assert torch.equal(new, gdr.gdr_beam_reorder(pool_c, idx, parents))
+        idx = new
+        par, tok = parents.tolist(), tokens.tolist()
+        hist = [[hist[b][par[b][j]] + [tok[b][j]] for j in range(W)] for b in range(B)]
+        for b in range(B):
+            for j in range(W):
+                pm, pc = torch.zeros(1, H, K, K, device=dev), torch.zeros(1, D, device=dev)
+                zero = torch.zeros(1, dtype=torch.int32, device=dev)
+                for v in hist[b][j][:-1]:
+                    step(torch.tensor([v], device=dev), pm, pc, zero)
+                assert torch.equal(pool_m[idx[b, j]], pm[0]) and torch.equal(pool_c[idx[b, j]], pc[0])
