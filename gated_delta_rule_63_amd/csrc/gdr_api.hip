@@ -416,7 +416,8 @@ gdr_status check_linear(const gdr_linear_problem* p) {
     if (p->total_tokens < 0 || p->num_seqs < 0 || p->num_channels <= 0) return GDR_ERROR_INVALID_VALUE;
     if (p->gate != GDR_LINEAR_LOG_DECAY && p->gate != GDR_LINEAR_SIGMOID) return GDR_ERROR_INVALID_VALUE;
     if (!dtype_ok(p->io_dtype)) return GDR_ERROR_INVALID_VALUE;
-    if (p->num_seqs > 65535) return GDR_ERROR_NOT_SUPPORTED;  // grid y limit
+    if (p->num_seqs > 65535) return GDR_ERROR_NOT_SUPPORTED;         // grid y limit
+    if (p->num_channels > (1 << 24)) return GDR_ERROR_NOT_SUPPORTED;  // row offsets are 32-bit
     // the launch grid counts tiles of 64 tokens by 64 channels in 32 bits
     const int64_t tiles = (p->total_tokens + 63) / 64, across = ((int64_t)p->num_channels + 63) / 64;
     if (tiles > 0x7FFFFFFF / across) return GDR_ERROR_NOT_SUPPORTED;
@@ -469,9 +470,8 @@ gdr_status gdr_linear_scan_fwd(const gdr_linear_problem* p, const void* x, const
     gdr::LinearArgs a{};
     a.x = x; a.gate = gate; a.cu = cu_seqlens; a.h0 = initial_state; a.y = y; a.ht = final_state;
     a.block_states = block_states;
-    a.runs = static_cast<float2*>(workspace);
     a.T = p->total_tokens; a.D = p->num_channels; a.N = p->num_seqs;
-    return status_of(gdr::launch_linear_scan(a, p->gate, p->io_dtype, false, stream));
+    return status_of(gdr::launch_linear_scan(a, static_cast<char*>(workspace), p->gate, p->io_dtype, false, stream));
 }
 
 gdr_status gdr_linear_scan_bwd(const gdr_linear_problem* p, const void* x, const void* gate, const int32_t* cu_seqlens,
@@ -490,10 +490,9 @@ gdr_status gdr_linear_scan_bwd(const gdr_linear_problem* p, const void* x, const
     gdr::LinearArgs a{};
     a.x = x; a.gate = gate; a.cu = cu_seqlens; a.h0 = initial_state;
     a.block_states = const_cast<float*>(block_states);
-    a.runs = static_cast<float2*>(workspace);
     a.dy = dy; a.dht = d_final_state; a.dx = dx; a.dgate = dgate; a.dh0 = d_initial_state;
     a.T = p->total_tokens; a.D = p->num_channels; a.N = p->num_seqs;
-    return status_of(gdr::launch_linear_scan(a, p->gate, p->io_dtype, true, stream));
+    return status_of(gdr::launch_linear_scan(a, static_cast<char*>(workspace), p->gate, p->io_dtype, true, stream));
 }
 
 gdr_status gdr_linear_decode_paged(const gdr_linear_problem* p, int32_t max_q_len, const void* x, const void* gate,

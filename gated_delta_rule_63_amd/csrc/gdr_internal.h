@@ -155,7 +155,8 @@ struct LinearArgs {
     void* y;                     // [T, D] io dtype
     float* ht;                   // [N, D] or NULL
     float* block_states;         // [ceil(T / kLinearBlock), D]: the state entering each block, or NULL
-    float2* runs;                // workspace: a word per (tile, channel)
+    uint32_t* ticket;            // workspace, set by the launcher: tiles handed out so far
+    uint64_t* runs;              // workspace: a word per (tile, channel)
     // backward
     const void* dy;              // [T, D] io dtype
     const float* dht;            // [N, D] or NULL (zeros)
@@ -174,7 +175,7 @@ struct LinearArgs {
 
 size_t linear_workspace(int64_t T, int64_t D);
 // kind 0: log-decay, 1: sigmoid.  Requires a.T >= 1 and a workspace of linear_workspace bytes.
-hipError_t launch_linear_scan(const LinearArgs& a, int kind, int io_dtype, bool backward, hipStream_t stream);
+hipError_t launch_linear_scan(const LinearArgs& a, char* ws, int kind, int io_dtype, bool backward, hipStream_t stream);
 hipError_t launch_linear_decode(const LinearArgs& a, int kind, int io_dtype, int st_dtype, hipStream_t stream);
 // dst[n] = src[n] (zeros without src) for empty sequences, or for all when cu is NULL.
 hipError_t launch_linear_empty(const int32_t* cu, const float* src, float* dst, int32_t N, int64_t D, hipStream_t stream);

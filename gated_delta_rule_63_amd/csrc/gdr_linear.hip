@@ -28,13 +28,79 @@ constexpr int kThreads = 64 * kWaves;
 constexpr int kLogGate = 0;
 
 // ---- a lane's VEC channels of one token, as loaded ----
+// hide(): the compiler forgets what it derived from the value, so that unpacked or decoded forms are made
+// again in the next pass over the tile instead of holding a second set of registers across the barriers.
+__device__ __forceinline__ void hide(float& x) { asm volatile("" : "+v"(x)); }
+
 template <typename T, int VEC> struct Chan;
-template <typename T> struct Chan<T, 4> : RawVec<T, 4> {
-    __device__ __forceinline__ static void put(void* p, int64_t i, const float* in) { Vec<T, 4>::store(p, i, in); }
+template <> struct Chan<float, 4> {
+    f32x4_t v;
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+        v = __builtin_bit_cast(f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
+    }
+    __device__ __forceinline__ void get(float* out) const {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) out[e] = v[e];
+    }
+    __device__ __forceinline__ void hide() { asm volatile("" : "+v"(v)); }
+    __device__ __forceinline__ static void put(__amdgpu_buffer_rsrc_t r, uint32_t off, const float* in) {
+        BufStore<float, 4>::store<0>(r, off, in);
+    }
 };
-template <typename T> struct Chan<T, 1> : RawElem<T> {
-    __device__ __forceinline__ void get(float* out) const { out[0] = RawElem<T>::get(); }
-    __device__ __forceinline__ static void put(void* p, int64_t i, const float* in) { Elem<T>::store(p, i, in[0]); }
+template <> struct Chan<bf16_t, 4> {
+    u32x2_t w;
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+        w = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, 0));
+    }
+    __device__ __forceinline__ void get(float* out) const {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            out[2 * e] = __uint_as_float(w[e] << 16);
+            out[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
+        }
+    }
+    __device__ __forceinline__ void hide() { asm volatile("" : "+v"(w)); }
+    __device__ __forceinline__ static void put(__amdgpu_buffer_rsrc_t r, uint32_t off, const float* in) {
+        BufStore<bf16_t, 4>::store<0>(r, off, in);
+    }
+};
+template <> struct Chan<float, 1> {
+    uint32_t w;
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+        w = __builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0);
+    }
+    __device__ __forceinline__ void get(float* out) const { out[0] = __uint_as_float(w); }
+    __device__ __forceinline__ void hide() { asm volatile("" : "+v"(w)); }
+    __device__ __forceinline__ static void put(__amdgpu_buffer_rsrc_t r, uint32_t off, const float* in) {
+        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(in[0]), r, off, 0, 0);
+    }
+};
+template <> struct Chan<bf16_t, 1> {
+    uint32_t w;
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+        w = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, off, 0, 0);
+    }
+    __device__ __forceinline__ void get(float* out) const { out[0] = __uint_as_float(w << 16); }
+    __device__ __forceinline__ void hide() { asm volatile("" : "+v"(w)); }
+    __device__ __forceinline__ static void put(__amdgpu_buffer_rsrc_t r, uint32_t off, const float* in) {
+        __builtin_amdgcn_raw_buffer_store_b16(f32_to_bf16(in[0]), r, off, 0, 0);
+    }
+};
+
+// A wave's rows of a [T, D] tensor: token w0 + i, this lane's channels.  The resource ends behind the last
+// valid row, and lanes without channels get an offset behind every resource, so that reads there give zeros
+// and writes nothing without a branch (rows of at most 2^24 channels keep every offset below 2^31).
+template <typename T> struct Rows {
+    __amdgpu_buffer_rsrc_t r;
+    uint32_t off, row;
+    __device__ __forceinline__ Rows(const void* p, int64_t D, int64_t w0, int rows, int64_t c, bool active) {
+        constexpr int B = Elem<T>::bytes;
+        char* base = const_cast<char*>(static_cast<const char*>(p)) + w0 * D * B;
+        r = __builtin_amdgcn_make_buffer_rsrc(base, 0, (int)(rows * D * B), 0x00020000);
+        off = active ? (uint32_t)(c * B) : 0x80000000u;
+        row = (uint32_t)(D * B);
+    }
+    __device__ __forceinline__ uint32_t at(int i) const { return off + i * row; }
 };
 
 template <int KIND, typename IO> struct GateT { typedef IO T; };
@@ -107,7 +173,10 @@ __device__ __forceinline__ float2 compose(float2 r1, float2 r2) {
 template <int KIND> struct RunDecay;
 template <> struct RunDecay<kLogGate> {
     float G = 0.0f;
-    __device__ __forceinline__ void add(float raw, float) { G += raw; }
+    __device__ __forceinline__ void add(float raw, float) {
+        G += raw;
+        hide(G);  // summed here and now, not from 64 kept gates at the end
+    }
     __device__ __forceinline__ float get() const { return encode_gate_log(G); }
 };
 template <> struct RunDecay<1> {
@@ -116,6 +185,8 @@ template <> struct RunDecay<1> {
         const Decay d(v);
         A = fmaf(d.a, A, d.rest * A);
         Q = fmaf(one_minus(v), 1.0f - Q, Q);
+        hide(A);
+        hide(Q);
     }
     __device__ __forceinline__ float get() const { return pick(A, Q); }
 };
@@ -127,37 +198,47 @@ struct Borders {
     __device__ __forceinline__ int seq(int i) const { return __builtin_amdgcn_readlane(n, i); }
 };
 
+// cu_seqlens is read with scalar loads: their results do not queue behind the tile's vector loads.
+typedef const __attribute__((address_space(4))) int32_t* ScalarInts;
+__device__ __forceinline__ ScalarInts scalar_ints(const int32_t* p) { return (ScalarInts)(uintptr_t)p; }
+
 __device__ __forceinline__ int64_t tokens_end(const LinearArgs& a) {
     if (!a.cu) return a.T;
-    const int64_t e = a.cu[a.N];
+    const int64_t e = scalar_ints(a.cu)[a.N];
     return e < a.T ? e : a.T;
 }
 
 template <int TPT> __device__ __forceinline__ Borders find_borders(const LinearArgs& a, int64_t w0, int64_t end) {
     static_assert(TPT <= 64, "one lane per token");
-    Borders b;
+    Borders b{0, 0, 0};
     const int lane = threadIdx.x & 63;
-    const int64_t t = w0 + lane;
-    const bool in = lane < TPT && t < end;
     if (!a.cu) {
-        b.n = 0;
-        b.first = __ballot(in && t == 0);
-        b.last = __ballot(in && t == end - 1);
+        if (w0 == 0) b.first = 1;
+        if (w0 < end && end <= w0 + TPT) b.last = 1ull << (end - 1 - w0);
         return b;
     }
-    int lo = 0, hi = a.N;  // the last n < N with cu[n] <= t: empty sequences at t come before it
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (a.cu[mid] <= t) lo = mid; else hi = mid;
+    if (w0 >= end) return b;
+    const ScalarInts cu = scalar_ints(a.cu);
+    int n = 0, hi = a.N;  // the last n < N with cu[n] <= w0: empty sequences at w0 come before it
+    while (hi - n > 1) {
+        const int mid = (n + hi) >> 1;
+        if (cu[mid] <= w0) n = mid; else hi = mid;
     }
-    b.n = lo;
-    b.first = __ballot(in && a.cu[lo] == t);
-    b.last = __ballot(in && a.cu[lo + 1] == t + 1);
+    b.n = n;
+    if (cu[n] == w0) b.first = 1;
+    while (n < a.N) {  // sequences that end in this run of tokens
+        const int64_t e = cu[n + 1];
+        if (e > w0 + TPT || e > end) break;
+        if (e > w0 && e > cu[n]) b.last |= 1ull << (e - 1 - w0);
+        if (++n == a.N || e == w0 + TPT || e == end) break;
+        if (e > w0 && cu[n + 1] > e) b.first |= 1ull << (e - w0);
+        if (lane >= e - w0) b.n = n;
+    }
     return b;
 }
 
-__device__ __forceinline__ float2* run_word(const LinearArgs& a, int64_t tile, int64_t c) {
-    return a.runs + tile * a.D + c;
+template <int TPT> __device__ __forceinline__ int rows_of(int64_t w0, int64_t end) {
+    return end <= w0 ? 0 : end - w0 < TPT ? (int)(end - w0) : TPT;
 }
 
 template <int VEC> __device__ __forceinline__ void load_state(const float* p, int64_t i, float* out) {
@@ -169,50 +250,158 @@ template <int VEC> __device__ __forceinline__ void store_state(float* p, int64_t
     for (int e = 0; e < VEC; ++e) p[i + e] = in[e];
 }
 
-// Writes the tile's run: each channel's 8 waves composed in the order FIRST .. LAST.
+// ---- the states between tiles ----
+// A tile publishes its run as soon as it has it, looks at the runs of the 8 tiles before it until one of them
+// is cut, and publishes the state behind itself as a cut run.  A word is one 64-bit value, written and
+// read whole at device scope, so it needs no flag and no fence: its decay is kEmpty until it is written.
+// Tiles are handed out by a counter in the order of the chain, so a tile waits only for tiles whose workgroups
+// have started.  These publish their runs without waiting for anything, the first one's is cut, and a tile
+// whose predecessor's is cut publishes a cut one: every wait ends.
+constexpr uint32_t kEmpty = 0xFFFFFFFFu;
+
+__device__ __forceinline__ uint64_t* run_word(const LinearArgs& a, int64_t at, int64_t c) { return a.runs + at * a.D + c; }
+
+__device__ __forceinline__ void publish(uint64_t* word, float2 r) {
+    const uint32_t v = r.x == r.x ? __float_as_uint(r.x) : 0x7FC00000u;  // no NaN may read as kEmpty
+    __hip_atomic_store(word, ((uint64_t)v << 32) | __float_as_uint(r.y), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+__global__ __launch_bounds__(256) void linear_init_kernel(const LinearArgs a, int64_t words) {
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i == 0) *a.ticket = 0;
+    for (int64_t k = i; k < words; k += (int64_t)gridDim.x * 256) a.runs[k] = ~0ull;
+}
+
+template <int VEC> struct TileShared {
+    float2 run[kWaves][64 * VEC];    // the waves' runs; then the run of all waves before each
+    float2 back[kWaves][64 * VEC];   // runs of earlier tiles
+    float carry[64 * VEC];           // the state entering the tile
+    int ticket;
+};
+
+// Which tile of the chain this workgroup takes.
+template <int VEC> __device__ __forceinline__ int64_t take_ticket(const LinearArgs& a, TileShared<VEC>& sh) {
+    if (a.tiles == 1) return blockIdx.x;
+    if (threadIdx.x == 0) sh.ticket = (int)atomicAdd(a.ticket, 1u);
+    __syncthreads();
+    return sh.ticket;
+}
+
+// After every wave has stored its run (and a barrier): fills sh.carry and turns sh.run into the runs of all
+// waves that come before each.  `at` is the tile's place in the chain; REVERSE: the waves' order is 7 .. 0.
 template <int VEC, bool REVERSE>
-__device__ __forceinline__ void publish_run(const LinearArgs& a, const float2 (*run)[64 * VEC], int64_t tile, int64_t c_tile) {
-    for (int c = threadIdx.x; c < 64 * VEC; c += kThreads) {
-        if (c_tile + c >= a.D) continue;
-        float2 r = run[REVERSE ? kWaves - 1 : 0][c];
+__device__ __forceinline__ void chain(const LinearArgs& a, TileShared<VEC>& sh, int64_t at, int64_t c_tile) {
+    constexpr int CH = 64 * VEC;
+    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+    float2 whole{0.0f, 0.0f};
+    if (tid < CH) {
+        float2 r = sh.run[REVERSE ? kWaves - 1 : 0][tid];
 #pragma unroll
-        for (int i = 1; i < kWaves; ++i) r = compose(r, run[REVERSE ? kWaves - 1 - i : i][c]);
-        *run_word(a, tile, c_tile + c) = r;
+        for (int i = 1; i < kWaves; ++i) {
+            float2& slot = sh.run[REVERSE ? kWaves - 1 - i : i][tid];
+            const float2 mine = slot;
+            slot = r;
+            r = compose(r, mine);
+        }
+        whole = r;
+        if (at == 0) whole = float2{kCut, r.y};  // nothing comes before: entered with 0
+        if (a.tiles > 1 && at + 1 < a.tiles && c_tile + tid < a.D) publish(run_word(a, at, c_tile + tid), whole);
+        sh.carry[tid] = 0.0f;
     }
+    if (at > 0) {
+        // Wave w holds the word of the tile w + 1 places back.  The state is carried forward tile by tile from
+        // the farthest cut run among them, so it is the same, bit for bit, whichever of them are cut already.
+        const int64_t from = at - 1 - w;
+        const bool look = from >= 0 && c_tile + lane * VEC < a.D;
+        float state = 0.0f;
+        for (;;) {
+            float2 got[VEC];
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) got[e] = float2{kCut, 0.0f};
+            if (look) {
+                uint64_t word[VEC];
+                for (;;) {
+                    bool empty = false;
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) {
+                        word[e] = __hip_atomic_load(run_word(a, from, c_tile + lane * VEC + e), __ATOMIC_RELAXED,
+                                                    __HIP_MEMORY_SCOPE_AGENT);
+                        empty |= (uint32_t)(word[e] >> 32) == kEmpty;
+                    }
+                    if (!empty) break;
+                    __builtin_amdgcn_s_sleep(1);
+                }
+#pragma unroll
+                for (int e = 0; e < VEC; ++e)
+                    got[e] = float2{__uint_as_float((uint32_t)(word[e] >> 32)), __uint_as_float((uint32_t)word[e])};
+            }
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) sh.back[w][lane * VEC + e] = got[e];
+            __syncthreads();
+            bool found = false;
+            if (tid < CH) {
+#pragma unroll
+                for (int i = kWaves - 1; i >= 0; --i) {
+                    const float2 r = sh.back[i][tid];
+                    found |= r.x == kCut;
+                    state = apply_run(r, state);
+                }
+            }
+            if (!__syncthreads_or(tid < CH && !found)) break;
+        }
+        if (tid < CH) {
+            sh.carry[tid] = state;
+            if (at + 1 < a.tiles && whole.x != kCut && c_tile + tid < a.D)
+                publish(run_word(a, at, c_tile + tid), float2{kCut, apply_run(whole, state)});
+        }
+    }
+    __syncthreads();
 }
 
 // =====================================================================================================
-// forward.  APPLY false: only the tile's run is written; true: the tile's entering state is read from the
-// same word, and outputs, final states and block states are written.
-template <int KIND, typename IO, int VEC, int TPT, bool APPLY>
-__global__ __launch_bounds__(kThreads) void linear_fwd_kernel(const LinearArgs a) {
+// forward
+#ifndef FB
+#define FB 4
+#endif
+#ifndef BB
+#define BB 4
+#endif
+#ifndef FT16
+#define FT16 16
+#endif
+#ifndef FT32
+#define FT32 8
+#endif
+template <int KIND, typename IO, int VEC, int TPT>
+__global__ __launch_bounds__(kThreads, FB) void linear_fwd_kernel(const LinearArgs a) {
     constexpr int L = kWaves * TPT;
+    __shared__ TileShared<VEC> sh;
+    const int64_t ticket = take_ticket(a, sh);
     const int lane = threadIdx.x & 63;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t tile = blockIdx.x / a.nch;
-    const int64_t c_tile = (int64_t)(blockIdx.x % a.nch) * (64 * VEC);
+    const int64_t tile = ticket / a.nch;
+    const int64_t c_tile = (ticket % a.nch) * (64 * VEC);
     const int64_t c = c_tile + lane * VEC;
     const bool active = c < a.D;
     const int64_t end = tokens_end(a);
     const int64_t w0 = tile * L + (int64_t)w * TPT;
-    const Borders bo = find_borders<TPT>(a, w0, end);
 
     typedef typename GateT<KIND, IO>::T GT;
-    __shared__ float2 run[kWaves][64 * VEC];
+    const int rows = rows_of<TPT>(w0, end);
     Chan<IO, VEC> x[TPT];
     float v[TPT][VEC];
+    {
+        const Rows<IO> rx(a.x, a.D, w0, rows, c, active);
+        const Rows<GT> rg(a.gate, a.D, w0, rows, c, active);
 #pragma unroll
-    for (int i = 0; i < TPT; ++i) {
-        const bool in = active && w0 + i < end;
-        const int64_t at = (w0 + i) * a.D + c;
-        Chan<GT, VEC> g{};
-        x[i] = Chan<IO, VEC>{};
-        if (in) {
-            g.load(a.gate, at);
-            x[i].load(a.x, at);
+        for (int i = 0; i < TPT; ++i) {
+            Chan<GT, VEC> g;
+            g.load(rg.r, rg.at(i));
+            x[i].load(rx.r, rx.at(i));
+            g.get(v[i]);
         }
-        g.get(v[i]);
     }
+    const Borders bo = find_borders<TPT>(a, w0, end);
     RunDecay<KIND> A[VEC];
     float B[VEC];
 #pragma unroll
@@ -230,72 +419,89 @@ __global__ __launch_bounds__(kThreads) void linear_fwd_kernel(const LinearArgs a
             v[i][e] = encode_gate<KIND>(raw);
             A[e].add(raw, v[i][e]);
             B[e] = Decay(v[i][e]).step(B[e], KIND == kLogGate ? xv[e] : one_minus(v[i][e]) * xv[e]);
+            hide(v[i][e]);
+            hide(B[e]);
         }
+        __builtin_amdgcn_sched_barrier(0);
     }
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) run[w][lane * VEC + e] = float2{bo.first ? kCut : A[e].get(), B[e]};
-    __syncthreads();
-    if constexpr (!APPLY) {
-        publish_run<VEC, false>(a, run, tile, c_tile);
-        return;
+    for (int e = 0; e < VEC; ++e) sh.run[w][lane * VEC + e] = float2{bo.first ? kCut : A[e].get(), B[e]};
+#pragma unroll
+    for (int i = 0; i < TPT; ++i) {
+        x[i].hide();
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) hide(v[i][e]);
     }
+    __syncthreads();
+    chain<VEC, false>(a, sh, tile, c_tile);
     if (!active) return;
     float h[VEC];
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) h[e] = tile > 0 ? run_word(a, tile, c + e)->y : 0.0f;
-    for (int i = 0; i < w; ++i)
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) h[e] = apply_run(run[i][lane * VEC + e], h[e]);
+    for (int e = 0; e < VEC; ++e) {
+        h[e] = sh.carry[lane * VEC + e];
+        if (w > 0) h[e] = apply_run(sh.run[w][lane * VEC + e], h[e]);
+    }
     if (a.block_states && w0 % kLinearBlock == 0 && w0 < a.T) store_state<VEC>(a.block_states, w0 / kLinearBlock * a.D + c, h);
+    const Rows<IO> ry(a.y, a.D, w0, rows, c, active);
 #pragma unroll
     for (int i = 0; i < TPT; ++i) {
-        if (w0 + i >= end) break;
         if ((bo.first >> i) & 1) load_state<VEC>(a.h0, (int64_t)bo.seq(i) * a.D + c, h);
         float xv[VEC];
         x[i].get(xv);
 #pragma unroll
         for (int e = 0; e < VEC; ++e)
             h[e] = Decay(v[i][e]).step(h[e], KIND == kLogGate ? xv[e] : one_minus(v[i][e]) * xv[e]);
-        Chan<IO, VEC>::put(a.y, (w0 + i) * a.D + c, h);
+        Chan<IO, VEC>::put(ry.r, ry.at(i), h);
+        __builtin_amdgcn_sched_barrier(0);
         if (((bo.last >> i) & 1) && a.ht) store_state<VEC>(a.ht, (int64_t)bo.seq(i) * a.D + c, h);
     }
 }
 
 // =====================================================================================================
 // backward.  The states are formed again from x and the tile's entering state (block_states); the carry
-// c = a (dy + c') runs from the last token to the first.
-template <int KIND, typename IO, int VEC, int TPT, bool APPLY>
-__global__ __launch_bounds__(kThreads) void linear_bwd_kernel(const LinearArgs a) {
+// c = a (dy + c') runs from the last token to the first, so the chain begins at the last tile.
+template <int KIND, typename IO, int VEC, int TPT>
+__global__ __launch_bounds__(kThreads, BB) void linear_bwd_kernel(const LinearArgs a) {
     constexpr int L = kWaves * TPT;
     static_assert(L % kLinearBlock == 0, "a tile begins at a block state");
+    __shared__ TileShared<VEC> sh;
+    __shared__ float2 fwd[kWaves][64 * VEC];
+    const int64_t ticket = take_ticket(a, sh);
     const int lane = threadIdx.x & 63;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t tile = blockIdx.x / a.nch;
-    const int64_t c_tile = (int64_t)(blockIdx.x % a.nch) * (64 * VEC);
+    const int64_t place = ticket / a.nch, tile = a.tiles - 1 - place;
+    const int64_t c_tile = (ticket % a.nch) * (64 * VEC);
     const int64_t c = c_tile + lane * VEC;
     const bool active = c < a.D;
     const int64_t end = tokens_end(a);
     const int64_t w0 = tile * L + (int64_t)w * TPT;
-    const Borders bo = find_borders<TPT>(a, w0, end);
 
     typedef typename GateT<KIND, IO>::T GT;
-    __shared__ float2 fwd[kWaves][64 * VEC], rev[kWaves][64 * VEC];
+    const int rows = rows_of<TPT>(w0, end);
     Chan<IO, VEC> x[TPT], dy[TPT];
     float v[TPT][VEC];
+    {
+        const Rows<IO> rx(a.x, a.D, w0, rows, c, active), rdy(a.dy, a.D, w0, rows, c, active);
+        const Rows<GT> rg(a.gate, a.D, w0, rows, c, active);
 #pragma unroll
-    for (int i = 0; i < TPT; ++i) {
-        const bool in = active && w0 + i < end;
-        const int64_t at = (w0 + i) * a.D + c;
-        Chan<GT, VEC> g{};
-        x[i] = Chan<IO, VEC>{};
-        dy[i] = Chan<IO, VEC>{};
-        if (in) {
-            g.load(a.gate, at);
-            dy[i].load(a.dy, at);
-            if constexpr (APPLY) x[i].load(a.x, at);
+        for (int i = 0; i < TPT; ++i) {
+            Chan<GT, VEC> g;
+            g.load(rg.r, rg.at(i));
+            x[i].load(rx.r, rx.at(i));
+            dy[i].load(rdy.r, rdy.at(i));
+            g.get(v[i]);
         }
-        g.get(v[i]);
     }
+    const Borders bo = find_borders<TPT>(a, w0, end);
+    auto hide_tile = [&] {
+#pragma unroll
+        for (int i = 0; i < TPT; ++i) {
+            x[i].hide();
+            dy[i].hide();
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) hide(v[i][e]);
+        }
+    };
     RunDecay<KIND> A[VEC];
     float B[VEC], C[VEC];
 #pragma unroll
@@ -303,7 +509,7 @@ __global__ __launch_bounds__(kThreads) void linear_bwd_kernel(const LinearArgs a
 #pragma unroll
     for (int i = 0; i < TPT; ++i) {
         if ((bo.first >> i) & 1) {
-            if (APPLY && active) load_state<VEC>(a.h0, (int64_t)bo.seq(i) * a.D + c, B);
+            if (active) load_state<VEC>(a.h0, (int64_t)bo.seq(i) * a.D + c, B);
         }
         float xv[VEC];
         x[i].get(xv);
@@ -312,9 +518,13 @@ __global__ __launch_bounds__(kThreads) void linear_bwd_kernel(const LinearArgs a
             const float raw = v[i][e];
             v[i][e] = encode_gate<KIND>(raw);
             A[e].add(raw, v[i][e]);
-            if constexpr (APPLY) B[e] = Decay(v[i][e]).step(B[e], KIND == kLogGate ? xv[e] : one_minus(v[i][e]) * xv[e]);
+            B[e] = Decay(v[i][e]).step(B[e], KIND == kLogGate ? xv[e] : one_minus(v[i][e]) * xv[e]);
+            hide(v[i][e]);
+            hide(B[e]);
         }
+        __builtin_amdgcn_sched_barrier(0);
     }
+    hide_tile();
 #pragma unroll
     for (int i = TPT - 1; i >= 0; --i) {
         if ((bo.last >> i) & 1) {
@@ -323,30 +533,32 @@ __global__ __launch_bounds__(kThreads) void linear_bwd_kernel(const LinearArgs a
         float dv[VEC];
         dy[i].get(dv);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) C[e] = Decay(v[i][e]).step(C[e] + dv[e], 0.0f);
+        for (int e = 0; e < VEC; ++e) {
+            C[e] = Decay(v[i][e]).step(C[e] + dv[e], 0.0f);
+            hide(C[e]);
+        }
+        __builtin_amdgcn_sched_barrier(0);
     }
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
         const float decay = A[e].get();
-        if constexpr (APPLY) fwd[w][lane * VEC + e] = float2{bo.first ? kCut : decay, B[e]};
-        rev[w][lane * VEC + e] = float2{bo.last ? kCut : decay, C[e]};
+        fwd[w][lane * VEC + e] = float2{bo.first ? kCut : decay, B[e]};
+        sh.run[w][lane * VEC + e] = float2{bo.last ? kCut : decay, C[e]};
     }
+    hide_tile();
     __syncthreads();
-    if constexpr (!APPLY) {
-        publish_run<VEC, true>(a, rev, tile, c_tile);
-        return;
-    }
+    chain<VEC, true>(a, sh, place, c_tile);
     if (!active) return;
     float h[VEC], cr[VEC];
     load_state<VEC>(a.block_states, tile * (L / kLinearBlock) * a.D + c, h);
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) cr[e] = tile + 1 < a.tiles ? run_word(a, tile, c + e)->y : 0.0f;
     for (int i = 0; i < w; ++i)
 #pragma unroll
         for (int e = 0; e < VEC; ++e) h[e] = apply_run(fwd[i][lane * VEC + e], h[e]);
-    for (int i = kWaves - 1; i > w; --i)
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) cr[e] = apply_run(rev[i][lane * VEC + e], cr[e]);
+    for (int e = 0; e < VEC; ++e) {
+        cr[e] = sh.carry[lane * VEC + e];
+        if (w < kWaves - 1) cr[e] = apply_run(sh.run[w][lane * VEC + e], cr[e]);
+    }
 
     // dgate = D u: u holds a h_{t-1}, or a (1 - a) (h_{t-1} - x)
     float u[TPT][VEC];
@@ -361,11 +573,16 @@ __global__ __launch_bounds__(kThreads) void linear_bwd_kernel(const LinearArgs a
             const float q = one_minus(v[i][e]);
             u[i][e] = KIND == kLogGate ? d.a * h[e] : d.a * q * (h[e] - xv[e]);
             h[e] = d.step(h[e], KIND == kLogGate ? xv[e] : q * xv[e]);
+            hide(u[i][e]);
+            hide(h[e]);
         }
+        __builtin_amdgcn_sched_barrier(0);
     }
+    hide_tile();
+    const Rows<IO> rdx(a.dx, a.D, w0, rows, c, active);
+    const Rows<GT> rdg(a.dgate, a.D, w0, rows, c, active);
 #pragma unroll
     for (int i = TPT - 1; i >= 0; --i) {
-        if (w0 + i >= end) continue;
         if ((bo.last >> i) & 1) load_state<VEC>(a.dht, (int64_t)bo.seq(i) * a.D + c, cr);
         float dv[VEC], dg[VEC];
         dy[i].get(dv);
@@ -376,23 +593,10 @@ __global__ __launch_bounds__(kThreads) void linear_bwd_kernel(const LinearArgs a
             cr[e] = Decay(v[i][e]).step(Dt, 0.0f);
             dv[e] = KIND == kLogGate ? Dt : one_minus(v[i][e]) * Dt;
         }
-        const int64_t at = (w0 + i) * a.D + c;
-        Chan<IO, VEC>::put(a.dx, at, dv);
-        Chan<GT, VEC>::put(a.dgate, at, dg);
+        Chan<IO, VEC>::put(rdx.r, rdx.at(i), dv);
+        Chan<GT, VEC>::put(rdg.r, rdg.at(i), dg);
+        __builtin_amdgcn_sched_barrier(0);
         if (((bo.first >> i) & 1) && a.dh0) store_state<VEC>(a.dh0, (int64_t)bo.seq(i) * a.D + c, cr);
-    }
-}
-
-// Turns every tile's run into the state that enters it, tile by tile (from the last for the backward pass).
-template <bool REVERSE> __global__ __launch_bounds__(64) void linear_carry_kernel(const LinearArgs a) {
-    const int64_t c = (int64_t)blockIdx.x * 64 + threadIdx.x;
-    if (c >= a.D) return;
-    float h = 0.0f;
-    for (int64_t i = 0; i < a.tiles; ++i) {
-        float2* word = run_word(a, REVERSE ? a.tiles - 1 - i : i, c);
-        const float2 r = *word;
-        *word = float2{0.0f, h};
-        h = apply_run(r, h);
     }
 }
 
@@ -412,20 +616,23 @@ __global__ __launch_bounds__(256) void linear_decode_kernel(const LinearArgs a) 
     const int slot = a.slots[n];
     if (slot < 0 || slot >= a.num_slots) return;
     const int64_t c = ((int64_t)blockIdx.x * 256 + threadIdx.x) * VEC;
-    if (c >= a.D) return;
+    const bool active = c < a.D;
     const int64_t bos = a.cu ? a.cu[n] : n;
     int64_t eos = a.cu ? a.cu[n + 1] : n + 1;
     if (eos > a.T) eos = a.T;
     typedef typename GateT<KIND, IO>::T GT;
+    const Rows<ST> rs(a.pool, a.D, slot, 1, c, active);
     Chan<ST, VEC> s;
-    s.load(a.pool, (int64_t)slot * a.D + c);
+    s.load(rs.r, rs.at(0));
     float h[VEC];
     s.get(h);
     for (int64_t t = bos; t < eos; ++t) {
+        const Rows<IO> rx(a.x, a.D, t, 1, c, active), ry(a.y, a.D, t, 1, c, active);
+        const Rows<GT> rg(a.gate, a.D, t, 1, c, active);
         Chan<GT, VEC> g;
         Chan<IO, VEC> x;
-        g.load(a.gate, t * a.D + c);
-        x.load(a.x, t * a.D + c);
+        g.load(rg.r, rg.at(0));
+        x.load(rx.r, rx.at(0));
         float gv[VEC], xv[VEC];
         g.get(gv);
         x.get(xv);
@@ -434,34 +641,22 @@ __global__ __launch_bounds__(256) void linear_decode_kernel(const LinearArgs a) 
             const float v = encode_gate<KIND>(gv[e]);
             h[e] = Decay(v).step(h[e], KIND == kLogGate ? xv[e] : one_minus(v) * xv[e]);
         }
-        Chan<IO, VEC>::put(a.y, t * a.D + c, h);
+        Chan<IO, VEC>::put(ry.r, ry.at(0), h);
     }
-    if (a.commit) Chan<ST, VEC>::put(a.pool, (int64_t)slot * a.D + c, h);
+    if (a.commit) Chan<ST, VEC>::put(rs.r, rs.at(0), h);
 }
 
-template <int KIND, typename IO, int VEC, int TPT> hipError_t run_fwd(LinearArgs a, hipStream_t s) {
+template <int KIND, typename IO, int VEC, int TPT, bool BACKWARD> hipError_t run_scan(LinearArgs a, hipStream_t s) {
     a.nch = (a.D + 64 * VEC - 1) / (64 * VEC);
     a.tiles = (a.T + kWaves * TPT - 1) / (kWaves * TPT);
     const int64_t blocks = a.tiles * a.nch;
     if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
     if (a.tiles > 1) {
-        linear_fwd_kernel<KIND, IO, VEC, TPT, false><<<dim3((unsigned)blocks), kThreads, 0, s>>>(a);
-        linear_carry_kernel<false><<<dim3((unsigned)((a.D + 63) / 64)), 64, 0, s>>>(a);
+        const int64_t words = a.tiles * a.D, need = (words + 2047) / 2048;
+        linear_init_kernel<<<dim3((unsigned)(need < 2048 ? need : 2048)), 256, 0, s>>>(a, words);
     }
-    linear_fwd_kernel<KIND, IO, VEC, TPT, true><<<dim3((unsigned)blocks), kThreads, 0, s>>>(a);
-    return hipGetLastError();
-}
-
-template <int KIND, typename IO, int VEC, int TPT> hipError_t run_bwd(LinearArgs a, hipStream_t s) {
-    a.nch = (a.D + 64 * VEC - 1) / (64 * VEC);
-    a.tiles = (a.T + kWaves * TPT - 1) / (kWaves * TPT);
-    const int64_t blocks = a.tiles * a.nch;
-    if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
-    if (a.tiles > 1) {
-        linear_bwd_kernel<KIND, IO, VEC, TPT, false><<<dim3((unsigned)blocks), kThreads, 0, s>>>(a);
-        linear_carry_kernel<true><<<dim3((unsigned)((a.D + 63) / 64)), 64, 0, s>>>(a);
-    }
-    linear_bwd_kernel<KIND, IO, VEC, TPT, true><<<dim3((unsigned)blocks), kThreads, 0, s>>>(a);
+    if constexpr (BACKWARD) linear_bwd_kernel<KIND, IO, VEC, TPT><<<dim3((unsigned)blocks), kThreads, 0, s>>>(a);
+    else linear_fwd_kernel<KIND, IO, VEC, TPT><<<dim3((unsigned)blocks), kThreads, 0, s>>>(a);
     return hipGetLastError();
 }
 
@@ -475,8 +670,8 @@ template <int KIND, typename IO> bool wide_ok(const LinearArgs& a) {
 }
 
 template <int KIND, typename IO> hipError_t scan(const LinearArgs& a, bool backward, hipStream_t s) {
-    if (wide_ok<KIND, IO>(a)) return backward ? run_bwd<KIND, IO, 4, 8>(a, s) : run_fwd<KIND, IO, 4, 8>(a, s);
-    return backward ? run_bwd<KIND, IO, 1, 8>(a, s) : run_fwd<KIND, IO, 1, 8>(a, s);
+    if (wide_ok<KIND, IO>(a)) return backward ? run_scan<KIND, IO, 4, 8, true>(a, s) : run_scan<KIND, IO, 4, Elem<IO>::bytes == 2 ? FT16 : FT32, false>(a, s);
+    return backward ? run_scan<KIND, IO, 1, 8, true>(a, s) : run_scan<KIND, IO, 1, 16, false>(a, s);
 }
 
 template <int KIND, typename IO, typename ST, int VEC> hipError_t decode_run(const LinearArgs& a, hipStream_t s) {
@@ -498,10 +693,13 @@ template <int KIND, typename IO> hipError_t decode_st(const LinearArgs& a, int s
 
 size_t linear_workspace(int64_t T, int64_t D) {
     const int64_t tiles = (T + kLinearBlock - 1) / kLinearBlock;
-    return tiles > 1 ? (size_t)tiles * (size_t)D * sizeof(float2) : 0;
+    return tiles > 1 ? 256 + (size_t)tiles * (size_t)D * sizeof(uint64_t) : 0;  // the counter, the words
 }
 
-hipError_t launch_linear_scan(const LinearArgs& a, int kind, int io_dtype, bool backward, hipStream_t s) {
+hipError_t launch_linear_scan(const LinearArgs& args, char* ws, int kind, int io_dtype, bool backward, hipStream_t s) {
+    LinearArgs a = args;
+    a.ticket = reinterpret_cast<uint32_t*>(ws);
+    a.runs = reinterpret_cast<uint64_t*>(ws + 256);
     hipError_t e;
     if (kind == kLogGate) e = io_dtype == 0 ? scan<0, float>(a, backward, s) : scan<0, bf16_t>(a, backward, s);
     else e = io_dtype == 0 ? scan<1, float>(a, backward, s) : scan<1, bf16_t>(a, backward, s);
