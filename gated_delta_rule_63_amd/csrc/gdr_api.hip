@@ -466,7 +466,7 @@ gdr_status gdr_linear_scan_fwd(const gdr_linear_problem* p, const void* x, const
     if ((st = check_device()) != GDR_SUCCESS) return st;
     const hipStream_t stream = static_cast<hipStream_t>(hip_stream);
     if (p->total_tokens == 0)
-        return status_of(gdr::launch_linear_empty(nullptr, initial_state, final_state, p->num_seqs, p->num_channels, stream));
+        return status_of(gdr::launch_linear_copy(initial_state, final_state, (int64_t)p->num_seqs * p->num_channels, stream));
     gdr::LinearArgs a{};
     a.x = x; a.gate = gate; a.cu = cu_seqlens; a.h0 = initial_state; a.y = y; a.ht = final_state;
     a.block_states = block_states;
@@ -486,7 +486,7 @@ gdr_status gdr_linear_scan_bwd(const gdr_linear_problem* p, const void* x, const
     if ((st = check_device()) != GDR_SUCCESS) return st;
     const hipStream_t stream = static_cast<hipStream_t>(hip_stream);
     if (p->total_tokens == 0)
-        return status_of(gdr::launch_linear_empty(nullptr, d_final_state, d_initial_state, p->num_seqs, p->num_channels, stream));
+        return status_of(gdr::launch_linear_copy(d_final_state, d_initial_state, (int64_t)p->num_seqs * p->num_channels, stream));
     gdr::LinearArgs a{};
     a.x = x; a.gate = gate; a.cu = cu_seqlens; a.h0 = initial_state;
     a.block_states = const_cast<float*>(block_states);

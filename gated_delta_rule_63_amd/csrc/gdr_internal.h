@@ -177,8 +177,8 @@ size_t linear_workspace(int64_t T, int64_t D);
 // kind 0: log-decay, 1: sigmoid.  Requires a.T >= 1 and a workspace of linear_workspace bytes.
 hipError_t launch_linear_scan(const LinearArgs& a, char* ws, int kind, int io_dtype, bool backward, hipStream_t stream);
 hipError_t launch_linear_decode(const LinearArgs& a, int kind, int io_dtype, int st_dtype, hipStream_t stream);
-// dst[n] = src[n] (zeros without src) for empty sequences, or for all when cu is NULL.
-hipError_t launch_linear_empty(const int32_t* cu, const float* src, float* dst, int32_t N, int64_t D, hipStream_t stream);
+// dst = src (zeros without src), count floats: the states of a batch of empty sequences.
+hipError_t launch_linear_copy(const float* src, float* dst, int64_t count, hipStream_t stream);
 
 // Beam search (gdr_beam.hip).
 constexpr int kBeamMaxBeams = 32, kBeamMaxOut = 64, kBeamMaxVocab = 1 << 20;

@@ -64,6 +64,34 @@ template <> struct Chan<bf16_t, 4> {
         BufStore<bf16_t, 4>::store<0>(r, off, in);
     }
 };
+template <> struct Chan<float, 2> {
+    u32x2_t w;
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+        w = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, 0));
+    }
+    __device__ __forceinline__ void get(float* out) const {
+        out[0] = __uint_as_float(w[0]);
+        out[1] = __uint_as_float(w[1]);
+    }
+    __device__ __forceinline__ void hide() { asm volatile("" : "+v"(w)); }
+    __device__ __forceinline__ static void put(__amdgpu_buffer_rsrc_t r, uint32_t off, const float* in) {
+        __builtin_amdgcn_raw_buffer_store_b64(u32x2_t{__float_as_uint(in[0]), __float_as_uint(in[1])}, r, off, 0, 0);
+    }
+};
+template <> struct Chan<bf16_t, 2> {
+    uint32_t w;
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+        w = __builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0);
+    }
+    __device__ __forceinline__ void get(float* out) const {
+        out[0] = __uint_as_float(w << 16);
+        out[1] = __uint_as_float(w & 0xFFFF0000u);
+    }
+    __device__ __forceinline__ void hide() { asm volatile("" : "+v"(w)); }
+    __device__ __forceinline__ static void put(__amdgpu_buffer_rsrc_t r, uint32_t off, const float* in) {
+        __builtin_amdgcn_raw_buffer_store_b32(pack_bf16x2(in[0], in[1]), r, off, 0, 0);
+    }
+};
 template <> struct Chan<float, 1> {
     uint32_t w;
     __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t off) {
@@ -98,6 +126,7 @@ template <typename T> struct Rows {
         char* base = const_cast<char*>(static_cast<const char*>(p)) + w0 * D * B;
         r = __builtin_amdgcn_make_buffer_rsrc(base, 0, (int)(rows * D * B), 0x00020000);
         off = active ? (uint32_t)(c * B) : 0x80000000u;
+        asm volatile("" : "+v"(off));  // another tensor's offsets are not kept for this one's
         row = (uint32_t)(D * B);
     }
     __device__ __forceinline__ uint32_t at(int i) const { return off + i * row; }
@@ -106,85 +135,76 @@ template <typename T> struct Rows {
 template <int KIND, typename IO> struct GateT { typedef IO T; };
 template <typename IO> struct GateT<kLogGate, IO> { typedef float T; };
 
-// ---- gates ----
+// ---- decays ----
 // A channel that forgets 1e-4 of its state per token needs that 1e-4 to more than the 2^-24 of 1 that a
-// rounded a holds: the error repeats every token and would grow to 2^-24 / 1e-4 of the result.  A gate is
-// therefore held as one float whose sign says which form it is: v = a - 1 <= -0 where a is near 1, v = a
-// elsewhere, and a step adds the part that the rounded a lacks.
-__device__ __forceinline__ float encode_gate_log(float g) {
-    // -0.125 < g <= -0: e^g - 1 by its series (next term below 1e-9 of the result); +0 gives a = 1
-    float p = fmaf(g, 1.0f / 720.0f, 1.0f / 120.0f);
-    p = fmaf(g, p, 1.0f / 24.0f);
+// rounded a holds: the error repeats every token and would grow to 2^-24 / 1e-4 of the result.  A decay is
+// therefore held as one float whose sign says which form it is: v = 1 - a >= +0 where a is near 1, v = -a
+// elsewhere.  Either way a h = (v's sign clear ? h : 0) - v h, one select and one fma.  (An infinite state
+// becomes a NaN at its next step: a h is inf - inf.)
+__device__ __forceinline__ bool near_one(float v) { return (int)__float_as_uint(v) >= 0; }
+__device__ __forceinline__ float mul_a(float v, float h) { return fmaf(-v, h, near_one(v) ? h : 0.0f); }
+__device__ __forceinline__ float one_minus(float v) { return near_one(v) ? v : 1.0f + v; }
+
+__device__ __forceinline__ float encode_log(float g) {
+    // -1/16 < g <= -0: 1 - e^g by its series (the next term is 1e-9 of the result); +0 gives a = 1.  Beyond,
+    // the rounding of a is at most 2^-23 / 0.06 = 2e-6 of the decay.
+    float p = fmaf(g, 1.0f / 120.0f, 1.0f / 24.0f);
     p = fmaf(g, p, 1.0f / 6.0f);
     p = fmaf(g, p, 0.5f);
     p = fmaf(g, p, 1.0f);
-    const uint32_t series = __float_as_uint(g * p) | 0x80000000u;
-    const bool near_one = __float_as_uint(g) - 0x80000000u < 0x3E000000u;
-    return near_one ? __uint_as_float(series) : exp_f32(g);
+    const bool near = __float_as_uint(g) - 0x80000000u < 0x3D800000u;
+    return near ? fabsf(g * p) : -exp_f32(g);
 }
 
-__device__ __forceinline__ float encode_gate_sigmoid(float z) {
+__device__ __forceinline__ float encode_sigmoid(float z) {
     const float e = exp_f32(-fabsf(z));
-    const float s = e * __builtin_amdgcn_rcpf(1.0f + e);  // the smaller of a and 1 - a
-    return z >= 0.0f ? __uint_as_float(__float_as_uint(s) | 0x80000000u) : s;
+    return __builtin_copysignf(e * __builtin_amdgcn_rcpf(1.0f + e), z);  // the smaller of a and 1 - a
 }
 
 template <int KIND> __device__ __forceinline__ float encode_gate(float raw) {
-    return KIND == kLogGate ? encode_gate_log(raw) : encode_gate_sigmoid(raw);
+    return KIND == kLogGate ? encode_log(raw) : encode_sigmoid(raw);
 }
 
-__device__ __forceinline__ bool is_complement(float v) { return (int)__float_as_uint(v) < 0; }
+// h_t from h_{t-1}: a h + x, or a h + (1 - a) x = (near 1 ? h : x) - v (h - x)
+template <int KIND> __device__ __forceinline__ float step(float v, float h, float x) {
+    if constexpr (KIND == kLogGate) return mul_a(v, h) + x;
+    return fmaf(-v, h - x, near_one(v) ? h : x);
+}
 
-struct Decay {
-    float a, rest;  // a rounded, and what it lacks
-    __device__ __forceinline__ explicit Decay(float v) {
-        const bool c = is_complement(v);
-        a = c ? 1.0f + v : v;
-        rest = c ? v - (a - 1.0f) : 0.0f;
-    }
-    // a h + b; h is bounded in the correction so that an infinite h stays infinite
-    __device__ __forceinline__ float step(float h, float b) const {
-        const float hc = __builtin_amdgcn_fmed3f(h, -3.0e38f, 3.0e38f);
-        return fmaf(a, h, fmaf(rest, hc, b));
-    }
-};
-
-__device__ __forceinline__ float one_minus(float v) { return is_complement(v) ? -v : 1.0f - v; }
-
-// ---- runs: (v, B), v the whole run's decay in the gates' form, or kCut ----
+// ---- runs: (v, B), v the whole run's decay in the same form, or kCut ----
 constexpr float kCut = __builtin_inff();
 
 // The state behind a run entered with state h.
-__device__ __forceinline__ float apply_run(float2 r, float h) { return r.x == kCut ? r.y : Decay(r.x).step(h, r.y); }
+__device__ __forceinline__ float apply_run(float2 r, float h) { return r.x == kCut ? r.y : mul_a(r.x, h) + r.y; }
 
 // 1 - A is kept where it is small and A where that is: a product of rounded decays near 1 would lose
 // their complements as a single rounded decay does.
-__device__ __forceinline__ float pick(float A, float Q) { return Q < 0.125f ? -Q : A; }
+__device__ __forceinline__ float pick(float A, float Q) { return Q < 0.125f ? Q : -A; }
 
 __device__ __forceinline__ float2 compose(float2 r1, float2 r2) {
     if (r2.x == kCut) return r2;
-    const float B = Decay(r2.x).step(r1.y, r2.y);
+    const float B = mul_a(r2.x, r1.y) + r2.y;
     if (r1.x == kCut) return float2{kCut, B};
-    const float q1 = one_minus(r1.x), q2 = one_minus(r2.x);
-    return float2{pick(Decay(r1.x).a * Decay(r2.x).a, fmaf(q2, 1.0f - q1, q1)), B};
+    const float q1 = one_minus(r1.x), a1 = near_one(r1.x) ? 1.0f - r1.x : -r1.x;
+    return float2{pick(mul_a(r2.x, a1), fmaf(one_minus(r2.x), 1.0f - q1, q1)), B};
 }
 
 // The decay of a run of gates: the log gates' sum, or the product of the decays beside its complement.
+// Each is summed as the run is walked, not from 64 kept gates at the end.
 template <int KIND> struct RunDecay;
 template <> struct RunDecay<kLogGate> {
     float G = 0.0f;
     __device__ __forceinline__ void add(float raw, float) {
         G += raw;
-        hide(G);  // summed here and now, not from 64 kept gates at the end
+        hide(G);
     }
-    __device__ __forceinline__ float get() const { return encode_gate_log(G); }
+    __device__ __forceinline__ float get() const { return encode_log(G); }
 };
 template <> struct RunDecay<1> {
     float A = 1.0f, Q = 0.0f;
     __device__ __forceinline__ void add(float, float v) {
-        const Decay d(v);
-        A = fmaf(d.a, A, d.rest * A);
-        Q = fmaf(one_minus(v), 1.0f - Q, Q);
+        A = mul_a(v, A);
+        Q = fmaf(v, 1.0f - Q, near_one(v) ? Q : 1.0f);
         hide(A);
         hide(Q);
     }
@@ -241,13 +261,37 @@ template <int TPT> __device__ __forceinline__ int rows_of(int64_t w0, int64_t en
     return end <= w0 ? 0 : end - w0 < TPT ? (int)(end - w0) : TPT;
 }
 
-template <int VEC> __device__ __forceinline__ void load_state(const float* p, int64_t i, float* out) {
+// Row n of a [N, D] fp32 tensor, this lane's channels; without a tensor, and for lanes without channels, zeros.
+template <int VEC> __device__ __forceinline__ void load_state(const float* p, int64_t n, int64_t D, int64_t c, float* out) {
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) out[e] = p ? p[i + e] : 0.0f;
+    for (int e = 0; e < VEC; ++e) out[e] = 0.0f;
+    if (p && c < D) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) out[e] = p[n * D + c + e];
+    }
 }
-template <int VEC> __device__ __forceinline__ void store_state(float* p, int64_t i, const float* in) {
+template <int VEC> __device__ __forceinline__ void store_state(float* p, int64_t n, int64_t D, int64_t c, const float* in) {
+    if (p && c < D) {
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) p[i + e] = in[e];
+        for (int e = 0; e < VEC; ++e) p[n * D + c + e] = in[e];
+    }
+}
+
+// Empty sequences have no token whose lane could write their final state (or its gradient): the workgroup
+// of the chain's first tile copies them, VEC channels per lane, a sequence per wave.
+template <int VEC> __device__ __forceinline__ void copy_empty(const LinearArgs& a, const float* src, float* dst, int64_t c) {
+    if (!a.cu || !dst) return;
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    for (int n0 = w * 64; n0 < a.N; n0 += kWaves * 64) {
+        const int n = n0 + lane;
+        uint64_t m = __ballot(n < a.N && a.cu[n < a.N ? n : 0] == a.cu[n < a.N ? n + 1 : 0]);
+        for (; m; m &= m - 1) {
+            const int s = n0 + __builtin_ctzll(m);
+            float h[VEC];
+            load_state<VEC>(src, s, a.D, c, h);
+            store_state<VEC>(dst, s, a.D, c, h);
+        }
+    }
 }
 
 // ---- the states between tiles ----
@@ -266,10 +310,10 @@ __device__ __forceinline__ void publish(uint64_t* word, float2 r) {
     __hip_atomic_store(word, ((uint64_t)v << 32) | __float_as_uint(r.y), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-__global__ __launch_bounds__(256) void linear_init_kernel(const LinearArgs a, int64_t words) {
+__global__ __launch_bounds__(256) void linear_init_kernel(const LinearArgs a, int64_t pairs) {
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (i == 0) *a.ticket = 0;
-    for (int64_t k = i; k < words; k += (int64_t)gridDim.x * 256) a.runs[k] = ~0ull;
+    if (i < pairs) reinterpret_cast<uint4*>(a.runs)[i] = uint4{~0u, ~0u, ~0u, ~0u};
 }
 
 template <int VEC> struct TileShared {
@@ -367,14 +411,15 @@ __device__ __forceinline__ void chain(const LinearArgs& a, TileShared<VEC>& sh, 
 #define BB 4
 #endif
 #ifndef FT16
-#define FT16 16
+#define FT16 32
 #endif
 #ifndef FT32
-#define FT32 8
+#define FT32 16
 #endif
 template <int KIND, typename IO, int VEC, int TPT>
 __global__ __launch_bounds__(kThreads, FB) void linear_fwd_kernel(const LinearArgs a) {
     constexpr int L = kWaves * TPT;
+    static_assert(L % kLinearBlock == 0, "the workspace holds a word per channel and block, block states begin runs");
     __shared__ TileShared<VEC> sh;
     const int64_t ticket = take_ticket(a, sh);
     const int lane = threadIdx.x & 63;
@@ -382,7 +427,7 @@ __global__ __launch_bounds__(kThreads, FB) void linear_fwd_kernel(const LinearAr
     const int64_t tile = ticket / a.nch;
     const int64_t c_tile = (ticket % a.nch) * (64 * VEC);
     const int64_t c = c_tile + lane * VEC;
-    const bool active = c < a.D;
+    const bool active = c < a.D;  // with VEC > 1 a lane's channels exist all or none
     const int64_t end = tokens_end(a);
     const int64_t w0 = tile * L + (int64_t)w * TPT;
 
@@ -408,9 +453,7 @@ __global__ __launch_bounds__(kThreads, FB) void linear_fwd_kernel(const LinearAr
     for (int e = 0; e < VEC; ++e) B[e] = 0.0f;
 #pragma unroll
     for (int i = 0; i < TPT; ++i) {
-        if ((bo.first >> i) & 1) {
-            if (active) load_state<VEC>(a.h0, (int64_t)bo.seq(i) * a.D + c, B);
-        }
+        if (__builtin_expect((bo.first >> i) & 1, 0)) load_state<VEC>(a.h0, bo.seq(i), a.D, c, B);
         float xv[VEC];
         x[i].get(xv);
 #pragma unroll
@@ -418,7 +461,7 @@ __global__ __launch_bounds__(kThreads, FB) void linear_fwd_kernel(const LinearAr
             const float raw = v[i][e];
             v[i][e] = encode_gate<KIND>(raw);
             A[e].add(raw, v[i][e]);
-            B[e] = Decay(v[i][e]).step(B[e], KIND == kLogGate ? xv[e] : one_minus(v[i][e]) * xv[e]);
+            B[e] = step<KIND>(v[i][e], B[e], xv[e]);
             hide(v[i][e]);
             hide(B[e]);
         }
@@ -434,27 +477,27 @@ __global__ __launch_bounds__(kThreads, FB) void linear_fwd_kernel(const LinearAr
     }
     __syncthreads();
     chain<VEC, false>(a, sh, tile, c_tile);
-    if (!active) return;
     float h[VEC];
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
         h[e] = sh.carry[lane * VEC + e];
         if (w > 0) h[e] = apply_run(sh.run[w][lane * VEC + e], h[e]);
     }
-    if (a.block_states && w0 % kLinearBlock == 0 && w0 < a.T) store_state<VEC>(a.block_states, w0 / kLinearBlock * a.D + c, h);
+    if (a.block_states && w0 % kLinearBlock == 0 && w0 < a.T) store_state<VEC>(a.block_states, w0 / kLinearBlock, a.D, c, h);
     const Rows<IO> ry(a.y, a.D, w0, rows, c, active);
 #pragma unroll
     for (int i = 0; i < TPT; ++i) {
-        if ((bo.first >> i) & 1) load_state<VEC>(a.h0, (int64_t)bo.seq(i) * a.D + c, h);
+        if (__builtin_expect((bo.first >> i) & 1, 0)) load_state<VEC>(a.h0, bo.seq(i), a.D, c, h);
         float xv[VEC];
         x[i].get(xv);
 #pragma unroll
         for (int e = 0; e < VEC; ++e)
-            h[e] = Decay(v[i][e]).step(h[e], KIND == kLogGate ? xv[e] : one_minus(v[i][e]) * xv[e]);
+            h[e] = step<KIND>(v[i][e], h[e], xv[e]);
         Chan<IO, VEC>::put(ry.r, ry.at(i), h);
         __builtin_amdgcn_sched_barrier(0);
-        if (((bo.last >> i) & 1) && a.ht) store_state<VEC>(a.ht, (int64_t)bo.seq(i) * a.D + c, h);
+        if (__builtin_expect((bo.last >> i) & 1, 0)) store_state<VEC>(a.ht, bo.seq(i), a.D, c, h);
     }
+    if (tile == 0) copy_empty<VEC>(a, a.h0, a.ht, c);
 }
 
 // =====================================================================================================
@@ -463,7 +506,7 @@ __global__ __launch_bounds__(kThreads, FB) void linear_fwd_kernel(const LinearAr
 template <int KIND, typename IO, int VEC, int TPT>
 __global__ __launch_bounds__(kThreads, BB) void linear_bwd_kernel(const LinearArgs a) {
     constexpr int L = kWaves * TPT;
-    static_assert(L % kLinearBlock == 0, "a tile begins at a block state");
+    static_assert(L % kLinearBlock == 0, "the workspace holds a word per channel and block, tiles begin at block states");
     __shared__ TileShared<VEC> sh;
     __shared__ float2 fwd[kWaves][64 * VEC];
     const int64_t ticket = take_ticket(a, sh);
@@ -472,7 +515,7 @@ __global__ __launch_bounds__(kThreads, BB) void linear_bwd_kernel(const LinearAr
     const int64_t place = ticket / a.nch, tile = a.tiles - 1 - place;
     const int64_t c_tile = (ticket % a.nch) * (64 * VEC);
     const int64_t c = c_tile + lane * VEC;
-    const bool active = c < a.D;
+    const bool active = c < a.D;  // with VEC > 1 a lane's channels exist all or none
     const int64_t end = tokens_end(a);
     const int64_t w0 = tile * L + (int64_t)w * TPT;
 
@@ -508,9 +551,7 @@ __global__ __launch_bounds__(kThreads, BB) void linear_bwd_kernel(const LinearAr
     for (int e = 0; e < VEC; ++e) B[e] = C[e] = 0.0f;
 #pragma unroll
     for (int i = 0; i < TPT; ++i) {
-        if ((bo.first >> i) & 1) {
-            if (active) load_state<VEC>(a.h0, (int64_t)bo.seq(i) * a.D + c, B);
-        }
+        if (__builtin_expect((bo.first >> i) & 1, 0)) load_state<VEC>(a.h0, bo.seq(i), a.D, c, B);
         float xv[VEC];
         x[i].get(xv);
 #pragma unroll
@@ -518,7 +559,7 @@ __global__ __launch_bounds__(kThreads, BB) void linear_bwd_kernel(const LinearAr
             const float raw = v[i][e];
             v[i][e] = encode_gate<KIND>(raw);
             A[e].add(raw, v[i][e]);
-            B[e] = Decay(v[i][e]).step(B[e], KIND == kLogGate ? xv[e] : one_minus(v[i][e]) * xv[e]);
+            B[e] = step<KIND>(v[i][e], B[e], xv[e]);
             hide(v[i][e]);
             hide(B[e]);
         }
@@ -527,14 +568,12 @@ __global__ __launch_bounds__(kThreads, BB) void linear_bwd_kernel(const LinearAr
     hide_tile();
 #pragma unroll
     for (int i = TPT - 1; i >= 0; --i) {
-        if ((bo.last >> i) & 1) {
-            if (active) load_state<VEC>(a.dht, (int64_t)bo.seq(i) * a.D + c, C);
-        }
+        if (__builtin_expect((bo.last >> i) & 1, 0)) load_state<VEC>(a.dht, bo.seq(i), a.D, c, C);
         float dv[VEC];
         dy[i].get(dv);
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
-            C[e] = Decay(v[i][e]).step(C[e] + dv[e], 0.0f);
+            C[e] = mul_a(v[i][e], C[e] + dv[e]);
             hide(C[e]);
         }
         __builtin_amdgcn_sched_barrier(0);
@@ -548,9 +587,8 @@ __global__ __launch_bounds__(kThreads, BB) void linear_bwd_kernel(const LinearAr
     hide_tile();
     __syncthreads();
     chain<VEC, true>(a, sh, place, c_tile);
-    if (!active) return;
     float h[VEC], cr[VEC];
-    load_state<VEC>(a.block_states, tile * (L / kLinearBlock) * a.D + c, h);
+    load_state<VEC>(a.block_states, tile * (L / kLinearBlock), a.D, c, h);
     for (int i = 0; i < w; ++i)
 #pragma unroll
         for (int e = 0; e < VEC; ++e) h[e] = apply_run(fwd[i][lane * VEC + e], h[e]);
@@ -564,15 +602,14 @@ __global__ __launch_bounds__(kThreads, BB) void linear_bwd_kernel(const LinearAr
     float u[TPT][VEC];
 #pragma unroll
     for (int i = 0; i < TPT; ++i) {
-        if ((bo.first >> i) & 1) load_state<VEC>(a.h0, (int64_t)bo.seq(i) * a.D + c, h);
+        if (__builtin_expect((bo.first >> i) & 1, 0)) load_state<VEC>(a.h0, bo.seq(i), a.D, c, h);
         float xv[VEC];
         x[i].get(xv);
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
-            const Decay d(v[i][e]);
-            const float q = one_minus(v[i][e]);
-            u[i][e] = KIND == kLogGate ? d.a * h[e] : d.a * q * (h[e] - xv[e]);
-            h[e] = d.step(h[e], KIND == kLogGate ? xv[e] : q * xv[e]);
+            const float vv = v[i][e], small = fabsf(vv);
+            u[i][e] = KIND == kLogGate ? mul_a(vv, h[e]) : fmaf(-small, small, small) * (h[e] - xv[e]);
+            h[e] = step<KIND>(vv, h[e], xv[e]);
             hide(u[i][e]);
             hide(h[e]);
         }
@@ -583,29 +620,28 @@ __global__ __launch_bounds__(kThreads, BB) void linear_bwd_kernel(const LinearAr
     const Rows<GT> rdg(a.dgate, a.D, w0, rows, c, active);
 #pragma unroll
     for (int i = TPT - 1; i >= 0; --i) {
-        if ((bo.last >> i) & 1) load_state<VEC>(a.dht, (int64_t)bo.seq(i) * a.D + c, cr);
+        if (__builtin_expect((bo.last >> i) & 1, 0)) load_state<VEC>(a.dht, bo.seq(i), a.D, c, cr);
         float dv[VEC], dg[VEC];
         dy[i].get(dv);
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
             const float Dt = dv[e] + cr[e];
             dg[e] = Dt * u[i][e];
-            cr[e] = Decay(v[i][e]).step(Dt, 0.0f);
-            dv[e] = KIND == kLogGate ? Dt : one_minus(v[i][e]) * Dt;
+            cr[e] = mul_a(v[i][e], Dt);
+            dv[e] = KIND == kLogGate ? Dt : fmaf(v[i][e], Dt, near_one(v[i][e]) ? 0.0f : Dt);
         }
         Chan<IO, VEC>::put(rdx.r, rdx.at(i), dv);
         Chan<GT, VEC>::put(rdg.r, rdg.at(i), dg);
         __builtin_amdgcn_sched_barrier(0);
-        if (((bo.first >> i) & 1) && a.dh0) store_state<VEC>(a.dh0, (int64_t)bo.seq(i) * a.D + c, cr);
+        if (__builtin_expect((bo.first >> i) & 1, 0)) store_state<VEC>(a.dh0, bo.seq(i), a.D, c, cr);
     }
+    if (place == 0) copy_empty<VEC>(a, a.dht, a.dh0, c);
 }
 
-// Empty sequences: the final state is the initial one, and so for the gradients.
-__global__ __launch_bounds__(256) void linear_empty_kernel(const int32_t* cu, const float* src, float* dst, int64_t D) {
-    const int64_t n = blockIdx.y;
-    if (cu && cu[n + 1] != cu[n]) return;
-    for (int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x; c < D; c += (int64_t)gridDim.x * 256)
-        dst[n * D + c] = src ? src[n * D + c] : 0.0f;
+// All sequences empty: the final states are the initial ones, and so for the gradients.
+__global__ __launch_bounds__(256) void linear_copy_kernel(const float* src, float* dst, int64_t count) {
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < count; i += (int64_t)gridDim.x * 256)
+        dst[i] = src ? src[i] : 0.0f;
 }
 
 // =====================================================================================================
@@ -638,8 +674,7 @@ __global__ __launch_bounds__(256) void linear_decode_kernel(const LinearArgs a) 
         x.get(xv);
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
-            const float v = encode_gate<KIND>(gv[e]);
-            h[e] = Decay(v).step(h[e], KIND == kLogGate ? xv[e] : one_minus(v) * xv[e]);
+            h[e] = step<KIND>(encode_gate<KIND>(gv[e]), h[e], xv[e]);
         }
         Chan<IO, VEC>::put(ry.r, ry.at(0), h);
     }
@@ -652,26 +687,34 @@ template <int KIND, typename IO, int VEC, int TPT, bool BACKWARD> hipError_t run
     const int64_t blocks = a.tiles * a.nch;
     if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
     if (a.tiles > 1) {
-        const int64_t words = a.tiles * a.D, need = (words + 2047) / 2048;
-        linear_init_kernel<<<dim3((unsigned)(need < 2048 ? need : 2048)), 256, 0, s>>>(a, words);
+        const int64_t pairs = (a.tiles * a.D + 1) / 2;  // the workspace holds the word behind an odd count too
+        linear_init_kernel<<<dim3((unsigned)((pairs + 255) / 256)), 256, 0, s>>>(a, pairs);
     }
     if constexpr (BACKWARD) linear_bwd_kernel<KIND, IO, VEC, TPT><<<dim3((unsigned)blocks), kThreads, 0, s>>>(a);
     else linear_fwd_kernel<KIND, IO, VEC, TPT><<<dim3((unsigned)blocks), kThreads, 0, s>>>(a);
     return hipGetLastError();
 }
 
-// Four channels per lane need whole vectors: rows of a multiple of four channels, and aligned tensors.
+// VEC channels per lane need whole vectors: rows of a multiple of VEC channels, and aligned tensors.
 bool aligned(const void* p, int bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
 
-template <int KIND, typename IO> bool wide_ok(const LinearArgs& a) {
-    const int io = 4 * Elem<IO>::bytes, gt = 4 * Elem<typename GateT<KIND, IO>::T>::bytes;
-    return a.D % 4 == 0 && aligned(a.x, io) && aligned(a.y, io) && aligned(a.dy, io) && aligned(a.dx, io) &&
+template <int KIND, typename IO, int VEC> bool vectors(const LinearArgs& a) {
+    const int io = VEC * Elem<IO>::bytes, gt = VEC * Elem<typename GateT<KIND, IO>::T>::bytes;
+    return a.D % VEC == 0 && aligned(a.x, io) && aligned(a.y, io) && aligned(a.dy, io) && aligned(a.dx, io) &&
            aligned(a.gate, gt) && aligned(a.dgate, gt);
 }
-
+#ifndef VW
+#define VW 2
+#endif
+#ifndef BT16
+#define BT16 16
+#endif
+#ifndef BT32
+#define BT32 16
+#endif
 template <int KIND, typename IO> hipError_t scan(const LinearArgs& a, bool backward, hipStream_t s) {
-    if (wide_ok<KIND, IO>(a)) return backward ? run_scan<KIND, IO, 4, 8, true>(a, s) : run_scan<KIND, IO, 4, Elem<IO>::bytes == 2 ? FT16 : FT32, false>(a, s);
-    return backward ? run_scan<KIND, IO, 1, 8, true>(a, s) : run_scan<KIND, IO, 1, 16, false>(a, s);
+    if (vectors<KIND, IO, VW>(a)) return backward ? run_scan<KIND, IO, VW, Elem<IO>::bytes == 2 ? BT16 : BT32, true>(a, s) : run_scan<KIND, IO, VW, Elem<IO>::bytes == 2 ? FT16 : FT32, false>(a, s);
+    return backward ? run_scan<KIND, IO, 1, 16, true>(a, s) : run_scan<KIND, IO, 1, 16, false>(a, s);
 }
 
 template <int KIND, typename IO, typename ST, int VEC> hipError_t decode_run(const LinearArgs& a, hipStream_t s) {
@@ -681,7 +724,7 @@ template <int KIND, typename IO, typename ST, int VEC> hipError_t decode_run(con
 }
 
 template <int KIND, typename IO, typename ST> hipError_t decode(const LinearArgs& a, hipStream_t s) {
-    if (wide_ok<KIND, IO>(a) && aligned(a.pool, 4 * Elem<ST>::bytes)) return decode_run<KIND, IO, ST, 4>(a, s);
+    if (vectors<KIND, IO, 4>(a) && aligned(a.pool, 4 * Elem<ST>::bytes)) return decode_run<KIND, IO, ST, 4>(a, s);
     return decode_run<KIND, IO, ST, 1>(a, s);
 }
 
@@ -693,25 +736,20 @@ template <int KIND, typename IO> hipError_t decode_st(const LinearArgs& a, int s
 
 size_t linear_workspace(int64_t T, int64_t D) {
     const int64_t tiles = (T + kLinearBlock - 1) / kLinearBlock;
-    return tiles > 1 ? 256 + (size_t)tiles * (size_t)D * sizeof(uint64_t) : 0;  // the counter, the words
+    return tiles > 1 ? 256 + ((size_t)tiles * (size_t)D + 1) * sizeof(uint64_t) : 0;  // the counter, the words
 }
 
 hipError_t launch_linear_scan(const LinearArgs& args, char* ws, int kind, int io_dtype, bool backward, hipStream_t s) {
     LinearArgs a = args;
     a.ticket = reinterpret_cast<uint32_t*>(ws);
     a.runs = reinterpret_cast<uint64_t*>(ws + 256);
-    hipError_t e;
-    if (kind == kLogGate) e = io_dtype == 0 ? scan<0, float>(a, backward, s) : scan<0, bf16_t>(a, backward, s);
-    else e = io_dtype == 0 ? scan<1, float>(a, backward, s) : scan<1, bf16_t>(a, backward, s);
-    if (e != hipSuccess) return e;
-    float* dst = backward ? a.dh0 : a.ht;
-    if (!a.cu || !dst) return hipSuccess;
-    return launch_linear_empty(a.cu, backward ? a.dht : a.h0, dst, a.N, a.D, s);
+    if (kind == kLogGate) return io_dtype == 0 ? scan<0, float>(a, backward, s) : scan<0, bf16_t>(a, backward, s);
+    return io_dtype == 0 ? scan<1, float>(a, backward, s) : scan<1, bf16_t>(a, backward, s);
 }
 
-hipError_t launch_linear_empty(const int32_t* cu, const float* src, float* dst, int32_t N, int64_t D, hipStream_t s) {
-    const unsigned nx = (unsigned)((D + 255) / 256 < 64 ? (D + 255) / 256 : 64);
-    linear_empty_kernel<<<dim3(nx, (unsigned)N), 256, 0, s>>>(cu, src, dst, D);
+hipError_t launch_linear_copy(const float* src, float* dst, int64_t count, hipStream_t s) {
+    const int64_t blocks = (count + 1023) / 1024;
+    linear_copy_kernel<<<dim3((unsigned)(blocks < 2048 ? blocks : 2048)), 256, 0, s>>>(src, dst, count);
     return hipGetLastError();
 }
 
