@@ -36,7 +36,7 @@ template <typename T, int VEC> struct Chan;
 template <> struct Chan<float, 4> {
     f32x4_t v;
     __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t off) {
-        v = __builtin_bit_cast(f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
+        v = __builtin_bit_cast(f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, kNonTemporal));
     }
     __device__ __forceinline__ void get(float* out) const {
 #pragma unroll
@@ -44,13 +44,13 @@ template <> struct Chan<float, 4> {
     }
     __device__ __forceinline__ void hide() { asm volatile("" : "+v"(v)); }
     __device__ __forceinline__ static void put(__amdgpu_buffer_rsrc_t r, uint32_t off, const float* in) {
-        BufStore<float, 4>::store<0>(r, off, in);
+        BufStore<float, 4>::store<kNonTemporal>(r, off, in);
     }
 };
 template <> struct Chan<bf16_t, 4> {
     u32x2_t w;
     __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t off) {
-        w = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, 0));
+        w = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, kNonTemporal));
     }
     __device__ __forceinline__ void get(float* out) const {
 #pragma unroll
@@ -61,13 +61,13 @@ template <> struct Chan<bf16_t, 4> {
     }
     __device__ __forceinline__ void hide() { asm volatile("" : "+v"(w)); }
     __device__ __forceinline__ static void put(__amdgpu_buffer_rsrc_t r, uint32_t off, const float* in) {
-        BufStore<bf16_t, 4>::store<0>(r, off, in);
+        BufStore<bf16_t, 4>::store<kNonTemporal>(r, off, in);
     }
 };
 template <> struct Chan<float, 2> {
     u32x2_t w;
     __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t off) {
-        w = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, 0));
+        w = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, kNonTemporal));
     }
     __device__ __forceinline__ void get(float* out) const {
         out[0] = __uint_as_float(w[0]);
@@ -75,13 +75,13 @@ template <> struct Chan<float, 2> {
     }
     __device__ __forceinline__ void hide() { asm volatile("" : "+v"(w)); }
     __device__ __forceinline__ static void put(__amdgpu_buffer_rsrc_t r, uint32_t off, const float* in) {
-        __builtin_amdgcn_raw_buffer_store_b64(u32x2_t{__float_as_uint(in[0]), __float_as_uint(in[1])}, r, off, 0, 0);
+        __builtin_amdgcn_raw_buffer_store_b64(u32x2_t{__float_as_uint(in[0]), __float_as_uint(in[1])}, r, off, 0, kNonTemporal);
     }
 };
 template <> struct Chan<bf16_t, 2> {
     uint32_t w;
     __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t off) {
-        w = __builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0);
+        w = __builtin_amdgcn_raw_buffer_load_b32(r, off, 0, kNonTemporal);
     }
     __device__ __forceinline__ void get(float* out) const {
         out[0] = __uint_as_float(w << 16);
@@ -89,29 +89,29 @@ template <> struct Chan<bf16_t, 2> {
     }
     __device__ __forceinline__ void hide() { asm volatile("" : "+v"(w)); }
     __device__ __forceinline__ static void put(__amdgpu_buffer_rsrc_t r, uint32_t off, const float* in) {
-        __builtin_amdgcn_raw_buffer_store_b32(pack_bf16x2(in[0], in[1]), r, off, 0, 0);
+        __builtin_amdgcn_raw_buffer_store_b32(pack_bf16x2(in[0], in[1]), r, off, 0, kNonTemporal);
     }
 };
 template <> struct Chan<float, 1> {
     uint32_t w;
     __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t off) {
-        w = __builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0);
+        w = __builtin_amdgcn_raw_buffer_load_b32(r, off, 0, kNonTemporal);
     }
     __device__ __forceinline__ void get(float* out) const { out[0] = __uint_as_float(w); }
     __device__ __forceinline__ void hide() { asm volatile("" : "+v"(w)); }
     __device__ __forceinline__ static void put(__amdgpu_buffer_rsrc_t r, uint32_t off, const float* in) {
-        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(in[0]), r, off, 0, 0);
+        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(in[0]), r, off, 0, kNonTemporal);
     }
 };
 template <> struct Chan<bf16_t, 1> {
     uint32_t w;
     __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t off) {
-        w = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, off, 0, 0);
+        w = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, off, 0, kNonTemporal);
     }
     __device__ __forceinline__ void get(float* out) const { out[0] = __uint_as_float(w << 16); }
     __device__ __forceinline__ void hide() { asm volatile("" : "+v"(w)); }
     __device__ __forceinline__ static void put(__amdgpu_buffer_rsrc_t r, uint32_t off, const float* in) {
-        __builtin_amdgcn_raw_buffer_store_b16(f32_to_bf16(in[0]), r, off, 0, 0);
+        __builtin_amdgcn_raw_buffer_store_b16(f32_to_bf16(in[0]), r, off, 0, kNonTemporal);
     }
 };
 
@@ -316,9 +316,13 @@ __global__ __launch_bounds__(256) void linear_init_kernel(const LinearArgs a, in
     if (i < pairs) reinterpret_cast<uint4*>(a.runs)[i] = uint4{~0u, ~0u, ~0u, ~0u};
 }
 
+#ifndef WB
+#define WB 1
+#endif
+constexpr int kBack = WB * kWaves;
 template <int VEC> struct TileShared {
     float2 run[kWaves][64 * VEC];    // the waves' runs; then the run of all waves before each
-    float2 back[kWaves][64 * VEC];   // runs of earlier tiles
+    float2 back[kBack][64 * VEC];   // runs of earlier tiles
     float carry[64 * VEC];           // the state entering the tile
     int ticket;
 };
@@ -355,37 +359,39 @@ __device__ __forceinline__ void chain(const LinearArgs& a, TileShared<VEC>& sh, 
     if (at > 0) {
         // Wave w holds the word of the tile w + 1 places back.  The state is carried forward tile by tile from
         // the farthest cut run among them, so it is the same, bit for bit, whichever of them are cut already.
-        const int64_t from = at - 1 - w;
-        const bool look = from >= 0 && c_tile + lane * VEC < a.D;
         float state = 0.0f;
         for (;;) {
-            float2 got[VEC];
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) got[e] = float2{kCut, 0.0f};
-            if (look) {
-                uint64_t word[VEC];
-                for (;;) {
-                    bool empty = false;
+            for (int k = 0; k < kBack / kWaves; ++k) {
+                const int64_t from = at - 1 - w - k * kWaves;
+                float2 got[VEC];
 #pragma unroll
-                    for (int e = 0; e < VEC; ++e) {
-                        word[e] = __hip_atomic_load(run_word(a, from, c_tile + lane * VEC + e), __ATOMIC_RELAXED,
-                                                    __HIP_MEMORY_SCOPE_AGENT);
-                        empty |= (uint32_t)(word[e] >> 32) == kEmpty;
+                for (int e = 0; e < VEC; ++e) got[e] = float2{kCut, 0.0f};
+                if (from >= 0 && c_tile + lane * VEC < a.D) {
+                    uint64_t word[VEC];
+                    for (;;) {
+                        bool empty = false;
+#pragma unroll
+                        for (int e = 0; e < VEC; ++e) {
+                            word[e] = __hip_atomic_load(run_word(a, from, c_tile + lane * VEC + e), __ATOMIC_RELAXED,
+                                                        __HIP_MEMORY_SCOPE_AGENT);
+                            empty |= (uint32_t)(word[e] >> 32) == kEmpty;
+                        }
+                        if (!empty) break;
+                        __builtin_amdgcn_s_sleep(1);
                     }
-                    if (!empty) break;
-                    __builtin_amdgcn_s_sleep(1);
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e)
+                        got[e] = float2{__uint_as_float((uint32_t)(word[e] >> 32)), __uint_as_float((uint32_t)word[e])};
                 }
 #pragma unroll
-                for (int e = 0; e < VEC; ++e)
-                    got[e] = float2{__uint_as_float((uint32_t)(word[e] >> 32)), __uint_as_float((uint32_t)word[e])};
+                for (int e = 0; e < VEC; ++e) sh.back[w + k * kWaves][lane * VEC + e] = got[e];
             }
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) sh.back[w][lane * VEC + e] = got[e];
             __syncthreads();
             bool found = false;
             if (tid < CH) {
 #pragma unroll
-                for (int i = kWaves - 1; i >= 0; --i) {
+                for (int i = kBack - 1; i >= 0; --i) {
                     const float2 r = sh.back[i][tid];
                     found |= r.x == kCut;
                     state = apply_run(r, state);
