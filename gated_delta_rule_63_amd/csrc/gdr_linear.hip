@@ -25,6 +25,7 @@ namespace {
 
 constexpr int kWaves = 8;
 constexpr int kThreads = 64 * kWaves;
+constexpr int kWavesPerSimd = 4;        // two workgroups per CU: at most 128 registers
 constexpr int kLogGate = 0;
 
 // ---- a lane's VEC channels of one token, as loaded ----
@@ -316,13 +317,9 @@ __global__ __launch_bounds__(256) void linear_init_kernel(const LinearArgs a, in
     if (i < pairs) reinterpret_cast<uint4*>(a.runs)[i] = uint4{~0u, ~0u, ~0u, ~0u};
 }
 
-#ifndef WB
-#define WB 1
-#endif
-constexpr int kBack = WB * kWaves;
 template <int VEC> struct TileShared {
     float2 run[kWaves][64 * VEC];    // the waves' runs; then the run of all waves before each
-    float2 back[kBack][64 * VEC];   // runs of earlier tiles
+    float2 back[kWaves][64 * VEC];   // runs of earlier tiles
     float carry[64 * VEC];           // the state entering the tile
     int ticket;
 };
@@ -359,39 +356,37 @@ __device__ __forceinline__ void chain(const LinearArgs& a, TileShared<VEC>& sh, 
     if (at > 0) {
         // Wave w holds the word of the tile w + 1 places back.  The state is carried forward tile by tile from
         // the farthest cut run among them, so it is the same, bit for bit, whichever of them are cut already.
+        const int64_t from = at - 1 - w;
+        const bool look = from >= 0 && c_tile + lane * VEC < a.D;
         float state = 0.0f;
         for (;;) {
+            float2 got[VEC];
 #pragma unroll
-            for (int k = 0; k < kBack / kWaves; ++k) {
-                const int64_t from = at - 1 - w - k * kWaves;
-                float2 got[VEC];
+            for (int e = 0; e < VEC; ++e) got[e] = float2{kCut, 0.0f};
+            if (look) {
+                uint64_t word[VEC];
+                for (;;) {
+                    bool empty = false;
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) got[e] = float2{kCut, 0.0f};
-                if (from >= 0 && c_tile + lane * VEC < a.D) {
-                    uint64_t word[VEC];
-                    for (;;) {
-                        bool empty = false;
-#pragma unroll
-                        for (int e = 0; e < VEC; ++e) {
-                            word[e] = __hip_atomic_load(run_word(a, from, c_tile + lane * VEC + e), __ATOMIC_RELAXED,
-                                                        __HIP_MEMORY_SCOPE_AGENT);
-                            empty |= (uint32_t)(word[e] >> 32) == kEmpty;
-                        }
-                        if (!empty) break;
-                        __builtin_amdgcn_s_sleep(1);
+                    for (int e = 0; e < VEC; ++e) {
+                        word[e] = __hip_atomic_load(run_word(a, from, c_tile + lane * VEC + e), __ATOMIC_RELAXED,
+                                                    __HIP_MEMORY_SCOPE_AGENT);
+                        empty |= (uint32_t)(word[e] >> 32) == kEmpty;
                     }
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e)
-                        got[e] = float2{__uint_as_float((uint32_t)(word[e] >> 32)), __uint_as_float((uint32_t)word[e])};
+                    if (!empty) break;
+                    __builtin_amdgcn_s_sleep(1);
                 }
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) sh.back[w + k * kWaves][lane * VEC + e] = got[e];
+                for (int e = 0; e < VEC; ++e)
+                    got[e] = float2{__uint_as_float((uint32_t)(word[e] >> 32)), __uint_as_float((uint32_t)word[e])};
             }
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) sh.back[w][lane * VEC + e] = got[e];
             __syncthreads();
             bool found = false;
             if (tid < CH) {
 #pragma unroll
-                for (int i = kBack - 1; i >= 0; --i) {
+                for (int i = kWaves - 1; i >= 0; --i) {
                     const float2 r = sh.back[i][tid];
                     found |= r.x == kCut;
                     state = apply_run(r, state);
@@ -410,20 +405,8 @@ __device__ __forceinline__ void chain(const LinearArgs& a, TileShared<VEC>& sh, 
 
 // =====================================================================================================
 // forward
-#ifndef FB
-#define FB 4
-#endif
-#ifndef BB
-#define BB 4
-#endif
-#ifndef FT16
-#define FT16 32
-#endif
-#ifndef FT32
-#define FT32 16
-#endif
 template <int KIND, typename IO, int VEC, int TPT>
-__global__ __launch_bounds__(kThreads, FB) void linear_fwd_kernel(const LinearArgs a) {
+__global__ __launch_bounds__(kThreads, kWavesPerSimd) void linear_fwd_kernel(const LinearArgs a) {
     constexpr int L = kWaves * TPT;
     static_assert(L % kLinearBlock == 0, "the workspace holds a word per channel and block, block states begin runs");
     __shared__ TileShared<VEC> sh;
@@ -510,7 +493,7 @@ __global__ __launch_bounds__(kThreads, FB) void linear_fwd_kernel(const LinearAr
 // backward.  The states are formed again from x and the tile's entering state (block_states); the carry
 // c = a (dy + c') runs from the last token to the first, so the chain begins at the last tile.
 template <int KIND, typename IO, int VEC, int TPT>
-__global__ __launch_bounds__(kThreads, BB) void linear_bwd_kernel(const LinearArgs a) {
+__global__ __launch_bounds__(kThreads, kWavesPerSimd) void linear_bwd_kernel(const LinearArgs a) {
     constexpr int L = kWaves * TPT;
     static_assert(L % kLinearBlock == 0, "the workspace holds a word per channel and block, tiles begin at block states");
     __shared__ TileShared<VEC> sh;
@@ -709,18 +692,27 @@ template <int KIND, typename IO, int VEC> bool vectors(const LinearArgs& a) {
     return a.D % VEC == 0 && aligned(a.x, io) && aligned(a.y, io) && aligned(a.dy, io) && aligned(a.dx, io) &&
            aligned(a.gate, gt) && aligned(a.dgate, gt);
 }
-#ifndef VW
-#define VW 2
-#endif
-#ifndef BT16
-#define BT16 16
-#endif
-#ifndef BT32
-#define BT32 16
-#endif
+constexpr int64_t kManyTiles = 128;
+
+template <int KIND, typename IO, int VEC, int TPT_FWD, int TPT_BWD>
+hipError_t scan_tiles(const LinearArgs& a, bool backward, hipStream_t s) {
+    return backward ? run_scan<KIND, IO, VEC, TPT_BWD, true>(a, s) : run_scan<KIND, IO, VEC, TPT_FWD, false>(a, s);
+}
+
+// Tiles.  Large ones (two channels per lane; 32 tokens per wave in bf16, 16 in fp32 and in the bf16 backward pass,
+// whose kept values fill the registers) have the shortest chain; small ones (8 tokens per wave) the shortest
+// time to the first output and more workgroups.  Forward, log gate, bf16, large / small: 64 x 1024 tokens x
+// channels 12.6 / 5.7 us, 333 x 4096 18.4 / 11.9, 2048 x 2048 20.5 / 22.4, 4096 x 2048 24.9 / 36.6, 8192 x 4096
+// 71.6 / 80.2: small below 128 large tiles.  The fp32 backward pass keeps 8 tokens per wave: 16 spill
+// (8192 x 4096: 143 us, 8 tokens 128).  Odd rows go one channel per lane.
 template <int KIND, typename IO> hipError_t scan(const LinearArgs& a, bool backward, hipStream_t s) {
-    if (vectors<KIND, IO, VW>(a)) return backward ? run_scan<KIND, IO, VW, Elem<IO>::bytes == 2 ? BT16 : BT32, true>(a, s) : run_scan<KIND, IO, VW, Elem<IO>::bytes == 2 ? FT16 : FT32, false>(a, s);
-    return backward ? run_scan<KIND, IO, 1, 16, true>(a, s) : run_scan<KIND, IO, 1, 16, false>(a, s);
+    constexpr bool kHalf = Elem<IO>::bytes == 2;
+    constexpr int F = kHalf ? 32 : 16, R = kHalf ? 16 : 8;
+    const int64_t tokens = kWaves * (backward ? R : F), channels = 128;
+    const bool many = (a.T + tokens - 1) / tokens * ((a.D + channels - 1) / channels) >= kManyTiles;
+    if (vectors<KIND, IO, 2>(a))
+        return many ? scan_tiles<KIND, IO, 2, F, R>(a, backward, s) : scan_tiles<KIND, IO, 2, 8, 8>(a, backward, s);
+    return many ? scan_tiles<KIND, IO, 1, 16, 16>(a, backward, s) : scan_tiles<KIND, IO, 1, 8, 8>(a, backward, s);
 }
 
 template <int KIND, typename IO, typename ST, int VEC> hipError_t decode_run(const LinearArgs& a, hipStream_t s) {

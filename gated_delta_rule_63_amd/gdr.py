@@ -488,61 +488,93 @@ def gdr_kda_decode_fused(q, k, v, conv_weight, conv_state, gate_in, gate_weight,
 
 
 # ---------------------------------------------------------------------------
+# The entry points below are called once per layer and step, with tens of microseconds of device time at
+# most: their checks are one pass per tensor, and pointers go to ctypes as plain integers.
+def _arg(t: Optional[torch.Tensor], name: str, shape, dtype, device: int):
+    """Checks a tensor and returns its address (None for None)."""
+    if t is None:
+        return None
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != device or not t.is_contiguous():
+        _check(t, name, shape, dtype)
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{device}")
+    return t.data_ptr()
+
+
+def _required(t: Optional[torch.Tensor], name: str, shape, dtype, device: int) -> int:
+    if t is None:
+        raise ValueError(f"{name} is required")
+    return _arg(t, name, shape, dtype, device)
+
+
 class _On:
     """The device and stream of a call: outputs and workspaces that the binding makes are allocated on the
     stream that uses them, and the launch goes to the tensors' device whatever the current one is."""
+    __slots__ = ("raw", "ctx")
 
-    def __init__(self, device: torch.device, stream):
-        self.stream = torch.cuda.current_stream(device) if stream is None else stream
-        if self.stream.device != device:
-            raise ValueError(f"stream of {self.stream.device}, tensors on {device}")
-        self.ptr = ctypes.c_void_p(self.stream.cuda_stream)
-        # entering a stream's context costs a few microseconds: only where it is not current already
+    def __init__(self, device: int, stream):
         self.ctx = None
-        if torch.cuda.current_device() != device.index or stream is not None:
-            self.ctx = torch.cuda.stream(self.stream)
+        if stream is not None:
+            if stream.device.index != device:
+                raise ValueError(f"stream of {stream.device}, tensors on cuda:{device}")
+            self.ctx = torch.cuda.stream(stream)
+            self.raw = stream.cuda_stream
+        else:
+            self.raw = torch._C._cuda_getCurrentRawStream(device)
+            if torch._C._cuda_getDevice() != device:
+                self.ctx = torch.cuda.device(device)
 
     def __enter__(self):
         if self.ctx is not None:
             self.ctx.__enter__()
-        return self.ptr
+        return self.raw
 
     def __exit__(self, *exc):
         if self.ctx is not None:
             self.ctx.__exit__(*exc)
 
 
-def _same_device(device: torch.device, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} is on {t.device}, expected {device}")
+def _workspace(workspace, need: int, device: int):
+    """(address, bytes, tensor to keep) of the caller's workspace, or of one made here."""
+    if workspace is None:
+        if need == 0:
+            return None, 0, None
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        return workspace.data_ptr(), need, workspace
+    _check(workspace, "workspace", dtype=torch.uint8)
+    if workspace.get_device() != device:
+        raise ValueError(f"workspace is on {workspace.device}, expected cuda:{device}")
+    return workspace.data_ptr(), workspace.numel(), workspace
 
 
-def _linear_problem(x, gate, gate_kind: int, num_seqs: int) -> LinearProblem:
-    if x.dim() != 2:
+def _linear_problem(x, gate, gate_kind: int, num_seqs: int):
+    """(problem, device, shape, gate's dtype, x's and gate's address)"""
+    shape, dtype = x.shape, x.dtype
+    if len(shape) != 2:
         raise ValueError("x is [T, D]")
-    _check(x, "x")
-    io = _dtype_code(x.dtype)
-    if gate_kind not in (GDR_LINEAR_LOG_DECAY, GDR_LINEAR_SIGMOID):
+    if gate_kind == GDR_LINEAR_LOG_DECAY:
+        gate_dtype = torch.float32
+    elif gate_kind == GDR_LINEAR_SIGMOID:
+        gate_dtype = dtype
+    else:
         raise ValueError("gate_kind is GDR_LINEAR_LOG_DECAY or GDR_LINEAR_SIGMOID")
-    _check(gate, "gate", x.shape, torch.float32 if gate_kind == GDR_LINEAR_LOG_DECAY else x.dtype)
-    return LinearProblem(x.shape[0], num_seqs, x.shape[1], gate_kind, io)
+    if not x.is_cuda:
+        raise ValueError("x must be a device tensor")
+    dev = x.get_device()
+    p = LinearProblem(shape[0], num_seqs, shape[1], gate_kind, _dtype_code(dtype))
+    return p, dev, shape, gate_dtype, _required(x, "x", shape, dtype, dev), _required(gate, "gate", shape, gate_dtype, dev)
 
 
-def _linear_blocks(T: int) -> int:
-    return -(-T // GDR_LINEAR_BLOCK)
+def _seqs(cu_seqlens) -> int:
+    if cu_seqlens is None:
+        return 1
+    if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
+        raise ValueError("cu_seqlens is [N + 1]")
+    return cu_seqlens.shape[0] - 1
 
 
 def gdr_linear_workspace_size(x, gate, gate_kind: int, num_seqs: int) -> int:
-    p = _linear_problem(x, gate, gate_kind, num_seqs)
-    return int(lib().gdr_linear_workspace_size(ctypes.byref(p)))
-
-
-def _workspace(workspace, need: int, device):
-    if workspace is None:
-        return torch.empty(need, dtype=torch.uint8, device=device) if need else None
-    _check(workspace, "workspace", dtype=torch.uint8)
-    return workspace
+    p = _linear_problem(x, gate, gate_kind, num_seqs)[0]
+    return lib().gdr_linear_workspace_size(ctypes.byref(p))
 
 
 def gdr_linear_scan_fwd(x, gate, gate_kind: int, cu_seqlens=None, initial_state=None, y=None, final_state=None,
@@ -553,27 +585,26 @@ def gdr_linear_scan_fwd(x, gate, gate_kind: int, cu_seqlens=None, initial_state=
     [ceil(T / GDR_LINEAR_BLOCK), D] for gdr_linear_scan_bwd as a third where it is asked for or given.
     ``workspace`` is a uint8 device tensor of at least gdr_linear_workspace_size bytes (allocated here if
     absent)."""
-    N = _num_seqs(cu_seqlens, 1)
-    p = _linear_problem(x, gate, gate_kind, N)
-    T, D = x.shape
-    with _On(x.device, stream) as sp:
+    N = _seqs(cu_seqlens)
+    p, dev, shape, _, px, pg = _linear_problem(x, gate, gate_kind, N)
+    T, D = shape
+    states, f32 = (N, D), torch.float32
+    with _On(dev, stream) as raw:
         if y is None:
             y = torch.empty_like(x)
         if final_state is None and output_final_state:
-            final_state = torch.empty((N, D), dtype=torch.float32, device=x.device)
+            final_state = torch.empty(states, dtype=f32, device=dev)
+        blocks = (-(-T // GDR_LINEAR_BLOCK), D)
         want_blocks = output_block_states or block_states is not None
-        if block_states is None and want_blocks:
-            block_states = torch.empty((_linear_blocks(T), D), dtype=torch.float32, device=x.device)
-        _check(y, "y", (T, D), x.dtype)
-        _check(initial_state, "initial_state", (N, D), torch.float32, optional=True)
-        _check(final_state, "final_state", (N, D), torch.float32, optional=True)
-        _check(block_states, "block_states", (_linear_blocks(T), D), torch.float32, optional=True)
-        ws = _workspace(workspace, int(lib().gdr_linear_workspace_size(ctypes.byref(p))), x.device)
-        _same_device(x.device, gate=gate, cu_seqlens=cu_seqlens, initial_state=initial_state, y=y,
-                     final_state=final_state, block_states=block_states, workspace=ws)
-        st = lib().gdr_linear_scan_fwd(ctypes.byref(p), _ptr(x), _ptr(gate), _ptr(cu_seqlens), _ptr(initial_state),
-                                       _ptr(y), _ptr(final_state), _ptr(block_states), _ptr(ws),
-                                       0 if ws is None else ws.numel(), sp)
+        if want_blocks and block_states is None:
+            block_states = torch.empty(blocks, dtype=f32, device=dev)
+        ref = ctypes.byref(p)
+        ws, nb, keep = _workspace(workspace, lib().gdr_linear_workspace_size(ref), dev)
+        st = _lib.gdr_linear_scan_fwd(ref, px, pg, _arg(cu_seqlens, "cu_seqlens", (N + 1,), torch.int32, dev),
+                                      _arg(initial_state, "initial_state", states, f32, dev),
+                                      _required(y, "y", shape, x.dtype, dev),
+                                      _arg(final_state, "final_state", states, f32, dev),
+                                      _arg(block_states, "block_states", blocks, f32, dev), ws, nb, raw)
     _raise(st, "gdr_linear_scan_fwd")
     return (y, final_state, block_states) if want_blocks else (y, final_state)
 
@@ -583,28 +614,27 @@ def gdr_linear_scan_bwd(x, gate, gate_kind: int, dy, block_states, cu_seqlens=No
                         output_d_initial_state: bool = True, workspace=None, stream=None):
     """Gradients of gdr_linear_scan_fwd: dy [T, D] (x's dtype), block_states as the forward call wrote
     them, d_final_state [N, D] fp32 or None.  Returns (dx, dgate, d_initial_state or None)."""
-    N = _num_seqs(cu_seqlens, 1)
-    p = _linear_problem(x, gate, gate_kind, N)
-    T, D = x.shape
-    _check(dy, "dy", (T, D), x.dtype)
-    _check(block_states, "block_states", (_linear_blocks(T), D), torch.float32)
-    with _On(x.device, stream) as sp:
-        dx = torch.empty_like(x) if dx is None else dx
-        dgate = torch.empty_like(gate) if dgate is None else dgate
+    N = _seqs(cu_seqlens)
+    p, dev, shape, gate_dtype, px, pg = _linear_problem(x, gate, gate_kind, N)
+    T, D = shape
+    states, f32 = (N, D), torch.float32
+    with _On(dev, stream) as raw:
+        if dx is None:
+            dx = torch.empty_like(x)
+        if dgate is None:
+            dgate = torch.empty_like(gate)
         if d_initial_state is None and output_d_initial_state:
-            d_initial_state = torch.empty((N, D), dtype=torch.float32, device=x.device)
-        _check(dx, "dx", (T, D), x.dtype)
-        _check(dgate, "dgate", (T, D), gate.dtype)
-        _check(initial_state, "initial_state", (N, D), torch.float32, optional=True)
-        _check(d_final_state, "d_final_state", (N, D), torch.float32, optional=True)
-        _check(d_initial_state, "d_initial_state", (N, D), torch.float32, optional=True)
-        ws = _workspace(workspace, int(lib().gdr_linear_workspace_size(ctypes.byref(p))), x.device)
-        _same_device(x.device, gate=gate, dy=dy, block_states=block_states, cu_seqlens=cu_seqlens,
-                     initial_state=initial_state, d_final_state=d_final_state, dx=dx, dgate=dgate,
-                     d_initial_state=d_initial_state, workspace=ws)
-        st = lib().gdr_linear_scan_bwd(ctypes.byref(p), _ptr(x), _ptr(gate), _ptr(cu_seqlens), _ptr(initial_state),
-                                       _ptr(block_states), _ptr(dy), _ptr(d_final_state), _ptr(dx), _ptr(dgate),
-                                       _ptr(d_initial_state), _ptr(ws), 0 if ws is None else ws.numel(), sp)
+            d_initial_state = torch.empty(states, dtype=f32, device=dev)
+        ref = ctypes.byref(p)
+        ws, nb, keep = _workspace(workspace, lib().gdr_linear_workspace_size(ref), dev)
+        st = _lib.gdr_linear_scan_bwd(ref, px, pg, _arg(cu_seqlens, "cu_seqlens", (N + 1,), torch.int32, dev),
+                                      _arg(initial_state, "initial_state", states, f32, dev),
+                                      _required(block_states, "block_states", (-(-T // GDR_LINEAR_BLOCK), D), f32, dev),
+                                      _required(dy, "dy", shape, x.dtype, dev),
+                                      _arg(d_final_state, "d_final_state", states, f32, dev),
+                                      _required(dx, "dx", shape, x.dtype, dev),
+                                      _required(dgate, "dgate", shape, gate_dtype, dev),
+                                      _arg(d_initial_state, "d_initial_state", states, f32, dev), ws, nb, raw)
     _raise(st, "gdr_linear_scan_bwd")
     return dx, dgate, d_initial_state
 
@@ -614,22 +644,22 @@ def gdr_linear_decode_paged(x, gate, gate_kind: int, pool, state_indices, cu_seq
     """Paged decode of the gated linear recurrence: pool [num_slots, D] (float32 or bfloat16),
     state_indices int32 [N] (negative = padded).  Returns y (rows of padded sequences are left as they
     were)."""
-    _check(state_indices, "state_indices", dtype=torch.int32)
+    if state_indices.dim() != 1:
+        raise ValueError("state_indices is [N]")
     N = state_indices.shape[0]
-    p = _linear_problem(x, gate, gate_kind, N)
-    T, D = x.shape
-    if cu_seqlens is not None:
-        _check(cu_seqlens, "cu_seqlens", (N + 1,), torch.int32)
+    p, dev, shape, _, px, pg = _linear_problem(x, gate, gate_kind, N)
     if pool.dim() != 2:
         raise ValueError("pool is [num_slots, D]")
-    _check(pool, "pool", (pool.shape[0], D))
-    with _On(x.device, stream) as sp:
-        y = torch.empty_like(x) if y is None else y
-        _check(y, "y", (T, D), x.dtype)
-        _same_device(x.device, gate=gate, pool=pool, state_indices=state_indices, cu_seqlens=cu_seqlens, y=y)
-        st = lib().gdr_linear_decode_paged(ctypes.byref(p), int(max_q_len), _ptr(x), _ptr(gate), _ptr(cu_seqlens),
-                                           _ptr(pool), _dtype_code(pool.dtype), pool.shape[0], _ptr(state_indices),
-                                           1 if commit else 0, _ptr(y), sp)
+    with _On(dev, stream) as raw:
+        if y is None:
+            y = torch.empty_like(x)
+        slots = pool.shape[0]
+        st = lib().gdr_linear_decode_paged(ctypes.byref(p), max_q_len, px, pg,
+                                           _arg(cu_seqlens, "cu_seqlens", (N + 1,), torch.int32, dev),
+                                           _arg(pool, "pool", (slots, shape[1]), pool.dtype, dev),
+                                           _dtype_code(pool.dtype), slots,
+                                           _arg(state_indices, "state_indices", (N,), torch.int32, dev),
+                                           1 if commit else 0, _required(y, "y", shape, x.dtype, dev), raw)
     _raise(st, "gdr_linear_decode_paged")
     return y
 
@@ -646,12 +676,12 @@ def _beam_problem(logits, num_out: int, eos_token: int) -> BeamProblem:
     if (sv != 1 and V > 1) or (B > 1 and W > 1 and sb != W * sw):
         raise ValueError("logits: the rows must be contiguous and evenly spaced")
     row = sw if W > 1 else sb if B > 1 else V
-    return BeamProblem(B, W, V, int(num_out), row, int(eos_token), _dtype_code(logits.dtype))
+    return BeamProblem(B, W, V, num_out, row, eos_token, _dtype_code(logits.dtype))
 
 
 def gdr_beam_workspace_size(logits, num_out: int) -> int:
     p = _beam_problem(logits, num_out, 0)
-    return int(lib().gdr_beam_workspace_size(ctypes.byref(p)))
+    return lib().gdr_beam_workspace_size(ctypes.byref(p))
 
 
 def gdr_beam_select(logits, scores, num_out: int, finished=None, eos_token: int = -1, out_scores=None,
@@ -661,24 +691,24 @@ def gdr_beam_select(logits, scores, num_out: int, finished=None, eos_token: int 
     bool or None.  Returns (scores fp32, parents int32, tokens int32), each [batch, num_out]."""
     p = _beam_problem(logits, num_out, eos_token)
     B, W, _ = logits.shape
-    dev = logits.device
-    _check(scores, "scores", (B, W), torch.float32)
-    if finished is not None and finished.dtype == torch.bool:
+    dev, i32 = logits.get_device(), torch.int32
+    shape = (B, max(0, num_out))
+    if finished is not None and finished.dtype is torch.bool:
         finished = finished.view(torch.uint8)
-    _check(finished, "finished", (B, W), torch.uint8, optional=True)
-    with _On(dev, stream) as sp:
-        shape = (B, max(0, int(num_out)))
-        out_scores = torch.empty(shape, dtype=torch.float32, device=dev) if out_scores is None else out_scores
-        out_parents = torch.empty(shape, dtype=torch.int32, device=dev) if out_parents is None else out_parents
-        out_tokens = torch.empty(shape, dtype=torch.int32, device=dev) if out_tokens is None else out_tokens
-        _check(out_scores, "out_scores", shape, torch.float32)
-        _check(out_parents, "out_parents", shape, torch.int32)
-        _check(out_tokens, "out_tokens", shape, torch.int32)
-        ws = _workspace(workspace, int(lib().gdr_beam_workspace_size(ctypes.byref(p))), dev)
-        _same_device(dev, scores=scores, finished=finished, out_scores=out_scores, out_parents=out_parents,
-                     out_tokens=out_tokens, workspace=ws)
-        st = lib().gdr_beam_select(ctypes.byref(p), _ptr(logits), _ptr(scores), _ptr(finished), _ptr(out_scores),
-                                   _ptr(out_parents), _ptr(out_tokens), _ptr(ws), 0 if ws is None else ws.numel(), sp)
+    with _On(dev, stream) as raw:
+        if out_scores is None:
+            out_scores = torch.empty(shape, dtype=torch.float32, device=dev)
+        if out_parents is None:
+            out_parents = torch.empty(shape, dtype=i32, device=dev)
+        if out_tokens is None:
+            out_tokens = torch.empty(shape, dtype=i32, device=dev)
+        ref = ctypes.byref(p)
+        ws, nb, keep = _workspace(workspace, lib().gdr_beam_workspace_size(ref), dev)
+        st = _lib.gdr_beam_select(ref, logits.data_ptr(), _required(scores, "scores", (B, W), torch.float32, dev),
+                                  _arg(finished, "finished", (B, W), torch.uint8, dev),
+                                  _required(out_scores, "out_scores", shape, torch.float32, dev),
+                                  _required(out_parents, "out_parents", shape, i32, dev),
+                                  _required(out_tokens, "out_tokens", shape, i32, dev), ws, nb, raw)
     _raise(st, "gdr_beam_select")
     return out_scores, out_parents, out_tokens
 
@@ -688,22 +718,21 @@ def gdr_beam_reorder(pool, state_indices, parents, slot_dim: int = 0, state_indi
     points take it) or [layers, num_slots, ...] (slot_dim 1), state_indices and parents int32 [batch,
     beams].  Returns the new beams' slots, int32 [batch, beams]; give the old ones to the calls for all
     pools of a model."""
-    if slot_dim not in (0, 1) or pool.dim() < slot_dim + 1:
+    shape = pool.shape
+    if slot_dim not in (0, 1) or len(shape) < slot_dim + 1:
         raise ValueError("pool is [num_slots, ...] with slot_dim 0 or [layers, num_slots, ...] with slot_dim 1")
     if state_indices.dim() != 2:
         raise ValueError("state_indices is [batch, beams]")
-    B, W = state_indices.shape
-    _check(pool, "pool")
-    _check(state_indices, "state_indices", dtype=torch.int32)
-    _check(parents, "parents", (B, W), torch.int32)
-    layers = pool.shape[0] if slot_dim else 1
-    slots = pool.shape[slot_dim]
-    slot_bytes = pool.element_size() * math.prod(pool.shape[slot_dim + 1:])
-    with _On(pool.device, stream) as sp:
-        out = torch.empty_like(state_indices) if state_indices_out is None else state_indices_out
-        _check(out, "state_indices_out", (B, W), torch.int32)
-        _same_device(pool.device, state_indices=state_indices, parents=parents, state_indices_out=out)
-        st = lib().gdr_beam_reorder(B, W, _ptr(parents), _ptr(state_indices), _ptr(out), _ptr(pool), layers, slots,
-                                    slot_bytes, sp)
+    if not pool.is_cuda:
+        raise ValueError("pool must be a device tensor")
+    rows, dev, i32 = state_indices.shape, pool.get_device(), torch.int32
+    slot_bytes = pool.element_size() * math.prod(shape[slot_dim + 1:])
+    with _On(dev, stream) as raw:
+        out = torch.empty(rows, dtype=i32, device=dev) if state_indices_out is None else state_indices_out
+        st = lib().gdr_beam_reorder(rows[0], rows[1], _required(parents, "parents", rows, i32, dev),
+                                    _arg(state_indices, "state_indices", rows, i32, dev),
+                                    _arg(out, "state_indices_out", rows, i32, dev),
+                                    _arg(pool, "pool", shape, pool.dtype, dev), shape[0] if slot_dim else 1,
+                                    shape[slot_dim], slot_bytes, raw)
     _raise(st, "gdr_beam_reorder")
     return out
