@@ -25,6 +25,7 @@ constexpr int kRowThreads = 256;
 constexpr int kRowWaves = kRowThreads / 64;
 constexpr int kWaveCap = 256;                      // entries above the threshold that a wave may list
 constexpr int kRowList = 2048;                     // >= kRowWaves * (kWaveCap + kBeamMaxOut), a power of two
+constexpr int kRowRanked = 128;                    // up to here counting ranks beats the sorting network
 constexpr int kMergeThreads = 256;
 constexpr int kMaxSplits = 64;
 
@@ -74,132 +75,161 @@ template <int THREADS, typename Swap> __device__ __forceinline__ void bitonic_so
 
 __device__ __forceinline__ int pow2_at_least(int n) { return n <= 2 ? 2 : 1 << (32 - __builtin_clz(n - 1)); }
 
-// PER logits per thread.  VECW of them at a time are neighbours (one aligned 16-byte load), or 1.
+// Ranks the n entries of list by counting the better ones, and writes those of rank < out in order.
+__device__ __forceinline__ void write_ranked(const uint64_t* list, int n, uint64_t* to, int out) {
+    for (int i = threadIdx.x; i < n; i += kRowThreads) {
+        const uint64_t mine = list[i];
+        int rank = 0;
+#pragma unroll 8
+        for (int j = 0; j < n; ++j) rank += list[j] > mine;
+        if (rank < out) to[rank] = mine;
+    }
+}
+
+template <int PER, bool CLEAN> __device__ __forceinline__ double sum_about(const float (&x)[PER], float about) {
+    double sum = 0.0;
+#pragma unroll
+    for (int i = 0; i < PER; i += 8) {
+        float p[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) p[e] = exp_f32((CLEAN ? clean(x[i + e]) : x[i + e]) - about);
+        sum += (double)(((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7])));
+    }
+    return sum;
+}
+
+// PER logits per thread, in groups of eight that keep their maximum: most groups are never looked at again.
+// VECW of a group at a time are neighbours (one aligned 16-byte load), or 1.
 template <typename IO, int PER, int VECW>
-__global__ __launch_bounds__(kRowThreads) void beam_rows_kernel(const BeamArgs a) {
+__global__ __launch_bounds__(kRowThreads, 4) void beam_rows_kernel(const BeamArgs a) {
+    constexpr int G = PER / 8;
     const int row = blockIdx.y, split = blockIdx.x;
-    const float score = a.scores[row];
-    // ended beams and beams without probability list nothing
-    if ((a.finished && a.finished[row]) || !(score > -__builtin_inff() && score < __builtin_inff())) return;
     const int tid = threadIdx.x, lane = tid & 63;
     const int base = split * a.chunk;
     const int64_t row_at = (int64_t)row * a.stride;
-
-    float x[PER];
-#pragma unroll
-    for (int j = 0; j < PER / VECW; ++j) {
-        const int v = base + (j * kRowThreads + tid) * VECW;
-        if constexpr (VECW == 1) {
-            x[j] = v < a.vocab ? Elem<IO>::load(a.logits, row_at + v) : -__builtin_inff();
-        } else {
-            if (v + VECW <= a.vocab) {
-                Vec<IO, VECW>::load(a.logits, row_at + v, &x[j * VECW]);
-            } else {
-#pragma unroll
-                for (int e = 0; e < VECW; ++e)
-                    x[j * VECW + e] = v + e < a.vocab ? Elem<IO>::load(a.logits, row_at + v + e) : -__builtin_inff();
-            }
-        }
-    }
-    float top = -__builtin_inff();
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        x[i] = clean(x[i]);
-        top = fmaxf(top, x[i]);
-    }
+    const float kNone = -__builtin_inff();
 
     __shared__ uint64_t list[kRowList];
     __shared__ double sh_sum[kRowWaves];
     __shared__ float sh_top[kRowWaves];
     __shared__ uint32_t sh_tau[kRowWaves];
     __shared__ int count;
+
+    const float score = a.scores[row];
+    // ended beams and beams without probability list nothing
+    if ((a.finished && a.finished[row]) || !(score > kNone && score < -kNone)) return;
+
+    // element i of a thread: token base + token_of(i)
+    auto token_of = [&](int i) { return ((i / VECW) * kRowThreads + tid) * VECW + i % VECW; };
+    float x[PER];
+    if (base + kRowThreads * PER <= a.vocab) {
+#pragma unroll
+        for (int j = 0; j < PER / VECW; ++j) {
+            const int64_t at = row_at + base + token_of(j * VECW);
+            if constexpr (VECW == 1) x[j] = Elem<IO>::load(a.logits, at);
+            else Vec<IO, VECW>::load(a.logits, at, &x[j * VECW]);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < PER / VECW; ++j) {
+            const int v = base + token_of(j * VECW);
+            if (VECW > 1 && v + VECW <= a.vocab) {
+                if constexpr (VECW > 1) Vec<IO, VECW>::load(a.logits, row_at + v, &x[j * VECW]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < VECW; ++e)
+                    x[j * VECW + e] = v + e < a.vocab ? Elem<IO>::load(a.logits, row_at + v + e) : kNone;
+            }
+        }
+    }
     if (tid == 0) count = 0;
+    float gmax[G], top = kNone;  // fmaxf passes over NaN
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+        const float* p = &x[g * 8];
+        gmax[g] = fmaxf(fmaxf(fmaxf(p[0], p[1]), fmaxf(p[2], p[3])), fmaxf(fmaxf(p[4], p[5]), fmaxf(p[6], p[7])));
+        gmax[g] = fmaxf(gmax[g], kNone) + 0.0f;  // -0 counts as 0
+        top = fmaxf(top, gmax[g]);
+    }
 
     // sum of exponentials about the thread's own maximum, eight at a time in 32 bits
-    const bool some = top > -__builtin_inff();
+    const bool some = top > kNone;
     const float about = some ? top : 0.0f;
-    double sum = 0.0;
-#pragma unroll
-    for (int i = 0; i < PER; i += 8) {
-        float p[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) p[e] = exp_f32(x[i + e] - about);
-        sum += (double)(((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7])));
-    }
+    double sum = sum_about<PER, false>(x, about);
+    if (sum != sum) sum = sum_about<PER, true>(x, about);  // a NaN logit counts as -inf
     const float wtop = wave_max(top);
     sum = wave_sum(some ? sum * (double)exp_f32(top - wtop) : 0.0);
 
     // tau: a logit that at least `out` of this wave's reach or pass (the out-th best of the lanes' maxima)
     const uint32_t mine = key_of(top);
-    uint32_t tau = 0;
+    uint32_t tau_key = 0;
     constexpr int kLowBit = Elem<IO>::bytes == 2 ? 16 : 0;
 #pragma unroll
     for (int bit = 31; bit >= kLowBit; --bit) {
-        const uint32_t t = tau | (1u << bit);
-        if (__popcll(__ballot(mine >= t)) >= a.out) tau = t;
+        const uint32_t t = tau_key | (1u << bit);
+        if (__popcll(__ballot(mine >= t)) >= a.out) tau_key = t;
     }
-    if (!(tau >> 31)) tau |= (1u << kLowBit) - 1;  // the keys of negative bf16 values end in ones
+    if (!(tau_key >> 31)) tau_key |= (1u << kLowBit) - 1;  // the keys of negative bf16 values end in ones
     if (lane == 0) {
         sh_sum[tid >> 6] = sum;
         sh_top[tid >> 6] = wtop;
-        sh_tau[tid >> 6] = tau;
+        sh_tau[tid >> 6] = tau_key;
     }
     __syncthreads();
-    float btop = sh_top[0];
-#pragma unroll
-    for (int i = 1; i < kRowWaves; ++i) btop = fmaxf(btop, sh_top[i]);
-    tau = sh_tau[0];
-#pragma unroll
-    for (int i = 1; i < kRowWaves; ++i) tau = max(tau, sh_tau[i]);
+    tau_key = max(max(sh_tau[0], sh_tau[1]), max(sh_tau[2], sh_tau[3]));
     if (tid == 0) {
+        const float btop = fmaxf(fmaxf(sh_top[0], sh_top[1]), fmaxf(sh_top[2], sh_top[3]));
         double s = 0.0;
         for (int i = 0; i < kRowWaves; ++i)
-            if (sh_top[i] > -__builtin_inff()) s += sh_sum[i] * (double)exp_f32(sh_top[i] - btop);
+            if (sh_top[i] > kNone) s += sh_sum[i] * (double)exp_f32(sh_top[i] - btop);
         a.sums[(int64_t)row * a.splits + split] = s;
         a.tops[(int64_t)row * a.splits + split] = btop;
     }
 
     // logits above tau, unless a few lanes hold very many of them: then tau becomes the wave's out-th best
-    const uint32_t none = key_of(-__builtin_inff());
-    tau = max(tau, none);
+    float tau = fmaxf(of_key(tau_key), kNone);
     int above = 0;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) above += __popcll(__ballot(key_of(x[i]) > tau));
+    for (int g = 0; g < G; ++g)
+        if (__ballot(gmax[g] > tau)) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) above += __popcll(__ballot(x[g * 8 + e] > tau));
+        }
     if (above > kWaveCap) {
         uint32_t t = 0;
         for (int bit = 31; bit >= 0; --bit) {
             const uint32_t u = t | (1u << bit);
             int c = 0;
 #pragma unroll
-            for (int i = 0; i < PER; ++i) c += __popcll(__ballot(key_of(x[i]) >= u));
+            for (int i = 0; i < PER; ++i) c += __popcll(__ballot(key_of(clean(x[i])) >= u));
             if (c >= a.out) t = u;
         }
-        tau = max(tau, t);
+        tau = fmaxf(tau, of_key(t));
     }
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        const bool take = key_of(x[i]) > tau;
-        const uint64_t m = __ballot(take);
-        if (!m) continue;
-        int at = 0;
-        if (lane == 0) at = atomicAdd(&count, __popcll(m));
-        at = __builtin_amdgcn_readfirstlane(at);
-        if (take) list[at + lanes_below(m)] = entry_of(x[i], base + ((i / VECW) * kRowThreads + tid) * VECW + i % VECW);
+    for (int g = 0; g < G; ++g) {
+        if (!__ballot(gmax[g] > tau)) continue;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const bool take = x[g * 8 + e] > tau;
+            const uint64_t m = __ballot(take);
+            if (!m) continue;
+            int at = 0;
+            if (lane == 0) at = atomicAdd(&count, __popcll(m));
+            at = __builtin_amdgcn_readfirstlane(at);
+            if (take) list[at + lanes_below(m)] = entry_of(x[g * 8 + e] + 0.0f, base + token_of(g * 8 + e));
+        }
     }
     // logits equal to tau: the wave's first `out` in the order of the tokens (-inf is never listed)
-    if (tau > none) {
+    if (tau > kNone) {
         int found = 0;
 #pragma unroll
         for (int j = 0; j < PER / VECW; ++j) {
-            uint64_t any = 0;
+            if (found >= a.out || !__ballot(gmax[j * VECW / 8] >= tau)) continue;
             int n = 0;
 #pragma unroll
-            for (int e = 0; e < VECW; ++e) {
-                const bool eq = key_of(x[j * VECW + e]) == tau;
-                any |= __ballot(eq);
-                n += eq;
-            }
-            if (!any || found >= a.out) continue;
+            for (int e = 0; e < VECW; ++e) n += x[j * VECW + e] == tau;
+            if (!__ballot(n > 0)) continue;
             // equal ones in lower lanes come first, then this lane's in order
             const int incl = (int)wave_inclusive_sum((float)n);
             int rank = found + incl - n;
@@ -210,26 +240,31 @@ __global__ __launch_bounds__(kRowThreads) void beam_rows_kernel(const BeamArgs a
             at = __builtin_amdgcn_readfirstlane(at);
 #pragma unroll
             for (int e = 0; e < VECW; ++e)
-                if (key_of(x[j * VECW + e]) == tau) {
-                    if (rank < a.out)
-                        list[at + rank - found] = entry_of(x[j * VECW + e], base + (j * kRowThreads + tid) * VECW + e);
+                if (x[j * VECW + e] == tau) {
+                    if (rank < a.out) list[at + rank - found] = entry_of(tau + 0.0f, base + token_of(j * VECW + e));
                     ++rank;
                 }
             found += total;
         }
     }
     __syncthreads();
-    const int n = count, np = pow2_at_least(n);
-    for (int i = n + tid; i < np; i += kRowThreads) list[i] = 0;
-    bitonic_sort<kRowThreads>(np, [&](int i, int j, bool down) {
-        const uint64_t p = list[i], q = list[j];
-        if ((p < q) == down && p != q) {
-            list[i] = q;
-            list[j] = p;
-        }
-    });
+    const int n = count;
     uint64_t* out = a.entries + ((int64_t)row * a.splits + split) * a.out;
-    for (int i = tid; i < a.out; i += kRowThreads) out[i] = i < n ? list[i] : 0;
+    if (n <= kRowRanked) {
+        write_ranked(list, n, out, a.out);
+    } else {
+        const int np = pow2_at_least(n);
+        for (int i = n + tid; i < np; i += kRowThreads) list[i] = 0;
+        bitonic_sort<kRowThreads>(np, [&](int i, int j, bool down) {
+            const uint64_t p = list[i], q = list[j];
+            if ((p < q) == down && p != q) {
+                list[i] = q;
+                list[j] = p;
+            }
+        });
+        for (int i = tid; i < a.out; i += kRowThreads) out[i] = list[i];
+    }
+    for (int i = n + tid; i < a.out; i += kRowThreads) out[i] = 0;
 }
 
 __device__ __forceinline__ uint64_t key_of64(double x) {
@@ -240,131 +275,154 @@ __device__ __forceinline__ double of_key64(uint64_t k) {
     return __longlong_as_double((int64_t)(k >> 63 ? k ^ 0x8000000000000000ull : ~k));
 }
 
+// A scored candidate; those in one list are all different.  Better ones come first: the higher key, then the
+// lower flat index.
+struct __align__(16) Candidate {
+    uint64_t key;
+    uint32_t flat;
+    __device__ __forceinline__ bool before(const Candidate& o) const {
+        return key > o.key || (key == o.key && flat < o.flat);
+    }
+};
+
+// Sorts the first n of an LDS list, n <= kMergeThreads by counting, more by a network over the next power of
+// two.  The counting loop reads eight candidates ahead of their comparisons: one at a time it waited for the
+// LDS in every step (32 candidates: 8000 cycles).
+__device__ __forceinline__ void sort_candidates(Candidate* list, int n) {
+    if (n <= kMergeThreads) {
+        const int tid = threadIdx.x;
+        Candidate mine{0, 0};
+        int rank = 0;
+        if (tid < n) {
+            mine = list[tid];
+#pragma unroll 8
+            for (int j = 0; j < n; ++j) rank += list[j].before(mine);
+        }
+        __syncthreads();
+        if (tid < n) list[rank] = mine;
+        __syncthreads();
+        return;
+    }
+    const int np = pow2_at_least(n);
+    for (int i = n + threadIdx.x; i < np; i += kMergeThreads) list[i] = Candidate{0, 0xFFFFFFFFu};
+    bitonic_sort<kMergeThreads>(np, [&](int i, int j, bool down) {
+        const Candidate p = list[i], q = list[j];
+        if (q.before(p) == down) {
+            list[i] = q;
+            list[j] = p;
+        }
+    });
+}
+
 template <typename IO> __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(const BeamArgs a) {
     const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    constexpr int kWavesM = kMergeThreads / 64;
-    const int W = a.beams, S = a.splits, K = a.out;
+    constexpr int kWavesM = kMergeThreads / 64, kHeld = 8;
+    const int W = a.beams, S = a.splits, K = a.out, lists = W * S, total = lists * K;
+    const float kNone = -__builtin_inff();
     extern __shared__ __align__(16) char smem[];
-    uint64_t* keys = reinterpret_cast<uint64_t*>(smem);                       // [kMergeList]
-    uint32_t* flat = reinterpret_cast<uint32_t*>(keys + a.merge_list);        // [kMergeList]
+    Candidate* best = reinterpret_cast<Candidate*>(smem);                     // [merge_list]
     __shared__ double lse[kBeamMaxBeams], red[kWavesM];
+    __shared__ float beam_score[kBeamMaxBeams];
     __shared__ int state[kBeamMaxBeams];                                      // 0: listed, 1: ended, 2: no candidates
     __shared__ int count, near_mask;
-    __shared__ uint64_t tau_key;
-    __shared__ uint32_t tau_flat;
 
-    for (int w = wave; w < W; w += kWavesM) {
-        const int64_t row = (int64_t)b * W + w;
+    // the first kHeld entries of every thread, in flight with the sums
+    const uint64_t* entries = a.entries + (int64_t)b * total;
+    uint64_t held[kHeld];
+#pragma unroll
+    for (int r = 0; r < kHeld; ++r) {
+        const int i = tid + r * kMergeThreads;
+        held[r] = i < total ? entries[i] : 0;
+    }
+    // log-sum-exp per beam: a group of `width` lanes holds its parts
+    const int width = pow2_at_least(S), per_wave = 64 / width;
+    for (int w0 = wave * per_wave; w0 < W; w0 += kWavesM * per_wave) {
+        const int w = w0 + lane / width, part = lane & (width - 1);
+        const bool in = w < W;
+        const int64_t row = (int64_t)b * W + (in ? w : 0);
         const float score = a.scores[row];
-        const bool real = score > -__builtin_inff() && score < __builtin_inff();
-        int st = !real ? 2 : (a.finished && a.finished[row]) ? 1 : 0;
-        double l = 0.0;
-        if (st == 0) {
-            const float m = lane < S ? a.tops[row * S + lane] : -__builtin_inff();
-            const float top = wave_max(m);
-            if (!(top > -__builtin_inff() && top < __builtin_inff())) {
-                st = 2;
-            } else {
-                // a part without a finite logit has the sum of nothing
-                const double part = lane < S && m > -__builtin_inff() ? a.sums[row * S + lane] * exp((double)m - (double)top) : 0.0;
-                l = (double)top + log(wave_sum(part));
-            }
-        }
-        if (lane == 0) {
-            lse[w] = l;
-            state[w] = st;
+        const bool ended = a.finished && a.finished[row];
+        const float m = in && part < S ? a.tops[row * S + part] : kNone;
+        const double mass = in && part < S ? a.sums[row * S + part] : 0.0;
+        float top = m;
+        for (int x = 1; x < width; x <<= 1) top = fmaxf(top, __shfl_xor(top, x));
+        // a part without a finite logit has the sum of nothing; rows of ended beams hold no parts
+        double sum = m > kNone ? mass * (double)exp_f32(m - top) : 0.0;
+        for (int x = 1; x < width; x <<= 1) sum += __shfl_xor(sum, x);
+        if (in && part == 0) {
+            const bool real = score > kNone && score < -kNone, finite = top > kNone && top < -kNone;
+            state[w] = !real ? 2 : ended ? 1 : finite ? 0 : 2;
+            lse[w] = (double)top + log(sum);
+            beam_score[w] = score;
         }
     }
     __syncthreads();
 
-    const int lists = W * S, total = lists * K;
+    // entry i's score and flat index; false: none
+    auto candidate = [&](int i, uint64_t e, uint64_t& key, uint32_t& at) {
+        const int w = i / (S * K);
+        const double score = (double)beam_score[w];
+        if (state[w] == 1 && i == w * S * K) {
+            key = key_of64(score);
+            at = (uint32_t)w * a.vocab + a.eos;
+            return true;
+        }
+        if (state[w] != 0 || !e) return false;
+        key = key_of64(score + ((double)of_key((uint32_t)(e >> 32)) - lse[w]));
+        at = (uint32_t)w * a.vocab + ~(uint32_t)e;
+        return true;
+    };
+    auto for_entries = [&](auto f) __attribute__((always_inline)) {
+#pragma unroll
+        for (int r = 0; r < kHeld; ++r)
+            if (tid + r * kMergeThreads < total) f(tid + r * kMergeThreads, held[r]);
+        for (int i = tid + kHeld * kMergeThreads; i < total; i += kMergeThreads) f(i, entries[i]);
+    };
     int n = 0;
     for (int pass = 0; pass < 2; ++pass) {
-        // score and flat index of entry i; false: none
-        auto candidate = [&](int i, uint64_t& key, uint32_t& at) {
-            const int w = i / (S * K);
-            if (state[w] == 1) {
-                if (i % (S * K) != 0 || a.eos < 0) return false;
-                key = key_of64((double)a.scores[(int64_t)b * W + w]);
-                at = (uint32_t)w * a.vocab + a.eos;
-                return true;
-            }
-            if (state[w] == 2) return false;
-            const uint64_t e = a.entries[((int64_t)b * W * S * K) + i];
-            if (!e) return false;
-            const double s = (double)a.scores[(int64_t)b * W + w] + ((double)of_key((uint32_t)(e >> 32)) - lse[w]);
-            key = key_of64(s);
-            at = (uint32_t)w * a.vocab + ~(uint32_t)e;
-            return true;
-        };
-        if (tid == 0) {
-            count = 0;
-            near_mask = 0;
-            tau_key = 0;
-            tau_flat = 0xFFFFFFFFu;
-        }
-        __syncthreads();
+        uint64_t tau_key = 0;
+        uint32_t tau_flat = 0xFFFFFFFFu;
         // with more lists than results, no result and not the one behind them comes after the (K+1)-th best of
         // the lists' first entries, and at most K lists hold better ones
         if (lists > K) {
-            for (int i = tid; i < lists; i += kMergeThreads) {
+            for_entries([&](int i, uint64_t e) __attribute__((always_inline)) {
+                if (i % K != 0) return;
                 uint64_t key = 0;
-                uint32_t at = 0xFFFFFFFFu;
-                candidate(i * K, key, at);
-                keys[i] = key;
-                flat[i] = at;
-            }
+                uint32_t at = 0x80000000u + i / K;  // an empty list stands behind all others, at a place of its own
+                candidate(i, e, key, at);
+                best[i / K] = Candidate{key, at};
+            });
             __syncthreads();
-            for (int i = tid; i < lists; i += kMergeThreads) {
-                const uint64_t key = keys[i];
-                const uint32_t at = flat[i];
-                int rank = 0;
-                for (int j = 0; j < lists; ++j) rank += keys[j] > key || (keys[j] == key && flat[j] < at);
-                if (rank == K && key) {
-                    tau_key = key;
-                    tau_flat = at;
-                }
-            }
-            __syncthreads();
+            sort_candidates(best, lists);
+            tau_key = best[K].key;
+            tau_flat = best[K].flat;
         }
-        for (int i = tid; i < total; i += kMergeThreads) {
+        if (tid == 0) {
+            count = 0;
+            near_mask = 0;
+        }
+        __syncthreads();
+        for_entries([&](int i, uint64_t e) __attribute__((always_inline)) {
             uint64_t key;
             uint32_t at;
-            if (!candidate(i, key, at)) continue;
+            if (!candidate(i, e, key, at)) return;
             if (key > tau_key || (key == tau_key && at < tau_flat)) {
-                const int p = atomicAdd(&count, 1);
-                keys[p] = key;
-                flat[p] = at;
-            }
-        }
-        __syncthreads();
-        if (tid == 0 && tau_key && count <= K) {
-            keys[count] = tau_key;
-            flat[count] = tau_flat;
-            ++count;
-        }
-        __syncthreads();
-        n = count;
-        const int np = pow2_at_least(n);
-        for (int i = n + tid; i < np; i += kMergeThreads) {
-            keys[i] = 0;
-            flat[i] = 0xFFFFFFFFu;
-        }
-        bitonic_sort<kMergeThreads>(np, [&](int i, int j, bool down) {
-            const uint64_t p = keys[i], q = keys[j];
-            const bool behind = p < q || (p == q && flat[i] > flat[j]);
-            if (behind == down) {
-                const uint32_t f = flat[i];
-                keys[i] = q;
-                flat[i] = flat[j];
-                keys[j] = p;
-                flat[j] = f;
+                best[atomicAdd(&count, 1)] = Candidate{key, at};
             }
         });
+        __syncthreads();
+        n = count;
+        if (tau_key && n <= K) {
+            if (tid == 0) best[n] = Candidate{tau_key, tau_flat};
+            ++n;
+            __syncthreads();
+        }
+        sort_candidates(best, n);
         if (pass == 1) break;
         for (int i = tid; i + 1 < n && i < K; i += kMergeThreads) {
-            const int w0 = flat[i] / a.vocab, w1 = flat[i + 1] / a.vocab;
-            if (w0 != w1 && of_key64(keys[i]) - of_key64(keys[i + 1]) < kNear) atomicOr(&near_mask, (1 << w0) | (1 << w1));
+            const int w0 = best[i].flat / a.vocab, w1 = best[i + 1].flat / a.vocab;
+            if (w0 != w1 && of_key64(best[i].key) - of_key64(best[i + 1].key) < kNear)
+                atomicOr(&near_mask, (1 << w0) | (1 << w1));
         }
         __syncthreads();
         const uint32_t near = (uint32_t)near_mask;
@@ -372,7 +430,7 @@ template <typename IO> __global__ __launch_bounds__(kMergeThreads) void beam_mer
         for (int w = 0; w < W; ++w) {
             if (!((near >> w) & 1) || state[w] != 0) continue;
             const int64_t at = ((int64_t)b * W + w) * a.stride;
-            float top = -__builtin_inff();
+            float top = kNone;
             for (int s = 0; s < S; ++s) top = fmaxf(top, a.tops[((int64_t)b * W + w) * S + s]);
             double sum = 0.0;
             for (int v = tid; v < a.vocab; v += kMergeThreads)
@@ -390,9 +448,9 @@ template <typename IO> __global__ __launch_bounds__(kMergeThreads) void beam_mer
     }
     const int have = min(n, K);
     for (int i = tid; i < have; i += kMergeThreads) {
-        a.out_scores[(int64_t)b * K + i] = (float)of_key64(keys[i]);
-        a.out_parents[(int64_t)b * K + i] = flat[i] / a.vocab;
-        a.out_tokens[(int64_t)b * K + i] = flat[i] % a.vocab;
+        a.out_scores[(int64_t)b * K + i] = (float)of_key64(best[i].key);
+        a.out_parents[(int64_t)b * K + i] = best[i].flat / a.vocab;
+        a.out_tokens[(int64_t)b * K + i] = best[i].flat % a.vocab;
     }
     // fewer candidates than asked for: those of probability zero follow, by the lower index
     if (have == K || wave != 0) return;
@@ -493,7 +551,7 @@ template <typename IO> hipError_t select(BeamArgs a, const BeamPlan& pl, hipStre
     if (most < a.out + 1) most = a.out + 1;
     a.merge_list = 2;
     while (a.merge_list < most) a.merge_list *= 2;
-    beam_merge_kernel<IO><<<a.batch, kMergeThreads, (size_t)a.merge_list * 12, s>>>(a);
+    beam_merge_kernel<IO><<<a.batch, kMergeThreads, (size_t)a.merge_list * sizeof(Candidate), s>>>(a);
     return hipGetLastError();
 }
 
