@@ -24,8 +24,7 @@ namespace {
 constexpr int kRowThreads = 256;
 constexpr int kRowWaves = kRowThreads / 64;
 constexpr int kWaveCap = 256;                      // entries above the threshold that a wave may list
-constexpr int kRowList = 2048;                     // >= kRowWaves * (kWaveCap + kBeamMaxOut), a power of two
-constexpr int kRowRanked = 128;                    // up to here counting ranks beats the sorting network
+constexpr int kWaveList = kWaveCap + kBeamMaxOut + 8;  // and those equal to it, and the padding to eight
 constexpr int kMergeThreads = 256;
 constexpr int kMaxSplits = 64;
 
@@ -45,15 +44,28 @@ __device__ __forceinline__ float clean(float x) { return x == x ? x + 0.0f : -__
 
 __device__ __forceinline__ uint64_t entry_of(float x, uint32_t token) { return ((uint64_t)key_of(x) << 32) | ~token; }
 
+// Reductions over the wave: four steps inside each row of 16 lanes by DPP, two across the rows.
 __device__ __forceinline__ float wave_max(float x) {
-#pragma unroll
-    for (int m = 1; m < 64; m <<= 1) x = fmaxf(x, __shfl_xor(x, m));
-    return x;
+    x = fmaxf(x, dpp_mov<0xB1>(x));
+    x = fmaxf(x, dpp_mov<0x4E>(x));
+    x = fmaxf(x, dpp_mov<0x141>(x));
+    x = fmaxf(x, dpp_mov<0x140>(x));
+    x = fmaxf(x, __shfl_xor(x, 16));
+    return fmaxf(x, __shfl_xor(x, 32));
+}
+template <int CTRL> __device__ __forceinline__ double dpp_mov64(double x) {
+    const uint64_t b = (uint64_t)__double_as_longlong(x);
+    const uint32_t lo = __float_as_uint(dpp_mov<CTRL>(__uint_as_float((uint32_t)b)));
+    const uint32_t hi = __float_as_uint(dpp_mov<CTRL>(__uint_as_float((uint32_t)(b >> 32))));
+    return __longlong_as_double((int64_t)((uint64_t)hi << 32 | lo));
 }
 __device__ __forceinline__ double wave_sum(double x) {
-#pragma unroll
-    for (int m = 1; m < 64; m <<= 1) x += __shfl_xor(x, m);
-    return x;
+    x += dpp_mov64<0xB1>(x);
+    x += dpp_mov64<0x4E>(x);
+    x += dpp_mov64<0x141>(x);
+    x += dpp_mov64<0x140>(x);
+    x += __shfl_xor(x, 16);
+    return x + __shfl_xor(x, 32);
 }
 
 __device__ __forceinline__ int lanes_below(uint64_t mask) {
@@ -74,17 +86,6 @@ template <int THREADS, typename Swap> __device__ __forceinline__ void bitonic_so
 }
 
 __device__ __forceinline__ int pow2_at_least(int n) { return n <= 2 ? 2 : 1 << (32 - __builtin_clz(n - 1)); }
-
-// Ranks the n entries of list by counting the better ones, and writes those of rank < out in order.
-__device__ __forceinline__ void write_ranked(const uint64_t* list, int n, uint64_t* to, int out) {
-    for (int i = threadIdx.x; i < n; i += kRowThreads) {
-        const uint64_t mine = list[i];
-        int rank = 0;
-#pragma unroll 8
-        for (int j = 0; j < n; ++j) rank += list[j] > mine;
-        if (rank < out) to[rank] = mine;
-    }
-}
 
 template <int PER, bool CLEAN> __device__ __forceinline__ double sum_about(const float (&x)[PER], float about) {
     double sum = 0.0;
@@ -109,18 +110,19 @@ __global__ __launch_bounds__(kRowThreads, 4) void beam_rows_kernel(const BeamArg
     const int64_t row_at = (int64_t)row * a.stride;
     const float kNone = -__builtin_inff();
 
-    __shared__ uint64_t list[kRowList];
+    __shared__ __align__(16) uint64_t list[kRowWaves][kWaveList];
     __shared__ double sh_sum[kRowWaves];
     __shared__ float sh_top[kRowWaves];
     __shared__ uint32_t sh_tau[kRowWaves];
-    __shared__ int count;
+    __shared__ int listed[kRowWaves];
 
     const float score = a.scores[row];
     // ended beams and beams without probability list nothing
     if ((a.finished && a.finished[row]) || !(score > kNone && score < -kNone)) return;
 
     // element i of a thread: token base + token_of(i)
-    auto token_of = [&](int i) { return ((i / VECW) * kRowThreads + tid) * VECW + i % VECW; };
+    uint32_t own = tid * VECW;
+    auto token_of = [&](int i) { return own + (i / VECW) * kRowThreads * VECW + i % VECW; };
     float x[PER];
     if (base + kRowThreads * PER <= a.vocab) {
 #pragma unroll
@@ -132,7 +134,7 @@ __global__ __launch_bounds__(kRowThreads, 4) void beam_rows_kernel(const BeamArg
     } else {
 #pragma unroll
         for (int j = 0; j < PER / VECW; ++j) {
-            const int v = base + token_of(j * VECW);
+            const int v = base + (int)token_of(j * VECW);
             if (VECW > 1 && v + VECW <= a.vocab) {
                 if constexpr (VECW > 1) Vec<IO, VECW>::load(a.logits, row_at + v, &x[j * VECW]);
             } else {
@@ -142,7 +144,6 @@ __global__ __launch_bounds__(kRowThreads, 4) void beam_rows_kernel(const BeamArg
             }
         }
     }
-    if (tid == 0) count = 0;
     float gmax[G], top = kNone;  // fmaxf passes over NaN
 #pragma unroll
     for (int g = 0; g < G; ++g) {
@@ -176,9 +177,12 @@ __global__ __launch_bounds__(kRowThreads, 4) void beam_rows_kernel(const BeamArg
         sh_tau[tid >> 6] = tau_key;
     }
     __syncthreads();
-    tau_key = max(max(sh_tau[0], sh_tau[1]), max(sh_tau[2], sh_tau[3]));
+#pragma unroll
+    for (int i = 0; i < kRowWaves; ++i) tau_key = max(tau_key, sh_tau[i]);
     if (tid == 0) {
-        const float btop = fmaxf(fmaxf(sh_top[0], sh_top[1]), fmaxf(sh_top[2], sh_top[3]));
+        float btop = sh_top[0];
+#pragma unroll
+        for (int i = 1; i < kRowWaves; ++i) btop = fmaxf(btop, sh_top[i]);
         double s = 0.0;
         for (int i = 0; i < kRowWaves; ++i)
             if (sh_top[i] > kNone) s += sh_sum[i] * (double)exp_f32(sh_top[i] - btop);
@@ -186,85 +190,83 @@ __global__ __launch_bounds__(kRowThreads, 4) void beam_rows_kernel(const BeamArg
         a.tops[(int64_t)row * a.splits + split] = btop;
     }
 
-    // logits above tau, unless a few lanes hold very many of them: then tau becomes the wave's out-th best
+    // Each wave lists its logits above tau.  Where a few lanes hold very many of them, tau becomes the wave's
+    // out-th best and the list is made again.
     float tau = fmaxf(of_key(tau_key), kNone);
-    int above = 0;
+    uint64_t* mylist = list[tid >> 6];
+    int found;
+    for (;;) {
 #pragma unroll
-    for (int g = 0; g < G; ++g)
-        if (__ballot(gmax[g] > tau)) {
+        for (int i = 0; i < PER; ++i) hide(x[i]);
+        asm volatile("" : "+v"(own));  // nor are 64 token numbers kept from pass to pass
+        found = 0;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) above += __popcll(__ballot(x[g * 8 + e] > tau));
+        for (int g = 0; g < G; ++g) {
+            if (!__ballot(gmax[g] > tau)) continue;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const bool take = x[g * 8 + e] > tau;
+                const uint64_t m = __ballot(take);
+                if (!m) continue;
+                const int at = found + lanes_below(m);
+                if (take && at < kWaveCap) mylist[at] = entry_of(x[g * 8 + e] + 0.0f, base + token_of(g * 8 + e));
+                found += __popcll(m);
+            }
         }
-    if (above > kWaveCap) {
+        if (found <= kWaveCap) break;
         uint32_t t = 0;
         for (int bit = 31; bit >= 0; --bit) {
-            const uint32_t u = t | (1u << bit);
+            const float u = of_key(t | (1u << bit));
             int c = 0;
 #pragma unroll
-            for (int i = 0; i < PER; ++i) c += __popcll(__ballot(key_of(clean(x[i])) >= u));
-            if (c >= a.out) t = u;
+            for (int i = 0; i < PER; ++i) c += __popcll(__ballot(x[i] >= u));
+            if (c >= a.out) t |= 1u << bit;
         }
-        tau = fmaxf(tau, of_key(t));
-    }
-#pragma unroll
-    for (int g = 0; g < G; ++g) {
-        if (!__ballot(gmax[g] > tau)) continue;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const bool take = x[g * 8 + e] > tau;
-            const uint64_t m = __ballot(take);
-            if (!m) continue;
-            int at = 0;
-            if (lane == 0) at = atomicAdd(&count, __popcll(m));
-            at = __builtin_amdgcn_readfirstlane(at);
-            if (take) list[at + lanes_below(m)] = entry_of(x[g * 8 + e] + 0.0f, base + token_of(g * 8 + e));
-        }
+        tau = of_key(t);  // fewer than `out` are above it
     }
     // logits equal to tau: the wave's first `out` in the order of the tokens (-inf is never listed)
     if (tau > kNone) {
-        int found = 0;
+        int equal = 0;
 #pragma unroll
         for (int j = 0; j < PER / VECW; ++j) {
-            if (found >= a.out || !__ballot(gmax[j * VECW / 8] >= tau)) continue;
+            if (equal >= a.out || !__ballot(gmax[j * VECW / 8] >= tau)) continue;
             int n = 0;
 #pragma unroll
             for (int e = 0; e < VECW; ++e) n += x[j * VECW + e] == tau;
             if (!__ballot(n > 0)) continue;
             // equal ones in lower lanes come first, then this lane's in order
             const int incl = (int)wave_inclusive_sum((float)n);
-            int rank = found + incl - n;
-            const int total = __builtin_amdgcn_readlane(incl, 63);
-            const int take = min(total, a.out - found);
-            int at = 0;
-            if (lane == 0) at = atomicAdd(&count, take);
-            at = __builtin_amdgcn_readfirstlane(at);
+            int rank = equal + incl - n;
 #pragma unroll
             for (int e = 0; e < VECW; ++e)
                 if (x[j * VECW + e] == tau) {
-                    if (rank < a.out) list[at + rank - found] = entry_of(tau + 0.0f, base + token_of(j * VECW + e));
+                    if (rank < a.out) mylist[found + rank] = entry_of(tau + 0.0f, base + token_of(j * VECW + e));
                     ++rank;
                 }
-            found += total;
+            equal += __builtin_amdgcn_readlane(incl, 63);
         }
+        found += min(equal, a.out);
     }
+    if (lane < 8) mylist[found + lane] = 0;  // to a multiple of eight: an entry better than none
+    if (lane == 0) listed[tid >> 6] = found;
     __syncthreads();
-    const int n = count;
+    // an entry's place is the number of better ones
     uint64_t* out = a.entries + ((int64_t)row * a.splits + split) * a.out;
-    if (n <= kRowRanked) {
-        write_ranked(list, n, out, a.out);
-    } else {
-        const int np = pow2_at_least(n);
-        for (int i = n + tid; i < np; i += kRowThreads) list[i] = 0;
-        bitonic_sort<kRowThreads>(np, [&](int i, int j, bool down) {
-            const uint64_t p = list[i], q = list[j];
-            if ((p < q) == down && p != q) {
-                list[i] = q;
-                list[j] = p;
-            }
-        });
-        for (int i = tid; i < a.out; i += kRowThreads) out[i] = list[i];
+    for (int i = lane; i < found; i += 64) {
+        const uint64_t mine = mylist[i];
+        int rank = 0;
+        for (int v = 0; v < kRowWaves; ++v) {
+            const int n = listed[v];
+            for (int j = 0; j < n; j += 8)
+#pragma unroll
+                for (int k = 0; k < 8; ++k) rank += list[v][j + k] > mine;
+        }
+        if (rank < a.out) out[rank] = mine;
     }
-    for (int i = n + tid; i < a.out; i += kRowThreads) out[i] = 0;
+    int all = 0;
+#pragma unroll
+    for (int v = 0; v < kRowWaves; ++v) all += listed[v];
+    for (int i = all + tid; i < a.out; i += kRowThreads) out[i] = 0;
 }
 
 __device__ __forceinline__ uint64_t key_of64(double x) {
@@ -286,20 +288,24 @@ struct __align__(16) Candidate {
 };
 
 // Sorts the first n of an LDS list, n <= kMergeThreads by counting, more by a network over the next power of
-// two.  The counting loop reads eight candidates ahead of their comparisons: one at a time it waited for the
-// LDS in every step (32 candidates: 8000 cycles).
-__device__ __forceinline__ void sort_candidates(Candidate* list, int n) {
+// two.  Counting: kMergeThreads / n threads per candidate share the comparisons, and each reads eight ahead of
+// comparing them (one at a time it waited for the LDS in every step: 32 candidates took 8000 cycles).  `rank`
+// is LDS scratch of kMergeThreads.
+__device__ __forceinline__ void sort_candidates(Candidate* list, int n, int* rank) {
     if (n <= kMergeThreads) {
-        const int tid = threadIdx.x;
+        const int tid = threadIdx.x, np = pow2_at_least(n), parts = kMergeThreads / np;
+        const int i = tid & (np - 1), part = tid / np, each = (n + parts - 1) / parts;
+        const int j0 = part * each, j1 = min(n, j0 + each);
         Candidate mine{0, 0};
-        int rank = 0;
-        if (tid < n) {
-            mine = list[tid];
+        if (i < n) mine = list[i];
+        rank[tid] = 0;
+        int before = 0;
 #pragma unroll 8
-            for (int j = 0; j < n; ++j) rank += list[j].before(mine);
-        }
+        for (int j = j0; j < j1; ++j) before += list[j].before(mine);
         __syncthreads();
-        if (tid < n) list[rank] = mine;
+        if (i < n && before) atomicAdd(&rank[i], before);
+        __syncthreads();
+        if (tid < n) list[rank[tid]] = mine;  // part 0: candidate tid
         __syncthreads();
         return;
     }
@@ -324,6 +330,7 @@ template <typename IO> __global__ __launch_bounds__(kMergeThreads) void beam_mer
     __shared__ double lse[kBeamMaxBeams], red[kWavesM];
     __shared__ float beam_score[kBeamMaxBeams];
     __shared__ int state[kBeamMaxBeams];                                      // 0: listed, 1: ended, 2: no candidates
+    __shared__ int rank[kMergeThreads];
     __shared__ int count, near_mask;
 
     // the first kHeld entries of every thread, in flight with the sums
@@ -359,8 +366,9 @@ template <typename IO> __global__ __launch_bounds__(kMergeThreads) void beam_mer
     __syncthreads();
 
     // entry i's score and flat index; false: none
+    const float per_beam = 1.0f / (float)(S * K);
     auto candidate = [&](int i, uint64_t e, uint64_t& key, uint32_t& at) {
-        const int w = i / (S * K);
+        const int w = (int)(((float)i + 0.5f) * per_beam);  // i / (S K): exact for i < 2^21
         const double score = (double)beam_score[w];
         if (state[w] == 1 && i == w * S * K) {
             key = key_of64(score);
@@ -393,7 +401,7 @@ template <typename IO> __global__ __launch_bounds__(kMergeThreads) void beam_mer
                 best[i / K] = Candidate{key, at};
             });
             __syncthreads();
-            sort_candidates(best, lists);
+            sort_candidates(best, lists, rank);
             tau_key = best[K].key;
             tau_flat = best[K].flat;
         }
@@ -417,7 +425,7 @@ template <typename IO> __global__ __launch_bounds__(kMergeThreads) void beam_mer
             ++n;
             __syncthreads();
         }
-        sort_candidates(best, n);
+        sort_candidates(best, n, rank);
         if (pass == 1) break;
         for (int i = tid; i + 1 < n && i < K; i += kMergeThreads) {
             const int w0 = best[i].flat / a.vocab, w1 = best[i + 1].flat / a.vocab;

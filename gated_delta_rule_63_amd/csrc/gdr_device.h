@@ -280,6 +280,10 @@ template <> struct RawElem<bf16_t> {
     __device__ __forceinline__ float get() const { return __uint_as_float(x << 16); }
 };
 
+// The compiler forgets what it derived from the value: unpacked, decoded or otherwise cheap forms are made again
+// where they are used instead of holding a second set of registers across a loop or a barrier.
+__device__ __forceinline__ void hide(float& x) { asm volatile("" : "+v"(x)); }
+
 // ---- 16-lane reductions through DPP ----------------------------------------
 // Lanes are grouped in DPP rows of 16.  After the four steps every lane of the row
 // holds the same, bitwise-identical sum (each step adds the same two operands in

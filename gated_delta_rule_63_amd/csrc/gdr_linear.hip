@@ -29,10 +29,6 @@ constexpr int kWavesPerSimd = 4;        // two workgroups per CU: at most 128 re
 constexpr int kLogGate = 0;
 
 // ---- a lane's VEC channels of one token, as loaded ----
-// hide(): the compiler forgets what it derived from the value, so that unpacked or decoded forms are made
-// again in the next pass over the tile instead of holding a second set of registers across the barriers.
-__device__ __forceinline__ void hide(float& x) { asm volatile("" : "+v"(x)); }
-
 template <typename T, int VEC> struct Chan;
 template <> struct Chan<float, 4> {
     f32x4_t v;
