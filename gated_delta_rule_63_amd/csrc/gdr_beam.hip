@@ -45,11 +45,14 @@ __device__ __forceinline__ float clean(float x) { return x == x ? x + 0.0f : -__
 __device__ __forceinline__ uint64_t entry_of(float x, uint32_t token) { return ((uint64_t)key_of(x) << 32) | ~token; }
 
 // Reductions over the wave: four steps inside each row of 16 lanes by DPP, two across the rows.
-__device__ __forceinline__ float wave_max(float x) {
+__device__ __forceinline__ float row16_max(float x) {
     x = fmaxf(x, dpp_mov<0xB1>(x));
     x = fmaxf(x, dpp_mov<0x4E>(x));
     x = fmaxf(x, dpp_mov<0x141>(x));
-    x = fmaxf(x, dpp_mov<0x140>(x));
+    return fmaxf(x, dpp_mov<0x140>(x));
+}
+__device__ __forceinline__ float wave_max(float x) {
+    x = row16_max(x);
     x = fmaxf(x, __shfl_xor(x, 16));
     return fmaxf(x, __shfl_xor(x, 32));
 }
@@ -59,11 +62,14 @@ template <int CTRL> __device__ __forceinline__ double dpp_mov64(double x) {
     const uint32_t hi = __float_as_uint(dpp_mov<CTRL>(__uint_as_float((uint32_t)(b >> 32))));
     return __longlong_as_double((int64_t)((uint64_t)hi << 32 | lo));
 }
-__device__ __forceinline__ double wave_sum(double x) {
+__device__ __forceinline__ double row16_sum64(double x) {
     x += dpp_mov64<0xB1>(x);
     x += dpp_mov64<0x4E>(x);
     x += dpp_mov64<0x141>(x);
-    x += dpp_mov64<0x140>(x);
+    return x + dpp_mov64<0x140>(x);
+}
+__device__ __forceinline__ double wave_sum(double x) {
+    x = row16_sum64(x);
     x += __shfl_xor(x, 16);
     return x + __shfl_xor(x, 32);
 }
@@ -322,7 +328,7 @@ __device__ __forceinline__ void sort_candidates(Candidate* list, int n, int* ran
 
 template <typename IO> __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(const BeamArgs a) {
     const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    constexpr int kWavesM = kMergeThreads / 64, kHeld = 8;
+    constexpr int kWavesM = kMergeThreads / 64, kHeld = 8 * kMergeThreads;
     const int W = a.beams, S = a.splits, K = a.out, lists = W * S, total = lists * K;
     const float kNone = -__builtin_inff();
     extern __shared__ __align__(16) char smem[];
@@ -333,16 +339,17 @@ template <typename IO> __global__ __launch_bounds__(kMergeThreads) void beam_mer
     __shared__ int rank[kMergeThreads];
     __shared__ int count, near_mask;
 
-    // the first kHeld entries of every thread, in flight with the sums
+    // the first entries go to the LDS, in flight with the sums
     const uint64_t* entries = a.entries + (int64_t)b * total;
-    uint64_t held[kHeld];
+    __shared__ uint64_t held[kHeld];
+    uint64_t mine[kHeld / kMergeThreads];
 #pragma unroll
-    for (int r = 0; r < kHeld; ++r) {
+    for (int r = 0; r < kHeld / kMergeThreads; ++r) {
         const int i = tid + r * kMergeThreads;
-        held[r] = i < total ? entries[i] : 0;
+        mine[r] = i < total ? entries[i] : 0;
     }
-    // log-sum-exp per beam: a group of `width` lanes holds its parts
-    const int width = pow2_at_least(S), per_wave = 64 / width;
+    // log-sum-exp per beam: a row of 16 lanes holds its parts, or a wave
+    const int width = S <= 16 ? 16 : 64, per_wave = 64 / width;
     for (int w0 = wave * per_wave; w0 < W; w0 += kWavesM * per_wave) {
         const int w = w0 + lane / width, part = lane & (width - 1);
         const bool in = w < W;
@@ -351,11 +358,10 @@ template <typename IO> __global__ __launch_bounds__(kMergeThreads) void beam_mer
         const bool ended = a.finished && a.finished[row];
         const float m = in && part < S ? a.tops[row * S + part] : kNone;
         const double mass = in && part < S ? a.sums[row * S + part] : 0.0;
-        float top = m;
-        for (int x = 1; x < width; x <<= 1) top = fmaxf(top, __shfl_xor(top, x));
+        const float top = width == 16 ? row16_max(m) : wave_max(m);
         // a part without a finite logit has the sum of nothing; rows of ended beams hold no parts
         double sum = m > kNone ? mass * (double)exp_f32(m - top) : 0.0;
-        for (int x = 1; x < width; x <<= 1) sum += __shfl_xor(sum, x);
+        sum = width == 16 ? row16_sum64(sum) : wave_sum(sum);
         if (in && part == 0) {
             const bool real = score > kNone && score < -kNone, finite = top > kNone && top < -kNone;
             state[w] = !real ? 2 : ended ? 1 : finite ? 0 : 2;
@@ -363,6 +369,8 @@ template <typename IO> __global__ __launch_bounds__(kMergeThreads) void beam_mer
             beam_score[w] = score;
         }
     }
+#pragma unroll
+    for (int r = 0; r < kHeld / kMergeThreads; ++r) held[tid + r * kMergeThreads] = mine[r];
     __syncthreads();
 
     // entry i's score and flat index; false: none
@@ -380,12 +388,7 @@ template <typename IO> __global__ __launch_bounds__(kMergeThreads) void beam_mer
         at = (uint32_t)w * a.vocab + ~(uint32_t)e;
         return true;
     };
-    auto for_entries = [&](auto f) __attribute__((always_inline)) {
-#pragma unroll
-        for (int r = 0; r < kHeld; ++r)
-            if (tid + r * kMergeThreads < total) f(tid + r * kMergeThreads, held[r]);
-        for (int i = tid + kHeld * kMergeThreads; i < total; i += kMergeThreads) f(i, entries[i]);
-    };
+    auto entry = [&](int i) { return i < kHeld ? held[i] : entries[i]; };
     int n = 0;
     for (int pass = 0; pass < 2; ++pass) {
         uint64_t tau_key = 0;
@@ -393,13 +396,12 @@ template <typename IO> __global__ __launch_bounds__(kMergeThreads) void beam_mer
         // with more lists than results, no result and not the one behind them comes after the (K+1)-th best of
         // the lists' first entries, and at most K lists hold better ones
         if (lists > K) {
-            for_entries([&](int i, uint64_t e) __attribute__((always_inline)) {
-                if (i % K != 0) return;
+            for (int l = tid; l < lists; l += kMergeThreads) {
                 uint64_t key = 0;
-                uint32_t at = 0x80000000u + i / K;  // an empty list stands behind all others, at a place of its own
-                candidate(i, e, key, at);
-                best[i / K] = Candidate{key, at};
-            });
+                uint32_t at = 0x80000000u + l;  // an empty list stands behind all others, at a place of its own
+                candidate(l * K, entry(l * K), key, at);
+                best[l] = Candidate{key, at};
+            }
             __syncthreads();
             sort_candidates(best, lists, rank);
             tau_key = best[K].key;
@@ -410,14 +412,12 @@ template <typename IO> __global__ __launch_bounds__(kMergeThreads) void beam_mer
             near_mask = 0;
         }
         __syncthreads();
-        for_entries([&](int i, uint64_t e) __attribute__((always_inline)) {
+        for (int i = tid; i < total; i += kMergeThreads) {
             uint64_t key;
             uint32_t at;
-            if (!candidate(i, e, key, at)) return;
-            if (key > tau_key || (key == tau_key && at < tau_flat)) {
-                best[atomicAdd(&count, 1)] = Candidate{key, at};
-            }
-        });
+            if (!candidate(i, entry(i), key, at)) continue;
+            if (key > tau_key || (key == tau_key && at < tau_flat)) best[atomicAdd(&count, 1)] = Candidate{key, at};
+        }
         __syncthreads();
         n = count;
         if (tau_key && n <= K) {
