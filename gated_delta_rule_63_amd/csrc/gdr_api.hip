@@ -511,7 +511,7 @@ gdr_status gdr_linear_decode_paged(const gdr_linear_problem* p, int32_t max_q_le
     if ((st = check_device()) != GDR_SUCCESS) return st;
     gdr::LinearArgs a{};
     a.x = x; a.gate = gate; a.cu = cu_seqlens; a.y = y;
-    a.pool = pool; a.slots = state_indices; a.num_slots = num_slots; a.commit = commit;
+    a.pool = pool; a.slots = state_indices; a.num_slots = num_slots; a.commit = commit; a.max_q_len = max_q_len;
     a.T = p->total_tokens; a.D = p->num_channels; a.N = p->num_seqs;
     return status_of(gdr::launch_linear_decode(a, p->gate, p->io_dtype, pool_dtype, static_cast<hipStream_t>(hip_stream)));
 }

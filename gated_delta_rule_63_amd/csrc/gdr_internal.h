@@ -166,7 +166,7 @@ struct LinearArgs {
     // decode
     void* pool;                  // [num_slots, D] state dtype
     const int32_t* slots;        // [N]; negative = padded sequence
-    int32_t num_slots, commit;
+    int32_t num_slots, commit, max_q_len;
     int64_t T, D;
     int32_t N;
     int32_t nch;                 // set by the launcher: workgroups across the channels, tiles along the tokens

@@ -630,40 +630,52 @@ __global__ __launch_bounds__(256) void linear_copy_kernel(const float* src, floa
 }
 
 // =====================================================================================================
-// decode against a paged pool: one thread per (sequence, VEC channels)
-template <int KIND, typename IO, typename ST, int VEC>
+// decode against a paged pool: one thread per (sequence, VEC channels).  The rows of AHEAD tokens are loaded
+// together with the state, then computed in order: 4 where sequences may have more than one (64 sequences of 1 to
+// 12 tokens, 4096 channels: 4.8 us, 7.0 with each token's rows loaded at its turn), else 1 (256 sequences: 3.9 us,
+// 4.3 with the empty loads of 4).
+template <int KIND, typename IO, typename ST, int VEC, int AHEAD>
 __global__ __launch_bounds__(256) void linear_decode_kernel(const LinearArgs a) {
     const int n = blockIdx.y;
-    const int slot = a.slots[n];
+    const int slot = scalar_ints(a.slots)[n];
     if (slot < 0 || slot >= a.num_slots) return;
     const int64_t c = ((int64_t)blockIdx.x * 256 + threadIdx.x) * VEC;
     const bool active = c < a.D;
-    const int64_t bos = a.cu ? a.cu[n] : n;
-    int64_t eos = a.cu ? a.cu[n + 1] : n + 1;
+    int64_t bos = n, eos = n + 1;
+    if (a.cu) {
+        bos = scalar_ints(a.cu)[n];
+        eos = scalar_ints(a.cu)[n + 1];
+    }
     if (eos > a.T) eos = a.T;
     typedef typename GateT<KIND, IO>::T GT;
     const Rows<ST> rs(a.pool, a.D, slot, 1, c, active);
     Chan<ST, VEC> s;
     s.load(rs.r, rs.at(0));
     float h[VEC];
-    s.get(h);
-    for (int64_t t = bos; t < eos; ++t) {
-        const Rows<IO> rx(a.x, a.D, t, 1, c, active), ry(a.y, a.D, t, 1, c, active);
-        const Rows<GT> rg(a.gate, a.D, t, 1, c, active);
-        Chan<GT, VEC> g;
-        Chan<IO, VEC> x;
-        g.load(rg.r, rg.at(0));
-        x.load(rx.r, rx.at(0));
-        float gv[VEC], xv[VEC];
-        g.get(gv);
-        x.get(xv);
+    for (int64_t t = bos; t < eos; t += AHEAD) {
+        const int rows = eos - t < AHEAD ? (int)(eos - t) : AHEAD;
+        const Rows<IO> rx(a.x, a.D, t, rows, c, active), ry(a.y, a.D, t, rows, c, active);
+        const Rows<GT> rg(a.gate, a.D, t, rows, c, active);
+        Chan<GT, VEC> g[AHEAD];
+        Chan<IO, VEC> x[AHEAD];
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            h[e] = step<KIND>(encode_gate<KIND>(gv[e]), h[e], xv[e]);
+        for (int i = 0; i < AHEAD; ++i) {
+            g[i].load(rg.r, rg.at(i));
+            x[i].load(rx.r, rx.at(i));
         }
-        Chan<IO, VEC>::put(ry.r, ry.at(0), h);
+        if (t == bos) s.get(h);
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            if (i == rows) break;
+            float gv[VEC], xv[VEC];
+            g[i].get(gv);
+            x[i].get(xv);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) h[e] = step<KIND>(encode_gate<KIND>(gv[e]), h[e], xv[e]);
+            Chan<IO, VEC>::put(ry.r, ry.at(i), h);
+        }
     }
-    if (a.commit) Chan<ST, VEC>::put(rs.r, rs.at(0), h);
+    if (a.commit && eos > bos) Chan<ST, VEC>::put(rs.r, rs.at(0), h);
 }
 
 template <int KIND, typename IO, int VEC, int TPT, bool BACKWARD> hipError_t run_scan(LinearArgs a, hipStream_t s) {
@@ -700,20 +712,28 @@ hipError_t scan_tiles(const LinearArgs& a, bool backward, hipStream_t s) {
 // time to the first output and more workgroups.  Forward, log gate, bf16, large / small: 64 x 1024 tokens x
 // channels 12.6 / 5.7 us, 333 x 4096 18.4 / 11.9, 2048 x 2048 20.5 / 22.4, 4096 x 2048 24.9 / 36.6, 8192 x 4096
 // 71.6 / 80.2: small below 128 large tiles.  The fp32 backward pass keeps 8 tokens per wave: 16 spill
-// (8192 x 4096: 143 us, 8 tokens 128).  Odd rows go one channel per lane.
+// (8192 x 4096: 143 us, 8 tokens 128).  Odd rows go one channel per lane, 16 tokens per wave in their large tiles
+// (333 x 515 10.7 / 9.4 us, 1000 x 515 11.9 / 12.0, 3001 x 515 16.3 / 21.2).
 template <int KIND, typename IO> hipError_t scan(const LinearArgs& a, bool backward, hipStream_t s) {
     constexpr bool kHalf = Elem<IO>::bytes == 2;
     constexpr int F = kHalf ? 32 : 16, R = kHalf ? 16 : 8;
-    const int64_t tokens = kWaves * (backward ? R : F), channels = 128;
-    const bool many = (a.T + tokens - 1) / tokens * ((a.D + channels - 1) / channels) >= kManyTiles;
+    // 65 to 128 tokens: one tile of 16 tokens per wave needs no chain (100 x 1024: 6.5 us, with a chain 9.2)
+    if (a.T > kLinearBlock && a.T <= kWaves * 16) return scan_tiles<KIND, IO, 1, 16, 16>(a, backward, s);
+    auto many = [&](int64_t tokens, int64_t channels) {
+        return (a.T + tokens - 1) / tokens * ((a.D + channels - 1) / channels) >= kManyTiles;
+    };
     if (vectors<KIND, IO, 2>(a))
-        return many ? scan_tiles<KIND, IO, 2, F, R>(a, backward, s) : scan_tiles<KIND, IO, 2, 8, 8>(a, backward, s);
-    return many ? scan_tiles<KIND, IO, 1, 16, 16>(a, backward, s) : scan_tiles<KIND, IO, 1, 8, 8>(a, backward, s);
+        return many(kWaves * (backward ? R : F), 128) ? scan_tiles<KIND, IO, 2, F, R>(a, backward, s)
+                                                      : scan_tiles<KIND, IO, 2, 8, 8>(a, backward, s);
+    return many(kWaves * 16, 64) ? scan_tiles<KIND, IO, 1, 16, 16>(a, backward, s)
+                                 : scan_tiles<KIND, IO, 1, 8, 8>(a, backward, s);
 }
 
 template <int KIND, typename IO, typename ST, int VEC> hipError_t decode_run(const LinearArgs& a, hipStream_t s) {
     const int64_t per = 256 * VEC;
-    linear_decode_kernel<KIND, IO, ST, VEC><<<dim3((unsigned)((a.D + per - 1) / per), (unsigned)a.N), 256, 0, s>>>(a);
+    const dim3 grid((unsigned)((a.D + per - 1) / per), (unsigned)a.N);
+    if (a.max_q_len > 1) linear_decode_kernel<KIND, IO, ST, VEC, 4><<<grid, 256, 0, s>>>(a);
+    else linear_decode_kernel<KIND, IO, ST, VEC, 1><<<grid, 256, 0, s>>>(a);
     return hipGetLastError();
 }
 
