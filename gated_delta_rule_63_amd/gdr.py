@@ -506,6 +506,10 @@ def _required(t: Optional[torch.Tensor], name: str, shape, dtype, device: int) -
     return _arg(t, name, shape, dtype, device)
 
 
+def _rows(n: int, m: int, dtype, device: int) -> torch.Tensor:
+    return torch.empty_strided((n, m), (m, 1), dtype=dtype, device=device)
+
+
 class _On:
     """The device and stream of a call: outputs and workspaces that the binding makes are allocated on the
     stream that uses them, and the launch goes to the tensors' device whatever the current one is."""
@@ -538,7 +542,7 @@ def _workspace(workspace, need: int, device: int):
     if workspace is None:
         if need == 0:
             return None, 0, None
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        workspace = torch.empty_strided((need,), (1,), dtype=torch.uint8, device=device)
         return workspace.data_ptr(), need, workspace
     _check(workspace, "workspace", dtype=torch.uint8)
     if workspace.get_device() != device:
@@ -593,11 +597,11 @@ def gdr_linear_scan_fwd(x, gate, gate_kind: int, cu_seqlens=None, initial_state=
         if y is None:
             y = torch.empty_like(x)
         if final_state is None and output_final_state:
-            final_state = torch.empty(states, dtype=f32, device=dev)
+            final_state = _rows(N, D, f32, dev)
         blocks = (-(-T // GDR_LINEAR_BLOCK), D)
         want_blocks = output_block_states or block_states is not None
         if want_blocks and block_states is None:
-            block_states = torch.empty(blocks, dtype=f32, device=dev)
+            block_states = _rows(*blocks, f32, dev)
         ref = ctypes.byref(p)
         ws, nb, keep = _workspace(workspace, lib().gdr_linear_workspace_size(ref), dev)
         st = _lib.gdr_linear_scan_fwd(ref, px, pg, _arg(cu_seqlens, "cu_seqlens", (N + 1,), torch.int32, dev),
@@ -624,7 +628,7 @@ def gdr_linear_scan_bwd(x, gate, gate_kind: int, dy, block_states, cu_seqlens=No
         if dgate is None:
             dgate = torch.empty_like(gate)
         if d_initial_state is None and output_d_initial_state:
-            d_initial_state = torch.empty(states, dtype=f32, device=dev)
+            d_initial_state = _rows(N, D, f32, dev)
         ref = ctypes.byref(p)
         ws, nb, keep = _workspace(workspace, lib().gdr_linear_workspace_size(ref), dev)
         st = _lib.gdr_linear_scan_bwd(ref, px, pg, _arg(cu_seqlens, "cu_seqlens", (N + 1,), torch.int32, dev),
@@ -697,11 +701,11 @@ def gdr_beam_select(logits, scores, num_out: int, finished=None, eos_token: int 
         finished = finished.view(torch.uint8)
     with _On(dev, stream) as raw:
         if out_scores is None:
-            out_scores = torch.empty(shape, dtype=torch.float32, device=dev)
+            out_scores = _rows(*shape, torch.float32, dev)
         if out_parents is None:
-            out_parents = torch.empty(shape, dtype=i32, device=dev)
+            out_parents = _rows(*shape, i32, dev)
         if out_tokens is None:
-            out_tokens = torch.empty(shape, dtype=i32, device=dev)
+            out_tokens = _rows(*shape, i32, dev)
         ref = ctypes.byref(p)
         ws, nb, keep = _workspace(workspace, lib().gdr_beam_workspace_size(ref), dev)
         st = _lib.gdr_beam_select(ref, logits.data_ptr(), _required(scores, "scores", (B, W), torch.float32, dev),
@@ -728,7 +732,7 @@ def gdr_beam_reorder(pool, state_indices, parents, slot_dim: int = 0, state_indi
     rows, dev, i32 = state_indices.shape, pool.get_device(), torch.int32
     slot_bytes = pool.element_size() * math.prod(shape[slot_dim + 1:])
     with _On(dev, stream) as raw:
-        out = torch.empty(rows, dtype=i32, device=dev) if state_indices_out is None else state_indices_out
+        out = _rows(*rows, i32, dev) if state_indices_out is None else state_indices_out
         st = lib().gdr_beam_reorder(rows[0], rows[1], _required(parents, "parents", rows, i32, dev),
                                     _arg(state_indices, "state_indices", rows, i32, dev),
                                     _arg(out, "state_indices_out", rows, i32, dev),

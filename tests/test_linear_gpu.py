@@ -112,6 +112,25 @@ def test_long_without_states_and_with_a_tail(D, kind):
     _run_both(_problem(6 + D, [2049], D, kind, "bf16", tail=64))
 
 
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("kind", ["log", "sigmoid"])
+@pytest.mark.parametrize("D", [640, 641])
+def test_large_tiles(D, kind, io):
+    """Enough tokens and channels for the large tiles, with borders inside them, at their ends, empty sequences
+    and rows behind the last one."""
+    _run_both(_problem(40 + D, [256, 255, 1, 0, 4096, 128, 64, 0, 1, 1, 1, 3389, 37], D, kind, io, tail=29))
+
+
+@pytest.mark.parametrize("T", [63, 64, 65, 100, 127, 128, 129, 256, 257])
+def test_lengths_around_the_tiles(T):
+    _run_both(_problem(60 + T, [T], 66, "log", "bf16"))
+    _run_both(_problem(61 + T, [T - 40, 40], 33, "sigmoid", "f32", tail=3))
+
+
+def test_a_long_chain_of_narrow_tiles():
+    _run_both(_problem(70, [30000], 64, "log", "f32"))
+
+
 def test_many_sequences_and_wide_rows():
     r = np.random.default_rng(9)
     _run_both(_problem(9, r.integers(0, 4, 3000).tolist(), 8, "log", "f32"))
