@@ -13,9 +13,11 @@
 // sequences' borders are.  The backward pass composes the same way from the right (c_t = a_t (dy_t +
 // c_{t+1}), cut at each sequence's last token).
 //
-// Layout: a lane owns VEC neighbouring channels, a wave a run of TPT tokens, the 8 waves of a workgroup
-// the 8 runs of a tile; a lane reads its channels' rows with one wide load each and walks them in time
-// order in registers, so no value crosses lanes.
+// Layout: a lane owns VEC neighbouring channels, a wave a run of TPT tokens, the W waves of a workgroup
+// the W runs of a tile; a lane holds its channels' rows in registers and walks them in time order, so no
+// value crosses lanes and every input is read once.  A large batch is bound by HBM and by how well the loads of
+// one workgroup cover the arithmetic of the other on its CU (32768 x 4096 bf16, log gate: 207 us, 5.2 TB/s, VALU
+// busy half the time; 65573 x 2048 fp32, one sequence: 284 us, 5.7 TB/s), a small one by the latency of a tile.
 #include "gdr_device.h"
 #include "gdr_internal.h"
 
@@ -23,9 +25,7 @@ namespace gdr {
 
 namespace {
 
-constexpr int kWaves = 8;
-constexpr int kThreads = 64 * kWaves;
-constexpr int kWavesPerSimd = 4;        // two workgroups per CU: at most 128 registers
+constexpr int kWavesPerSimd = 4;        // two workgroups of 8 waves per CU: at most 128 registers
 constexpr int kLogGate = 0;
 
 // ---- a lane's VEC channels of one token, as loaded ----
@@ -276,10 +276,10 @@ template <int VEC> __device__ __forceinline__ void store_state(float* p, int64_t
 
 // Empty sequences have no token whose lane could write their final state (or its gradient): the workgroup
 // of the chain's first tile copies them, VEC channels per lane, a sequence per wave.
-template <int VEC> __device__ __forceinline__ void copy_empty(const LinearArgs& a, const float* src, float* dst, int64_t c) {
+template <int VEC, int W> __device__ __forceinline__ void copy_empty(const LinearArgs& a, const float* src, float* dst, int64_t c) {
     if (!a.cu || !dst) return;
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-    for (int n0 = w * 64; n0 < a.N; n0 += kWaves * 64) {
+    for (int n0 = w * 64; n0 < a.N; n0 += W * 64) {
         const int n = n0 + lane;
         uint64_t m = __ballot(n < a.N && a.cu[n < a.N ? n : 0] == a.cu[n < a.N ? n + 1 : 0]);
         for (; m; m &= m - 1) {
@@ -313,15 +313,17 @@ __global__ __launch_bounds__(256) void linear_init_kernel(const LinearArgs a, in
     if (i < pairs) reinterpret_cast<uint4*>(a.runs)[i] = uint4{~0u, ~0u, ~0u, ~0u};
 }
 
-template <int VEC> struct TileShared {
-    float2 run[kWaves][64 * VEC];    // the waves' runs; then the run of all waves before each
-    float2 back[kWaves][64 * VEC];   // runs of earlier tiles
+constexpr int kBack = 8;              // tiles that a tile looks back to
+
+template <int VEC, int W> struct TileShared {
+    float2 run[W][64 * VEC];         // the waves' runs; then the run of all waves before each
+    float2 back[kBack][64 * VEC];    // runs of earlier tiles
     float carry[64 * VEC];           // the state entering the tile
     int ticket;
 };
 
 // Which tile of the chain this workgroup takes.
-template <int VEC> __device__ __forceinline__ int64_t take_ticket(const LinearArgs& a, TileShared<VEC>& sh) {
+template <int VEC, int W> __device__ __forceinline__ int64_t take_ticket(const LinearArgs& a, TileShared<VEC, W>& sh) {
     if (a.tiles == 1) return blockIdx.x;
     if (threadIdx.x == 0) sh.ticket = (int)atomicAdd(a.ticket, 1u);
     __syncthreads();
@@ -329,17 +331,18 @@ template <int VEC> __device__ __forceinline__ int64_t take_ticket(const LinearAr
 }
 
 // After every wave has stored its run (and a barrier): fills sh.carry and turns sh.run into the runs of all
-// waves that come before each.  `at` is the tile's place in the chain; REVERSE: the waves' order is 7 .. 0.
-template <int VEC, bool REVERSE>
-__device__ __forceinline__ void chain(const LinearArgs& a, TileShared<VEC>& sh, int64_t at, int64_t c_tile) {
+// waves that come before each.  `at` is the tile's place in the chain; REVERSE: the waves' order is W-1 .. 0.
+template <int VEC, int W, bool REVERSE>
+__device__ __forceinline__ void chain(const LinearArgs& a, TileShared<VEC, W>& sh, int64_t at, int64_t c_tile) {
+    static_assert(64 * W >= 64 * VEC && kBack % (W < kBack ? W : kBack) == 0, "a thread per channel, whole rounds of waves");
     constexpr int CH = 64 * VEC;
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
     float2 whole{0.0f, 0.0f};
     if (tid < CH) {
-        float2 r = sh.run[REVERSE ? kWaves - 1 : 0][tid];
+        float2 r = sh.run[REVERSE ? W - 1 : 0][tid];
 #pragma unroll
-        for (int i = 1; i < kWaves; ++i) {
-            float2& slot = sh.run[REVERSE ? kWaves - 1 - i : i][tid];
+        for (int i = 1; i < W; ++i) {
+            float2& slot = sh.run[REVERSE ? W - 1 - i : i][tid];
             const float2 mine = slot;
             slot = r;
             r = compose(r, mine);
@@ -350,39 +353,42 @@ __device__ __forceinline__ void chain(const LinearArgs& a, TileShared<VEC>& sh, 
         sh.carry[tid] = 0.0f;
     }
     if (at > 0) {
-        // Wave w holds the word of the tile w + 1 places back.  The state is carried forward tile by tile from
+        // Wave w reads the word of the tile w + 1 places back.  The state is carried forward tile by tile from
         // the farthest cut run among them, so it is the same, bit for bit, whichever of them are cut already.
-        const int64_t from = at - 1 - w;
-        const bool look = from >= 0 && c_tile + lane * VEC < a.D;
         float state = 0.0f;
         for (;;) {
-            float2 got[VEC];
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) got[e] = float2{kCut, 0.0f};
-            if (look) {
-                uint64_t word[VEC];
-                for (;;) {
-                    bool empty = false;
+            for (int k = 0; k < kBack; k += W) {
+                if (w + k >= kBack) break;
+                const int64_t from = at - 1 - w - k;
+                float2 got[VEC];
 #pragma unroll
-                    for (int e = 0; e < VEC; ++e) {
-                        word[e] = __hip_atomic_load(run_word(a, from, c_tile + lane * VEC + e), __ATOMIC_RELAXED,
-                                                    __HIP_MEMORY_SCOPE_AGENT);
-                        empty |= (uint32_t)(word[e] >> 32) == kEmpty;
+                for (int e = 0; e < VEC; ++e) got[e] = float2{kCut, 0.0f};
+                if (from >= 0 && c_tile + lane * VEC < a.D) {
+                    uint64_t word[VEC];
+                    for (;;) {
+                        bool empty = false;
+#pragma unroll
+                        for (int e = 0; e < VEC; ++e) {
+                            word[e] = __hip_atomic_load(run_word(a, from, c_tile + lane * VEC + e), __ATOMIC_RELAXED,
+                                                        __HIP_MEMORY_SCOPE_AGENT);
+                            empty |= (uint32_t)(word[e] >> 32) == kEmpty;
+                        }
+                        if (!empty) break;
+                        __builtin_amdgcn_s_sleep(1);
                     }
-                    if (!empty) break;
-                    __builtin_amdgcn_s_sleep(1);
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e)
+                        got[e] = float2{__uint_as_float((uint32_t)(word[e] >> 32)), __uint_as_float((uint32_t)word[e])};
                 }
 #pragma unroll
-                for (int e = 0; e < VEC; ++e)
-                    got[e] = float2{__uint_as_float((uint32_t)(word[e] >> 32)), __uint_as_float((uint32_t)word[e])};
+                for (int e = 0; e < VEC; ++e) sh.back[w + k][lane * VEC + e] = got[e];
             }
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) sh.back[w][lane * VEC + e] = got[e];
             __syncthreads();
             bool found = false;
             if (tid < CH) {
 #pragma unroll
-                for (int i = kWaves - 1; i >= 0; --i) {
+                for (int i = kBack - 1; i >= 0; --i) {
                     const float2 r = sh.back[i][tid];
                     found |= r.x == kCut;
                     state = apply_run(r, state);
@@ -401,11 +407,11 @@ __device__ __forceinline__ void chain(const LinearArgs& a, TileShared<VEC>& sh, 
 
 // =====================================================================================================
 // forward
-template <int KIND, typename IO, int VEC, int TPT>
-__global__ __launch_bounds__(kThreads, kWavesPerSimd) void linear_fwd_kernel(const LinearArgs a) {
-    constexpr int L = kWaves * TPT;
+template <int KIND, typename IO, int VEC, int W, int TPT>
+__global__ __launch_bounds__(64 * W, kWavesPerSimd) void linear_fwd_kernel(const LinearArgs a) {
+    constexpr int L = W * TPT;
     static_assert(L % kLinearBlock == 0, "the workspace holds a word per channel and block, block states begin runs");
-    __shared__ TileShared<VEC> sh;
+    __shared__ TileShared<VEC, W> sh;
     const int64_t ticket = take_ticket(a, sh);
     const int lane = threadIdx.x & 63;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -461,7 +467,7 @@ __global__ __launch_bounds__(kThreads, kWavesPerSimd) void linear_fwd_kernel(con
         for (int e = 0; e < VEC; ++e) hide(v[i][e]);
     }
     __syncthreads();
-    chain<VEC, false>(a, sh, tile, c_tile);
+    chain<VEC, W, false>(a, sh, tile, c_tile);
     float h[VEC];
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
@@ -482,18 +488,18 @@ __global__ __launch_bounds__(kThreads, kWavesPerSimd) void linear_fwd_kernel(con
         __builtin_amdgcn_sched_barrier(0);
         if (__builtin_expect((bo.last >> i) & 1, 0)) store_state<VEC>(a.ht, bo.seq(i), a.D, c, h);
     }
-    if (tile == 0) copy_empty<VEC>(a, a.h0, a.ht, c);
+    if (tile == 0) copy_empty<VEC, W>(a, a.h0, a.ht, c);
 }
 
 // =====================================================================================================
 // backward.  The states are formed again from x and the tile's entering state (block_states); the carry
 // c = a (dy + c') runs from the last token to the first, so the chain begins at the last tile.
-template <int KIND, typename IO, int VEC, int TPT>
-__global__ __launch_bounds__(kThreads, kWavesPerSimd) void linear_bwd_kernel(const LinearArgs a) {
-    constexpr int L = kWaves * TPT;
+template <int KIND, typename IO, int VEC, int W, int TPT>
+__global__ __launch_bounds__(64 * W, kWavesPerSimd) void linear_bwd_kernel(const LinearArgs a) {
+    constexpr int L = W * TPT;
     static_assert(L % kLinearBlock == 0, "the workspace holds a word per channel and block, tiles begin at block states");
-    __shared__ TileShared<VEC> sh;
-    __shared__ float2 fwd[kWaves][64 * VEC];
+    __shared__ TileShared<VEC, W> sh;
+    __shared__ float2 fwd[W][64 * VEC];
     const int64_t ticket = take_ticket(a, sh);
     const int lane = threadIdx.x & 63;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -571,7 +577,7 @@ __global__ __launch_bounds__(kThreads, kWavesPerSimd) void linear_bwd_kernel(con
     }
     hide_tile();
     __syncthreads();
-    chain<VEC, true>(a, sh, place, c_tile);
+    chain<VEC, W, true>(a, sh, place, c_tile);
     float h[VEC], cr[VEC];
     load_state<VEC>(a.block_states, tile * (L / kLinearBlock), a.D, c, h);
     for (int i = 0; i < w; ++i)
@@ -580,7 +586,7 @@ __global__ __launch_bounds__(kThreads, kWavesPerSimd) void linear_bwd_kernel(con
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
         cr[e] = sh.carry[lane * VEC + e];
-        if (w < kWaves - 1) cr[e] = apply_run(sh.run[w][lane * VEC + e], cr[e]);
+        if (w < W - 1) cr[e] = apply_run(sh.run[w][lane * VEC + e], cr[e]);
     }
 
     // dgate = D u: u holds a h_{t-1}, or a (1 - a) (h_{t-1} - x)
@@ -620,7 +626,7 @@ __global__ __launch_bounds__(kThreads, kWavesPerSimd) void linear_bwd_kernel(con
         __builtin_amdgcn_sched_barrier(0);
         if (__builtin_expect((bo.first >> i) & 1, 0)) store_state<VEC>(a.dh0, bo.seq(i), a.D, c, cr);
     }
-    if (place == 0) copy_empty<VEC>(a, a.dht, a.dh0, c);
+    if (place == 0) copy_empty<VEC, W>(a, a.dht, a.dh0, c);
 }
 
 // All sequences empty: the final states are the initial ones, and so for the gradients.
@@ -678,17 +684,17 @@ __global__ __launch_bounds__(256) void linear_decode_kernel(const LinearArgs a) 
     if (a.commit && eos > bos) Chan<ST, VEC>::put(rs.r, rs.at(0), h);
 }
 
-template <int KIND, typename IO, int VEC, int TPT, bool BACKWARD> hipError_t run_scan(LinearArgs a, hipStream_t s) {
+template <int KIND, typename IO, int VEC, int W, int TPT, bool BACKWARD> hipError_t run_scan(LinearArgs a, hipStream_t s) {
     a.nch = (a.D + 64 * VEC - 1) / (64 * VEC);
-    a.tiles = (a.T + kWaves * TPT - 1) / (kWaves * TPT);
+    a.tiles = (a.T + W * TPT - 1) / (W * TPT);
     const int64_t blocks = a.tiles * a.nch;
     if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
     if (a.tiles > 1) {
         const int64_t pairs = (a.tiles * a.D + 1) / 2;  // the workspace holds the word behind an odd count too
         linear_init_kernel<<<dim3((unsigned)((pairs + 255) / 256)), 256, 0, s>>>(a, pairs);
     }
-    if constexpr (BACKWARD) linear_bwd_kernel<KIND, IO, VEC, TPT><<<dim3((unsigned)blocks), kThreads, 0, s>>>(a);
-    else linear_fwd_kernel<KIND, IO, VEC, TPT><<<dim3((unsigned)blocks), kThreads, 0, s>>>(a);
+    if constexpr (BACKWARD) linear_bwd_kernel<KIND, IO, VEC, W, TPT><<<dim3((unsigned)blocks), 64 * W, 0, s>>>(a);
+    else linear_fwd_kernel<KIND, IO, VEC, W, TPT><<<dim3((unsigned)blocks), 64 * W, 0, s>>>(a);
     return hipGetLastError();
 }
 
@@ -702,31 +708,37 @@ template <int KIND, typename IO, int VEC> bool vectors(const LinearArgs& a) {
 }
 constexpr int64_t kManyTiles = 128;
 
-template <int KIND, typename IO, int VEC, int TPT_FWD, int TPT_BWD>
+template <int KIND, typename IO, int VEC, int W, int TPT_FWD, int TPT_BWD>
 hipError_t scan_tiles(const LinearArgs& a, bool backward, hipStream_t s) {
-    return backward ? run_scan<KIND, IO, VEC, TPT_BWD, true>(a, s) : run_scan<KIND, IO, VEC, TPT_FWD, false>(a, s);
+    return backward ? run_scan<KIND, IO, VEC, W, TPT_BWD, true>(a, s) : run_scan<KIND, IO, VEC, W, TPT_FWD, false>(a, s);
 }
 
-// Tiles.  Large ones (two channels per lane; 32 tokens per wave in bf16, 16 in fp32 and in the bf16 backward pass,
-// whose kept values fill the registers) have the shortest chain; small ones (8 tokens per wave) the shortest
-// time to the first output and more workgroups.  Forward, log gate, bf16, large / small: 64 x 1024 tokens x
-// channels 12.6 / 5.7 us, 333 x 4096 18.4 / 11.9, 2048 x 2048 20.5 / 22.4, 4096 x 2048 24.9 / 36.6, 8192 x 4096
-// 71.6 / 80.2: small below 128 large tiles.  The fp32 backward pass keeps 8 tokens per wave: 16 spill
-// (8192 x 4096: 143 us, 8 tokens 128).  Odd rows go one channel per lane, 16 tokens per wave in their large tiles
-// (333 x 515 10.7 / 9.4 us, 1000 x 515 11.9 / 12.0, 3001 x 515 16.3 / 21.2).
+// Tiles (us of device time, log gate, bf16, forward; T x D).
+//  - One tile needs no chain, and no launch before it.  Up to 64 tokens 8 per wave (64 x 1024: 5.7); to 128, 16
+//    (100 x 1024: 6.4, with a chain 9.2); to 256, 16 waves of 16 (200 x 1024: 7.9, with a chain 9.7); to 512 the
+//    forward pass has 16 waves of 32 (333 x 1024: 12.2, with a chain 10.5, but a launch less: 12.9 for a call
+//    among others, with a chain 14.9).
+//  - Chains of large tiles: two channels per lane; 32 tokens per wave in bf16, 16 in fp32 and in the bf16 backward
+//    pass, whose kept values fill the registers.  The fp32 backward pass keeps 8: 16 spill (8192 x 4096: 143, 8
+//    tokens 128).  Tiles of 4 or 16 waves were slower (32768 x 4096: 8 waves 207, 4 waves 219, 16 waves 247).
+//  - Chains of small ones (8 tokens per wave) have more workgroups: large / small 333 x 4096 18.4 / 11.9,
+//    2048 x 2048 20.5 / 22.4, 4096 x 2048 24.9 / 36.6: small below 128 large tiles.
+//  - Odd rows go one channel per lane, 16 tokens per wave in their large tiles (333 x 515 10.7 / 9.4, 1000 x 515
+//    11.9 / 12.0, 3001 x 515 16.3 / 21.2).
 template <int KIND, typename IO> hipError_t scan(const LinearArgs& a, bool backward, hipStream_t s) {
     constexpr bool kHalf = Elem<IO>::bytes == 2;
-    constexpr int F = kHalf ? 32 : 16, R = kHalf ? 16 : 8;
-    // 65 to 128 tokens: one tile of 16 tokens per wave needs no chain (100 x 1024: 6.5 us, with a chain 9.2)
-    if (a.T > kLinearBlock && a.T <= kWaves * 16) return scan_tiles<KIND, IO, 1, 16, 16>(a, backward, s);
+    constexpr int F = kHalf ? 32 : 16, R = kHalf ? 16 : 8, W = 8;
+    if (a.T > 64 && a.T <= 128) return scan_tiles<KIND, IO, 1, W, 16, 16>(a, backward, s);
+    if (a.T > 128 && a.T <= 256) return scan_tiles<KIND, IO, 1, 16, 16, 16>(a, backward, s);
+    if (!backward && a.T > 256 && a.T <= 512) return run_scan<KIND, IO, 1, 16, 32, false>(a, s);
     auto many = [&](int64_t tokens, int64_t channels) {
         return (a.T + tokens - 1) / tokens * ((a.D + channels - 1) / channels) >= kManyTiles;
     };
     if (vectors<KIND, IO, 2>(a))
-        return many(kWaves * (backward ? R : F), 128) ? scan_tiles<KIND, IO, 2, F, R>(a, backward, s)
-                                                      : scan_tiles<KIND, IO, 2, 8, 8>(a, backward, s);
-    return many(kWaves * 16, 64) ? scan_tiles<KIND, IO, 1, 16, 16>(a, backward, s)
-                                 : scan_tiles<KIND, IO, 1, 8, 8>(a, backward, s);
+        return many(W * (backward ? R : F), 128) ? scan_tiles<KIND, IO, 2, W, F, R>(a, backward, s)
+                                                 : scan_tiles<KIND, IO, 2, W, 8, 8>(a, backward, s);
+    return many(W * 16, 64) ? scan_tiles<KIND, IO, 1, W, 16, 16>(a, backward, s)
+                            : scan_tiles<KIND, IO, 1, W, 8, 8>(a, backward, s);
 }
 
 template <int KIND, typename IO, typename ST, int VEC> hipError_t decode_run(const LinearArgs& a, hipStream_t s) {

@@ -121,7 +121,7 @@ def test_large_tiles(D, kind, io):
     _run_both(_problem(40 + D, [256, 255, 1, 0, 4096, 128, 64, 0, 1, 1, 1, 3389, 37], D, kind, io, tail=29))
 
 
-@pytest.mark.parametrize("T", [63, 64, 65, 100, 127, 128, 129, 256, 257])
+@pytest.mark.parametrize("T", [63, 64, 65, 100, 127, 128, 129, 255, 256, 257, 400, 512, 513])
 def test_lengths_around_the_tiles(T):
     _run_both(_problem(60 + T, [T], 66, "log", "bf16"))
     _run_both(_problem(61 + T, [T - 40, 40], 33, "sigmoid", "f32", tail=3))
