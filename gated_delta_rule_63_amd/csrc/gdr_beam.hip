@@ -119,7 +119,7 @@ __global__ __launch_bounds__(kRowThreads, 4) void beam_rows_kernel(const BeamArg
     __shared__ __align__(16) uint64_t list[kRowWaves][kWaveList];
     __shared__ double sh_sum[kRowWaves];
     __shared__ float sh_top[kRowWaves];
-    __shared__ uint32_t sh_tau[kRowWaves];
+    __shared__ uint32_t sh_key[kRowThreads];
     __shared__ int listed[kRowWaves];
 
     const float score = a.scores[row];
@@ -167,24 +167,27 @@ __global__ __launch_bounds__(kRowThreads, 4) void beam_rows_kernel(const BeamArg
     const float wtop = wave_max(top);
     sum = wave_sum(some ? sum * (double)exp_f32(top - wtop) : 0.0);
 
-    // tau: a logit that at least `out` of this wave's reach or pass (the out-th best of the lanes' maxima)
-    const uint32_t mine = key_of(top);
-    uint32_t tau_key = 0;
-    constexpr int kLowBit = Elem<IO>::bytes == 2 ? 16 : 0;
-#pragma unroll
-    for (int bit = 31; bit >= kLowBit; --bit) {
-        const uint32_t t = tau_key | (1u << bit);
-        if (__popcll(__ballot(mine >= t)) >= a.out) tau_key = t;
-    }
-    if (!(tau_key >> 31)) tau_key |= (1u << kLowBit) - 1;  // the keys of negative bf16 values end in ones
+    sh_key[tid] = key_of(top);
     if (lane == 0) {
         sh_sum[tid >> 6] = sum;
         sh_top[tid >> 6] = wtop;
-        sh_tau[tid >> 6] = tau_key;
     }
     __syncthreads();
+    // tau: a logit that at least `out` threads reach or pass, the out-th best of the threads' maxima.  (With the
+    // best of the four waves' own such values a wave listed 13 logits instead of 4, and ranked 50 instead of 16.)
+    uint32_t key[kRowWaves], tau_key = 0;
 #pragma unroll
-    for (int i = 0; i < kRowWaves; ++i) tau_key = max(tau_key, sh_tau[i]);
+    for (int i = 0; i < kRowWaves; ++i) key[i] = sh_key[i * 64 + lane];
+    constexpr int kLowBit = Elem<IO>::bytes == 2 ? 16 : 0;
+#pragma unroll 4
+    for (int bit = 31; bit >= kLowBit; --bit) {
+        const uint32_t t = tau_key | (1u << bit);
+        int c = 0;
+#pragma unroll
+        for (int i = 0; i < kRowWaves; ++i) c += __popcll(__ballot(key[i] >= t));
+        if (c >= a.out) tau_key = t;
+    }
+    if (!(tau_key >> 31)) tau_key |= (1u << kLowBit) - 1;  // the keys of negative bf16 values end in ones
     if (tid == 0) {
         float btop = sh_top[0];
 #pragma unroll
@@ -196,22 +199,23 @@ __global__ __launch_bounds__(kRowThreads, 4) void beam_rows_kernel(const BeamArg
         a.tops[(int64_t)row * a.splits + split] = btop;
     }
 
-    // Each wave lists its logits above tau.  Where a few lanes hold very many of them, tau becomes the wave's
-    // out-th best and the list is made again.
-    float tau = fmaxf(of_key(tau_key), kNone);
+    // Each wave lists its logits from tau on (-inf is never listed).  Where these are very many (few threads hold
+    // them, or many are equal), tau becomes the wave's out-th best: those above it are listed again, and of those
+    // equal to it the first `out` in the order of the tokens.
+    float from = fmaxf(of_key(tau_key), -3.402823466e38f);
     uint64_t* mylist = list[tid >> 6];
-    int found;
-    for (;;) {
+    int found, ties = 0;
+    for (bool exact = false;; exact = true) {
 #pragma unroll
         for (int i = 0; i < PER; ++i) hide(x[i]);
         asm volatile("" : "+v"(own));  // nor are 64 token numbers kept from pass to pass
         found = 0;
 #pragma unroll
         for (int g = 0; g < G; ++g) {
-            if (!__ballot(gmax[g] > tau)) continue;
+            if (!__ballot(gmax[g] >= from)) continue;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const bool take = x[g * 8 + e] > tau;
+                const bool take = x[g * 8 + e] >= from;
                 const uint64_t m = __ballot(take);
                 if (!m) continue;
                 const int at = found + lanes_below(m);
@@ -219,7 +223,7 @@ __global__ __launch_bounds__(kRowThreads, 4) void beam_rows_kernel(const BeamArg
                 found += __popcll(m);
             }
         }
-        if (found <= kWaveCap) break;
+        if (exact || found <= kWaveCap) break;
         uint32_t t = 0;
         for (int bit = 31; bit >= 0; --bit) {
             const float u = of_key(t | (1u << bit));
@@ -228,10 +232,8 @@ __global__ __launch_bounds__(kRowThreads, 4) void beam_rows_kernel(const BeamArg
             for (int i = 0; i < PER; ++i) c += __popcll(__ballot(x[i] >= u));
             if (c >= a.out) t |= 1u << bit;
         }
-        tau = of_key(t);  // fewer than `out` are above it
-    }
-    // logits equal to tau: the wave's first `out` in the order of the tokens (-inf is never listed)
-    if (tau > kNone) {
+        const float tau = of_key(t);
+        from = of_key(t + 1);  // the next float: fewer than `out` reach it
         int equal = 0;
 #pragma unroll
         for (int j = 0; j < PER / VECW; ++j) {
@@ -246,18 +248,45 @@ __global__ __launch_bounds__(kRowThreads, 4) void beam_rows_kernel(const BeamArg
 #pragma unroll
             for (int e = 0; e < VECW; ++e)
                 if (x[j * VECW + e] == tau) {
-                    if (rank < a.out) mylist[found + rank] = entry_of(tau + 0.0f, base + token_of(j * VECW + e));
+                    if (rank < a.out) mylist[kBeamMaxOut + rank] = entry_of(tau + 0.0f, base + token_of(j * VECW + e));
                     ++rank;
                 }
             equal += __builtin_amdgcn_readlane(incl, 63);
         }
-        found += min(equal, a.out);
+        ties = min(equal, a.out);
+    }
+    if (ties > 0) {  // they stand behind room for `out` better ones
+        uint64_t e = 0;
+        if (lane < ties) e = mylist[kBeamMaxOut + lane];
+        if (lane < ties) mylist[found + lane] = e;
+        found += ties;
     }
     if (lane < 8) mylist[found + lane] = 0;  // to a multiple of eight: an entry better than none
     if (lane == 0) listed[tid >> 6] = found;
     __syncthreads();
     // an entry's place is the number of better ones
     uint64_t* out = a.entries + ((int64_t)row * a.splits + split) * a.out;
+    int before[kRowWaves], all = 0;
+#pragma unroll
+    for (int v = 0; v < kRowWaves; ++v) {
+        before[v] = all;
+        all += listed[v];
+    }
+    if (all <= 64) {
+        if (tid >= 64) return;
+        uint64_t mine = 0;
+#pragma unroll
+        for (int v = 0; v < kRowWaves; ++v)
+            if (lane >= before[v] && lane - before[v] < listed[v]) mine = list[v][lane - before[v]];
+        int rank = 0;
+        for (int j = 0; j < all; ++j) {
+            const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)mine, j), hi = __builtin_amdgcn_readlane((uint32_t)(mine >> 32), j);
+            rank += ((uint64_t)hi << 32 | lo) > mine;
+        }
+        if (lane < all && rank < a.out) out[rank] = mine;
+        if (lane >= all && lane < a.out) out[lane] = 0;
+        return;
+    }
     for (int i = lane; i < found; i += 64) {
         const uint64_t mine = mylist[i];
         int rank = 0;
@@ -269,10 +298,6 @@ __global__ __launch_bounds__(kRowThreads, 4) void beam_rows_kernel(const BeamArg
         }
         if (rank < a.out) out[rank] = mine;
     }
-    int all = 0;
-#pragma unroll
-    for (int v = 0; v < kRowWaves; ++v) all += listed[v];
-    for (int i = all + tid; i < a.out; i += kRowThreads) out[i] = 0;
 }
 
 __device__ __forceinline__ uint64_t key_of64(double x) {

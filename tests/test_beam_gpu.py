@@ -54,6 +54,33 @@ def test_largest_vocabulary_and_many_rows():
     _compare(_logits(2, 150, 7, 600), _scores(2, 150, 7), 14, "f32")
 
 
+@pytest.mark.parametrize("io,offset", [("bf16", 1), ("bf16", 3), ("f32", 1), ("f32", 2)])
+def test_rows_that_begin_between_multiples_of_16_bytes(io, offset):
+    lg, sc = _logits(30 + offset, 2, 3, 5003), _scores(31, 2, 3)
+    lg[:, :, :9] += 8.0   # good candidates at both ends of the rows
+    lg[:, :, -9:] += 8.0
+    t = _dev_logits(lg, io, 0)
+    flat = torch.empty(t.numel() + offset, dtype=t.dtype, device="cuda")
+    view = flat[offset:].view(t.shape)
+    view.copy_(t)
+    want = beam.select(f64(t), sc.astype(np.float64), 20)
+    s, p, tok = gdr.gdr_beam_select(view, to_dev(sc), 20)
+    assert np.array_equal(to_host(p), want[1]) and np.array_equal(to_host(tok), want[2])
+
+
+def test_most_lists():
+    """32 beams over 2^20 tokens in fp32: the most parts that a merge sees.  Distinct random logits."""
+    g = torch.Generator(device="cuda").manual_seed(3)
+    lg = torch.randn(1, 32, 1 << 20, device="cuda", generator=g)
+    sc = to_dev(_scores(32, 1, 32))
+    s, p, t = gdr.gdr_beam_select(lg, sc, 64)
+    x = lg[0].double()
+    x = x - torch.logsumexp(x, 1, keepdim=True) + sc[0].double()[:, None]
+    best, at = x.flatten().topk(64)
+    assert bool((best[:-1] > best[1:]).all())
+    assert torch.equal(p[0].long() * (1 << 20) + t[0].long(), at)
+
+
 @pytest.mark.parametrize("io", ["bf16", "f32"])
 def test_ties_go_to_the_lower_index(io):
     for sd in (0.0, 0.25):  # all equal; a handful of distinct values
