@@ -200,6 +200,27 @@ def test_select_captured_and_on_another_stream():
     assert all(torch.equal(a, b) for a, b in zip(other, want))
 
 
+def test_select_offsets_past_32_bits():
+    """Rows behind 2^31 logits: the last batch rows against the oracle."""
+    B, W, V = 3300, 16, 41000
+    lg = torch.randn(B, W, V, device="cuda", dtype=torch.bfloat16, generator=torch.Generator(device="cuda").manual_seed(2))
+    sc = _scores(33, B, W)
+    s, p, t = gdr.gdr_beam_select(lg, to_dev(sc), 8)
+    want = beam.select(f64(lg[-2:]), sc[-2:].astype(np.float64), 8)
+    assert np.array_equal(to_host(p)[-2:], want[1]) and np.array_equal(to_host(t)[-2:], want[2])
+
+
+def test_reorder_offsets_past_32_bits():
+    pool = torch.empty(2, 1100, 1 << 20, dtype=torch.bfloat16, device="cuda")
+    pool[1, 1099] = 3.0
+    pool[1, 1098] = 4.0
+    pool[0, 1099] = 5.0
+    idx, par = np.array([[1099, 1098]], np.int32), np.array([[0, 0]], np.int32)
+    new = gdr.gdr_beam_reorder(pool, to_dev(idx), to_dev(par), slot_dim=1)
+    assert to_host(new).tolist() == [[1099, 1098]]
+    assert bool((pool[1, 1098] == 3.0).all()) and bool((pool[0, 1098] == 5.0).all())
+
+
 # ---------------------------------------------------------------------------------------------------
 @pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("B,W,layers,shape", [(1, 1, 1, (8,)), (3, 4, 1, (2, 128, 64)), (2, 32, 3, (77,)), (5, 7, 2, (1, 1)),

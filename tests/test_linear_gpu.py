@@ -288,6 +288,68 @@ def test_another_stream():
     assert all(bool((b == i).all()) for i, b in enumerate(big))
 
 
+def test_two_streams_at_once():
+    """Chains of two calls in flight together, each with its own workspace."""
+    p, q = _problem(16, [9000], 512, "log", "bf16"), _problem(17, [7000, 3000], 513, "sigmoid", "f32")
+    d, e = _dev(p), _dev(q)
+    want, want2 = _forward(p, d), _forward(q, e)
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    for s in (s1, s2):
+        s.wait_stream(torch.cuda.current_stream())
+    got = [(_forward(p, d, stream=s1), _forward(q, e, stream=s2)) for _ in range(5)]
+    torch.cuda.synchronize()
+    for a, b in got:
+        assert all(torch.equal(x, y) for x, y in zip(a, want)) and all(torch.equal(x, y) for x, y in zip(b, want2))
+
+
+def test_batches_without_tokens():
+    x, g = torch.empty(0, 40, device="cuda"), torch.empty(0, 40, device="cuda")
+    h0, cu = torch.randn(3, 40, device="cuda"), torch.zeros(4, dtype=torch.int32, device="cuda")
+    y, final, blocks = gdr.gdr_linear_scan_fwd(x, g, gdr.GDR_LINEAR_LOG_DECAY, cu_seqlens=cu, initial_state=h0,
+                                               output_block_states=True)
+    dx, dg, dh0 = gdr.gdr_linear_scan_bwd(x, g, gdr.GDR_LINEAR_LOG_DECAY, x, blocks, cu_seqlens=cu, initial_state=h0,
+                                          d_final_state=h0 * 2)
+    assert y.shape == x.shape and torch.equal(final, h0) and torch.equal(dh0, h0 * 2)
+    y, final = gdr.gdr_linear_scan_fwd(x, g, gdr.GDR_LINEAR_LOG_DECAY, cu_seqlens=cu)
+    assert bool((final == 0).all())
+    y, final = gdr.gdr_linear_scan_fwd(x, g, gdr.GDR_LINEAR_LOG_DECAY, cu_seqlens=cu[:1])   # no sequences
+    assert final.shape == (0, 40)
+    # all sequences empty, rows behind them
+    x, g = torch.randn(300, 40, device="cuda"), -torch.rand(300, 40, device="cuda")
+    y = torch.full_like(x, 7.0)
+    _, final = gdr.gdr_linear_scan_fwd(x, g, gdr.GDR_LINEAR_LOG_DECAY, cu_seqlens=cu, initial_state=h0, y=y)
+    assert torch.equal(final, h0) and bool((y == 7.0).all())
+
+
+def test_offsets_past_32_bits():
+    """2^31 elements and more: the last rows (for the gradients: the first), which gates of one half forget
+    everything 300 tokens away from, against the oracle on those rows alone."""
+    T, D, n = (1 << 20) + 77, 2112, 300
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randn(T, D, device="cuda", dtype=torch.bfloat16, generator=g)
+    z = torch.randn(T, D, device="cuda", dtype=torch.bfloat16, generator=g)
+    y, final, blocks = gdr.gdr_linear_scan_fwd(x, z, gdr.GDR_LINEAR_SIGMOID, output_block_states=True)
+    f = linear.scan(f64(x[-n:]), f64(z[-n:]), linear.SIGMOID, [0, n])
+    _check(f64(y[-40:]), f["y"][-40:], f["err"][-40:], HALF["bf16"], "y")
+    _check(f64(final), f["final"], f["err_final"], U, "final")
+    del y
+    dx, dz, dh0 = gdr.gdr_linear_scan_bwd(x, z, gdr.GDR_LINEAR_SIGMOID, x, blocks)
+    for rows, keep in ((slice(0, n), slice(0, 40)), (slice(T - n, T), slice(n - 40, n))):
+        b = linear.grads(f64(x[rows]), f64(z[rows]), linear.SIGMOID, [0, n], f64(x[rows]))
+        _check(f64(dx[rows])[keep], b["dx"][keep], b["err_dx"][keep], HALF["bf16"], "dx")
+        _check(f64(dz[rows])[keep], b["dgate"][keep], b["err_dgate"][keep], HALF["bf16"], "dz")
+        if rows.start == 0:
+            _check(f64(dh0), b["dh0"], b["err_dh0"], U, "dh0")
+    # a pool of the same size: its last slot
+    slots = torch.tensor([T - 1, 5], dtype=torch.int32, device="cuda")
+    before = f64(x[[T - 1, 5, T - 2]])
+    o = gdr.gdr_linear_decode_paged(z[:2].contiguous(), z[2:4].contiguous(), gdr.GDR_LINEAR_SIGMOID, x, slots)
+    want, last, err, err_last = linear.decode_paged(f64(z[:2]), f64(z[2:4]), linear.SIGMOID, [0, 1, 2], before, [0, 1])
+    _check(f64(o), want, err, HALF["bf16"], "y")
+    _check(f64(x[[T - 1, 5]]), np.stack([last[0], last[1]]), np.stack([err_last[0], err_last[1]]), HALF["bf16"], "pool")
+    assert np.array_equal(f64(x[T - 2]), before[2])
+
+
 # ---------------------------------------------------------------------------------------------------
 @pytest.mark.parametrize("kind", ["log", "sigmoid"])
 @pytest.mark.parametrize("io", ["bf16", "f32"])
