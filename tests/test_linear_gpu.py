@@ -2,11 +2,11 @@
 
 Tolerance per value: u * C * e + half * |value| + tiny, with u = 2^-24, e the oracle's error sum (what a
 rounding of every step to u relative accuracy can add up to), half the half step of the stored type and
-C = 24: per token the kernels round the gate (its exponential to 2 u, a reciprocal to 2 u, their product u,
-the compensated part u), the input b (3 u), the step (2 u), and, where runs are composed, the run's decay
-(2 u) and its application (2 u, once for the waves of a tile and once for the tiles), and the first pass
-over a run repeats the same roundings as the second: 12 + 12.  The backward pass adds the same terms again
-in its own sums (the oracle's e of the gradients holds both)."""
+C = 24: per token the kernels round the gate's exponential and reciprocal (2 u each), their product (u) and
+the complement (u), the input b (3 u), the step (2 u), and, where runs are composed, the run's decay (2 u)
+and its application (2 u, once for the waves of a tile and once for the tiles), and the first pass over a
+run repeats the same roundings as the second: 12 + 12.  The backward pass adds the same terms again in its
+own sums (the oracle's e of the gradients holds both)."""
 import numpy as np
 import pytest
 import torch
