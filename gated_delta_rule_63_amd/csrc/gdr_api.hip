@@ -417,7 +417,7 @@ gdr_status check_linear(const gdr_linear_problem* p) {
     if (p->gate != GDR_LINEAR_LOG_DECAY && p->gate != GDR_LINEAR_SIGMOID) return GDR_ERROR_INVALID_VALUE;
     if (!dtype_ok(p->io_dtype)) return GDR_ERROR_INVALID_VALUE;
     if (p->num_seqs > 65535) return GDR_ERROR_NOT_SUPPORTED;         // grid y limit
-    if (p->num_channels > (1 << 24)) return GDR_ERROR_NOT_SUPPORTED;  // row offsets are 32-bit
+    if (p->num_channels > (1 << 22)) return GDR_ERROR_NOT_SUPPORTED;  // row offsets are 32-bit
     // the launch grid counts tiles of 64 tokens by 64 channels in 32 bits
     const int64_t tiles = (p->total_tokens + 63) / 64, across = ((int64_t)p->num_channels + 63) / 64;
     if (tiles > 0x7FFFFFFF / across) return GDR_ERROR_NOT_SUPPORTED;

@@ -28,11 +28,13 @@ constexpr int kWaveList = kWaveCap + kBeamMaxOut + 8;  // and those equal to it,
 constexpr int kMergeThreads = 256;
 constexpr int kMaxSplits = 64;
 
-// Bound of the difference between the 32-bit sums' log and the true one: every exponential carries the
-// hardware's 2^-23 and its argument's rounding, at most |d| 2^-23 for a distance d to the maximum; what
-// lies beyond |d| = 20 is below 2^20 e^-20 = 2e-3 of the sum.  (1 + 20) 2^-23 = 2.5e-6, plus 3 additions
-// in 32 bits (2e-7); two beams' scores are in the right order if they differ by more than twice this.
-constexpr double kNear = 6e-6;
+// Bound of the difference between the 32-bit sums' log and the true one.  A logit's share passes four
+// exponentials (about the thread's maximum, then the thread's, the wave's and the part's weight); each carries
+// the hardware's 2^-23 and its argument's rounding, |d| 2^-23 for a distance d, and the four distances add up to
+// the logit's distance to the row's maximum.  What lies beyond 20 is below 2^20 e^-20 = 2e-3 of the sum.
+// (4 + 20) 2^-23 = 2.9e-6, plus 3 additions in 32 bits (2e-7): two beams' scores are in the right order if they
+// differ by more than twice 3.1e-6.
+constexpr double kNear = 7e-6;
 
 // Keys in ascending order of the float they stand for.  -0 counts as 0, NaN as -inf.
 __device__ __forceinline__ uint32_t key_of(float x) {
@@ -559,7 +561,7 @@ template <typename T> __global__ __launch_bounds__(kCopyThreads) void beam_reord
 template <typename T> hipError_t reorder(const ReorderArgs& a, hipStream_t s) {
     const int64_t units = a.slot_bytes / sizeof(T), per = kCopyThreads * kCopyUnroll;
     const int64_t parts = (units + per - 1) / per;
-    if (parts > 0x7FFFFFFF) return hipErrorInvalidValue;
+    if (parts >= (1ll << 32) / kCopyThreads) return hipErrorInvalidValue;  // a launch has fewer than 2^32 threads
     beam_reorder_kernel<T><<<dim3((unsigned)parts, (unsigned)(a.batch * a.beams), (unsigned)a.layers), kCopyThreads, 0, s>>>(a);
     return hipGetLastError();
 }

@@ -114,7 +114,7 @@ template <> struct Chan<bf16_t, 1> {
 
 // A wave's rows of a [T, D] tensor: token w0 + i, this lane's channels.  The resource ends behind the last
 // valid row, and lanes without channels get an offset behind every resource, so that reads there give zeros
-// and writes nothing without a branch (rows of at most 2^24 channels keep every offset below 2^31).
+// and writes nothing without a branch (32 rows of at most 2^22 channels keep every offset below 2^30).
 template <typename T> struct Rows {
     __amdgpu_buffer_rsrc_t r;
     uint32_t off, row;
@@ -176,7 +176,7 @@ __device__ __forceinline__ float apply_run(float2 r, float h) { return r.x == kC
 
 // 1 - A is kept where it is small and A where that is: a product of rounded decays near 1 would lose
 // their complements as a single rounded decay does.
-__device__ __forceinline__ float pick(float A, float Q) { return Q < 0.125f ? Q : -A; }
+__device__ __forceinline__ float pick(float A, float Q) { return Q >= 0.0f && Q < 0.125f ? fabsf(Q) : -A; }
 
 __device__ __forceinline__ float2 compose(float2 r1, float2 r2) {
     if (r2.x == kCut) return r2;
@@ -688,7 +688,7 @@ template <int KIND, typename IO, int VEC, int W, int TPT, bool BACKWARD> hipErro
     a.nch = (a.D + 64 * VEC - 1) / (64 * VEC);
     a.tiles = (a.T + W * TPT - 1) / (W * TPT);
     const int64_t blocks = a.tiles * a.nch;
-    if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
+    if (blocks >= (1ll << 32) / (64 * W)) return hipErrorInvalidValue;  // a launch has fewer than 2^32 threads
     if (a.tiles > 1) {
         const int64_t pairs = (a.tiles * a.D + 1) / 2;  // the workspace holds the word behind an odd count too
         linear_init_kernel<<<dim3((unsigned)((pairs + 255) / 256)), 256, 0, s>>>(a, pairs);

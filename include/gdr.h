@@ -355,8 +355,9 @@ GDR_API gdr_status gdr_kda_decode_fused(const gdr_problem* p, int32_t max_q_len,
  *
  * Layouts: x, y, dy, dx [T, D] io_dtype; gate, dgate [T, D]; states [N, D] fp32; cu_seqlens as above,
  * except that cu_seqlens[N] may be less than T: rows behind the last sequence are neither read nor
- * written.  States are held in fp32 throughout; any channel count from 1 to 2^24 is accepted.  An infinity
- * or a NaN stays within its sequence and channel.
+ * written.  States are held in fp32 throughout; any channel count from 1 to 2^22 is accepted.  A NaN
+ * stays within its sequence and channel, and so does an infinite input; a state that becomes infinite is a
+ * NaN from the next token on.
  */
 typedef enum gdr_linear_gate {
     GDR_LINEAR_LOG_DECAY = 0,
@@ -368,7 +369,7 @@ typedef enum gdr_linear_gate {
 typedef struct gdr_linear_problem {
     int64_t total_tokens;   /* T                                                         */
     int32_t num_seqs;       /* N <= 65535                                                */
-    int32_t num_channels;   /* D in 1..2^24                                              */
+    int32_t num_channels;   /* D in 1..2^22                                              */
     gdr_linear_gate gate;
     gdr_dtype io_dtype;
 } gdr_linear_problem;

@@ -27,7 +27,7 @@ def _bwd(p, x=PTR, gate=PTR, cu=PTR, bs=PTR, dy=PTR, dx=PTR, dg=PTR, dh0=None, w
 @pytest.mark.parametrize("call", [_fwd, _bwd])
 @pytest.mark.parametrize("p,expect", [
     (None, 1), (_lp(T=-1), 1), (_lp(N=-1), 1), (_lp(D=0), 1), (_lp(gate=2), 1), (_lp(io=3), 1),
-    (_lp(N=0), 1), (_lp(N=65536), 2), (_lp(T=1 << 40, D=1 << 20), 2)])
+    (_lp(N=0), 1), (_lp(N=65536), 2), (_lp(T=1 << 40, D=1 << 20), 2), (_lp(D=(1 << 22) + 1), 2)])
 def test_scan_rejects_bad_metadata(call, p, expect):
     assert call(p) == expect
 

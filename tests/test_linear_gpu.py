@@ -321,6 +321,24 @@ def test_batches_without_tokens():
     assert torch.equal(final, h0) and bool((y == 7.0).all())
 
 
+@pytest.mark.parametrize("T", [1, 300])
+def test_widest_rows(T):
+    """2^22 channels, the most: constant gates, so that every channel's state is known."""
+    D = 1 << 22
+    x = torch.full((T, D), 2.0, device="cuda", dtype=torch.bfloat16)
+    g = torch.full((T, D), float(np.log(0.5)), device="cuda")
+    y, final, blocks = gdr.gdr_linear_scan_fwd(x, g, gdr.GDR_LINEAR_LOG_DECAY, output_block_states=True)
+    want = 4.0 * (1.0 - 0.5 ** np.arange(1, T + 1))   # the oracle's error sum is below 40 here
+    for t in {0, T - 1, T // 2}:
+        assert bool(((y[t].float() - want[t]).abs() <= HALF["bf16"] * want[t] + 24 * U * 40).all())
+    assert bool(((final[0] - want[-1]).abs() <= 24 * U * 40).all())
+    del y
+    dx, dg, dh0 = gdr.gdr_linear_scan_bwd(x, g, gdr.GDR_LINEAR_LOG_DECAY, x, blocks)
+    D0 = 4.0 * (1.0 - 0.5 ** T)                        # gradients run the other way
+    assert bool(((dx[0].float() - D0).abs() <= HALF["bf16"] * D0 + 24 * U * 40).all())
+    assert bool(((dh0[0] - D0 / 2).abs() <= 24 * U * 40).all()) and bool((dg[0] == 0).all())
+
+
 def test_offsets_past_32_bits():
     """2^31 elements and more: the last rows (for the gradients: the first), which gates of one half forget
     everything 300 tokens away from, against the oracle on those rows alone."""
