@@ -9,7 +9,8 @@
 //   merge  one workgroup per batch row: log-sum-exp per beam from the parts in 64 bits, scores of the
 //          listed entries in 64 bits, the best `out` of them.  The sums come from 32-bit exponentials, so
 //          scores of different beams closer than kNear could stand in the wrong order: where two
-//          neighbours of the result are that close, their beams' sums are formed again in 64 bits.
+//          neighbours of the result are that close, or candidates behind it that close to its last one,
+//          their beams' sums are formed again in 64 bits.
 //
 // Reordering: a parent's first child keeps its slot; the other children take, in order, the slots of
 // parents without children, and only these are copied.  What is read (slots of parents with children) and
@@ -30,10 +31,10 @@ constexpr int kMaxSplits = 64;
 
 // Bound of the difference between the 32-bit sums' log and the true one.  A logit's share passes four
 // exponentials (about the thread's maximum, then the thread's, the wave's and the part's weight); each carries
-// the hardware's 2^-23 and its argument's rounding, |d| 2^-23 for a distance d, and the four distances add up to
-// the logit's distance to the row's maximum.  What lies beyond 20 is below 2^20 e^-20 = 2e-3 of the sum.
-// (4 + 20) 2^-23 = 2.9e-6, plus 3 additions in 32 bits (2e-7): two beams' scores are in the right order if they
-// differ by more than twice 3.1e-6.
+// the hardware's 2^-23 and for a distance d its roundings (the difference, its product with log2 e, log2 e itself),
+// 2.25 |d| 2^-24, and the four distances add up to the logit's distance to the row's maximum.  What lies beyond
+// 20 is below 2^20 e^-20 = 2e-3 of the sum.  (4 + 22.5) 2^-23 = 3.2e-6, plus 3 additions in 32 bits (2e-7): two
+// beams' scores are in the right order if they differ by more than twice 3.4e-6.
 constexpr double kNear = 7e-6;
 
 // Keys in ascending order of the float they stand for.  -0 counts as 0, NaN as -inf.
@@ -364,7 +365,8 @@ template <typename IO> __global__ __launch_bounds__(kMergeThreads) void beam_mer
     __shared__ float beam_score[kBeamMaxBeams];
     __shared__ int state[kBeamMaxBeams];                                      // 0: listed, 1: ended, 2: no candidates
     __shared__ int rank[kMergeThreads];
-    __shared__ int count, near_mask;
+    __shared__ int count;
+    __shared__ uint32_t near_mask, behind_mask, tau_mask;                     // a bit per beam
 
     // the first entries go to the LDS, in flight with the sums
     const uint64_t* entries = a.entries + (int64_t)b * total;
@@ -436,7 +438,7 @@ template <typename IO> __global__ __launch_bounds__(kMergeThreads) void beam_mer
         }
         if (tid == 0) {
             count = 0;
-            near_mask = 0;
+            near_mask = behind_mask = tau_mask = 0;
         }
         __syncthreads();
         for (int i = tid; i < total; i += kMergeThreads) {
@@ -444,6 +446,7 @@ template <typename IO> __global__ __launch_bounds__(kMergeThreads) void beam_mer
             uint32_t at;
             if (!candidate(i, entry(i), key, at)) continue;
             if (key > tau_key || (key == tau_key && at < tau_flat)) best[atomicAdd(&count, 1)] = Candidate{key, at};
+            else if (of_key64(tau_key) - of_key64(key) < kNear) atomicOr(&tau_mask, 1u << (at / a.vocab));
         }
         __syncthreads();
         n = count;
@@ -454,13 +457,23 @@ template <typename IO> __global__ __launch_bounds__(kMergeThreads) void beam_mer
         }
         sort_candidates(best, n, rank);
         if (pass == 1) break;
-        for (int i = tid; i + 1 < n && i < K; i += kMergeThreads) {
-            const int w0 = best[i].flat / a.vocab, w1 = best[i + 1].flat / a.vocab;
-            if (w0 != w1 && of_key64(best[i].key) - of_key64(best[i + 1].key) < kNear)
-                atomicOr(&near_mask, (1 << w0) | (1 << w1));
+        // neighbours of the result, and what is near its last one: one beam's equal logits may stand between that
+        // and another beam's, in the list or not listed because they stand behind tau
+        const double last = n >= K ? of_key64(best[K - 1].key) : 0.0;
+        for (int i = tid; i < n; i += kMergeThreads) {
+            const uint32_t w0 = best[i].flat / a.vocab;
+            if (i + 1 < min(n, K)) {
+                const uint32_t w1 = best[i + 1].flat / a.vocab;
+                if (w0 != w1 && of_key64(best[i].key) - of_key64(best[i + 1].key) < kNear)
+                    atomicOr(&near_mask, (1u << w0) | (1u << w1));
+            } else if (i >= K - 1 && last - of_key64(best[i].key) < kNear) {
+                atomicOr(&behind_mask, 1u << w0);
+            }
         }
         __syncthreads();
-        const uint32_t near = (uint32_t)near_mask;
+        uint32_t behind = behind_mask, near = near_mask;
+        if (n >= K && last - of_key64(tau_key) < kNear) behind |= tau_mask;
+        if (behind & (behind - 1)) near |= behind;  // more than one beam
         if (!near) break;
         for (int w = 0; w < W; ++w) {
             if (!((near >> w) & 1) || state[w] != 0) continue;

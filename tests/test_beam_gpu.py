@@ -174,6 +174,30 @@ def test_near_ties_between_beams_are_settled_in_64_bits():
         assert np.allclose(got, every[:12], rtol=0, atol=1e-12)
 
 
+@pytest.mark.parametrize("V,K,equal", [(3001, 1, 2), (3001, 4, 6), (40000, 1, 2), (40000, 4, 9), (40000, 64, 300)])
+def test_near_ties_behind_equal_candidates(V, K, equal):
+    """The last result and those behind it are one beam's equal logits; another beam's best comes behind them
+    all by the 32-bit sums, or before them, and is better by less than one fp32 step of its score."""
+    B, r = 64, np.random.default_rng(23 + V + K)
+    lg = (r.normal(size=(B, 2, V)) * 2).astype(np.float32).astype(np.float64)
+    sc = np.full((B, 2), -0.5, np.float32)
+    for b in range(B):
+        lg[b, 0, r.choice(V, equal, replace=False)] = lg[b, 0].max()
+        top = lg[b].max(1)
+        lse = top + np.log(np.exp(lg[b] - top[:, None]).sum(1))
+        first = float(sc[b, 0]) + (top[0] - lse[0])
+        lg[b, 1] = np.minimum(lg[b, 1], top[1] - 1e-3 * (np.arange(V) != lg[b, 1].argmax()))
+        lse1 = top[1] + np.log(np.exp(lg[b, 1].astype(np.float32).astype(np.float64) - top[1]).sum())
+        s = np.float32(first - (top[1] - lse1))
+        while float(s) + (top[1] - lse1) <= first:
+            s = np.nextafter(s, np.float32(np.inf))
+        sc[b, 1] = s
+    want = beam.select(lg.astype(np.float32).astype(np.float64), sc.astype(np.float64), K)
+    assert np.all(want[1][:, 0] == 1) and np.all(want[1][:, 1:] == 0)
+    assert K == 1 or np.all(want[0][:, 0] - want[0][:, 1] > 1e-12)
+    _compare(lg, sc, K, "f32")
+
+
 def test_select_captured_and_on_another_stream():
     lg, sc = _logits(20, 3, 4, 20000), _scores(21, 3, 4)
     d, dsc = _dev_logits(lg, "bf16", 0), to_dev(sc)
