@@ -2,7 +2,8 @@
 // where the chosen beams expect them.
 //
 // Selection: s[w, v] = score[w] + logit[w, v] - log sum_v e^logit[w, v]; the best of the W V candidates
-// of a batch row in descending order, equal ones by the lower w V + v.
+// of a batch row in descending order, equal ones by the lower beam, in a beam by the higher logit (different
+// logits can give the same 64-bit score), then by the lower token.
 //   rows   one workgroup per (row, part of the vocabulary), its logits in registers, read once: maximum,
 //          sum of exponentials, and the part's best `out` entries by (logit, lower token).  Within a beam
 //          the order of the candidates is the order of their logits, so these lists are exact.
@@ -312,15 +313,24 @@ __device__ __forceinline__ double of_key64(uint64_t k) {
     return __longlong_as_double((int64_t)(k >> 63 ? k ^ 0x8000000000000000ull : ~k));
 }
 
-// A scored candidate; those in one list are all different.  Better ones come first: the higher key, then the
-// lower flat index.
+// A scored candidate; those in one list are all different.  Better ones come first: the higher score, then the
+// higher `tie`, which holds the lower beam, the higher logit and the lower token, from its top bits down.  Of two
+// entries of one list the one that stands first there is therefore the better candidate, also where their scores
+// round to the same value: how many candidates the merge can hold follows from it.
+static_assert(kBeamMaxBeams <= 32 && kBeamMaxVocab <= 1 << 20, "5 bits of beam, 32 of logit, 20 of token");
+constexpr uint32_t kTokenBits = (1u << 20) - 1;
 struct __align__(16) Candidate {
     uint64_t key;
-    uint32_t flat;
+    uint64_t tie;
     __device__ __forceinline__ bool before(const Candidate& o) const {
-        return key > o.key || (key == o.key && flat < o.flat);
+        return key > o.key || (key == o.key && tie > o.tie);
     }
+    __device__ __forceinline__ uint32_t beam() const { return kBeamMaxBeams - 1 - (uint32_t)(tie >> 52); }
+    __device__ __forceinline__ uint32_t token() const { return ~(uint32_t)tie & kTokenBits; }
 };
+__device__ __forceinline__ uint64_t tie_of(int w, uint32_t logit_key, uint32_t token) {
+    return (uint64_t)(kBeamMaxBeams - 1 - w) << 52 | (uint64_t)logit_key << 20 | (~token & kTokenBits);
+}
 
 // Sorts the first n of an LDS list, n <= kMergeThreads by counting, more by a network over the next power of
 // two.  Counting: kMergeThreads / n threads per candidate share the comparisons, and each reads eight ahead of
@@ -345,7 +355,7 @@ __device__ __forceinline__ void sort_candidates(Candidate* list, int n, int* ran
         return;
     }
     const int np = pow2_at_least(n);
-    for (int i = n + threadIdx.x; i < np; i += kMergeThreads) list[i] = Candidate{0, 0xFFFFFFFFu};
+    for (int i = n + threadIdx.x; i < np; i += kMergeThreads) list[i] = Candidate{0, 0};
     bitonic_sort<kMergeThreads>(np, [&](int i, int j, bool down) {
         const Candidate p = list[i], q = list[j];
         if (q.before(p) == down) {
@@ -405,39 +415,35 @@ template <typename IO> __global__ __launch_bounds__(kMergeThreads) void beam_mer
     for (int r = 0; r < kHeld / kMergeThreads; ++r) held[tid + r * kMergeThreads] = mine[r];
     __syncthreads();
 
-    // entry i's score and flat index; false: none
+    // entry i's candidate; false: none
     const float per_beam = 1.0f / (float)(S * K);
-    auto candidate = [&](int i, uint64_t e, uint64_t& key, uint32_t& at) {
+    auto candidate = [&](int i, uint64_t e, Candidate& c) {
         const int w = (int)(((float)i + 0.5f) * per_beam);  // i / (S K): exact for i < 2^21
         const double score = (double)beam_score[w];
         if (state[w] == 1 && i == w * S * K) {
-            key = key_of64(score);
-            at = (uint32_t)w * a.vocab + a.eos;
+            c = Candidate{key_of64(score), tie_of(w, 0, a.eos)};
             return true;
         }
         if (state[w] != 0 || !e) return false;
-        key = key_of64(score + ((double)of_key((uint32_t)(e >> 32)) - lse[w]));
-        at = (uint32_t)w * a.vocab + ~(uint32_t)e;
+        const uint32_t logit = (uint32_t)(e >> 32);
+        c = Candidate{key_of64(score + ((double)of_key(logit) - lse[w])), tie_of(w, logit, ~(uint32_t)e)};
         return true;
     };
     auto entry = [&](int i) { return i < kHeld ? held[i] : entries[i]; };
     int n = 0;
     for (int pass = 0; pass < 2; ++pass) {
-        uint64_t tau_key = 0;
-        uint32_t tau_flat = 0xFFFFFFFFu;
+        Candidate tau{0, 0};
         // with more lists than results, no result and not the one behind them comes after the (K+1)-th best of
         // the lists' first entries, and at most K lists hold better ones
         if (lists > K) {
             for (int l = tid; l < lists; l += kMergeThreads) {
-                uint64_t key = 0;
-                uint32_t at = 0x80000000u + l;  // an empty list stands behind all others, at a place of its own
-                candidate(l * K, entry(l * K), key, at);
-                best[l] = Candidate{key, at};
+                Candidate c{0, (uint64_t)l};  // an empty list stands behind all others, at a place of its own
+                candidate(l * K, entry(l * K), c);
+                best[l] = c;
             }
             __syncthreads();
             sort_candidates(best, lists, rank);
-            tau_key = best[K].key;
-            tau_flat = best[K].flat;
+            tau = best[K];
         }
         if (tid == 0) {
             count = 0;
@@ -445,16 +451,19 @@ template <typename IO> __global__ __launch_bounds__(kMergeThreads) void beam_mer
         }
         __syncthreads();
         for (int i = tid; i < total; i += kMergeThreads) {
-            uint64_t key;
-            uint32_t at;
-            if (!candidate(i, entry(i), key, at)) continue;
-            if (key > tau_key || (key == tau_key && at < tau_flat)) best[atomicAdd(&count, 1)] = Candidate{key, at};
-            else if (of_key64(tau_key) - of_key64(key) < kNear) atomicOr(&tau_mask, 1u << (at / a.vocab));
+            Candidate c;
+            if (!candidate(i, entry(i), c)) continue;
+            if (c.before(tau)) {
+                const int at = atomicAdd(&count, 1);
+                if (at < a.merge_list) best[at] = c;  // more are only there if another call writes this workspace
+            } else if (of_key64(tau.key) - of_key64(c.key) < kNear) {
+                atomicOr(&tau_mask, 1u << c.beam());
+            }
         }
         __syncthreads();
-        n = count;
-        if (tau_key && n <= K) {
-            if (tid == 0) best[n] = Candidate{tau_key, tau_flat};
+        n = min(count, a.merge_list);
+        if (tau.key && n <= K) {
+            if (tid == 0) best[n] = tau;
             ++n;
             __syncthreads();
         }
@@ -464,9 +473,9 @@ template <typename IO> __global__ __launch_bounds__(kMergeThreads) void beam_mer
         // and another beam's, in the list or not listed because they stand behind tau
         const double last = n >= K ? of_key64(best[K - 1].key) : 0.0;
         for (int i = tid; i < n; i += kMergeThreads) {
-            const uint32_t w0 = best[i].flat / a.vocab;
+            const uint32_t w0 = best[i].beam();
             if (i + 1 < min(n, K)) {
-                const uint32_t w1 = best[i + 1].flat / a.vocab;
+                const uint32_t w1 = best[i + 1].beam();
                 if (w0 != w1 && of_key64(best[i].key) - of_key64(best[i + 1].key) < kNear)
                     atomicOr(&near_mask, (1u << w0) | (1u << w1));
             } else if (i >= K - 1 && last - of_key64(best[i].key) < kNear) {
@@ -475,7 +484,7 @@ template <typename IO> __global__ __launch_bounds__(kMergeThreads) void beam_mer
         }
         __syncthreads();
         uint32_t behind = behind_mask, near = near_mask;
-        if (n >= K && last - of_key64(tau_key) < kNear) behind |= tau_mask;
+        if (n >= K && last - of_key64(tau.key) < kNear) behind |= tau_mask;
         if (behind & (behind - 1)) near |= behind;  // more than one beam
         if (!near) break;
         for (int w = 0; w < W; ++w) {
@@ -502,8 +511,8 @@ template <typename IO> __global__ __launch_bounds__(kMergeThreads) void beam_mer
     const int have = min(n, K);
     for (int i = tid; i < have; i += kMergeThreads) {
         a.out_scores[(int64_t)b * K + i] = (float)of_key64(best[i].key);
-        a.out_parents[(int64_t)b * K + i] = best[i].flat / a.vocab;
-        a.out_tokens[(int64_t)b * K + i] = best[i].flat % a.vocab;
+        a.out_parents[(int64_t)b * K + i] = best[i].beam();
+        a.out_tokens[(int64_t)b * K + i] = best[i].token();
     }
     // fewer candidates than asked for: those of probability zero follow, by the lower index
     if (have == K || wave != 0) return;
@@ -599,8 +608,8 @@ template <typename IO, int PER> hipError_t rows(const BeamArgs& a, hipStream_t s
 template <typename IO> hipError_t select(BeamArgs a, const BeamPlan& pl, hipStream_t s) {
     hipError_t e = pl.per_thread == 16 ? rows<IO, 16>(a, s) : pl.per_thread == 32 ? rows<IO, 32>(a, s) : rows<IO, 64>(a, s);
     if (e != hipSuccess) return e;
-    // the merge keeps the entries of at most `out` lists and one more where these are fewer than out + 1;
-    // the lists' first entries stand there before
+    // the merge keeps the entries of at most `out` lists, `out` each, and one more where these are fewer than
+    // out + 1; the lists' first entries stand there before
     int most = a.out * a.out;
     const int lists = a.beams * a.splits;
     if (most < lists) most = lists;

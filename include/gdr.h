@@ -426,8 +426,10 @@ GDR_API gdr_status gdr_linear_decode_paged(const gdr_linear_problem* p, int32_t 
  * gdr_beam_reorder moves the chosen parents' states (any pool of the decode entry points).
  *
  * Candidate (w, v) of a batch row scores  scores[w] + logits[w, v] - log sum_u e^logits[w, u].
- * The num_out best are written in descending order, equal ones by the lower w * vocab + v; the order
- * is that of the scores in 64 bits, whatever io_dtype.
+ * The num_out best are written in descending order; the order is that of the scores in 64 bits,
+ * whatever io_dtype.  Equal ones stand by the lower w, those of one beam by the higher logit (where the
+ * 64-bit score of a beam with scores[w] = -1e30, say, no longer tells its logits apart), equal logits by
+ * the lower v.
  *   - a -inf or NaN logit has probability zero; a row without a finite logit, or with a +inf one, and a
  *     beam whose score is not finite have no candidate above -inf
  *   - an ended beam (finished[w] != 0) has one candidate, (w, eos_token) with its score unchanged

@@ -3,11 +3,12 @@ import numpy as np
 
 
 def select(logits, scores, num_out, finished=None, eos_token=-1):
-    """logits [B, W, V] fp64, scores [B, W]: (scores fp64, parents, tokens), each [B, num_out]."""
+    """logits [B, W, V] fp64, scores [B, W]: (scores fp64, parents, tokens), each [B, num_out].  Equal scores
+    stand by the lower beam, in a beam by the higher logit, then by the lower token."""
     B, W, V = logits.shape
     out = np.empty((B, num_out)), np.empty((B, num_out), np.int32), np.empty((B, num_out), np.int32)
     for b in range(B):
-        p = np.full((W, V), -np.inf)
+        p, inside = np.full((W, V), -np.inf), np.zeros((W, V))
         for w in range(W):
             if not np.isfinite(scores[b, w]):
                 continue
@@ -19,8 +20,9 @@ def select(logits, scores, num_out, finished=None, eos_token=-1):
             if not np.isfinite(top):
                 continue
             p[w] = scores[b, w] + (x - (top + np.log(np.exp(x - top).sum())))
+            inside[w] = x
         flat = p.ravel()
-        best = np.lexsort((np.arange(W * V), -flat))[:num_out]
+        best = np.lexsort((np.arange(W * V), -inside.ravel(), np.arange(W * V) // V, -flat))[:num_out]
         out[0][b], out[1][b], out[2][b] = flat[best], best // V, best % V
     return out
 

@@ -150,6 +150,30 @@ def test_ended_beams(io):
         _compare(lg, sc, 10, io, finished=fin, eos=eos)
 
 
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("dead", [-1e9, -1e30, float(np.finfo(np.float32).min)])
+@pytest.mark.parametrize("W,V,K", [(4, 32000, 8), (4, 32000, 16), (8, 131072, 16), (3, 131072, 64), (4, 700, 8)])
+def test_beams_of_a_large_negative_score(W, V, K, dead, io):
+    """A search's first step with finite scores for the beams that do not count yet: their logits round to the
+    same 64-bit score, in more lists than results.  Then with fewer tokens left to the live beam than results."""
+    lg = _logits(41 + K, 2, W, V)
+    sc = np.full((2, W), dead, np.float32)
+    sc[0, 0] = sc[1, W - 1] = 0.0
+    _compare(lg, sc, K, io)
+    lg[0, 0, 3:] = lg[1, W - 1, 3:] = -np.inf
+    _compare(lg, sc, K, io)
+
+
+@pytest.mark.parametrize("K", [8, 16, 64])
+def test_logits_that_round_to_equal_scores(K):
+    """Logits of 1e-17, and of 1e-17 beside one of 3: in a score of -10 they make no difference, their order does."""
+    lg = _logits(45, 1, 4, 32000) * 1e-17
+    _compare(lg, _scores(46, 1, 4), K, "f32")
+    _compare(lg, np.full((1, 4), -5.0, np.float32), K, "f32")
+    lg[0, :, 777] = 3.0
+    _compare(lg, _scores(46, 1, 4), K, "f32")
+
+
 def test_near_ties_between_beams_are_settled_in_64_bits():
     """Beams whose candidates differ by 1e-8 to 1e-6, below what 32-bit sums resolve."""
     r = np.random.default_rng(19)

@@ -77,6 +77,18 @@ def test_select_by_brute_force():
         assert [(w, v) for _, w, v in every[:7]] == list(zip(p[b], t[b]))
 
 
+def test_select_tells_equal_scores_apart_by_beam_logit_and_token():
+    lg = np.array([[[1.0, 2.0, 3.0, 3.0], [4.0, 1.0, 2.0, 2.0], [0.0, 0.0, 0.0, 0.0]]])
+    # in scores of -1e30 the logits make no difference: the lower beam first, there the higher logit
+    _, p, t = beam.select(lg, np.array([[-1e30, -1e30, 0.0]]), 4)
+    assert list(zip(p[0], t[0])) == [(2, 0), (2, 1), (2, 2), (2, 3)]
+    _, p, t = beam.select(lg[:, :2], np.array([[-1e30, -1e30]]), 4)
+    assert list(zip(p[0], t[0])) == [(0, 2), (0, 3), (0, 1), (0, 0)]
+    lg[0, 0, 3] = -np.inf
+    _, p, t = beam.select(lg[:, :2], np.array([[-1e30, -1e30]]), 4)
+    assert list(zip(p[0], t[0])) == [(0, 2), (0, 1), (0, 0), (1, 0)]
+
+
 def test_reorder_moves_every_state_once():
     r = np.random.default_rng(4)
     for _ in range(50):
