@@ -377,6 +377,7 @@ template <typename IO> __global__ __launch_bounds__(kMergeThreads) void beam_mer
     __shared__ double lse[kBeamMaxBeams], red[kWavesM];
     __shared__ float beam_score[kBeamMaxBeams];
     __shared__ int state[kBeamMaxBeams];                                      // 0: listed, 1: ended, 2: no candidates
+    static_assert(kBeamMaxBeams <= 64, "a lane per beam");
     __shared__ int rank[kMergeThreads];
     __shared__ int count;
     __shared__ uint32_t near_mask, behind_mask, tau_mask;                     // a bit per beam
@@ -486,9 +487,11 @@ template <typename IO> __global__ __launch_bounds__(kMergeThreads) void beam_mer
         uint32_t behind = behind_mask, near = near_mask;
         if (n >= K && last - of_key64(tau.key) < kNear) behind |= tau_mask;
         if (behind & (behind - 1)) near |= behind;  // more than one beam
+        near &= (uint32_t)__ballot(lane < W && state[lane < W ? lane : 0] == 0);  // an ended beam's score has no sum
+        __syncthreads();  // every wave has read the masks before they are cleared, and all go on or none
         if (!near) break;
         for (int w = 0; w < W; ++w) {
-            if (!((near >> w) & 1) || state[w] != 0) continue;
+            if (!((near >> w) & 1)) continue;
             const int64_t at = ((int64_t)b * W + w) * a.stride;
             float top = kNone;
             for (int s = 0; s < S; ++s) top = fmaxf(top, a.tops[((int64_t)b * W + w) * S + s]);

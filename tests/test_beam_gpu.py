@@ -174,6 +174,28 @@ def test_logits_that_round_to_equal_scores(K):
     _compare(lg, _scores(46, 1, 4), K, "f32")
 
 
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("W,V,K", [(4, 900, 8), (8, 32000, 16), (5, 4096, 5), (32, 600, 64), (8, 32000, 4), (2, 70000, 3)])
+def test_ended_beams_of_equal_scores(W, V, K, io):
+    """Some or all beams of a row have ended with one score or with scores a step apart, with as many lists as
+    results, fewer and more: these scores are exact, and the live beams' candidates may lie as near to them."""
+    B = 12
+    lg, sc = _logits(48, B, W, V), _scores(49, B, W)
+    fin = np.zeros((B, W), np.uint8)
+    for b in range(B):
+        some = np.random.default_rng(50 + b).permutation(W)[:W if b % 3 == 0 else max(2, W // 2)]
+        fin[b, some] = 1
+        sc[b, some] = sc[b, some[0]] + (0 if b % 2 else 1) * np.float32(1e-6) * np.arange(len(some), dtype=np.float32)
+    x = lg[1].max(1) - np.log(np.exp(lg[1]).sum(1))
+    live = np.flatnonzero(fin[1] == 0)
+    if len(live):  # a live beam's best candidate beside the ended ones
+        sc[1, live[0]] = np.float32(sc[1, fin[1] == 1][0] - x[live[0]])
+    fin[2] = 1
+    sc[2] = -3.0
+    for eos in (0, V - 1):
+        _compare(lg, sc, K, io, finished=fin, eos=eos)
+
+
 def test_near_ties_between_beams_are_settled_in_64_bits():
     """Beams whose candidates differ by 1e-8 to 1e-6, below what 32-bit sums resolve."""
     r = np.random.default_rng(19)
