@@ -35,8 +35,13 @@ constexpr int kMaxSplits = 64;
 // the hardware's 2^-23 and for a distance d its roundings (the difference, its product with log2 e, log2 e itself),
 // 2.25 |d| 2^-24, and the four distances add up to the logit's distance to the row's maximum.  What lies beyond
 // 20 is below 2^20 e^-20 = 2e-3 of the sum.  (4 + 22.5) 2^-23 = 3.2e-6, plus 3 additions in 32 bits (2e-7): two
-// beams' scores are in the right order if they differ by more than twice 3.4e-6.
+// beams' scores are in the right order if they differ by more than twice 3.4e-6, and by what their own roundings
+// to 64 bits come to beyond that: half a step, at most 2^-53 of the score, in each of the two and in each of
+// the two that exact sums would give.
 constexpr double kNear = 7e-6;
+__device__ __forceinline__ bool near_scores(double better, double worse) {
+    return better - worse < kNear + fmax(fabs(better), fabs(worse)) * 0x1p-51;
+}
 
 // Keys in ascending order of the float they stand for.  -0 counts as 0, NaN as -inf.
 __device__ __forceinline__ uint32_t key_of(float x) {
@@ -457,7 +462,7 @@ template <typename IO> __global__ __launch_bounds__(kMergeThreads) void beam_mer
             if (c.before(tau)) {
                 const int at = atomicAdd(&count, 1);
                 if (at < a.merge_list) best[at] = c;  // more are only there if another call writes this workspace
-            } else if (of_key64(tau.key) - of_key64(c.key) < kNear) {
+            } else if (near_scores(of_key64(tau.key), of_key64(c.key))) {
                 atomicOr(&tau_mask, 1u << c.beam());
             }
         }
@@ -477,15 +482,15 @@ template <typename IO> __global__ __launch_bounds__(kMergeThreads) void beam_mer
             const uint32_t w0 = best[i].beam();
             if (i + 1 < min(n, K)) {
                 const uint32_t w1 = best[i + 1].beam();
-                if (w0 != w1 && of_key64(best[i].key) - of_key64(best[i + 1].key) < kNear)
+                if (w0 != w1 && near_scores(of_key64(best[i].key), of_key64(best[i + 1].key)))
                     atomicOr(&near_mask, (1u << w0) | (1u << w1));
-            } else if (i >= K - 1 && last - of_key64(best[i].key) < kNear) {
+            } else if (i >= K - 1 && near_scores(last, of_key64(best[i].key))) {
                 atomicOr(&behind_mask, 1u << w0);
             }
         }
         __syncthreads();
         uint32_t behind = behind_mask, near = near_mask;
-        if (n >= K && last - of_key64(tau.key) < kNear) behind |= tau_mask;
+        if (n >= K && near_scores(last, of_key64(tau.key))) behind |= tau_mask;
         if (behind & (behind - 1)) near |= behind;  // more than one beam
         near &= (uint32_t)__ballot(lane < W && state[lane < W ? lane : 0] == 0);  // an ended beam's score has no sum
         __syncthreads();  // every wave has read the masks before they are cleared, and all go on or none

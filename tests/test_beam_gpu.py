@@ -220,6 +220,25 @@ def test_near_ties_between_beams_are_settled_in_64_bits():
         assert np.allclose(got, every[:12], rtol=0, atol=1e-12)
 
 
+@pytest.mark.parametrize("K", [1, 2, 5])
+def test_scores_that_round_to_coarse_steps(K):
+    """Two beams with the same logits in another order and scores of -1e11, whose 64-bit steps are 2^-16.  The
+    best candidates are equal and lie beside the middle between two steps: 32-bit sums that differ by 1e-8 put
+    them on different ones."""
+    B, V, step = 128, 3001, 2.0 ** -16
+    lg, r = np.empty((B, 2, V)), np.random.default_rng(60)
+    for b in range(B):
+        x = (r.normal(size=V) * 2.5).astype(np.float32)
+        x[0] = np.nextafter(x.max(), np.float32(100))
+        tops = (x[:1].view(np.int32) + np.arange(4000, dtype=np.int32)).view(np.float32).astype(np.float64)
+        rest = x[1:].astype(np.float64)
+        at = (tops - (tops + np.log1p(np.exp(rest[None] - tops[:, None]).sum(1)))) / step
+        off = np.abs(at - np.floor(at) - 0.5)
+        x[0] = tops[np.where(off > 1e-6, off, 1.0).argmin()]  # 1e-6 steps are 1.5e-11: far more than 64-bit sums err
+        lg[b] = x, r.permutation(x)
+    _compare(lg, np.full((B, 2), -1e11, np.float32), K, "f32")
+
+
 @pytest.mark.parametrize("V,K,equal", [(3001, 1, 2), (3001, 4, 6), (40000, 1, 2), (40000, 4, 9), (40000, 64, 300)])
 def test_near_ties_behind_equal_candidates(V, K, equal):
     """The last result and those behind it are one beam's equal logits; another beam's best comes behind them
