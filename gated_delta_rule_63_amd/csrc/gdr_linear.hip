@@ -353,10 +353,13 @@ __device__ __forceinline__ void chain(const LinearArgs& a, TileShared<VEC, W>& s
         sh.carry[tid] = 0.0f;
     }
     if (at > 0) {
-        // Wave w reads the word of the tile w + 1 places back.  The state is carried forward tile by tile from
-        // the farthest cut run among them, so it is the same, bit for bit, whichever of them are cut already.
-        float state = 0.0f;
+        // Wave w reads the word of the tile w + 1 places back.  The state is carried forward tile by tile; a cut run
+        // sets it whatever stood before, so the nearest one decides.  That run's B is apply_run(whole, state) of the
+        // same chain, so the state is the same, bit for bit, whichever of the tiles are cut already.  A pass
+        // in which a channel meets no cut run gives it no state, and its words are looked at again.
+        float state;
         for (;;) {
+            state = 0.0f;
 #pragma unroll
             for (int k = 0; k < kBack; k += W) {
                 if (w + k >= kBack) break;
