@@ -550,7 +550,12 @@ gdr_status gdr_beam_reorder(int32_t batch, int32_t beams, const int32_t* parents
     if ((int64_t)batch * beams > 65535 || num_layers > 65535) return GDR_ERROR_NOT_SUPPORTED;  // grid y/z limits
     if (batch == 0 || num_layers == 0) return GDR_SUCCESS;
     if (!(parents && state_indices && state_indices_out && pool)) return GDR_ERROR_INVALID_VALUE;
-    if (state_indices_out == state_indices || state_indices_out == parents) return GDR_ERROR_INVALID_VALUE;
+    // the slots are written while other workgroups still read the old ones and the parents
+    const int64_t out = (int64_t)reinterpret_cast<uintptr_t>(state_indices_out), bytes = (int64_t)batch * beams * sizeof(int32_t);
+    for (const int32_t* in : {state_indices, parents}) {
+        const int64_t away = out - (int64_t)reinterpret_cast<uintptr_t>(in);
+        if (away > -bytes && away < bytes) return GDR_ERROR_INVALID_VALUE;
+    }
     gdr_status st = check_device();
     if (st != GDR_SUCCESS) return st;
     gdr::ReorderArgs a{};

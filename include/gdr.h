@@ -469,7 +469,7 @@ GDR_API gdr_status gdr_beam_select(const gdr_beam_problem* p, const void* logits
  *
  *   parents            int32 [batch, beams], values 0..beams-1
  *   state_indices      int32 [batch, beams]: each beam's slot, distinct and < num_slots
- *   state_indices_out  int32 [batch, beams] (written): the slots of the new beams; must not be
+ *   state_indices_out  int32 [batch, beams] (written): the slots of the new beams; must not overlap
  *                      state_indices or parents.  The same call for another pool that is indexed by
  *                      the same slots takes the same state_indices
  *   pool               [num_layers, num_slots] slots of slot_bytes bytes (a multiple of 2) each

@@ -348,6 +348,22 @@ def test_reorder_leaves_padded_and_invalid_rows():
     assert np.array_equal(to_host(new), want) and torch.equal(pool, before)
 
 
+def test_reorder_writes_slots_beside_those_it_reads_but_not_over_them():
+    idx, par = np.array([[4, 2, 0]], np.int32), np.array([[2, 2, 1]], np.int32)
+    buf = torch.zeros(9, dtype=torch.int32, device="cuda")
+    buf[:3], buf[6:] = to_dev(par[0]), to_dev(idx[0])
+    pool = torch.randn(6, 16, device="cuda")
+    want, after = beam.reorder(idx, par, 6)[0], pool.clone()
+    after[4] = pool[0]
+    args = pool, buf[6:].view(1, 3), buf[:3].view(1, 3)
+    for at in (2, 4, 5):
+        with pytest.raises(gdr.GdrError):
+            gdr.gdr_beam_reorder(*args, state_indices_out=buf[at:at + 3].view(1, 3))
+    new = gdr.gdr_beam_reorder(*args, state_indices_out=buf[3:6].view(1, 3))
+    torch.cuda.synchronize()
+    assert np.array_equal(to_host(new), want) and torch.equal(pool, after)
+
+
 def test_reorder_unaligned_slots():
     for n in (1, 3, 6, 10):                   # slots of 2, 6, 12, 20 bytes
         pool = torch.randn(2, 8, n, device="cuda").bfloat16()

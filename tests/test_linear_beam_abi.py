@@ -110,6 +110,12 @@ def test_reorder_rejects_bad_metadata():
     assert _reo(B=0) == 0 and _reo(L=0) == 0
 
 
+def test_reorder_rejects_slots_written_over_those_it_reads():
+    for base in (0x1000, 0x2000):                          # parents, state_indices: 2 x 4 entries of 4 bytes
+        for off in (-28, -4, 0, 4, 28):
+            assert _reo(out=ctypes.c_void_p(base + off)) == 1, (hex(base), off)
+
+
 def test_binding_refuses_host_tensors():
     x = torch.zeros(4, 8)
     with pytest.raises(ValueError):
