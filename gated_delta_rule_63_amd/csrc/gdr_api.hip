@@ -424,6 +424,16 @@ gdr_status check_linear(const gdr_linear_problem* p) {
     return GDR_SUCCESS;
 }
 
+bool overlap(const void* p, const void* q, int64_t bytes) {
+    if (!p || !q) return false;
+    const int64_t away = (int64_t)(reinterpret_cast<uintptr_t>(p) - reinterpret_cast<uintptr_t>(q));
+    return away > -bytes && away < bytes;
+}
+
+// A sequence's first tile reads its initial state (or the gradient of its final one) again while the last may
+// have written the other, so the two are kept apart.
+int64_t states_bytes(const gdr_linear_problem* p) { return (int64_t)p->num_seqs * p->num_channels * sizeof(float); }
+
 // Checks that both directions of the scan share.
 gdr_status check_linear_scan(const gdr_linear_problem* p, const int32_t* cu_seqlens, const void* workspace,
                              size_t workspace_bytes) {
@@ -463,6 +473,7 @@ gdr_status gdr_linear_scan_fwd(const gdr_linear_problem* p, const void* x, const
     if (p->total_tokens > 0 && !(x && gate && y)) return GDR_ERROR_INVALID_VALUE;
     if ((st = check_linear_scan(p, cu_seqlens, workspace, workspace_bytes)) != GDR_SUCCESS) return st;
     if (p->num_seqs == 0 || (p->total_tokens == 0 && !final_state)) return GDR_SUCCESS;
+    if (p->total_tokens > 0 && overlap(final_state, initial_state, states_bytes(p))) return GDR_ERROR_INVALID_VALUE;
     if ((st = check_device()) != GDR_SUCCESS) return st;
     const hipStream_t stream = static_cast<hipStream_t>(hip_stream);
     if (p->total_tokens == 0)
@@ -483,6 +494,7 @@ gdr_status gdr_linear_scan_bwd(const gdr_linear_problem* p, const void* x, const
     if (p->total_tokens > 0 && !(x && gate && block_states && dy && dx && dgate)) return GDR_ERROR_INVALID_VALUE;
     if ((st = check_linear_scan(p, cu_seqlens, workspace, workspace_bytes)) != GDR_SUCCESS) return st;
     if (p->num_seqs == 0 || (p->total_tokens == 0 && !d_initial_state)) return GDR_SUCCESS;
+    if (p->total_tokens > 0 && overlap(d_initial_state, d_final_state, states_bytes(p))) return GDR_ERROR_INVALID_VALUE;
     if ((st = check_device()) != GDR_SUCCESS) return st;
     const hipStream_t stream = static_cast<hipStream_t>(hip_stream);
     if (p->total_tokens == 0)
@@ -551,11 +563,9 @@ gdr_status gdr_beam_reorder(int32_t batch, int32_t beams, const int32_t* parents
     if (batch == 0 || num_layers == 0) return GDR_SUCCESS;
     if (!(parents && state_indices && state_indices_out && pool)) return GDR_ERROR_INVALID_VALUE;
     // the slots are written while other workgroups still read the old ones and the parents
-    const int64_t out = (int64_t)reinterpret_cast<uintptr_t>(state_indices_out), bytes = (int64_t)batch * beams * sizeof(int32_t);
-    for (const int32_t* in : {state_indices, parents}) {
-        const int64_t away = out - (int64_t)reinterpret_cast<uintptr_t>(in);
-        if (away > -bytes && away < bytes) return GDR_ERROR_INVALID_VALUE;
-    }
+    const int64_t bytes = (int64_t)batch * beams * sizeof(int32_t);
+    if (overlap(state_indices_out, state_indices, bytes) || overlap(state_indices_out, parents, bytes))
+        return GDR_ERROR_INVALID_VALUE;
     gdr_status st = check_device();
     if (st != GDR_SUCCESS) return st;
     gdr::ReorderArgs a{};

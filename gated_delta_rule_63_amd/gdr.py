@@ -585,7 +585,8 @@ def gdr_linear_scan_fwd(x, gate, gate_kind: int, cu_seqlens=None, initial_state=
                         output_final_state: bool = True, block_states=None, output_block_states: bool = False,
                         workspace=None, stream=None):
     """Gated linear recurrence over a packed batch: x [T, D], gate [T, D] (fp32 log-decay, or x's dtype
-    before the sigmoid), initial_state [N, D] fp32.  Returns (y, final_state or None), and block_states
+    before the sigmoid), initial_state [N, D] fp32 (not the same memory as final_state).  Returns (y,
+    final_state or None), and block_states
     [ceil(T / GDR_LINEAR_BLOCK), D] for gdr_linear_scan_bwd as a third where it is asked for or given.
     ``workspace`` is a uint8 device tensor of at least gdr_linear_workspace_size bytes (allocated here if
     absent)."""

@@ -383,7 +383,8 @@ GDR_API size_t gdr_linear_workspace_size(const gdr_linear_problem* p);
  *
  *   cu_seqlens     int32 [N+1]; may be NULL only when N == 1 (one sequence of T tokens)
  *   initial_state  fp32 [N, D] or NULL (zeros)
- *   final_state    fp32 [N, D] or NULL.  An empty sequence's is its initial state
+ *   final_state    fp32 [N, D] or NULL.  An empty sequence's is its initial state.  Unlike the entry
+ *                  points above, it must not overlap initial_state (refused)
  *   block_states   fp32 [ceil(T / GDR_LINEAR_BLOCK), D] or NULL: the state behind the tokens before
  *                  each block, which gdr_linear_scan_bwd takes
  *   workspace      gdr_linear_workspace_size(p) bytes, 256-byte aligned, contents need not be
@@ -401,7 +402,7 @@ GDR_API gdr_status gdr_linear_scan_fwd(const gdr_linear_problem* p,
  *
  *   d_final_state    fp32 [N, D] or NULL (zeros)
  *   dx, dgate        [T, D] (written)
- *   d_initial_state  fp32 [N, D] or NULL (not written)
+ *   d_initial_state  fp32 [N, D] or NULL (not written); must not overlap d_final_state (refused)
  */
 GDR_API gdr_status gdr_linear_scan_bwd(const gdr_linear_problem* p,
                                const void* x, const void* gate,

@@ -49,6 +49,14 @@ def test_scan_accepts_empty_batches_without_the_device():
     assert _bwd(_lp(T=0, N=3), x=None, gate=None, bs=None, dy=None, dx=None, dg=None, ws=None, nb=0) == 0
 
 
+@pytest.mark.parametrize("off", [-508, -4, 0, 4, 508])
+def test_scan_rejects_states_written_over_those_it_reads(off):
+    """2 x 64 fp32 states: 512 bytes."""
+    L, p, here, there = gdr.lib(), ctypes.byref(_lp()), ctypes.c_void_p(0x10000), ctypes.c_void_p(0x10000 + off)
+    assert L.gdr_linear_scan_fwd(p, PTR, PTR, PTR, here, PTR, there, None, PTR, 1 << 20, None) == 1
+    assert L.gdr_linear_scan_bwd(p, PTR, PTR, PTR, None, PTR, PTR, here, PTR, PTR, there, PTR, 1 << 20, None) == 1
+
+
 def test_scan_workspace_size():
     size = lambda **k: gdr.lib().gdr_linear_workspace_size(ctypes.byref(_lp(**k)))  # noqa: E731
     assert size(T=0) == 0 and size(D=0) == 0

@@ -273,6 +273,31 @@ def test_calls_are_repeatable_and_captured():
             assert torch.equal(a, b)
 
 
+def test_states_beside_each_other():
+    """Initial and final states, and their gradients, as neighbours in one buffer, and over one another."""
+    p = _problem(18, [700, 41], 64, "log", "f32")
+    d = _dev(p)
+    want = _forward(p, d)
+    bw = dict(cu_seqlens=d["cu"], initial_state=d["h0"])
+    want_b = gdr.gdr_linear_scan_bwd(d["x"], d["gate"], p["kind"], d["dy"], want[2], d_final_state=d["dF"], **bw)
+    buf = torch.empty(5, 64, device="cuda")
+    buf[:2] = d["dF"]
+    got = gdr.gdr_linear_scan_bwd(d["x"], d["gate"], p["kind"], d["dy"], want[2], d_final_state=buf[:2],
+                                  d_initial_state=buf[2:4], **bw)
+    for a, b in zip(got, want_b):
+        assert torch.equal(a, b)
+    with pytest.raises(gdr.GdrError):
+        gdr.gdr_linear_scan_bwd(d["x"], d["gate"], p["kind"], d["dy"], want[2], d_final_state=buf[:2],
+                                d_initial_state=buf[1:3], **bw)
+    buf[2:4] = d["h0"]
+    d["h0"] = buf[2:4]
+    for a, b in zip(_forward(p, d, final_state=buf[:2]), want):
+        assert torch.equal(a, b)
+    for at in (1, 2, 3):
+        with pytest.raises(gdr.GdrError):
+            _forward(p, d, final_state=buf[at:at + 2])
+
+
 def test_another_stream():
     p = _problem(15, [5000], 512, "log", "bf16")
     d = _dev(p)
