@@ -500,6 +500,13 @@ def _arg(t: Optional[torch.Tensor], name: str, shape, dtype, device: int):
     return t.data_ptr()
 
 
+_INT32_MAX = 0x7FFFFFFF  # of the C ABI's 32-bit fields: ctypes would cut a larger size off
+
+
+def _too_large(names: str, *sizes):
+    raise ValueError(f"{names}: {sizes} do not fit into 32 bits")
+
+
 def _required(t: Optional[torch.Tensor], name: str, shape, dtype, device: int) -> int:
     if t is None:
         raise ValueError(f"{name} is required")
@@ -564,6 +571,8 @@ def _linear_problem(x, gate, gate_kind: int, num_seqs: int):
     if not x.is_cuda:
         raise ValueError("x must be a device tensor")
     dev = x.get_device()
+    if (num_seqs | shape[1]) > _INT32_MAX:
+        _too_large("sequences, channels", num_seqs, shape[1])
     p = LinearProblem(shape[0], num_seqs, shape[1], gate_kind, _dtype_code(dtype))
     return p, dev, shape, gate_dtype, _required(x, "x", shape, dtype, dev), _required(gate, "gate", shape, gate_dtype, dev)
 
@@ -659,6 +668,8 @@ def gdr_linear_decode_paged(x, gate, gate_kind: int, pool, state_indices, cu_seq
         if y is None:
             y = torch.empty_like(x)
         slots = pool.shape[0]
+        if (slots | max_q_len) > _INT32_MAX:
+            _too_large("slots, max_q_len", slots, max_q_len)
         st = lib().gdr_linear_decode_paged(ctypes.byref(p), max_q_len, px, pg,
                                            _arg(cu_seqlens, "cu_seqlens", (N + 1,), torch.int32, dev),
                                            _arg(pool, "pool", (slots, shape[1]), pool.dtype, dev),
@@ -681,6 +692,8 @@ def _beam_problem(logits, num_out: int, eos_token: int) -> BeamProblem:
     if (sv != 1 and V > 1) or (B > 1 and W > 1 and sb != W * sw):
         raise ValueError("logits: the rows must be contiguous and evenly spaced")
     row = sw if W > 1 else sb if B > 1 else V
+    if max(B | W | V, num_out, eos_token) > _INT32_MAX:
+        _too_large("batch, beams, vocab, num_out, eos_token", B, W, V, num_out, eos_token)
     return BeamProblem(B, W, V, num_out, row, eos_token, _dtype_code(logits.dtype))
 
 
@@ -732,6 +745,8 @@ def gdr_beam_reorder(pool, state_indices, parents, slot_dim: int = 0, state_indi
         raise ValueError("pool must be a device tensor")
     rows, dev, i32 = state_indices.shape, pool.get_device(), torch.int32
     slot_bytes = pool.element_size() * math.prod(shape[slot_dim + 1:])
+    if (rows[0] | rows[1] | shape[0] | shape[slot_dim]) > _INT32_MAX:
+        _too_large("batch, beams, layers, slots", *rows, shape[0], shape[slot_dim])
     with _On(dev, stream) as raw:
         out = _rows(*rows, i32, dev) if state_indices_out is None else state_indices_out
         st = lib().gdr_beam_reorder(rows[0], rows[1], _required(parents, "parents", rows, i32, dev),

@@ -364,6 +364,29 @@ def test_widest_rows(T):
     assert bool(((dh0[0] - D0 / 2).abs() <= 24 * U * 40).all()) and bool((dg[0] == 0).all())
 
 
+def test_sizes_past_32_bits_are_refused():
+    """2^32 + 64 channels, tokens of a vocabulary or slots: not taken for 64 of them."""
+    n, i32 = (1 << 32) + 64, torch.int32
+    x, idx = torch.empty(1, n, dtype=torch.bfloat16, device="cuda"), torch.zeros(1, dtype=i32, device="cuda")
+    with pytest.raises(ValueError):
+        gdr.gdr_linear_scan_fwd(x, x, gdr.GDR_LINEAR_SIGMOID)
+    with pytest.raises(ValueError):
+        gdr.gdr_linear_decode_paged(x, x, gdr.GDR_LINEAR_SIGMOID, x, idx)
+    with pytest.raises(ValueError):
+        gdr.gdr_linear_decode_paged(x[:, :1].contiguous(), x[:, :1].contiguous(), gdr.GDR_LINEAR_SIGMOID, x.view(n, 1), idx)
+    with pytest.raises(ValueError):
+        gdr.gdr_beam_select(x[None], torch.zeros(1, 1, device="cuda"), 1)
+    with pytest.raises(ValueError):
+        gdr.gdr_beam_reorder(x.view(n, 1), idx[None], idx[None])
+    some = torch.zeros(1, 1, 8, device="cuda")
+    for bad in (dict(num_out=(1 << 32) + 1), dict(num_out=1, eos_token=1 << 32, finished=torch.zeros(1, 1, dtype=torch.uint8, device="cuda"))):
+        with pytest.raises(ValueError):
+            gdr.gdr_beam_select(some, some[:, :, 0].contiguous(), **bad)
+    one = torch.zeros(1, 8, device="cuda")
+    with pytest.raises(ValueError):
+        gdr.gdr_linear_decode_paged(one, one, gdr.GDR_LINEAR_LOG_DECAY, one, idx, max_q_len=(1 << 32) + 1)
+
+
 def test_offsets_past_32_bits():
     """2^31 elements and more: the last rows (for the gradients: the first), which gates of one half forget
     everything 300 tokens away from, against the oracle on those rows alone."""
