@@ -356,8 +356,9 @@ GDR_API gdr_status gdr_kda_decode_fused(const gdr_problem* p, int32_t max_q_len,
  * Layouts: x, y, dy, dx [T, D] io_dtype; gate, dgate [T, D]; states [N, D] fp32; cu_seqlens as above,
  * except that cu_seqlens[N] may be less than T: rows behind the last sequence are neither read nor
  * written.  States are held in fp32 throughout; any channel count from 1 to 2^22 is accepted.  A NaN
- * stays within its sequence and channel, and so does an infinite input; a state that becomes infinite is a
- * NaN from the next token on.
+ * stays within its sequence and channel, and so does an infinite input.  A state that becomes infinite is a
+ * NaN from the next token on, and with GDR_LINEAR_SIGMOID, whose step forms h[t-1] - x[t], an infinite x
+ * can make it one at once: that difference has to stay below fp32's 3.4e38.
  */
 typedef enum gdr_linear_gate {
     GDR_LINEAR_LOG_DECAY = 0,

@@ -227,6 +227,42 @@ def test_special_values_stay_in_their_sequence_and_channel(T):
     assert np.isfinite(f64(dh0)[[0, 2]]).all()
 
 
+@pytest.mark.parametrize("T", [40, 900])
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_special_values_of_the_sigmoid_gate(T, io):
+    """Lowest values as inputs and gates are ordinary numbers; infinities and NaN stay where they are."""
+    p = _problem(19, [T, T, T], 68, "sigmoid", "f32")
+    low = inputs.widen(inputs.f32_to_bf16_bits(np.array([-3.3e38], np.float32)))[0]
+    x, z = p["x"].astype(np.float64), p["gate"].astype(np.float64)
+    x[T + 4, 1], x[T + 5, 2], z[T + 6, 3], z[T + 7, 4] = low, -low, low, -low   # forget all, keep all
+    x[T + 5, 10], x[T + 5, 11], x[T + 6, 12], z[T + 7, 13] = np.inf, -np.inf, np.nan, np.nan
+    z[T + 5, 10:12] = 3.0, -3.0                  # a near 1, a near 0
+    z[T + 8, 14], z[T + 9, 15] = -np.inf, np.inf
+    p["x"], p["gate"], p["io"] = _cast(x, io), _cast(z, io), io
+    p["dy"] = _cast(p["dy"], io)
+    d = _dev(p)
+    y, final, blocks = _forward(p, d)
+    dx, dz, dh0 = gdr.gdr_linear_scan_bwd(d["x"], d["gate"], p["kind"], d["dy"], blocks, cu_seqlens=d["cu"],
+                                          initial_state=d["h0"], d_final_state=d["dF"])
+    y, dx, dz = f64(y), f64(dx), f64(dz)
+    with np.errstate(invalid="ignore"):
+        f = linear.scan(_wide(p["x"]), _wide(p["gate"]), p["kind"], p["cu"], p["h0"])
+    rest = [c for c in range(68) if c not in (10, 11, 12, 13)]
+    for s in (slice(0, T), slice(2 * T, 3 * T)):
+        _check(y[s], f["y"][s], f["err"][s], HALF[io], "other sequences")
+        assert np.isfinite(dx[s]).all() and np.isfinite(dz[s]).all()
+    mid = slice(T, 2 * T)
+    _check(y[mid][:, rest], f["y"][mid][:, rest], f["err"][mid][:, rest], HALF[io], "other channels")
+    for c, t in ((10, 5), (11, 5), (12, 6), (13, 7)):
+        assert np.isfinite(y[T:T + t, c]).all() and not np.isfinite(y[T + t:2 * T, c]).any()
+    assert np.isposinf(y[T + 5, 10])
+    for t, c in ((6, 3), (8, 14)):
+        assert y[T + t, c] == _wide(p["x"])[T + t, c]
+    plain = [c for c in rest if c not in (1, 2)]  # the lowest values' gates have gradients past fp32
+    assert np.isfinite(dx[:, plain]).all() and np.isfinite(dz[:, plain]).all()
+    assert np.isfinite(f64(dh0)[[0, 2]]).all()
+
+
 def test_misaligned_rows_take_the_narrow_path():
     p = _problem(13, [300, 20], 64, "sigmoid", "bf16")
     d = _dev(p)
