@@ -376,6 +376,34 @@ def test_reorder_unaligned_slots():
 
 
 # ---------------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("W,io,pool_dt", [(4, "bf16", "f32"), (3, "bf16", "bf16"), (2, "f32", "f32")])
+def test_reorder_of_the_kda_decode_front(W, io, pool_dt):
+    """The front's two pools, states and convolution windows: a step, the reordering, a step from the new slots,
+    which equals the step from copies of the parents' states in slots of their own."""
+    p = inputs.kda_front_problem(70 + W, B=6, q_len=1, H=2, R=16, W=W, num_slots=9, io_dtype=io, pool_dtype=pool_dt)
+    d = {n: to_dev(getattr(p, n)) for n in ("q", "k", "v", "conv_weight", "gate_in", "gate_weight", "A_log", "dt_bias", "b",
+                                            "conv_bias", "norm_weight", "norm_gate")}
+
+    def step(pool, conv, slots):
+        return gdr.gdr_kda_decode_fused(d["q"], d["k"], d["v"], d["conv_weight"], conv, d["gate_in"], d["gate_weight"],
+                                        d["A_log"], d["dt_bias"], d["b"], pool, slots, scale=p.scale,
+                                        conv_bias=d["conv_bias"], norm_weight=d["norm_weight"], norm_gate=d["norm_gate"])
+    pool, conv, idx = to_dev(p.pool), to_dev(p.conv_state), to_dev(p.state_indices)
+    step(pool, conv, idx)
+    par = to_dev(np.array([[1, 1, 0], [2, 2, 2]], np.int32))
+    old = idx.view(2, 3).long()
+    of_parent = old.gather(1, par.long()).flatten()
+    want_pool, want_conv = pool[of_parent].clone(), conv[of_parent].clone()
+    new = gdr.gdr_beam_reorder(pool, idx.view(2, 3), par)
+    assert torch.equal(new, gdr.gdr_beam_reorder(conv, idx.view(2, 3), par))
+    at = new.flatten().long()
+    assert torch.equal(pool[at], want_pool) and torch.equal(conv[at], want_conv)
+    o = step(pool, conv, new.flatten())
+    want = step(want_pool, want_conv, torch.arange(6, dtype=torch.int32, device="cuda"))
+    torch.cuda.synchronize()
+    assert torch.equal(o, want) and torch.equal(pool[at], want_pool) and torch.equal(conv[at], want_conv)
+
+
 def test_beam_search_over_paged_states():
     """Decode, selection and reordering together: a small model of one delta-rule layer and one linear
     layer, 2 searches of 3 beams for 6 steps.  The states in the slots of each beam, after every step, equal
