@@ -456,6 +456,7 @@ GDR_API size_t gdr_beam_workspace_size(const gdr_beam_problem* p);
  *   scores       [batch, beams] fp32: each beam's log-probability so far
  *   finished     [batch, beams] bytes, or NULL (none has ended)
  *   out_scores, out_parents, out_tokens   [batch, num_out] fp32, int32 (beam w), int32 (token v)
+ *                (out_scores may be scores where num_out == beams)
  *   workspace    gdr_beam_workspace_size(p) bytes, 256-byte aligned, need not be initialised; calls
  *                that may overlap need one each
  */

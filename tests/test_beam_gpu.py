@@ -404,6 +404,15 @@ def test_reorder_of_the_kda_decode_front(W, io, pool_dt):
     assert torch.equal(o, want) and torch.equal(pool[at], want_pool) and torch.equal(conv[at], want_conv)
 
 
+def test_scores_updated_in_place():
+    """out_scores may be scores where there are as many results as beams."""
+    lg, sc = _logits(71, 5, 6, 9000), _scores(72, 5, 6)
+    d, held = _dev_logits(lg, "bf16", 0), to_dev(sc)
+    want = gdr.gdr_beam_select(d, held, 6)
+    got = gdr.gdr_beam_select(d, held, 6, out_scores=held)
+    assert got[0] is held and all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 def test_beam_search_over_paged_states():
     """Decode, selection and reordering together: a small model of one delta-rule layer and one linear
     layer, 2 searches of 3 beams for 6 steps.  The states in the slots of each beam, after every step, equal
