@@ -513,7 +513,7 @@ gdr_status gdr_linear_decode_paged(const gdr_linear_problem* p, int32_t max_q_le
     gdr_status st = check_linear(p);
     if (st != GDR_SUCCESS) return st;
     if (max_q_len < 1 || max_q_len > 12) return GDR_ERROR_INVALID_VALUE;
-    if (!pool || num_slots <= 0 || !state_indices) return GDR_ERROR_INVALID_VALUE;
+    if (!pool || num_slots <= 0 || (p->num_seqs > 0 && !state_indices)) return GDR_ERROR_INVALID_VALUE;
     if (!dtype_ok(pool_dtype)) return GDR_ERROR_INVALID_VALUE;
     if (commit != 0 && commit != 1) return GDR_ERROR_INVALID_VALUE;
     if (p->total_tokens > 0 && !(x && gate && y)) return GDR_ERROR_INVALID_VALUE;

@@ -79,6 +79,11 @@ def test_decode_rejects_bad_metadata():
     assert _dec(_lp(T=0, N=4), cu=PTR) == 0
 
 
+def test_decode_of_no_sequences_needs_no_indices():
+    assert _dec(_lp(T=0, N=0), x=None, gate=None, idx=None, y=None) == 0
+    assert _dec(_lp(T=0, N=1), cu=PTR, x=None, gate=None, idx=None, y=None) == 1
+
+
 def _bp(B=2, W=4, V=100, K=8, stride=100, eos=0, io=1):
     return gdr.BeamProblem(B, W, V, K, stride, eos, io)
 

@@ -137,6 +137,14 @@ def test_many_sequences_and_wide_rows():
     _run_both(_problem(10, [40, 100], 4100, "sigmoid", "bf16"))
 
 
+def test_decode_of_no_sequences():
+    x, i = torch.empty(0, 40, device="cuda"), torch.empty(0, dtype=torch.int32, device="cuda")
+    pool = torch.randn(3, 40, device="cuda")
+    before = pool.clone()
+    y = gdr.gdr_linear_decode_paged(x, x, gdr.GDR_LINEAR_LOG_DECAY, pool, i)
+    assert y.shape == (0, 40) and torch.equal(pool, before)
+
+
 @pytest.mark.parametrize("D", [64, 65])
 def test_no_cu_seqlens_equals_one_sequence(D):
     p = _problem(11, [1000], D, "log", "bf16")
