@@ -413,6 +413,86 @@ def test_scores_updated_in_place():
     assert got[0] is held and all(torch.equal(a, b) for a, b in zip(got, want))
 
 
+def test_largest_batches():
+    """65504 rows of beams (65535 is the most), and a reordering of as many and of 65535 layers."""
+    B, W, V, K = 2047, 32, 67, 4
+    g = torch.Generator(device="cuda").manual_seed(4)
+    lg, sc = torch.randn(B, W, V, device="cuda", generator=g), torch.rand(B, W, device="cuda", generator=g)
+    s, p, t = gdr.gdr_beam_select(lg, sc, K)
+    x = lg.double()
+    best, at = (x - torch.logsumexp(x, 2, keepdim=True) + sc.double()[:, :, None]).flatten(1).topk(K + 1)
+    clear = (best[:, :-1] - best[:, 1:] > 1e-12).all(1)     # distinct to the rounding of 64-bit sums
+    assert int(clear.sum()) > B - 3
+    assert torch.equal((p.long() * V + t.long())[clear], at[clear, :K])
+    pool = torch.randn(B * W, 2, device="cuda")
+    idx = torch.randperm(B * W, device="cuda", generator=g).view(B, W).int()
+    want = pool[idx.long().gather(1, p.long()[:, torch.arange(W) % K]).flatten()]
+    new = gdr.gdr_beam_reorder(pool, idx, p[:, torch.arange(W) % K].contiguous())
+    assert torch.equal(pool[new.flatten().long()], want)
+    pool = torch.randn(65535, 3, 2, device="cuda")
+    after = pool.clone()
+    after[:, 0] = pool[:, 2]
+    new = gdr.gdr_beam_reorder(pool, to_dev(np.array([[2, 0]], np.int32)), torch.zeros(1, 2, dtype=torch.int32, device="cuda"), slot_dim=1)
+    assert new.tolist() == [[2, 0]] and torch.equal(pool, after)
+
+
+def test_empty_batches_and_strided_rows():
+    i32 = torch.int32
+    out = gdr.gdr_beam_select(torch.empty(0, 4, 100, device="cuda"), torch.empty(0, 4, device="cuda"), 7)
+    assert [t.shape for t in out] == [(0, 7)] * 3
+    pool = torch.randn(5, 8, device="cuda")
+    none = torch.empty(0, 4, dtype=i32, device="cuda")
+    assert gdr.gdr_beam_reorder(pool, none, none).shape == (0, 4)
+    lg = torch.randn(6, 5, 333, device="cuda")
+    sc = to_dev(_scores(73, 6, 5))
+    for rows in ((slice(None), slice(2, 3)), (slice(3, 4), slice(1, 4)), (slice(1, 5), slice(None))):
+        want = gdr.gdr_beam_select(lg[rows].contiguous(), sc[rows].contiguous(), 9)
+        got = gdr.gdr_beam_select(lg[rows], sc[rows].contiguous(), 9)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    for bad in (lg[:, 1:3], lg[:, :, ::2], lg.transpose(0, 1)):
+        with pytest.raises(ValueError):
+            gdr.gdr_beam_select(bad, sc[:bad.shape[0], :bad.shape[1]].contiguous(), 9)
+
+
+def test_a_captured_step_of_the_search():
+    """Decode, selection and reordering of a linear layer's states in one graph, replayed with eager work between
+    the replays: each step as the eager one from the same states."""
+    B, W, D, V = 3, 4, 192, 1000
+    g = torch.Generator(device="cuda").manual_seed(6)
+    emb = torch.randn(V, D, device="cuda", generator=g)
+    gate = -torch.rand(V, D, device="cuda", generator=g)
+    head = torch.randn(D, V, device="cuda", generator=g) * 0.3
+
+    def fresh():
+        gg = torch.Generator(device="cuda").manual_seed(7)
+        return dict(pool=torch.randn(B * W + 3, D, device="cuda", generator=gg), idx=torch.arange(B * W, device="cuda").view(B, W).int(),
+                    scores=-torch.rand(B, W, device="cuda", generator=gg), tok=torch.zeros(B, W, dtype=torch.int32, device="cuda"))
+
+    def step(s):
+        t = s["tok"].flatten().long()
+        y = gdr.gdr_linear_decode_paged(emb[t], gate[t], gdr.GDR_LINEAR_LOG_DECAY, s["pool"], s["idx"].flatten())
+        sc, par, tok = gdr.gdr_beam_select((y @ head).view(B, W, V), s["scores"], W)
+        new = gdr.gdr_beam_reorder(s["pool"], s["idx"], par)
+        s["scores"].copy_(sc)
+        s["tok"].copy_(tok)
+        s["idx"].copy_(new)
+    a, b = fresh(), fresh()
+    warm = fresh()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(warm)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(a)
+    for _ in range(4):
+        graph.replay()
+        step(b)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a[k], b[k]) for k in a)
+
+
 def test_beam_search_over_paged_states():
     """Decode, selection and reordering together: a small model of one delta-rule layer and one linear
     layer, 2 searches of 3 beams for 6 steps.  The states in the slots of each beam, after every step, equal

@@ -137,6 +137,24 @@ def test_many_sequences_and_wide_rows():
     _run_both(_problem(10, [40, 100], 4100, "sigmoid", "bf16"))
 
 
+def test_most_sequences():
+    """65535 sequences, a third of them empty, in a scan and in a decode step."""
+    r = np.random.default_rng(21)
+    _run_both(_problem(22, r.integers(0, 3, 65535).tolist(), 3, "sigmoid", "f32", tail=5))
+    N, D = 65535, 12
+    x, g = torch.randn(N, D, device="cuda"), -torch.rand(N, D, device="cuda")
+    pool, slots = torch.randn(N + 9, D, device="cuda"), torch.randperm(N + 9, device="cuda")[:N].int()
+    slots[5::7] = -1
+    live = slots >= 0
+    want = pool.double()
+    want[slots[live].long()] = g[live].double().exp() * want[slots[live].long()] + x[live].double()
+    y = gdr.gdr_linear_decode_paged(x, g, gdr.GDR_LINEAR_LOG_DECAY, pool, slots, y=torch.full_like(x, 7.0))
+    # an exponential (4 u: 2^-23 of the instruction and its argument's rounding), a product and a sum
+    bound = 7 * U * (want.abs() + 2 * x.abs().max().item() + 2 * pool.abs().max().item())
+    assert bool(((pool.double() - want).abs() <= bound).all())
+    assert torch.equal(y[live], pool[slots[live].long()]) and bool((y[~live] == 7.0).all())
+
+
 def test_decode_of_no_sequences():
     x, i = torch.empty(0, 40, device="cuda"), torch.empty(0, dtype=torch.int32, device="cuda")
     pool = torch.randn(3, 40, device="cuda")
