@@ -37,10 +37,10 @@ constexpr int kMaxSplits = 64;
 // 20 is below 2^20 e^-20 = 2e-3 of the sum.  (4 + 22.5) 2^-23 = 3.2e-6, plus 3 additions in 32 bits (2e-7): two
 // beams' scores are in the right order if they differ by more than twice 3.4e-6, and by what their own roundings
 // to 64 bits come to beyond that: half a step, at most 2^-53 of the score, in each of the two and in each of
-// the two that exact sums would give.
+// the two that exact sums would give (2^-51, and as much again for the better one's step being the next larger).
 constexpr double kNear = 7e-6;
 __device__ __forceinline__ bool near_scores(double better, double worse) {
-    return better - worse < kNear + fmax(fabs(better), fabs(worse)) * 0x1p-51;
+    return better - worse < fma(fabs(worse), 0x1p-50, kNear);
 }
 
 // Keys in ascending order of the float they stand for.  -0 counts as 0, NaN as -inf.
@@ -493,6 +493,7 @@ template <typename IO> __global__ __launch_bounds__(kMergeThreads) void beam_mer
         if (n >= K && near_scores(last, of_key64(tau.key))) behind |= tau_mask;
         if (behind & (behind - 1)) near |= behind;  // more than one beam
         near &= (uint32_t)__ballot(lane < W && state[lane < W ? lane : 0] == 0);  // an ended beam's score has no sum
+        near = __builtin_amdgcn_readfirstlane(near);  // one value: the loop over beams stays scalar (401 us, 408 without)
         __syncthreads();  // every wave has read the masks before they are cleared, and all go on or none
         if (!near) break;
         for (int w = 0; w < W; ++w) {
