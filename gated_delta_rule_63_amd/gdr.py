@@ -598,7 +598,8 @@ def gdr_linear_scan_fwd(x, gate, gate_kind: int, cu_seqlens=None, initial_state=
     final_state or None), and block_states
     [ceil(T / GDR_LINEAR_BLOCK), D] for gdr_linear_scan_bwd as a third where it is asked for or given.
     ``workspace`` is a uint8 device tensor of at least gdr_linear_workspace_size bytes (allocated here if
-    absent)."""
+    absent).  Like every function here it records nothing for autograd: a layer that trains calls this and
+    gdr_linear_scan_bwd from a torch.autograd.Function's forward and backward."""
     N = _seqs(cu_seqlens)
     p, dev, shape, _, px, pg = _linear_problem(x, gate, gate_kind, N)
     T, D = shape

@@ -360,6 +360,33 @@ def test_states_beside_each_other():
             _forward(p, d, final_state=buf[at:at + 2])
 
 
+@pytest.mark.parametrize("kind,io", [("log", "f32"), ("sigmoid", "bf16")])
+def test_the_two_scans_as_an_autograd_function(kind, io):
+    """The layer that a user writes from them: its gradients are the gradients of every input."""
+    class Scan(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, gate, h0, cu):
+            y, final, blocks = gdr.gdr_linear_scan_fwd(x, gate, KINDS[kind], cu_seqlens=cu, initial_state=h0,
+                                                       output_block_states=True)
+            ctx.save_for_backward(x, gate, h0, cu, blocks)
+            return y, final
+
+        @staticmethod
+        def backward(ctx, dy, d_final):
+            x, gate, h0, cu, blocks = ctx.saved_tensors
+            return *gdr.gdr_linear_scan_bwd(x, gate, KINDS[kind], dy.contiguous(), blocks, cu_seqlens=cu, initial_state=h0,
+                                            d_final_state=d_final.contiguous()), None
+    p = _problem(23, [130, 0, 77, 1], 66, kind, io)
+    d = _dev(p)
+    leaves = [d[k].requires_grad_() for k in ("x", "gate", "h0")]
+    y, final = Scan.apply(*leaves, d["cu"])
+    torch.autograd.backward([y, final], [d["dy"], d["dF"]])
+    w = {k: _wide(p[k]) for k in ("x", "gate", "dy", "h0", "dF")}
+    b = linear.grads(w["x"], w["gate"], p["kind"], p["cu"], w["dy"], w["h0"], w["dF"])
+    for t, name in zip(leaves, ("dx", "dgate", "dh0")):
+        _check(f64(t.grad), b[name], b["err_" + name], HALF["bf16"] if t.dtype == torch.bfloat16 else U, name)
+
+
 def test_another_stream():
     p = _problem(15, [5000], 512, "log", "bf16")
     d = _dev(p)
