@@ -720,10 +720,15 @@ hipError_t scan_tiles(const LinearArgs& a, bool backward, hipStream_t s) {
 }
 
 // Tiles (us of device time, log gate, bf16, forward; T x D).
-//  - One tile needs no chain, and no launch before it.  Up to 64 tokens 8 per wave (64 x 1024: 5.7); to 128, 16
-//    (100 x 1024: 6.4, with a chain 9.2); to 256, 16 waves of 16 (200 x 1024: 7.9, with a chain 9.7); to 512 the
-//    forward pass has 16 waves of 32 (333 x 1024: 12.2, with a chain 10.5, but a launch less: 12.9 for a call
-//    among others, with a chain 14.9).
+//  - One tile needs no chain, and no launch before it.  Up to 64 tokens 8 per wave (64 x 1024: 5.7); to 128, 16; to
+//    256, 16 waves of 16; to 512 the forward pass has 16 waves of 32.  One tile / what longer scans take, as replayed
+//    in a graph, at 1024, 4096, 16384 and 65536 channels:
+//      100 tokens  6.4 / 9.3    6.6 / 10.1   7.1 / 13.6   13.7 / 18.8, backward  8.5 / 10.7 and 22.0 / 16.7 at the ends
+//      200 tokens  7.9 / 9.9    8.3 / 11.3   9.1 / 14.8   34.7 / 22.7, backward 10.9 / 11.6 and 50.3 / 48.1
+//      333 tokens 12.3 / 10.4  12.7 / 12.1  13.9 / 21.4   56.5 / 53.9
+//    (fp32 at 65536 channels 20 / 16, 39 / 44, 63 / 62).  Up to 16384 channels only 257 to 512 tokens of up to 4096
+//    come out longer, by 2.7 at most; a call of its own saves more with the launch there (333 x 1024: 11.6 among
+//    others, with a chain 14.4; 512 x 4096: 13.4 / 14.4).
 //  - Chains of large tiles: two channels per lane; 32 tokens per wave in bf16, 16 in fp32 and in the bf16 backward
 //    pass, whose kept values fill the registers.  The fp32 backward pass keeps 8: 16 spill (8192 x 4096: 143, 8
 //    tokens 128).  Tiles of 4 or 16 waves were slower (32768 x 4096: 8 waves 207, 4 waves 219, 16 waves 247).
