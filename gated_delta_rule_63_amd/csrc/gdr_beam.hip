@@ -549,9 +549,9 @@ template <typename IO> __global__ __launch_bounds__(kMergeThreads) void beam_mer
 constexpr int kCopyThreads = 256;
 constexpr int kCopyUnroll = 4;
 
-// HBM-bound.  94 copies of 2 MiB states (394 MB moved): 63 us, 6.2 TB/s, with 16 KiB per workgroup and
-// non-temporal stores; 72 with ordinary stores, 69 with non-temporal loads too, 115 to 137 with 32 KiB per
-// workgroup, whatever the loads and stores.
+// HBM-bound.  94 copies of 2 MiB states: 63 us with 16 KiB per workgroup and non-temporal stores; 72 with ordinary
+// stores, 69 with non-temporal loads too, 115 to 137 with 32 KiB per workgroup, whatever the loads and stores.  201 MB
+// are written and 143 read (a parent's copies share one read through the caches): 5.4 TB/s.
 // One workgroup per (part of a slot, child, layer); every wave works out the child's slot for itself.
 template <typename T> __global__ __launch_bounds__(kCopyThreads) void beam_reorder_kernel(const ReorderArgs a) {
     const int child = blockIdx.y % a.beams, b = blockIdx.y / a.beams;

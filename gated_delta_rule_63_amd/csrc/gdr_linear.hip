@@ -727,7 +727,7 @@ hipError_t scan_tiles(const LinearArgs& a, bool backward, hipStream_t s) {
 //      200 tokens  7.9 / 9.9    8.3 / 11.3   9.1 / 14.8   34.7 / 22.7, backward 10.9 / 11.6 and 50.3 / 48.1
 //      333 tokens 12.3 / 10.4  12.7 / 12.1  13.9 / 21.4   56.5 / 53.9
 //    (fp32 at 65536 channels 20 / 16, 39 / 44, 63 / 62).  Up to 16384 channels only 257 to 512 tokens of up to 4096
-//    come out longer, by 2.7 at most; a call of its own saves more with the launch there (333 x 1024: 11.6 among
+//    come out longer, by 3.1 at most; a call of its own saves more with the launch there (333 x 1024: 11.6 among
 //    others, with a chain 14.4; 512 x 4096: 13.4 / 14.4).
 //  - Chains of large tiles: two channels per lane; 32 tokens per wave in bf16, 16 in fp32 and in the bf16 backward
 //    pass, whose kept values fill the registers.  The fp32 backward pass keeps 8: 16 spill (8192 x 4096: 143, 8
