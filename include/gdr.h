@@ -431,7 +431,8 @@ GDR_API gdr_status gdr_linear_decode_paged(const gdr_linear_problem* p, int32_t 
  * The num_out best are written in descending order; the order is that of the scores in 64 bits,
  * whatever io_dtype.  Equal ones stand by the lower w, those of one beam by the higher logit (where the
  * 64-bit score of a beam with scores[w] = -1e30, say, no longer tells its logits apart), equal logits by
- * the lower v.
+ * the lower v.  (Equal are the 64-bit values: beams of different rows and scores whose candidates differ
+ * by less than the rounding of a 64-bit sum can stand either way.)
  *   - a -inf or NaN logit has probability zero; a row without a finite logit, or with a +inf one, and a
  *     beam whose score is not finite have no candidate above -inf
  *   - an ended beam (finished[w] != 0) has one candidate, (w, eos_token) with its score unchanged
