@@ -577,3 +577,170 @@ gdr_status gdr_beam_reorder(int32_t batch, int32_t beams, const int32_t* parents
 }
 
 }  // extern "C"
+
+// ---- full attention ---------------------------------------------------------------------------
+namespace {
+
+int elem_bytes(int dtype) { return dtype == GDR_BF16 ? 2 : 4; }
+
+bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
+gdr_status check_attn(const gdr_attn_problem* p) {
+    if (!p) return GDR_ERROR_INVALID_VALUE;
+    if (p->total_tokens < 0 || p->num_seqs < 0) return GDR_ERROR_INVALID_VALUE;
+    if (p->num_q_heads <= 0 || p->num_kv_heads <= 0 || p->num_q_heads % p->num_kv_heads != 0) return GDR_ERROR_INVALID_VALUE;
+    if (!dtype_ok(p->io_dtype) || p->head_dim <= 0) return GDR_ERROR_INVALID_VALUE;
+    if (!(p->scale >= -3.0e38f && p->scale <= 3.0e38f)) return GDR_ERROR_INVALID_VALUE;  // NaN fails too
+    if (p->num_seqs == 0 && p->total_tokens > 0) return GDR_ERROR_INVALID_VALUE;
+    if (!head_dim_ok(p->head_dim)) return GDR_ERROR_NOT_SUPPORTED;
+    if (p->num_seqs > 65535 || p->num_q_heads > 65535 || p->total_tokens > 0x7FFFFFFF - 1023) return GDR_ERROR_NOT_SUPPORTED;
+    return GDR_SUCCESS;
+}
+
+// rows of `heads` heads, `stride` elements apart
+bool rows_ok(const gdr_attn_problem* p, const void* t, int heads, int64_t stride) {
+    return aligned16(t) && stride >= (int64_t)heads * p->head_dim && stride <= (INT64_C(1) << 40) &&
+           stride % (16 / elem_bytes(p->io_dtype)) == 0;
+}
+
+int64_t rows_bytes(const gdr_attn_problem* p, int heads, int64_t stride) {
+    return ((p->total_tokens - 1) * stride + (int64_t)heads * p->head_dim) * elem_bytes(p->io_dtype);
+}
+
+bool ranges_meet(const void* a, int64_t na, const void* b, int64_t nb) {
+    if (!a || !b) return false;
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + (uintptr_t)nb && y < x + (uintptr_t)na;
+}
+
+int page_shift(int32_t page_size) {
+    for (int s = 4; s <= 16; ++s)
+        if (page_size == 1 << s) return s;
+    return -1;
+}
+
+gdr_status check_pages(const gdr_attn_problem* p, const gdr_kv_pages* c) {
+    if (!c->k || !c->v || !aligned16(c->k) || !aligned16(c->v)) return GDR_ERROR_INVALID_VALUE;
+    if (c->num_pages <= 0 || c->max_pages < 0 || page_shift(c->page_size) < 0) return GDR_ERROR_INVALID_VALUE;
+    if (p->num_seqs > 0 && c->max_pages > 0 && !c->table) return GDR_ERROR_INVALID_VALUE;
+    // positions in the cache are 32-bit
+    if (((int64_t)c->max_pages << page_shift(c->page_size)) > 0x7FFFFFFF) return GDR_ERROR_NOT_SUPPORTED;
+    return GDR_SUCCESS;
+}
+
+// |scale| log2(e); a zero scale as the smallest normal number, so that a masked score times it stays -inf
+float score_factor(float scale) {
+    const float c = (scale < 0 ? -scale : scale) * 1.4426950408889634f;
+    return c < 1.17549435e-38f ? 1.17549435e-38f : c;
+}
+
+}  // namespace
+
+extern "C" {
+
+gdr_status gdr_rope_append_paged(const gdr_attn_problem* p, const gdr_rotary* r, const void* q, const void* k, const void* v,
+                                 const int32_t* cu_seqlens, const int32_t* context_lens, const gdr_kv_pages* pages,
+                                 void* q_out, void* k_out, void* hip_stream) {
+    gdr_status st = check_attn(p);
+    if (st != GDR_SUCCESS) return st;
+    if (!r) return GDR_ERROR_INVALID_VALUE;
+    if (r->rotary_dim < 0 || r->rotary_dim > p->head_dim || r->rotary_dim % 2 != 0) return GDR_ERROR_INVALID_VALUE;
+    if (r->num_axes < 1 || r->num_axes > 8 || (r->interleaved != 0 && r->interleaved != 1)) return GDR_ERROR_INVALID_VALUE;
+    if (r->rotary_dim > 0 && (!r->inv_freq || (!r->positions && r->num_axes != 1 && p->total_tokens > 0))) return GDR_ERROR_INVALID_VALUE;
+    if (pages && (st = check_pages(p, pages)) != GDR_SUCCESS) return st;
+    if (!cu_seqlens && p->num_seqs != 1 && p->total_tokens != p->num_seqs) return GDR_ERROR_INVALID_VALUE;
+    if (p->num_seqs == 0 || p->total_tokens == 0) return GDR_SUCCESS;
+    const int HQ = p->num_q_heads, HK = p->num_kv_heads;
+    const int64_t dense_q = (int64_t)HQ * p->head_dim, dense_k = (int64_t)HK * p->head_dim;
+    if (!k || (!q) != (!q_out) || (!pages && !k_out)) return GDR_ERROR_INVALID_VALUE;
+    if (!rows_ok(p, k, HK, p->k_stride) || !aligned16(k_out)) return GDR_ERROR_INVALID_VALUE;
+    if (q && (!rows_ok(p, q, HQ, p->q_stride) || !aligned16(q_out))) return GDR_ERROR_INVALID_VALUE;
+    if (pages && (!v || !rows_ok(p, v, HK, p->v_stride))) return GDR_ERROR_INVALID_VALUE;
+    // outputs over inputs: only a dense tensor onto itself, where every thread writes what it alone has read
+    const void* in[3] = {q, k, pages ? v : nullptr};
+    const int64_t size[3] = {rows_bytes(p, HQ, p->q_stride), rows_bytes(p, HK, p->k_stride), rows_bytes(p, HK, p->v_stride)};
+    void* out[2] = {q_out, k_out};
+    const int64_t out_size[2] = {rows_bytes(p, HQ, dense_q), rows_bytes(p, HK, dense_k)};
+    for (int i = 0; i < 2; ++i)
+        for (int j = 0; j < 3; ++j) {
+            const bool itself = i == j && out[i] == in[j] && (i == 0 ? p->q_stride == dense_q : p->k_stride == dense_k);
+            if (!itself && ranges_meet(out[i], out_size[i], in[j], size[j])) return GDR_ERROR_INVALID_VALUE;
+        }
+    if (ranges_meet(q_out, out_size[0], k_out, out_size[1])) return GDR_ERROR_INVALID_VALUE;
+    if ((st = check_device()) != GDR_SUCCESS) return st;
+    gdr::RopeArgs a{};
+    a.q = q; a.k = k; a.v = v;
+    a.q_stride = p->q_stride; a.k_stride = p->k_stride; a.v_stride = p->v_stride;
+    a.cu = cu_seqlens; a.one_token = p->total_tokens == p->num_seqs; a.context = context_lens;
+    a.freq = r->inv_freq; a.positions = r->positions;
+    a.axes = r->num_axes; a.rotary = r->rotary_dim; a.interleaved = r->interleaved;
+    if (pages) {
+        a.k_pages = pages->k; a.v_pages = pages->v; a.table = pages->table;
+        a.num_pages = pages->num_pages; a.max_pages = pages->max_pages; a.page_shift = page_shift(pages->page_size);
+    }
+    a.q_out = q_out; a.k_out = k_out;
+    a.T = p->total_tokens; a.N = p->num_seqs; a.HQ = HQ; a.HK = HK;
+    return status_of(gdr::launch_rope_append(a, p->head_dim, p->io_dtype, static_cast<hipStream_t>(hip_stream)));
+}
+
+gdr_status gdr_attn_prefill_fwd(const gdr_attn_problem* p, const void* q, const void* k, const void* v,
+                                const int32_t* cu_seqlens, void* o, float* lse, void* hip_stream) {
+    gdr_status st = check_attn(p);
+    if (st != GDR_SUCCESS) return st;
+    if (p->num_seqs > 1 && !cu_seqlens) return GDR_ERROR_INVALID_VALUE;
+    if (p->num_seqs == 0 || p->total_tokens == 0) return GDR_SUCCESS;
+    if (!(q && k && v && o) || !aligned16(o)) return GDR_ERROR_INVALID_VALUE;
+    if (!rows_ok(p, q, p->num_q_heads, p->q_stride) || !rows_ok(p, k, p->num_kv_heads, p->k_stride) ||
+        !rows_ok(p, v, p->num_kv_heads, p->v_stride))
+        return GDR_ERROR_INVALID_VALUE;
+    if (gdr::attn_prefill_tiles(p->total_tokens) * p->num_q_heads > 0x7FFFFFFF) return GDR_ERROR_NOT_SUPPORTED;  // grid
+    if ((st = check_device()) != GDR_SUCCESS) return st;
+    gdr::AttnPrefillArgs a{};
+    a.q = q; a.k = k; a.v = v;
+    a.q_stride = p->q_stride; a.k_stride = p->k_stride; a.v_stride = p->v_stride;
+    a.cu = cu_seqlens; a.o = o; a.lse = lse;
+    a.T = p->total_tokens; a.N = p->num_seqs; a.HQ = p->num_q_heads; a.HK = p->num_kv_heads;
+    a.c = score_factor(p->scale); a.negate = p->scale < 0;
+    return status_of(gdr::launch_attn_prefill(a, p->head_dim, p->io_dtype, static_cast<hipStream_t>(hip_stream)));
+}
+
+size_t gdr_attn_workspace_size(const gdr_attn_problem* p, int32_t max_q_len, int32_t num_groups) {
+    if (check_attn(p) != GDR_SUCCESS || max_q_len < 1 || max_q_len > 12) return 0;
+    if (num_groups < 0 || num_groups > 65535 || p->num_seqs == 0 || p->total_tokens == 0) return 0;
+    return gdr::attn_paged_plan(p->total_tokens, p->num_seqs, p->num_q_heads, p->num_kv_heads, p->head_dim, max_q_len,
+                                num_groups).total;
+}
+
+gdr_status gdr_attn_decode_paged(const gdr_attn_problem* p, int32_t max_q_len, const void* q, const int32_t* cu_seqlens,
+                                 const int32_t* context_lens, const gdr_kv_pages* pages, int32_t num_groups,
+                                 const int32_t* group_offsets, const int32_t* prefix_lens, void* o, float* lse,
+                                 void* workspace, size_t workspace_bytes, void* hip_stream) {
+    gdr_status st = check_attn(p);
+    if (st != GDR_SUCCESS) return st;
+    if (max_q_len < 1 || max_q_len > 12 || num_groups < 0 || !pages) return GDR_ERROR_INVALID_VALUE;
+    if ((st = check_pages(p, pages)) != GDR_SUCCESS) return st;
+    if (num_groups > 65535) return GDR_ERROR_NOT_SUPPORTED;
+    if (!cu_seqlens && p->total_tokens != p->num_seqs) return GDR_ERROR_INVALID_VALUE;
+    if (p->total_tokens > (int64_t)p->num_seqs * max_q_len) return GDR_ERROR_INVALID_VALUE;
+    if (p->total_tokens * p->num_q_heads > 0x7FFFFFFF) return GDR_ERROR_NOT_SUPPORTED;
+    if (p->num_seqs == 0 || p->total_tokens == 0) return GDR_SUCCESS;
+    if (!(q && o && context_lens) || !aligned16(o) || !rows_ok(p, q, p->num_q_heads, p->q_stride)) return GDR_ERROR_INVALID_VALUE;
+    if (num_groups > 0 && !(group_offsets && prefix_lens)) return GDR_ERROR_INVALID_VALUE;
+    const gdr::AttnPagedPlan pl = gdr::attn_paged_plan(p->total_tokens, p->num_seqs, p->num_q_heads, p->num_kv_heads,
+                                                       p->head_dim, max_q_len, num_groups);
+    if (!workspace || workspace_bytes < pl.total) return GDR_ERROR_INVALID_VALUE;
+    if (reinterpret_cast<uintptr_t>(workspace) % 256 != 0) return GDR_ERROR_INVALID_VALUE;
+    if ((st = check_device()) != GDR_SUCCESS) return st;
+    gdr::AttnPagedArgs a{};
+    a.q = q; a.q_stride = p->q_stride; a.cu = cu_seqlens; a.context = context_lens;
+    a.k_pages = pages->k; a.v_pages = pages->v; a.table = pages->table;
+    a.num_pages = pages->num_pages; a.max_pages = pages->max_pages; a.page_shift = page_shift(pages->page_size);
+    a.groups = num_groups; a.group_offsets = group_offsets; a.prefix_lens = prefix_lens;
+    a.o = o; a.lse = lse;
+    a.T = p->total_tokens; a.N = p->num_seqs; a.HQ = p->num_q_heads; a.HK = p->num_kv_heads;
+    a.c = score_factor(p->scale); a.negate = p->scale < 0;
+    return status_of(gdr::launch_attn_paged(a, pl, static_cast<char*>(workspace), p->head_dim, p->io_dtype,
+                                            static_cast<hipStream_t>(hip_stream)));
+}
+
+}  // extern "C"

@@ -220,4 +220,81 @@ struct ReorderArgs {
 
 hipError_t launch_beam_reorder(const ReorderArgs& a, hipStream_t stream);
 
+// Rotary positions and the paged cache's new rows (gdr_rope.hip).  Strides in elements from one token's row to the
+// next; q_out, k_out dense.
+struct RopeArgs {
+    const void *q, *k, *v;       // [T, HQ | HK, D] io dtype; q may be NULL, v without pages
+    int64_t q_stride, k_stride, v_stride;
+    const int32_t* cu;           // [N + 1]; NULL: one sequence, or one token per sequence (one_token)
+    bool one_token;
+    const int32_t* context;      // [N]: tokens in the cache before these, negative = padded; NULL: 0
+    const float* freq;           // [axes, rotary / 2]
+    const int32_t* positions;    // [axes, T] or NULL
+    int32_t axes, rotary, interleaved;
+    void *k_pages, *v_pages;     // [num_pages, HK, 1 << page_shift, D] or NULL
+    const int32_t* table;        // [N, max_pages]
+    int32_t num_pages, max_pages, page_shift;
+    void *q_out, *k_out;         // k_out may be NULL
+    int64_t T;
+    int32_t N, HQ, HK;
+    int32_t per;                 // set by the launcher: tokens per workgroup
+};
+
+hipError_t launch_rope_append(RopeArgs a, int D, int io_dtype, hipStream_t stream);
+
+// Attention over packed prompts (gdr_attn.hip).  Strides in elements from one token's row to the next.
+struct AttnPrefillArgs {
+    const void *q, *k, *v;       // [T, HQ | HK, D] io dtype
+    int64_t q_stride, k_stride, v_stride;
+    const int32_t* cu;           // [N + 1], or NULL: one sequence
+    void* o;                     // [T, HQ, D]
+    float* lse;                  // [T, HQ] or NULL
+    int64_t T;
+    int32_t N, HQ, HK;
+    float c;                     // |scale| log2(e), above 0
+    bool negate;                 // scale < 0: the scores' sign is taken into q
+    int32_t tiles;               // set by the launcher
+};
+
+int64_t attn_prefill_tiles(int64_t T);
+hipError_t launch_attn_prefill(AttnPrefillArgs a, int D, int io_dtype, hipStream_t stream);
+
+// Attention against a paged cache (gdr_attn_paged.hip).
+struct AttnPagedArgs {
+    const void* q;               // [T, HQ, D] io dtype
+    int64_t q_stride;            // elements from one token's row to the next
+    const int32_t* cu;           // [N + 1]; NULL: one token per sequence
+    const int32_t* context;      // [N]: tokens before these, negative = padded
+    const void *k_pages, *v_pages;   // [num_pages, HK, 1 << page_shift, D] io dtype
+    const int32_t* table;        // [N, max_pages]
+    int32_t num_pages, max_pages, page_shift;
+    int32_t groups;              // 0: nothing is shared
+    const int32_t* group_offsets;    // [groups + 1]
+    const int32_t* prefix_lens;  // [groups]
+    void* o;                     // [T, HQ, D]
+    float* lse;                  // [T, HQ] or NULL
+    int64_t T;
+    int32_t N, HQ, HK;
+    float c;                     // as AttnPrefillArgs
+    bool negate;
+    // set by the launcher
+    int32_t per;                 // query heads per key head
+    int32_t workers, rows, prefix_rows;   // workgroups; rows of a block of one sequence's, of one group's
+    int64_t capacity;            // tokens a row of the table can hold
+    // workspace, written by the plan kernel: tiles and row blocks before each unit, per key head
+    int64_t *cum, *prefix_cum;
+    int32_t *item, *prefix_item;
+    int32_t *pre, *group;        // [N]: keys read with the group's prefix, the group or -1
+    int32_t *prefix, *rep;       // [groups]: keys of the prefix, the sequence whose pages hold them
+    char *slots, *prefix_slots;  // parts: [rows, D] fp32, maxima, sums
+};
+
+struct AttnPagedPlan {
+    int32_t workers, rows, prefix_rows;
+    size_t cum, item, pre, group, prefix_cum, prefix_item, prefix, rep, slots, prefix_slots, total;
+};
+
+AttnPagedPlan attn_paged_plan(int64_t T, int32_t N, int32_t HQ, int32_t HK, int D, int32_t max_q_len, int32_t groups);
+hipError_t launch_attn_paged(AttnPagedArgs a, const AttnPagedPlan& p, char* ws, int D, int io_dtype, hipStream_t stream);
+
 }  // namespace gdr

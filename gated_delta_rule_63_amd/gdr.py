@@ -10,7 +10,8 @@ Names follow the C entry points: ``gdr_recurrent_fwd``, ``gdr_chunk_fwd``,
 ``gdr_chunk_fwd_noalloc``, ``gdr_chunk_workspace_size``, ``gdr_decode_paged``,
 ``gdr_gating_prepass``, ``gdr_decode_paged_gated``, ``gdr_kda_decode_fused``, ``gdr_linear_scan_fwd``,
 ``gdr_linear_scan_bwd``, ``gdr_linear_decode_paged``, ``gdr_linear_workspace_size``, ``gdr_beam_select``,
-``gdr_beam_workspace_size``, ``gdr_beam_reorder``, ``gdr_status_string``.
+``gdr_beam_workspace_size``, ``gdr_beam_reorder``, ``gdr_rope_append_paged``, ``gdr_attn_prefill_fwd``,
+``gdr_attn_decode_paged``, ``gdr_attn_workspace_size``, ``gdr_status_string``.
 """
 from __future__ import annotations
 
@@ -93,6 +94,42 @@ class BeamProblem(ctypes.Structure):
     ]
 
 
+class AttnProblem(ctypes.Structure):
+    _fields_ = [
+        ("total_tokens", ctypes.c_int64),
+        ("num_seqs", ctypes.c_int32),
+        ("num_q_heads", ctypes.c_int32),
+        ("num_kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+        ("q_stride", ctypes.c_int64),
+        ("k_stride", ctypes.c_int64),
+        ("v_stride", ctypes.c_int64),
+        ("io_dtype", ctypes.c_int),
+    ]
+
+
+class KvPages(ctypes.Structure):
+    _fields_ = [
+        ("k", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("table", ctypes.c_void_p),
+        ("num_pages", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("max_pages", ctypes.c_int32),
+    ]
+
+
+class Rotary(ctypes.Structure):
+    _fields_ = [
+        ("inv_freq", ctypes.c_void_p),
+        ("positions", ctypes.c_void_p),
+        ("rotary_dim", ctypes.c_int32),
+        ("num_axes", ctypes.c_int32),
+        ("interleaved", ctypes.c_int32),
+    ]
+
+
 class Problem(ctypes.Structure):
     _fields_ = [
         ("total_tokens", ctypes.c_int64),
@@ -167,6 +204,15 @@ def lib():
         L.gdr_beam_select.argtypes = [BP, vp, vp, vp, vp, vp, vp, vp, sz, vp]
         L.gdr_beam_reorder.restype = ctypes.c_int
         L.gdr_beam_reorder.argtypes = [i32, i32, vp, vp, vp, vp, i32, i32, i64, vp]
+        AP, KP = ctypes.POINTER(AttnProblem), ctypes.POINTER(KvPages)
+        L.gdr_rope_append_paged.restype = ctypes.c_int
+        L.gdr_rope_append_paged.argtypes = [AP, ctypes.POINTER(Rotary), vp, vp, vp, vp, vp, KP, vp, vp, vp]
+        L.gdr_attn_prefill_fwd.restype = ctypes.c_int
+        L.gdr_attn_prefill_fwd.argtypes = [AP, vp, vp, vp, vp, vp, vp, vp]
+        L.gdr_attn_workspace_size.restype = sz
+        L.gdr_attn_workspace_size.argtypes = [AP, i32, i32]
+        L.gdr_attn_decode_paged.restype = ctypes.c_int
+        L.gdr_attn_decode_paged.argtypes = [AP, i32, vp, vp, vp, KP, i32, vp, vp, vp, vp, vp, sz, vp]
         _lib = L
     return _lib
 
@@ -757,3 +803,184 @@ def gdr_beam_reorder(pool, state_indices, parents, slot_dim: int = 0, state_indi
                                     shape[slot_dim], slot_bytes, raw)
     _raise(st, "gdr_beam_reorder")
     return out
+
+
+# ---------------------------------------------------------------------------
+def _token_rows(t, name: str, heads, dim, dtype, device: int):
+    """(address, elements between tokens) of [T, heads, dim] whose heads are contiguous in a token's row."""
+    if t is None:
+        raise ValueError(f"{name} is required")
+    shape = t.shape
+    if len(shape) != 3 or shape[1] != heads or shape[2] != dim:
+        raise ValueError(f"{name}: expected shape (T, {heads}, {dim}), got {tuple(shape)}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{device}")
+    st, sh, sd = t.stride()
+    if sd != 1 or (sh != dim and heads > 1):
+        raise ValueError(f"{name}: a token's heads must be contiguous")
+    return t.data_ptr(), st if shape[0] > 1 else heads * dim
+
+
+def _attn_problem(q, k, num_seqs: int, scale, kv_heads: int):
+    """(problem with q's stride, device, io dtype, q's address)"""
+    if q.dim() != 3:
+        raise ValueError("q is [T, HQ, D]")
+    if not q.is_cuda:
+        raise ValueError("q must be a device tensor")
+    T, HQ, D = q.shape
+    dev, dtype = q.get_device(), q.dtype
+    if (num_seqs | HQ | kv_heads | D) > _INT32_MAX:
+        _too_large("sequences, heads, channels", num_seqs, HQ, kv_heads, D)
+    pq, sq = _token_rows(q, "q", HQ, D, dtype, dev)
+    if scale is None:
+        scale = 1.0 / math.sqrt(max(D, 1))
+    p = AttnProblem(T, num_seqs, HQ, kv_heads, D, scale, sq, 0, 0, _dtype_code(dtype))
+    return p, dev, dtype, pq
+
+
+def _kv_pages(k_pages, v_pages, page_table, num_seqs: int, heads, dim, dtype, device: int) -> KvPages:
+    if k_pages.dim() != 4:
+        raise ValueError("k_pages is [num_pages, HKV, page_size, D]")
+    n, _, size, _ = k_pages.shape
+    shape = (n, heads, size, dim)
+    if page_table is None or page_table.dim() != 2:
+        raise ValueError("page_table is [N, max_pages]")
+    most = page_table.shape[1]
+    if (n | size | most) > _INT32_MAX:
+        _too_large("pages, page_size, max_pages", n, size, most)
+    return KvPages(_arg(k_pages, "k_pages", shape, dtype, device), _required(v_pages, "v_pages", shape, dtype, device),
+                   _arg(page_table, "page_table", (num_seqs, most), torch.int32, device), n, size, most)
+
+
+def gdr_rope_append_paged(q, k, v=None, inv_freq=None, k_pages=None, v_pages=None, page_table=None, context_lens=None,
+                          cu_seqlens=None, positions=None, interleaved: bool = False, q_out=None, k_out=None,
+                          output_k: bool = True, stream=None):
+    """Rotary positions on q [T, HQ, D] and k [T, HKV, D] (views of a fused projection's rows are taken as they are),
+    k and v written to the cache's pages k_pages, v_pages [num_pages, HKV, page_size, D] through page_table int32
+    [N, max_pages] behind the context_lens int32 [N] tokens that are there (negative = padded).  inv_freq fp32 [R/2],
+    or [axes, R/2] with positions int32 [axes, T]; positions None (one axis): the token's place in its sequence;
+    inv_freq None: no rotation.  Without k_pages nothing is stored.  cu_seqlens None: one token per sequence, or
+    one sequence where context_lens has one entry or is absent.  Returns (q_out, k_out or None); both may be given, and may
+    be q and k where these are dense (in place).  ``output_k=False`` with a cache: k goes there only."""
+    if k.dim() != 3:
+        raise ValueError("k is [T, HKV, D]")
+    T, HK, D = k.shape
+    if cu_seqlens is not None:
+        N = _seqs(cu_seqlens)
+    else:
+        N = context_lens.shape[0] if context_lens is not None else page_table.shape[0] if page_table is not None else 1
+    p, dev, dtype, pq = _attn_problem(q, k, N, 1.0, HK)
+    if q.shape[0] != T:
+        raise ValueError("q and k hold different numbers of tokens")
+    pk, p.k_stride = _token_rows(k, "k", HK, q.shape[2], dtype, dev)
+    pv, pages = None, None
+    if k_pages is not None:
+        pv, p.v_stride = _token_rows(v, "v", HK, D, dtype, dev)
+        if v.shape[0] != T:
+            raise ValueError("v and k hold different numbers of tokens")
+        pages = ctypes.byref(_kv_pages(k_pages, v_pages, page_table, N, HK, D, dtype, dev))
+    f32, i32 = torch.float32, torch.int32
+    if inv_freq is None:
+        r = Rotary(None, None, 0, 1, 1 if interleaved else 0)
+    else:
+        axes = 1 if inv_freq.dim() == 1 else inv_freq.shape[0]
+        half = inv_freq.shape[-1]
+        if inv_freq.dim() not in (1, 2) or (axes | 2 * half) > _INT32_MAX:
+            raise ValueError("inv_freq is [R/2] or [axes, R/2]")
+        pos = None
+        if positions is not None:
+            if positions.dim() == 1 and axes == 1:
+                pos = _arg(positions, "positions", (T,), i32, dev)
+            else:
+                pos = _arg(positions, "positions", (axes, T), i32, dev)
+        r = Rotary(_arg(inv_freq, "inv_freq", inv_freq.shape, f32, dev), pos, 2 * half, axes, 1 if interleaved else 0)
+    with _On(dev, stream) as raw:
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=dtype, device=q.device)
+        if k_out is None and (output_k or k_pages is None):
+            k_out = torch.empty(k.shape, dtype=dtype, device=q.device)
+        st = lib().gdr_rope_append_paged(ctypes.byref(p), ctypes.byref(r), pq, pk, pv,
+                                         _arg(cu_seqlens, "cu_seqlens", (N + 1,), i32, dev),
+                                         _arg(context_lens, "context_lens", (N,), i32, dev), pages,
+                                         _required(q_out, "q_out", q.shape, dtype, dev),
+                                         _arg(k_out, "k_out", k.shape, dtype, dev), raw)
+    _raise(st, "gdr_rope_append_paged")
+    return q_out, k_out
+
+
+def gdr_attn_prefill_fwd(q, k, v, cu_seqlens=None, scale=None, o=None, lse=None, output_lse: bool = False, stream=None):
+    """Causal attention over packed prompts: q [T, HQ, D], k, v [T, HKV, D] (views of a fused projection's rows are
+    taken as they are), cu_seqlens int32 [N+1] (None: one sequence).  scale None: 1/sqrt(D).  Returns o [T, HQ, D], and
+    lse fp32 [T, HQ] as a second where it is asked for or given.  Nothing is recorded for autograd."""
+    if k.dim() != 3:
+        raise ValueError("k is [T, HKV, D]")
+    T, HK, D = k.shape
+    N = _seqs(cu_seqlens)
+    p, dev, dtype, pq = _attn_problem(q, k, N, scale, HK)
+    if q.shape[0] != T or v.shape[0] != T:
+        raise ValueError("q, k and v hold different numbers of tokens")
+    pk, p.k_stride = _token_rows(k, "k", HK, q.shape[2], dtype, dev)
+    pv, p.v_stride = _token_rows(v, "v", HK, q.shape[2], dtype, dev)
+    want_lse = output_lse or lse is not None
+    with _On(dev, stream) as raw:
+        if o is None:
+            o = torch.empty(q.shape, dtype=dtype, device=q.device)
+        if want_lse and lse is None:
+            lse = _rows(T, q.shape[1], torch.float32, dev)
+        st = lib().gdr_attn_prefill_fwd(ctypes.byref(p), pq, pk, pv, _arg(cu_seqlens, "cu_seqlens", (N + 1,), torch.int32, dev),
+                                        _required(o, "o", q.shape, dtype, dev),
+                                        _arg(lse, "lse", (T, q.shape[1]), torch.float32, dev), raw)
+    _raise(st, "gdr_attn_prefill_fwd")
+    return (o, lse) if want_lse else o
+
+
+def gdr_attn_workspace_size(q, k_pages, num_seqs: int, max_q_len: int = 1, num_groups: int = 0) -> int:
+    p = _attn_problem(q, None, num_seqs, 1.0, k_pages.shape[1])[0]
+    return lib().gdr_attn_workspace_size(ctypes.byref(p), max_q_len, num_groups)
+
+
+def gdr_attn_decode_paged(q, k_pages, v_pages, page_table, context_lens, cu_seqlens=None, max_q_len: int = 1,
+                          group_offsets=None, prefix_lens=None, scale=None, o=None, lse=None, output_lse: bool = False,
+                          workspace=None, stream=None):
+    """1..12 tokens of each sequence (q [T, HQ, D]; cu_seqlens int32 [N+1], None: one each) against the paged cache
+    k_pages, v_pages [num_pages, HKV, page_size, D] through page_table int32 [N, max_pages]; the cache holds these
+    tokens already, behind context_lens int32 [N] others (negative = padded).  group_offsets int32 [G+1], prefix_lens
+    int32 [G]: consecutive sequences whose first prefix_lens[g] tokens are the same; their whole pages are read once
+    for the group.  Returns o (rows of padded sequences are left as they were), and lse fp32 [T, HQ] as a second
+    where it is asked for or given.  ``workspace`` is a uint8 device tensor of at least gdr_attn_workspace_size
+    bytes (allocated here if absent)."""
+    if k_pages.dim() != 4:
+        raise ValueError("k_pages is [num_pages, HKV, page_size, D]")
+    if context_lens.dim() != 1:
+        raise ValueError("context_lens is [N]")
+    N, HK, i32 = context_lens.shape[0], k_pages.shape[1], torch.int32
+    p, dev, dtype, pq = _attn_problem(q, None, N, scale, HK)
+    T, HQ, D = q.shape
+    pages = _kv_pages(k_pages, v_pages, page_table, N, HK, D, dtype, dev)
+    groups = 0
+    if group_offsets is not None:
+        if group_offsets.dim() != 1 or group_offsets.shape[0] < 1:
+            raise ValueError("group_offsets is [G + 1]")
+        groups = group_offsets.shape[0] - 1
+        if prefix_lens is None:
+            raise ValueError("prefix_lens is required with group_offsets")
+    if (groups | max_q_len) > _INT32_MAX:
+        _too_large("groups, max_q_len", groups, max_q_len)
+    want_lse = output_lse or lse is not None
+    with _On(dev, stream) as raw:
+        if o is None:
+            o = torch.empty(q.shape, dtype=dtype, device=q.device)
+        if want_lse and lse is None:
+            lse = _rows(T, HQ, torch.float32, dev)
+        ref = ctypes.byref(p)
+        ws, nb, keep = _workspace(workspace, lib().gdr_attn_workspace_size(ref, max_q_len, groups), dev)
+        st = _lib.gdr_attn_decode_paged(ref, max_q_len, pq, _arg(cu_seqlens, "cu_seqlens", (N + 1,), i32, dev),
+                                        _required(context_lens, "context_lens", (N,), i32, dev), ctypes.byref(pages),
+                                        groups, _arg(group_offsets, "group_offsets", (groups + 1,), i32, dev),
+                                        _arg(prefix_lens, "prefix_lens", (groups,), i32, dev),
+                                        _required(o, "o", q.shape, dtype, dev),
+                                        _arg(lse, "lse", (T, HQ), torch.float32, dev), ws, nb, raw)
+    _raise(st, "gdr_attn_decode_paged")
+    return (o, lse) if want_lse else o

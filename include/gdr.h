@@ -485,6 +485,116 @@ GDR_API gdr_status gdr_beam_reorder(int32_t batch, int32_t beams, const int32_t*
                             void* pool, int32_t num_layers, int32_t num_slots, int64_t slot_bytes,
                             void* hip_stream);
 
+/*
+ * Full attention, the layers that hybrid stacks put between delta-rule ones, in serving: the position rotation with
+ * the write of keys and values into a paged cache, attention over whole prompts, and 1..12 tokens per sequence
+ * against the cache.  Query head h attends with key head h / (HQ / HKV):
+ *
+ *     o[t,h] = sum_j p_j v[j,h']       p = softmax over the visible j of  scale q[t,h] . k[j,h']
+ *     lse[t,h] = log sum_j e^(scale q[t,h] . k[j,h'])
+ *
+ * A row that sees nothing has o = 0 and lse = -inf.  What a row does not see has no part in it: infinities and NaN
+ * in the keys and values of other sequences, of later tokens and of the cache's unused rows included.
+ * Scores, the softmax and the sums are held in fp32; with bf16 I/O the weights p are rounded to bf16 (relative to
+ * the row's running maximum) for the product with v, whose products are exact and summed in fp32.
+ *
+ * Layouts: q, o [T, HQ, D], k, v [T, HKV, D] io_dtype.  q, k and v may be views of wider rows (a fused projection's):
+ * a token's heads are contiguous, tokens q_stride, k_stride, v_stride elements apart.  Outputs are dense.  Every
+ * pointer and stride is a multiple of 16 bytes.  cu_seqlens as above, except that cu_seqlens[N] may be less than
+ * T: rows behind the last sequence are neither read nor written.
+ */
+typedef struct gdr_attn_problem {
+    int64_t total_tokens;   /* T <= 2^31 - 1024                                              */
+    int32_t num_seqs;       /* N <= 65535                                                    */
+    int32_t num_q_heads;    /* HQ <= 65535, a multiple of HKV                                */
+    int32_t num_kv_heads;   /* HKV                                                           */
+    int32_t head_dim;       /* D in {64, 128}                                                */
+    float scale;            /* finite; 1/sqrt(D) in the usual setting                        */
+    int64_t q_stride;       /* elements from one token's row to the next, >= HQ D            */
+    int64_t k_stride;       /* >= HKV D                                                      */
+    int64_t v_stride;       /* >= HKV D                                                      */
+    gdr_dtype io_dtype;     /* of q, k, v, o and the cache                                   */
+} gdr_attn_problem;
+
+/*
+ * The cache: token c of sequence n is row c % page_size of page table[n, c / page_size], per key head contiguous.
+ * An entry of the table outside 0..num_pages-1 is no page: what would be there is not stored and not seen, and so
+ * it is with tokens from max_pages * page_size on.
+ */
+typedef struct gdr_kv_pages {
+    void* k;                /* [num_pages, HKV, page_size, D] io_dtype                       */
+    void* v;
+    const int32_t* table;   /* [N, max_pages]                                                */
+    int32_t num_pages;      /* >= 1                                                          */
+    int32_t page_size;      /* a power of two, 16..65536                                     */
+    int32_t max_pages;      /* >= 0                                                          */
+} gdr_kv_pages;
+
+/*
+ * Rotary positions: pair i of R / 2 turns by theta = sum_a position_a inv_freq[a, i] (formed in 64 bits),
+ * (x, y) -> (x cos - y sin, y cos + x sin).  Several axes (time, height, width) are several rows of inv_freq; an
+ * axis that a pair does not follow has 0 there.  Channels from R on are left as they are.
+ */
+typedef struct gdr_rotary {
+    const float* inv_freq;      /* [num_axes, R / 2]; may be NULL when R == 0                */
+    const int32_t* positions;   /* [num_axes, T], or NULL (one axis): the token's place in its sequence */
+    int32_t rotary_dim;         /* R, even, 0..D                                             */
+    int32_t num_axes;           /* 1..8                                                      */
+    int32_t interleaved;        /* 0: pairs (i, i + R/2); 1: pairs (2i, 2i + 1)              */
+} gdr_rotary;
+
+/*
+ * gdr_rope_append_paged -- q and k rotated, k and v written to the cache behind the tokens that are there.
+ *
+ *   cu_seqlens     int32 [N+1]; NULL: one sequence (N == 1) or one token per sequence (T == N)
+ *   context_lens   int32 [N]: tokens in the cache before these (0 for a prompt), NULL: 0.  Token i of sequence n
+ *                  is token context_lens[n] + i of the cache.  Negative: a padded sequence, nothing of it is
+ *                  read or written
+ *   pages          the cache, or NULL: nothing is stored (v is not read)
+ *   q, q_out       NULL together: only k and v.  q_out may be q where q is dense
+ *   k_out          [T, HKV, D] rotated keys for gdr_attn_prefill_fwd, or NULL (with a cache).  May be k where k
+ *                  is dense
+ * Two tokens of one call never share a row of the cache as long as the sequences' pages are their own.
+ */
+GDR_API gdr_status gdr_rope_append_paged(const gdr_attn_problem* p, const gdr_rotary* rotary,
+                                 const void* q, const void* k, const void* v,
+                                 const int32_t* cu_seqlens, const int32_t* context_lens,
+                                 const gdr_kv_pages* pages, void* q_out, void* k_out, void* hip_stream);
+
+/*
+ * gdr_attn_prefill_fwd -- causal attention over packed prompts: a token sees its sequence's tokens up to itself.
+ *
+ *   cu_seqlens     int32 [N+1]; may be NULL only when N == 1 (one sequence of T tokens)
+ *   lse            fp32 [T, HQ] or NULL
+ */
+GDR_API gdr_status gdr_attn_prefill_fwd(const gdr_attn_problem* p, const void* q, const void* k, const void* v,
+                                const int32_t* cu_seqlens, void* o, float* lse, void* hip_stream);
+
+/*
+ * gdr_attn_decode_paged -- 1..12 tokens of each sequence against the cache, which holds them already
+ * (gdr_rope_append_paged): token i of sequence n sees the tokens 0 .. context_lens[n] + i.
+ *
+ *   max_q_len, cu_seqlens   as in gdr_decode_paged
+ *   context_lens   int32 [N]; negative: a padded sequence, skipped, its o and lse rows untouched
+ *   num_groups     0, or the number of groups of consecutive sequences that share a prefix: group g is the sequences
+ *                  group_offsets[g] .. group_offsets[g+1]-1 (int32 [num_groups+1], non-decreasing from 0; sequences
+ *                  behind the last group share nothing), and the first prefix_lens[g] (int32 [num_groups]) tokens of
+ *                  each of them, none of which is longer than its context, are the same.  The whole pages among
+ *                  these are read once for the group, through the table row of its first sequence that is not
+ *                  padded; the rest of every sequence through its own
+ *   lse            fp32 [T, HQ] or NULL
+ *   workspace      gdr_attn_workspace_size bytes, 256-byte aligned, contents need not be initialised; calls that
+ *                  may overlap need one each
+ * p->k_stride and p->v_stride are not used.  T * HQ < 2^31.  The result does not depend on what else is in the
+ * batch by more than the order of fp32 sums.
+ */
+GDR_API size_t gdr_attn_workspace_size(const gdr_attn_problem* p, int32_t max_q_len, int32_t num_groups);
+GDR_API gdr_status gdr_attn_decode_paged(const gdr_attn_problem* p, int32_t max_q_len, const void* q,
+                                 const int32_t* cu_seqlens, const int32_t* context_lens,
+                                 const gdr_kv_pages* pages, int32_t num_groups, const int32_t* group_offsets,
+                                 const int32_t* prefix_lens, void* o, float* lse,
+                                 void* workspace, size_t workspace_bytes, void* hip_stream);
+
 /* Human-readable name of a status code (static string, never NULL; unknown codes map to
  * "GDR_ERROR_UNKNOWN").  The codes stand for the loud contract checks of the pages' entry
  * points: a device-capability check (cuLA PR #113, review thread on SM90 availability) and a
