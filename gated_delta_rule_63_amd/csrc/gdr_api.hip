@@ -599,7 +599,7 @@ gdr_status check_attn(const gdr_attn_problem* p) {
 
 // rows of `heads` heads, `stride` elements apart
 bool rows_ok(const gdr_attn_problem* p, const void* t, int heads, int64_t stride) {
-    return aligned16(t) && stride >= (int64_t)heads * p->head_dim && stride <= (INT64_C(1) << 40) &&
+    return aligned16(t) && stride >= (int64_t)heads * p->head_dim && stride <= (1 << 22) &&
            stride % (16 / elem_bytes(p->io_dtype)) == 0;
 }
 

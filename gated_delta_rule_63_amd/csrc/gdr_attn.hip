@@ -11,15 +11,15 @@
 namespace gdr {
 namespace {
 
-constexpr int kRows = 128, kKeys = 64;
+constexpr int kRows = 128;
 
 template <typename T, int D>
 __global__ __launch_bounds__(256, 2) void attn_prefill_kernel(AttnPrefillArgs a) {
     using L = AttnTile<T, D>;
     using C = AttnCore<T, D>;
-    __shared__ __align__(1024) char lds[2 * kKeys * L::row_bytes];
-    char* const sk = lds;
-    char* const sv = lds + kKeys * L::row_bytes;
+    constexpr int kKeys = L::row_bytes == 512 ? 32 : 64, blocks = kKeys / 32;   // two tiles of K and V fit twice into a CU's LDS
+    constexpr int tile_bytes = kKeys * L::row_bytes;
+    __shared__ __align__(1024) char lds[4 * tile_bytes];
 
     int tile, head;
     {
@@ -48,58 +48,66 @@ __global__ __launch_bounds__(256, 2) void attn_prefill_kernel(AttnPrefillArgs a)
 
     typename C::Q q;
     C::load_q(static_cast<const char*>(a.q) + ((int64_t)tc * a.q_stride + (int64_t)head * D) * L::es, half, a.negate, q);
-    f32x16_t o[D / 32] = {};
-    float m = kNegInf, l = 0.0f;
+    AttnRow<T, D> r;
     const char* const kb = static_cast<const char*>(a.k) + (int64_t)kvh * D * L::es;
     const char* const vb = static_cast<const char*>(a.v) + (int64_t)kvh * D * L::es;
 
+    // the lane's places in a tile's copies; rows behind the last token stand for it (no row sees them)
+    constexpr int per = L::template per<kKeys, 4>();
+    const uint32_t ks = (uint32_t)a.k_stride * L::es, vs = (uint32_t)a.v_stride * L::es;
+    uint32_t ko[per], vo[per];
+    auto places = [&](int last) {
+#pragma unroll
+        for (int i = 0; i < per; ++i) {
+            const int first = 64 * (per * wave + i), row = min(L::copy_row(first, lane), last);
+            ko[i] = row * ks + L::template copy_byte<false>(first, lane);
+            vo[i] = row * vs + L::template copy_byte<true>(first, lane);
+        }
+    };
+    auto stage = [&](int j0, uint32_t to) {
+        if (j0 + kKeys > end) places(end - 1 - j0);
+        const char* const k0 = kb + (int64_t)j0 * a.k_stride * L::es;
+        const char* const v0 = vb + (int64_t)j0 * a.v_stride * L::es;
+#pragma unroll
+        for (int i = 0; i < per; ++i) {
+            copy_to_lds(k0, ko[i], to + 1024 * (per * wave + i));
+            copy_to_lds(v0, vo[i], to + tile_bytes + 1024 * (per * wave + i));
+        }
+    };
+    const uint32_t base = lds_address(lds);
+    places(kKeys - 1);
+    stage(lo, base);
+    typename C::At at(base, base + tile_bytes, lane);
+    uint32_t to = base + 2 * tile_bytes;
     for (int j0 = lo; j0 < hi; j0 += kKeys) {
-        L::template stage<kKeys, 4, false>(sk, wave, lane, [&](int r) { return kb + (int64_t)min(j0 + r, end - 1) * a.k_stride * L::es; });
-        L::template stage<kKeys, 4, true>(sv, wave, lane, [&](int r) { return vb + (int64_t)min(j0 + r, end - 1) * a.v_stride * L::es; });
-        wait_loads();
+        wait_copies();
         __syncthreads();
+        if (j0 + kKeys < hi) stage(j0 + kKeys, to);
         if (j0 < whi && j0 + kKeys > wlo) {
-            f32x16_t s[2] = {C::scores(sk, 0, lane, q), C::scores(sk, 1, lane, q)};
+            f32x16_t s[blocks];
+#pragma unroll
+            for (int b = 0; b < blocks; ++b) s[b] = C::scores(b, at, q);
             if (j0 + kKeys - 1 > wfirst || j0 < wlate) {
 #pragma unroll
-                for (int b = 0; b < 2; ++b)
+                for (int b = 0; b < blocks; ++b)
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         const int j = j0 + 32 * b + key_of(i, half);
                         s[b][i] = j >= start && j <= t ? s[b][i] : kNegInf;
                     }
             }
-            float mx = s[0][0];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) mx = fmaxf(mx, s[i >> 4][i & 15]);
-            const float mn = fmaxf(m, both_max(mx));
-            const float base = mn == kNegInf ? 0.0f : mn * a.c;
-            const float alpha = __builtin_amdgcn_exp2f(m * a.c - base);
-            m = mn;
-            l *= alpha;
-#pragma unroll
-            for (int b = 0; b < D / 32; ++b) o[b] *= alpha;
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                const float p = __builtin_amdgcn_exp2f(fmaf(s[i >> 4][i & 15], a.c, -base));
-                s[i >> 4][i & 15] = p;
-                l += p;
-            }
-            C::accumulate(sv, 0, lane, s[0], o);
-            C::accumulate(sv, 1, lane, s[1], o);
+            r.add(s, a.c, 0, at);
         }
-        __syncthreads();
+        const uint32_t by = to - base == 0 ? (uint32_t)(-2 * tile_bytes) : 2 * tile_bytes;
+        at.move(by);
+        to -= by;
     }
-    l = both_sum(l);
-    const float inv = l > 0.0f ? 1.0f / l : l == 0.0f ? 0.0f : l;
+    const float l = both_sum(r.l), inv = reciprocal_sum(l);
     char* row = t < end ? static_cast<char*>(a.o) + ((int64_t)t * a.HQ + head) * L::row_bytes : nullptr;
 #pragma unroll
-    for (int b = 0; b < D / 32; ++b) {
-        o[b] *= inv;
-        C::store(row, b, half, o[b]);
-    }
-    if (a.lse && t < end && half == 0)
-        a.lse[(int64_t)t * a.HQ + head] = l == 0.0f ? kNegInf : (m * a.c + __builtin_amdgcn_logf(l)) * kLn2;
+    for (int b = 0; b < D / 32; ++b) r.o[b] *= inv;
+    C::store(row, half, r.o);
+    if (a.lse && t < end && half == 0) a.lse[(int64_t)t * a.HQ + head] = log_sum(r.m * a.c, l);
 }
 
 template <typename T, int D>

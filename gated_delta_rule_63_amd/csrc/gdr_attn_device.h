@@ -36,13 +36,18 @@ __device__ __forceinline__ float both_sum(float x) {
     return __uint_as_float(p[0]) + __uint_as_float(p[1]);
 }
 
-__device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
-
-// 16 bytes per lane from global memory to lds + 16 * lane (lds is the wave's)
-__device__ __forceinline__ void copy_to_lds(const char* g, char* lds) {
-    __builtin_amdgcn_global_load_lds((__attribute__((address_space(1))) const void*)(g),
-                                     (__attribute__((address_space(3))) void*)(lds), 16, 0, 0);
+// ---- asynchronous copies to the LDS -------------------------------------------------------------------------
+// 16 bytes per lane from base + off to lds + 16 * lane (base and lds are the wave's).  Written as assembly because
+// the compiler, which cannot tell a tile being filled from the one being read, would otherwise wait for the copies
+// in flight before the first transposing read; nothing is returned in registers, and wait_copies() is the wait
+// that the copies need before a barrier makes them visible.
+typedef __attribute__((address_space(3))) const char lds_char;
+__device__ __forceinline__ uint32_t lds_address(const void* p) { return (uint32_t)(uintptr_t)(lds_char*)(p); }
+__device__ __forceinline__ void copy_to_lds(const char* base, uint32_t off, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
+                 : : "v"(off), "s"(base), "s"(lds) : "memory");
 }
+__device__ __forceinline__ void wait_copies() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
 // sequence of a token below cu[N]: the last n with cu[n] <= t (so an empty sequence is never found)
 __device__ __forceinline__ int find_seq(const int32_t* cu, int N, int t) {
@@ -56,30 +61,24 @@ __device__ __forceinline__ int find_seq(const int32_t* cu, int N, int t) {
 
 // Layout of a staged tile: rows of D elements in 16-byte chunks, chunk c of row r at place c ^ swizzle(r), so that
 // neither the score product's reads (the same chunk of consecutive rows) nor the transposing reads of V (four
-// rows, two chunks each) meet in a bank.  The copy to the LDS writes 64 consecutive places per instruction;
-// the lanes fetch the chunks that belong there.
+// rows, two chunks each) meet in a bank.  A copy writes 64 consecutive places per instruction; the lanes fetch
+// the chunks that belong there.
 template <typename T, int D> struct AttnTile {
     static constexpr int es = Elem<T>::bytes;
     static constexpr int row_bytes = D * es;
     static constexpr int chunks = row_bytes / 16;
     __device__ __forceinline__ static int swz_k(int row) { return row & 7; }
     __device__ __forceinline__ static int swz_v(int row) { return es == 2 ? (row & 3) << 1 : 0; }
-
-    // rows [0, ROWS) of a tile by WAVES waves; at(row) gives a row's address
-    template <int ROWS, int WAVES, bool V, typename F>
-    __device__ __forceinline__ static void stage(char* lds, int wave, int lane, F at) {
-        constexpr int per = ROWS * chunks / 64 / WAVES;
-        static_assert(per * 64 * WAVES == ROWS * chunks, "whole instructions");
-#pragma unroll
-        for (int i = 0; i < per; ++i) {
-            const int first = (wave * per + i) * 64;
-            const int place = first + lane;
-            const int row = place / chunks;
-            const int c = (place % chunks) ^ (V ? swz_v(row) : swz_k(row));
-            copy_to_lds(at(row) + 16 * c, lds + 16 * first);
-        }
+    // instruction i of a wave's copies fills the places 64 (per * wave + i) ..; the lane's row and byte in the row
+    template <int ROWS, int WAVES> static constexpr int per() { return ROWS * chunks / 64 / WAVES; }
+    __device__ __forceinline__ static int copy_row(int first, int lane) { return (first + lane) / chunks; }
+    template <bool V> __device__ __forceinline__ static int copy_byte(int first, int lane) {
+        const int row = copy_row(first, lane);
+        return 16 * (((first + lane) % chunks) ^ (V ? swz_v(row) : swz_k(row)));
     }
 };
+
+__device__ __forceinline__ void hide_int(uint32_t& x) { asm volatile("" : "+v"(x)); }
 
 // ---- products on 32 query rows, 32 keys at a time ---------------------------------------------------------
 // Lane l: query row l % 32, half l / 32.  Score register i of a block is key 8 (i / 4) + 4 half + i % 4.
@@ -101,52 +100,81 @@ template <int D> struct AttnCore<bf16_t, D> {
             q[s] = __builtin_bit_cast(bf16x8_t, w);
         }
     }
-    __device__ __forceinline__ static f32x16_t scores(const char* k, int block, int lane, const Q& q) {
-        const int row = 32 * block + (lane & 31), half = lane >> 5;
+    // Addresses of the lane's reads in a tile.  Steps s and s + 4 are 128 bytes apart under every swizzle, and so are
+    // the channel blocks b and b + 2: four and two registers, the rest is in the instructions' offsets.
+    struct At {
+        uint32_t k[4], v[2];
+        __device__ __forceinline__ void move(uint32_t by) {
+#pragma unroll
+            for (int s = 0; s < 4; ++s) hide_int(k[s] += by);
+#pragma unroll
+            for (int b = 0; b < 2; ++b) hide_int(v[b] += by);
+        }
+        __device__ __forceinline__ At(uint32_t k0, uint32_t v0, int lane) {
+            const int row = lane & 31, half = lane >> 5, grp = lane >> 4, r = (lane >> 2) & 3;
+#pragma unroll
+            for (int s = 0; s < 4; ++s) k[s] = k0 + row * L::row_bytes + 16 * ((2 * s + half) ^ L::swz_k(row));
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+                v[b] = v0 + (4 * (grp >> 1) + r) * L::row_bytes + 16 * ((4 * b + 2 * (grp & 1) + ((lane & 3) >> 1)) ^ L::swz_v(r)) +
+                       8 * (lane & 1);
+        }
+    };
+    __device__ __forceinline__ static f32x16_t scores(int block, const At& at, const Q& q) {
+        typedef __attribute__((address_space(3))) const bf16x8_t lds_v8;
         f32x16_t acc = {};
 #pragma unroll
         for (int s = 0; s < steps; ++s) {
-            const bf16x8_t a = *reinterpret_cast<const bf16x8_t*>(k + row * L::row_bytes + 16 * ((2 * s + half) ^ L::swz_k(row)));
+            const bf16x8_t a = *(lds_v8*)(uintptr_t)(at.k[s & 3] + (128 * (s >> 2) + 32 * block * L::row_bytes));
             acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, q[s], acc, 0, 0, 0);
         }
         return acc;
     }
     // V^T operand: channels 32 b + l % 32, the 16 keys of half-block t of a block, in the scores' order
-    __device__ __forceinline__ static bf16x8_t values(const char* v, int block, int t, int b, int lane) {
+    __device__ __forceinline__ static bf16x8_t values(int block, int t, int b, const At& at) {
         typedef short v4i16 __attribute__((ext_vector_type(4)));
         typedef __attribute__((address_space(3))) v4i16 lds_v4i16;
-        const int grp = lane >> 4, r = (lane >> 2) & 3;
-        const int row = 32 * block + 16 * t + 4 * (grp >> 1) + r;
-        const int c = 4 * b + 2 * (grp & 1) + ((lane & 3) >> 1);
-        const char* p = v + row * L::row_bytes + 16 * (c ^ L::swz_v(r)) + 8 * (lane & 1);
-        const v4i16 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(p));
-        const v4i16 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(p + 8 * L::row_bytes));
+        const uint32_t off = 128 * (b >> 1) + (32 * block + 16 * t) * L::row_bytes;
+        const v4i16 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(uintptr_t)(at.v[b & 1] + off));
+        const v4i16 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(uintptr_t)(at.v[b & 1] + (off + 8 * L::row_bytes)));
         return __builtin_bit_cast(bf16x8_t, s16x8_t{x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]});
     }
-    __device__ __forceinline__ static void accumulate(const char* v, int block, int lane, const f32x16_t& p, f32x16_t* o) {
+    // o += V^T p, with the weights rounded to bf16; their sum takes them as they are, for the sake of lse
+    __device__ __forceinline__ static void accumulate(int block, const At& at, const f32x16_t& p, f32x16_t* o, float& l) {
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-            uint4 w;
-            w.x = pack_bf16x2(p[8 * t + 0], p[8 * t + 1]);
-            w.y = pack_bf16x2(p[8 * t + 2], p[8 * t + 3]);
-            w.z = pack_bf16x2(p[8 * t + 4], p[8 * t + 5]);
-            w.w = pack_bf16x2(p[8 * t + 6], p[8 * t + 7]);
-            const bf16x8_t pb = __builtin_bit_cast(bf16x8_t, w);
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                w[i] = pack_bf16x2(p[8 * t + 2 * i], p[8 * t + 2 * i + 1]);
+                l += p[8 * t + 2 * i] + p[8 * t + 2 * i + 1];
+            }
+            const bf16x8_t pb = __builtin_bit_cast(bf16x8_t, uint4{w[0], w[1], w[2], w[3]});
 #pragma unroll
             for (int b = 0; b < D / 32; ++b)
-                o[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(values(v, block, t, b, lane), pb, o[b], 0, 0, 0);
+                o[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(values(block, t, b, at), pb, o[b], 0, 0, 0);
         }
     }
-    // the lane's 16 values of channels 32 b .. 32 b + 31 (after the exchange 16 half .. + 15 in two runs of eight)
-    __device__ __forceinline__ static void store(char* row, int b, int half, const f32x16_t& o) {
+    // the lane's half of its query row; the halves exchange values so that each writes runs of eight
+    __device__ __forceinline__ static void store(char* row, int half, const f32x16_t* o) {
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
-            uint32_t a0 = pack_bf16x2(o[8 * g + 0], o[8 * g + 1]), a1 = pack_bf16x2(o[8 * g + 2], o[8 * g + 3]);
-            uint32_t b0 = pack_bf16x2(o[8 * g + 4], o[8 * g + 5]), b1 = pack_bf16x2(o[8 * g + 6], o[8 * g + 7]);
-            const auto x = __builtin_amdgcn_permlane32_swap(a0, b0, false, false);
-            const auto y = __builtin_amdgcn_permlane32_swap(a1, b1, false, false);
-            if (row) *reinterpret_cast<uint4*>(row + 64 * b + 32 * g + 16 * half) = uint4{x[0], y[0], x[1], y[1]};
-        }
+        for (int b = 0; b < D / 32; ++b)
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                const uint32_t a0 = pack_bf16x2(o[b][8 * g + 0], o[b][8 * g + 1]), a1 = pack_bf16x2(o[b][8 * g + 2], o[b][8 * g + 3]);
+                const uint32_t b0 = pack_bf16x2(o[b][8 * g + 4], o[b][8 * g + 5]), b1 = pack_bf16x2(o[b][8 * g + 6], o[b][8 * g + 7]);
+                const auto x = __builtin_amdgcn_permlane32_swap(a0, b0, false, false);
+                const auto y = __builtin_amdgcn_permlane32_swap(a1, b1, false, false);
+                if (row) *reinterpret_cast<uint4*>(row + 64 * b + 32 * g + 16 * half) = uint4{x[0], y[0], x[1], y[1]};
+            }
+    }
+    __device__ __forceinline__ static void store_part(float* row, int half, const f32x16_t* o) {
+#pragma unroll
+        for (int b = 0; b < D / 32; ++b)
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+                *reinterpret_cast<f32x4_t*>(row + 32 * b + 8 * g + 4 * half) =
+                    f32x4_t{o[b][4 * g], o[b][4 * g + 1], o[b][4 * g + 2], o[b][4 * g + 3]};
     }
 };
 
@@ -159,35 +187,100 @@ template <int D> struct AttnCore<float, D> {
 #pragma unroll
         for (int s = 0; s < steps; ++s) q[s] = *reinterpret_cast<const f32x4_t*>(row + 16 * (2 * s + half)) * sign;
     }
-    __device__ __forceinline__ static f32x16_t scores(const char* k, int block, int lane, const Q& q) {
-        const int row = 32 * block + (lane & 31), half = lane >> 5;
+    // Row r of channel block b stands for channel (D / 32) r + b, so that a lane's operands of all blocks are
+    // neighbours.
+    static constexpr int nb = D / 32;
+    typedef float vec_t __attribute__((ext_vector_type(nb)));
+    struct At {
+        uint32_t k[4], v;
+        __device__ __forceinline__ void move(uint32_t by) {
+#pragma unroll
+            for (int s = 0; s < 4; ++s) hide_int(k[s] += by);
+            hide_int(v += by);
+        }
+        __device__ __forceinline__ At(uint32_t k0, uint32_t v0, int lane) {
+            const int row = lane & 31, half = lane >> 5;
+#pragma unroll
+            for (int s = 0; s < 4; ++s) k[s] = k0 + row * L::row_bytes + 16 * ((2 * s + half) ^ L::swz_k(row));
+            v = v0 + 4 * half * L::row_bytes + 4 * nb * row;
+        }
+    };
+    __device__ __forceinline__ static f32x16_t scores(int block, const At& at, const Q& q) {
+        typedef __attribute__((address_space(3))) const f32x4_t lds_v4;
         f32x16_t acc = {};
 #pragma unroll
         for (int s = 0; s < steps; ++s) {
-            const f32x4_t a = *reinterpret_cast<const f32x4_t*>(k + row * L::row_bytes + 16 * ((2 * s + half) ^ L::swz_k(row)));
+            const f32x4_t a = *(lds_v4*)(uintptr_t)(at.k[s & 3] + (128 * (s >> 2) + 32 * block * L::row_bytes));
 #pragma unroll
             for (int e = 0; e < 4; ++e) acc = __builtin_amdgcn_mfma_f32_32x32x2f32(a[e], q[s][e], acc, 0, 0, 0);
         }
         return acc;
     }
-    __device__ __forceinline__ static float value(const char* v, int block, int i, int b, int lane) {
-        const int row = 32 * block + key_of(i, lane >> 5);
-        return *reinterpret_cast<const float*>(v + row * L::row_bytes + 4 * (32 * b + (lane & 31)));
+    __device__ __forceinline__ static void accumulate(int block, const At& at, const f32x16_t& p, f32x16_t* o, float& l) {
+        typedef __attribute__((address_space(3))) const vec_t lds_vec;
+        vec_t a[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) a[i] = *(lds_vec*)(uintptr_t)(at.v + (32 * block + key_of(i, 0)) * L::row_bytes);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            l += p[i];
+#pragma unroll
+            for (int b = 0; b < nb; ++b) o[b] = __builtin_amdgcn_mfma_f32_32x32x2f32(a[i][b], p[i], o[b], 0, 0, 0);
+        }
     }
-    __device__ __forceinline__ static void accumulate(const char* v, int block, int lane, const f32x16_t& p, f32x16_t* o) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-#pragma unroll
-            for (int b = 0; b < D / 32; ++b)
-                o[b] = __builtin_amdgcn_mfma_f32_32x32x2f32(value(v, block, i, b, lane), p[i], o[b], 0, 0, 0);
+    __device__ __forceinline__ static void store(char* row, int half, const f32x16_t* o) {
+        if (row) store_part(reinterpret_cast<float*>(row), half, o);
     }
-    __device__ __forceinline__ static void store(char* row, int b, int half, const f32x16_t& o) {
+    __device__ __forceinline__ static void store_part(float* row, int half, const f32x16_t* o) {
 #pragma unroll
-        for (int g = 0; g < 4; ++g)
-            if (row)
-                *reinterpret_cast<f32x4_t*>(row + 128 * b + 32 * g + 16 * half) =
-                    f32x4_t{o[4 * g], o[4 * g + 1], o[4 * g + 2], o[4 * g + 3]};
+        for (int i = 0; i < 16; ++i) {
+            vec_t x;
+#pragma unroll
+            for (int b = 0; b < nb; ++b) x[b] = o[b][i];
+            *reinterpret_cast<vec_t*>(row + nb * key_of(i, half)) = x;
+        }
     }
 };
+
+// ---- running softmax of a wave's 32 rows ----------------------------------------------------------------------
+// Weights are e^(x - m) with x = scale * score and m a running reference: the maximum of the row so far, moved only
+// when a score passes it by more than 2^8 (in which case what is there is rescaled).  The weights stay below 2^8,
+// their sum far from fp32's range, and most tiles leave the output's registers alone.
+constexpr float kSlack = 8.0f;
+
+template <typename T, int D> struct AttnRow {
+    using C = AttnCore<T, D>;
+    f32x16_t o[D / 32] = {};
+    float m = kNegInf;   // of the raw scores
+    float l = 0.0f;      // sum of the lane's weights (its half of the keys)
+
+    // adds NB blocks of scores; first: the first of these blocks in the tile
+    template <int NB>
+    __device__ __forceinline__ void add(f32x16_t (&s)[NB], float c, int first, const typename C::At& at) {
+        float mx = s[0][0];
+#pragma unroll
+        for (int i = 1; i < 16 * NB; ++i) mx = fmaxf(mx, s[i >> 4][i & 15]);
+        mx = both_max(mx);
+        if (__any((mx - m) * c > kSlack || (m == kNegInf && mx > kNegInf))) {
+            const float mn = fmaxf(m, mx);
+            const float alpha = m == kNegInf ? 0.0f : __builtin_amdgcn_exp2f((m - mn) * c);
+            m = mn;
+            l *= alpha;
+#pragma unroll
+            for (int b = 0; b < D / 32; ++b) o[b] *= alpha;
+        }
+        const float base = m == kNegInf ? 0.0f : m * c;
+#pragma unroll
+        for (int i = 0; i < 16 * NB; ++i) s[i >> 4][i & 15] = __builtin_amdgcn_exp2f(fmaf(s[i >> 4][i & 15], c, -base));
+#pragma unroll
+        for (int b = 0; b < NB; ++b) C::accumulate(first + b, at, s[b], o, l);
+    }
+};
+
+// 1 / l; 0 for a row that saw nothing; a NaN stays one
+__device__ __forceinline__ float reciprocal_sum(float l) { return l == 0.0f ? 0.0f : 1.0f / l; }
+__device__ __forceinline__ float log_sum(float base, float l) {
+    return l == 0.0f ? kNegInf : (base + __builtin_amdgcn_logf(l)) * kLn2;
+}
 
 }  // namespace gdr

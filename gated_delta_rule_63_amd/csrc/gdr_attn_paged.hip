@@ -156,12 +156,12 @@ __global__ __launch_bounds__(64 * KW * RW) void attn_paged_kernel(AttnPagedArgs 
     using C = AttnCore<T, D>;
     constexpr int WAVES = KW * RW, blocks = 2 / KW;
     __shared__ __align__(1024) char lds[2 * kKeys * L::row_bytes];
-    char* const sk = lds;
-    char* const sv = lds + kKeys * L::row_bytes;
+    const uint32_t sk = lds_address(lds), sv = sk + kKeys * L::row_bytes;
     __shared__ float xch[KW == 2 ? RW * 64 * 18 : 1];
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), half = lane >> 5;
     const int kw = wave % KW, rw = wave / KW;
+    const typename C::At at_(lds_address(lds), lds_address(lds) + kKeys * L::row_bytes, lane);
     const int64_t* cum = prefix ? a.prefix_cum : a.cum;
     const int* item = prefix ? a.prefix_item : a.item;
     const int units = prefix ? a.groups : a.N;
@@ -190,8 +190,7 @@ __global__ __launch_bounds__(64 * KW * RW) void attn_paged_kernel(AttnPagedArgs 
         const int seen = ctx < 0 ? 0 : (int)min((int64_t)ctx + (token - seq_first(a, seq)) + 1, (int64_t)un.key1);
         typename C::Q q;
         C::load_q(static_cast<const char*>(a.q) + ((int64_t)token * a.q_stride + (int64_t)head * D) * L::es, half, a.negate, q);
-        f32x16_t o[D / 32] = {};
-        float m = kNegInf, l = 0.0f;
+        AttnRow<T, D> acc;
         const int32_t* const table = a.table + (int64_t)un.table * a.max_pages;
 
         for (int ti = first; ti < first + count; ++ti) {
@@ -203,47 +202,37 @@ __global__ __launch_bounds__(64 * KW * RW) void attn_paged_kernel(AttnPagedArgs 
                 return static_cast<const char*>(pages) +
                        ((((int64_t)p * a.HK + kvh) << a.page_shift) + (j & ((1 << a.page_shift) - 1))) * L::row_bytes;
             };
-            L::template stage<kKeys, WAVES, false>(sk, wave, lane, [&](int row) { return at(a.k_pages, row); });
-            L::template stage<kKeys, WAVES, true>(sv, wave, lane, [&](int row) { return at(a.v_pages, row); });
-            wait_loads();
+            constexpr int per = L::template per<kKeys, WAVES>();
+#pragma unroll
+            for (int i = 0; i < per; ++i) {
+                const int f = 64 * (per * wave + i), row = L::copy_row(f, lane);
+                const char* kp = at(a.k_pages, row) + L::template copy_byte<false>(f, lane);
+                const char* vp = at(a.v_pages, row) + L::template copy_byte<true>(f, lane);
+                asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" : : "v"(kp), "s"(sk + 16 * f) : "memory");
+                asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" : : "v"(vp), "s"(sv + 16 * f) : "memory");
+            }
+            wait_copies();
             __syncthreads();
             f32x16_t s[blocks];
-            float mx = kNegInf;
 #pragma unroll
             for (int b = 0; b < blocks; ++b) {
                 const int block = KW == 2 ? kw : b;
-                s[b] = C::scores(sk, block, lane, q);
+                s[b] = C::scores(block, at_, q);
 #pragma unroll
                 for (int g = 0; g < 2; ++g) {
                     const int j16 = j0 + 32 * block + 16 * g;
                     const int p = j16 < un.key1 ? table[j16 >> a.page_shift] : -1;
                     const int lim = p >= 0 && p < a.num_pages ? seen : 0;
 #pragma unroll
-                    for (int i = 8 * g; i < 8 * g + 8; ++i) {
+                    for (int i = 8 * g; i < 8 * g + 8; ++i)
                         s[b][i] = j0 + 32 * block + key_of(i, half) < lim ? s[b][i] : kNegInf;
-                        mx = fmaxf(mx, s[b][i]);
-                    }
                 }
             }
-            const float mn = fmaxf(m, both_max(mx));
-            const float base = mn == kNegInf ? 0.0f : mn * a.c;
-            const float alpha = __builtin_amdgcn_exp2f(m * a.c - base);
-            m = mn;
-            l *= alpha;
-#pragma unroll
-            for (int b = 0; b < D / 32; ++b) o[b] *= alpha;
-#pragma unroll
-            for (int b = 0; b < blocks; ++b) {
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    s[b][i] = __builtin_amdgcn_exp2f(fmaf(s[b][i], a.c, -base));
-                    l += s[b][i];
-                }
-                C::accumulate(sv, KW == 2 ? kw : b, lane, s[b], o);
-            }
+            acc.add(s, a.c, KW == 2 ? kw : 0, at_);
             __syncthreads();
         }
-        l = both_sum(l);
+        float l = both_sum(acc.l), m = acc.m;
+        f32x16_t* const o = acc.o;
         if constexpr (KW == 2) {   // the two waves of a row block: the odd one's part joins the even one's
             float* const mine = xch + rw * 64 * 18 + lane;
             if (kw == 1) { mine[16 * 64] = m; mine[17 * 64] = l; }
@@ -267,21 +256,18 @@ __global__ __launch_bounds__(64 * KW * RW) void attn_paged_kernel(AttnPagedArgs 
         if (kw == 0) {
             if (whole && !a.groups) {
                 const bool store = real && ctx >= 0;
-                const float inv = l > 0.0f ? 1.0f / l : l == 0.0f ? 0.0f : l;
+                const float inv = reciprocal_sum(l);
                 char* row = store ? static_cast<char*>(a.o) + ((int64_t)token * a.HQ + head) * L::row_bytes : nullptr;
 #pragma unroll
-                for (int b = 0; b < D / 32; ++b) {
-                    o[b] *= inv;
-                    C::store(row, b, half, o[b]);
-                }
+                for (int b = 0; b < D / 32; ++b) o[b] *= inv;
+                C::store(row, half, o);
                 if (a.lse && store && half == 0)
-                    a.lse[(int64_t)token * a.HQ + head] = l == 0.0f ? kNegInf : (m * a.c + __builtin_amdgcn_logf(l)) * kLn2;
+                    a.lse[(int64_t)token * a.HQ + head] = log_sum(m * a.c, l);
             } else if (real) {
                 const int64_t slot = whole ? 2 * (int64_t)a.workers + (int64_t)kvh * item[units] + item[u] + rb : open_slot(w, first > 0);
                 float* s = reinterpret_cast<float*>(slots + slot * slot_bytes);
                 const int row = 32 * rw + (lane & 31);
-#pragma unroll
-                for (int b = 0; b < D / 32; ++b) AttnCore<float, D>::store(reinterpret_cast<char*>(s + row * D), b, half, o[b]);
+                C::store_part(s + row * D, half, o);
                 if (half == 0) {
                     s[32 * RW * D + row] = m == kNegInf ? kNegInf : m * a.c;
                     s[32 * RW * D + 32 * RW + row] = l;
@@ -334,10 +320,10 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnPagedArgs a) {
         }
     }
     if (written) return;
-    const float inv = l > 0.0f ? 1.0f / l : l == 0.0f ? 0.0f : l;
+    const float inv = reciprocal_sum(l);
 #pragma unroll
     for (int i = 0; i < V; ++i) Elem<T>::store(a.o, id * D + V * lane + i, o[i] * inv);
-    if (a.lse && lane == 0) a.lse[id] = l == 0.0f ? kNegInf : (m + __builtin_amdgcn_logf(l)) * kLn2;
+    if (a.lse && lane == 0) a.lse[id] = log_sum(m, l);
 }
 
 template <typename T, int D>

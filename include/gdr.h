@@ -499,7 +499,7 @@ GDR_API gdr_status gdr_beam_reorder(int32_t batch, int32_t beams, const int32_t*
  * the row's running maximum) for the product with v, whose products are exact and summed in fp32.
  *
  * Layouts: q, o [T, HQ, D], k, v [T, HKV, D] io_dtype.  q, k and v may be views of wider rows (a fused projection's):
- * a token's heads are contiguous, tokens q_stride, k_stride, v_stride elements apart.  Outputs are dense.  Every
+ * a token's heads are contiguous, tokens q_stride, k_stride, v_stride elements (at most 2^22) apart.  Outputs are dense.  Every
  * pointer and stride is a multiple of 16 bytes.  cu_seqlens as above, except that cu_seqlens[N] may be less than
  * T: rows behind the last sequence are neither read nor written.
  */
