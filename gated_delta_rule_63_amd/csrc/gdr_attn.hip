@@ -20,6 +20,9 @@ __global__ __launch_bounds__(256, 2) void attn_prefill_kernel(AttnPrefillArgs a)
     constexpr int kKeys = L::row_bytes == 512 ? 32 : 64, blocks = kKeys / 32;   // two tiles of K and V fit twice into a CU's LDS
     constexpr int tile_bytes = kKeys * L::row_bytes;
     __shared__ __align__(1024) char lds[4 * tile_bytes];
+    __shared__ uint32_t special_rows[2][2];
+    if (threadIdx.x < 4) special_rows[threadIdx.x >> 1][threadIdx.x & 1] = 0;
+    int turn = 0;
 
     int tile, head;
     {
@@ -44,6 +47,7 @@ __global__ __launch_bounds__(256, 2) void attn_prefill_kernel(AttnPrefillArgs a)
     const int lo = a.cu ? a.cu[find_seq(a.cu, a.N, t0)] : 0;
     const int wlo = __builtin_amdgcn_readfirstlane(start), wfirst = t0 + 32 * wave;
     const int wlate = __builtin_amdgcn_readlane(start, 31);
+    const int latest = a.cu ? a.cu[find_seq(a.cu, a.N, min(t0 + kRows, end) - 1)] : 0;
     const int hi = min(t0 + kRows, end), whi = min(wfirst + 32, end);
 
     typename C::Q q;
@@ -83,20 +87,26 @@ __global__ __launch_bounds__(256, 2) void attn_prefill_kernel(AttnPrefillArgs a)
         wait_copies();
         __syncthreads();
         if (j0 + kKeys < hi) stage(j0 + kKeys, to);
+        uint64_t special = 0;
+        if (j0 + kKeys - 1 > t0 || j0 < latest) {
+            special = take_out_specials<T, D, kKeys, 4>(2 * base + 3 * tile_bytes - to, special_rows, turn, wave, lane);
+            turn ^= 1;
+        }
         if (j0 < whi && j0 + kKeys > wlo) {
             f32x16_t s[blocks];
 #pragma unroll
             for (int b = 0; b < blocks; ++b) s[b] = C::scores(b, at, q);
-            if (j0 + kKeys - 1 > wfirst || j0 < wlate) {
+            auto seen = [&](int j) { return j >= start && j <= t; };
+            if (j0 + kKeys - 1 > wfirst || j0 < wlate)
 #pragma unroll
                 for (int b = 0; b < blocks; ++b)
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const int j = j0 + 32 * b + key_of(i, half);
-                        s[b][i] = j >= start && j <= t ? s[b][i] : kNegInf;
-                    }
-            }
+                    for (int i = 0; i < 16; ++i) s[b][i] = seen(j0 + 32 * b + key_of(i, half)) ? s[b][i] : kNegInf;
             r.add(s, a.c, 0, at);
+            for (; special; special &= special - 1) {
+                const int j = j0 + __builtin_ctzll(special);
+                if (seen(j) && j < end) C::add_specials(vb + (int64_t)j * a.v_stride * L::es, half, r.o);
+            }
         }
         const uint32_t by = to - base == 0 ? (uint32_t)(-2 * tile_bytes) : 2 * tile_bytes;
         at.move(by);

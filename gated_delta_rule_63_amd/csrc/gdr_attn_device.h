@@ -78,6 +78,8 @@ template <typename T, int D> struct AttnTile {
     }
 };
 
+// what is behind is not begun before
+__device__ __forceinline__ void apart() { asm volatile("" ::: "memory"); }
 __device__ __forceinline__ void hide_int(uint32_t& x) { asm volatile("" : "+v"(x)); }
 
 // ---- products on 32 query rows, 32 keys at a time ---------------------------------------------------------
@@ -155,6 +157,27 @@ template <int D> struct AttnCore<bf16_t, D> {
                 o[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(values(block, t, b, at), pb, o[b], 0, 0, 0);
         }
     }
+    // elements of a 32-bit word that are not finite: all bits of theirs
+    __device__ __forceinline__ static uint32_t not_finite(uint32_t w) {
+        const uint32_t m = ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
+        return m | (m - (m >> 15));
+    }
+    // o += the values of a row in global memory that are not finite
+    __device__ __forceinline__ static void add_specials(const char* row, int half, f32x16_t* o) {
+#pragma unroll
+        for (int b = 0; b < D / 32; ++b)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const uint2 w = *reinterpret_cast<const uint2*>(row + 64 * b + 16 * g + 8 * half);
+                const uint32_t x[4] = {w.x << 16, w.x & 0xFFFF0000u, w.y << 16, w.y & 0xFFFF0000u};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float f = __uint_as_float(x[e]);
+                    o[b][4 * g + e] += __builtin_isfinite(f) ? 0.0f : f;
+                }
+                apart();
+            }
+    }
     // the lane's half of its query row; the halves exchange values so that each writes runs of eight
     __device__ __forceinline__ static void store(char* row, int half, const f32x16_t* o) {
 #pragma unroll
@@ -228,6 +251,16 @@ template <int D> struct AttnCore<float, D> {
             for (int b = 0; b < nb; ++b) o[b] = __builtin_amdgcn_mfma_f32_32x32x2f32(a[i][b], p[i], o[b], 0, 0, 0);
         }
     }
+    __device__ __forceinline__ static uint32_t not_finite(uint32_t w) { return (w & 0x7F800000u) == 0x7F800000u ? ~0u : 0u; }
+    __device__ __forceinline__ static void add_specials(const char* row, int half, f32x16_t* o) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const vec_t x = *reinterpret_cast<const vec_t*>(row + 4 * nb * key_of(i, half));
+#pragma unroll
+            for (int b = 0; b < nb; ++b) o[b][i] += __builtin_isfinite(x[b]) ? 0.0f : x[b];
+            apart();
+        }
+    }
     __device__ __forceinline__ static void store(char* row, int half, const f32x16_t* o) {
         if (row) store_part(reinterpret_cast<float*>(row), half, o);
     }
@@ -276,6 +309,33 @@ template <typename T, int D> struct AttnRow {
         for (int b = 0; b < NB; ++b) C::accumulate(first + b, at, s[b], o, l);
     }
 };
+
+// Values that are not finite, in a tile of which some row does not see some key: 0 * inf must not reach that row.
+// Before the tile is used they become 0 in the LDS; the rows that see them then add them as they are.  `rows` holds
+// a bit per key, in two turns: the turn after the next barrier is cleared behind this one's.
+template <typename T, int D, int KEYS, int WAVES>
+__device__ __forceinline__ uint64_t take_out_specials(uint32_t v, uint32_t (*rows)[2], int turn, int wave, int lane) {
+    using L = AttnTile<T, D>;
+    typedef __attribute__((address_space(3))) uint4 lds_u4;
+    constexpr int per = L::template per<KEYS, WAVES>();
+#pragma unroll
+    for (int i = 0; i < per; ++i) {
+        const int first = 64 * (per * wave + i);
+        lds_u4* const p = (lds_u4*)(uintptr_t)(v + 16 * (first + lane));
+        uint4 w{p->x, p->y, p->z, p->w};
+        const uint4 bad{AttnCore<T, D>::not_finite(w.x), AttnCore<T, D>::not_finite(w.y), AttnCore<T, D>::not_finite(w.z),
+                        AttnCore<T, D>::not_finite(w.w)};
+        if (bad.x | bad.y | bad.z | bad.w) {
+            const int row = L::copy_row(first, lane);
+            atomicOr(&rows[turn][row >> 5], 1u << (row & 31));
+            p->x = w.x & ~bad.x; p->y = w.y & ~bad.y; p->z = w.z & ~bad.z; p->w = w.w & ~bad.w;
+        }
+    }
+    __syncthreads();
+    if (threadIdx.x < 2) rows[turn ^ 1][threadIdx.x] = 0;
+    const uint32_t lo = __builtin_amdgcn_readfirstlane(rows[turn][0]), hi = __builtin_amdgcn_readfirstlane(rows[turn][1]);
+    return (uint64_t)hi << 32 | lo;
+}
 
 // 1 / l; 0 for a row that saw nothing; a NaN stays one
 __device__ __forceinline__ float reciprocal_sum(float l) { return l == 0.0f ? 0.0f : 1.0f / l; }

@@ -281,20 +281,21 @@ struct AttnPagedArgs {
     int32_t per;                 // query heads per key head
     int32_t workers, rows, prefix_rows;   // workgroups; rows of a block of one sequence's, of one group's
     int64_t capacity;            // tokens a row of the table can hold
-    // workspace, written by the plan kernel: tiles and row blocks before each unit, per key head
-    int64_t *cum, *prefix_cum;
-    int32_t *item, *prefix_item;
+    // workspace
+    int64_t *start, *prefix_start;   // [N + 1], [groups + 1]: tiles before each unit on the line of a key head
+    int32_t *item, *prefix_item;     // row blocks before each unit
     int32_t *pre, *group;        // [N]: keys read with the group's prefix, the group or -1
     int32_t *prefix, *rep;       // [groups]: keys of the prefix, the sequence whose pages hold them
+    int32_t* first;              // [groups + 1]: the groups' first sequences
     char *slots, *prefix_slots;  // parts: [rows, D] fp32, maxima, sums
 };
 
 struct AttnPagedPlan {
     int32_t workers, rows, prefix_rows;
-    size_t cum, item, pre, group, prefix_cum, prefix_item, prefix, rep, slots, prefix_slots, total;
+    size_t start, item, pre, group, prefix_start, prefix_item, prefix, rep, first, slots, prefix_slots, total;
 };
 
-AttnPagedPlan attn_paged_plan(int64_t T, int32_t N, int32_t HQ, int32_t HK, int D, int32_t max_q_len, int32_t groups);
+AttnPagedPlan attn_paged_plan(int64_t T, int32_t N, int32_t HQ, int32_t HK, int D, int io_bytes, int32_t max_q_len, int32_t groups);
 hipError_t launch_attn_paged(AttnPagedArgs a, const AttnPagedPlan& p, char* ws, int D, int io_dtype, hipStream_t stream);
 
 }  // namespace gdr

@@ -301,3 +301,70 @@ def test_decode_views_of_wider_rows():
     t[:, 3:7] = d["q"]
     d["q"] = t[:, 3:7]
     _decode_check(d)
+
+
+# ---------------------------------------------------------------------------
+# values that are not finite reach the rows that see them, and no others
+def _put(t, w, index, value):
+    t[index] = value
+    w[index] = value
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("D", [64, 128])
+def test_prefill_special_values(D, io):
+    """In a value: that channel of the rows that see it.  In a key or a query: NaN in those rows.  Other sequences,
+    earlier tokens, other heads: as if it were not there."""
+    r = np.random.default_rng(17 + D)
+    lens, HQ, HK = [70, 90, 40, 130], 4, 2
+    cu = np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
+    T = int(cu[-1])
+    (q, qw), (k, kw), (v, vw) = normal(r, (T, HQ, D), io), normal(r, (T, HK, D), io), normal(r, (T, HK, D), io)
+    clean = attn.prefill(qw, kw, vw, cu, 1 / np.sqrt(D))
+    spots = [(75, 0, 3, np.nan), (100, 1, D - 1, np.inf), (100, 0, 0, -np.inf), (159, 0, 7, np.nan), (160, 1, 9, np.inf),
+             (170, 1, 9, -np.inf), (330 - 1, 1, 5, np.nan)]
+    for j, h, c, x in spots:
+        _put(v, vw, (j, h, c), x)
+    o, lse = gdr.gdr_attn_prefill_fwd(q, k, v, cu_seqlens=to_dev(cu), output_lse=True)
+    o, lse, want = f64(o), f64(lse), clean["o"].copy()
+    end = np.repeat(cu[1:], lens)
+    for j, h, c, x in spots:
+        for hh in (2 * h, 2 * h + 1):
+            with np.errstate(invalid="ignore"):
+                want[j:end[j], hh, c] += x
+    check_attention(o, lse, {**clean, "o": want}, io, np.arange(T))
+    # a key and a query
+    _put(k, kw, (80, 1, 2), np.nan)
+    _put(q, qw, (20, 0, 0), np.nan)
+    o, lse = (f64(x) for x in gdr.gdr_attn_prefill_fwd(q, k, v, cu_seqlens=to_dev(cu), output_lse=True))
+    want[80:160, 2:], want[20, 0] = np.nan, np.nan
+    ref = {**clean, "o": want, "lse": clean["lse"].copy()}
+    ref["lse"][80:160, 2:], ref["lse"][20, 0] = np.nan, np.nan
+    check_attention(o, lse, ref, io, np.arange(T))
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("HQ", [2, 8, 16])
+def test_decode_special_values(HQ, D, io):
+    """The cache's unused rows and pages hold NaN; drafted tokens hold values that earlier ones must not feel."""
+    d = _decode_inputs(41 + HQ + D, io, D, HQ, 2, [12, 5, 1, 12, 9], [60, 3, 100, 250, 500], 16)
+    used = np.zeros(d["kw"].shape[0::2][:2], bool)
+    for n, (c, m) in enumerate(zip(d["ctx"], d["lens"])):
+        for j in range(int(c) + m):
+            used[attn.place(d["table"], used.shape[0], 16, n, j)] = True
+    for t, w in ((d["k"], d["kw"]), (d["v"], d["vw"])):
+        t[to_dev(~used)[:, None, :, None].expand(t.shape)] = float("nan")
+        w[np.broadcast_to(~used[:, None, :, None], w.shape)] = np.nan
+    clean = attn.decode(d["qw"], d["cu"], d["ctx"], d["kw"], d["vw"], d["table"], 1 / np.sqrt(D))
+    want, per = clean["o"].copy(), HQ // 2
+    for n, j, h, c, x in [(0, 65, 0, 1, np.nan), (0, 70, 1, D - 1, np.inf), (3, 250, 1, 0, -np.inf), (3, 261, 0, 9, np.inf),
+                          (4, 508, 1, 4, np.nan), (1, 7, 0, 2, np.inf), (4, 100, 1, 8, -np.inf)]:
+        p, row = attn.place(d["table"], used.shape[0], 16, n, j)
+        _put(d["v"], d["vw"], (p, h, row, c), x)
+        for i in range(d["lens"][n]):
+            if j <= d["ctx"][n] + i:
+                with np.errstate(invalid="ignore"):
+                    want[d["cu"][n] + i, h * per:(h + 1) * per, c] += x
+    o, lse = _decode_call(d, output_lse=True)
+    check_attention(f64(o), f64(lse), {**clean, "o": want}, io, np.arange(len(want)))
