@@ -70,8 +70,8 @@ __global__ __launch_bounds__(256, 2) void attn_prefill_kernel(AttnPrefillArgs a)
     };
     auto stage = [&](int j0, uint32_t to) {
         if (j0 + kKeys > end) places(end - 1 - j0);
-        const char* const k0 = kb + (int64_t)j0 * a.k_stride * L::es;
-        const char* const v0 = vb + (int64_t)j0 * a.v_stride * L::es;
+        const char* const k0 = copy_base(kb + (int64_t)j0 * a.k_stride * L::es);
+        const char* const v0 = copy_base(vb + (int64_t)j0 * a.v_stride * L::es);
 #pragma unroll
         for (int i = 0; i < per; ++i) {
             copy_to_lds(k0, ko[i], to + 1024 * (per * wave + i));

@@ -43,7 +43,19 @@ __device__ __forceinline__ float both_sum(float x) {
 // that the copies need before a barrier makes them visible.
 typedef __attribute__((address_space(3))) const char lds_char;
 __device__ __forceinline__ uint32_t lds_address(const void* p) { return (uint32_t)(uintptr_t)(lds_char*)(p); }
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+__device__ __forceinline__ int64_t uniform(int64_t x) {
+    return (int64_t)((uint64_t)(uint32_t)uniform((int)(x >> 32)) << 32 | (uint32_t)uniform((int)x));
+}
+// A base address for copies: in scalar registers, and settled there, should a vector instruction have written them
+// (five wait states, of which the copy has two; the compiler does not look into assembly for this).
+__device__ __forceinline__ const char* copy_base(const char* p) {
+    p = reinterpret_cast<const char*>(uniform((int64_t)reinterpret_cast<uintptr_t>(p)));
+    asm volatile("s_nop 3" : "+s"(p));
+    return p;
+}
 __device__ __forceinline__ void copy_to_lds(const char* base, uint32_t off, uint32_t lds) {
+    lds = (uint32_t)uniform((int)lds);
     asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
                  : : "v"(off), "s"(base), "s"(lds) : "memory");
 }

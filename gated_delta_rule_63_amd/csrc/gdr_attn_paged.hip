@@ -82,16 +82,17 @@ __device__ __forceinline__ Unit unit_of(const AttnPagedArgs& a, int u, int block
     Unit r;
     if (PREFIX) {
         const int s = a.first[u], e = a.first[u + 1];
-        r.tok0 = seq_first(a, s);
-        r.rows = (seq_first(a, e) - r.tok0) * a.per;
         r.key0 = 0;
         r.key1 = a.prefix[u];
+        r.tok0 = seq_first(a, s);
+        r.rows = (seq_first(a, e) - r.tok0) * a.per;
     } else {
+        const int ctx = a.context[u];
+        r.key0 = a.groups ? a.pre[u] : 0;
         r.tok0 = seq_first(a, u);
         const int tokens = seq_first(a, u + 1) - r.tok0;
         r.rows = tokens * a.per;
-        r.key0 = a.groups ? a.pre[u] : 0;
-        r.key1 = keys_of(a, a.context[u], tokens);
+        r.key1 = keys_of(a, ctx, tokens);
     }
     const bool some = r.key1 > r.key0 && r.rows > 0;
     r.tiles = some ? (r.key1 - r.key0 + kKeys - 1) / kKeys : 0;
@@ -170,24 +171,105 @@ __device__ __forceinline__ int find_unit(const AttnPagedArgs& a, int units, int 
         }
         t0 += __shfl(t, 63); n0 += __shfl(n, 63);
     }
-    tiles = t0;
-    items = n0;
-    return __builtin_amdgcn_readfirstlane(u);
+    tiles = uniform(t0);
+    items = uniform(n0);
+    return uniform(u);
 }
 
 // Parts of a unit's row block: the slots they are in.  Workgroup w has one for a block that it goes on with and one for a
 // block that it leaves unfinished; where outputs are joined anyway, a block that it holds whole has one of its own.
 __device__ __forceinline__ int64_t open_slot(int64_t w, bool continued) { return 2 * w + (continued ? 0 : 1); }
 
-// A place on the line: row block `rb` of unit `u` for key head `kvh`, tiles [tile, tile + count) of it.
+// A place on the line: tiles [tile, tile + count) of a unit's row block.
 struct Item {
-    Unit un;
-    int kvh, u, rb, tile, count, items;
-    int64_t tiles;
+    int token0, row0, rows;    // the unit's first token; the block's first row and the unit's rows
+    int key0, key1;            // the unit's keys
+    int table;                 // row of the page table
+    int tile, count, tiles;
+    int kvh;
+    int item;                  // row blocks before it on the line of a key head
+    int unit;
 };
+constexpr int kItems = 64;     // found at a time
+
+// The items of the line from x on, up to xe and kItems of them, by one wave: 64 units at a time.  `next` is where the
+// rest begins.
+template <bool PREFIX, int THREADS>
+__device__ __forceinline__ int find_items(const AttnPagedArgs& a, int units, int block_rows, const Line<THREADS>& line, int64_t x,
+                                          int64_t xe, Item* items, int64_t& next, int64_t* starts, int32_t* item_starts) {
+    const int lane = threadIdx.x & 63;
+    const int64_t tot = line.tiles[THREADS];
+    const int kvh = (int)(x / tot);
+    const int64_t y = x - kvh * tot, ye = min(tot, xe - kvh * tot);   // one key head's line at a time
+    int64_t t0;
+    int n0;
+    const int u = find_unit<PREFIX>(a, units, block_rows, line, y, t0, n0) + lane;
+    Unit un{};
+    if (u < units) un = unit_of<PREFIX>(a, u, block_rows);
+    const int64_t mine = (int64_t)un.tiles * un.blocks;
+    int64_t t = mine;
+    int n = un.blocks;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+        const int64_t tt = __shfl_up(t, d);
+        const int nn = __shfl_up(n, d);
+        if (lane >= d) { t += tt; n += nn; }
+    }
+    const int64_t behind = t0 + t;             // of the lane's unit
+    t = behind - mine;
+    n = n0 + n - un.blocks;
+    const int64_t a0 = max(t, y), a1 = min(behind, ye);   // the unit's tiles in the stretch
+    const int rb0 = a0 < a1 ? (int)((a0 - t) / un.tiles) : 0, rb1 = a0 < a1 ? (int)((a1 - t - 1) / un.tiles) : -1;
+    int count = rb1 - rb0 + 1, at = count;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+        const int c = __shfl_up(at, d);
+        if (lane >= d) at += c;
+    }
+    const int all = __shfl(at, 63);
+    at -= count;
+    if (count > 0) {
+        int table = u;
+        if (PREFIX) table = a.rep[u];
+        for (int rb = rb0; rb <= rb1 && at + rb - rb0 < kItems; ++rb) {
+            const int64_t r = t + (int64_t)rb * un.tiles;
+            Item it;
+            it.token0 = un.tok0; it.row0 = rb * block_rows; it.rows = un.rows;
+            it.key0 = un.key0; it.key1 = un.key1; it.table = table;
+            it.tile = (int)(max(r, y) - r);
+            it.count = (int)(min(r + un.tiles, ye) - r) - it.tile;
+            it.tiles = un.tiles; it.kvh = kvh; it.item = n + rb;
+            it.unit = u;
+            items[at + rb - rb0] = it;
+        }
+        // whoever begins a unit tells the last kernel where it is on the line
+        if (kvh == 0 && t >= y) { starts[u] = t; item_starts[u] = n; }
+    }
+    // behind the last unit looked at, or the first item that there was no room for
+    int64_t end = min(ye, (int64_t)__shfl(behind, 63));
+    if (all > kItems) {
+        const bool cut = count > 0 && at <= kItems && at + count > kItems;
+        const uint64_t who = __ballot(cut);
+        const int k = __builtin_ctzll(who);
+        const int64_t from = t + (int64_t)(rb0 + kItems - at) * un.tiles;
+        end = __shfl(from, k);
+    }
+    next = kvh * tot + end;
+    return min(all, kItems);
+}
+
+// an item that every lane holds alike, in scalar registers
+__device__ __forceinline__ Item same(const Item& it) {
+    Item r;
+    r.token0 = uniform(it.token0); r.row0 = uniform(it.row0); r.rows = uniform(it.rows);
+    r.key0 = uniform(it.key0); r.key1 = uniform(it.key1); r.table = uniform(it.table);
+    r.tile = uniform(it.tile); r.count = uniform(it.count); r.tiles = uniform(it.tiles);
+    r.kvh = uniform(it.kvh); r.item = uniform(it.item); r.unit = uniform(it.unit);
+    return r;
+}
 
 template <typename T, int D, int KW, int RW, bool PREFIX>
-__global__ __launch_bounds__(64 * KW * RW) void attn_paged_kernel(AttnPagedArgs a) {
+__global__ __launch_bounds__(64 * KW * RW, 2) void attn_paged_kernel(AttnPagedArgs a) {
     using L = AttnTile<T, D>;
     using C = AttnCore<T, D>;
     constexpr int WAVES = KW * RW, THREADS = 64 * WAVES, blocks = 2 / KW, block_rows = 32 * RW;
@@ -195,49 +277,37 @@ __global__ __launch_bounds__(64 * KW * RW) void attn_paged_kernel(AttnPagedArgs 
     __shared__ __align__(1024) char lds[4 * tile_bytes];
     __shared__ float xch[KW == 2 ? RW * 64 * 18 : 1];
     __shared__ Line<THREADS> line;
+    __shared__ Item items[kItems];
+    __shared__ int64_t rest;
+    __shared__ int found;
     __shared__ uint32_t special_rows[2][2];
 
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), half = lane >> 5;
+    const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6), half = lane >> 5;
     const int kw = wave % KW, rw = wave / KW;
     const int units = PREFIX ? a.groups : a.N;
     char* const slots = PREFIX ? a.prefix_slots : a.slots;
     int64_t* const starts = PREFIX ? a.prefix_start : a.start;
     int32_t* const item_starts = PREFIX ? a.prefix_item : a.item;
     constexpr int64_t slot_bytes = (int64_t)block_rows * (D + 2) * 4;
-    const int64_t w = blockIdx.x;
+    const int w = blockIdx.x;
     if (threadIdx.x < 4) special_rows[threadIdx.x >> 1][threadIdx.x & 1] = 0;
     int turn = 0;
 
     sum_up<PREFIX>(a, units, block_rows, line);
-    const int64_t tot = line.tiles[THREADS], all = tot * a.HK, per = stretch(a, all);
-    const int all_items = line.items[THREADS];
-    if (w == 0 && threadIdx.x == 0) { starts[units] = tot; item_starts[units] = all_items; }
-    int64_t x = w * per;
-    const int64_t xe = min(x + per, all);
-    if (x >= xe) return;
+    if (w == 0 && threadIdx.x == 0) { starts[units] = line.tiles[THREADS]; item_starts[units] = line.items[THREADS]; }
+    if (!PREFIX && threadIdx.x == 0) a.open[w].parts = 0;
 
-    auto item_at = [&](int64_t x) {
-        Item it;
-        it.kvh = (int)(x / tot);
-        const int64_t y = x - it.kvh * tot;
-        it.u = find_unit<PREFIX>(a, units, block_rows, line, y, it.tiles, it.items);
-        it.un = unit_of<PREFIX>(a, it.u, block_rows);
-        const int inside = (int)(y - it.tiles);
-        it.rb = __builtin_amdgcn_readfirstlane(inside / it.un.tiles);
-        it.tile = __builtin_amdgcn_readfirstlane(inside % it.un.tiles);
-        it.count = (int)min((int64_t)(it.un.tiles - it.tile), xe - x);
-        it.un.key0 = __builtin_amdgcn_readfirstlane(it.un.key0);
-        it.un.key1 = __builtin_amdgcn_readfirstlane(it.un.key1);
-        it.kvh = __builtin_amdgcn_readfirstlane(it.kvh);
-        return it;
-    };
-    auto table_of = [&](const Item& it) {
-        const int n = PREFIX ? __builtin_amdgcn_readfirstlane(a.rep[it.u]) : it.u;
-        return a.table + (int64_t)n * a.max_pages;
-    };
-    auto page_at = [&](const int32_t* table, int j) {
-        const int p = uniform_load(table + (j >> a.page_shift));
-        return p >= 0 && p < a.num_pages ? p : -1;
+    // pages of a tile's four runs of 16 keys; -1: none
+    struct Pages { int p[4]; };
+    auto pages_of = [&](int row, int j0, int key1) {
+        const int32_t* const table = a.table + (int64_t)row * a.max_pages;
+        int p[4];
+#pragma unroll
+        for (int g = 0; g < 4; ++g) p[g] = uniform_load(table + (min(j0 + 16 * g, key1 - 1) >> a.page_shift));
+        Pages r;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) r.p[g] = j0 + 16 * g < key1 && p[g] >= 0 && p[g] < a.num_pages ? p[g] : -1;
+        return r;
     };
 
     // the lane's places in the copies of 16 rows
@@ -250,14 +320,16 @@ __global__ __launch_bounds__(64 * KW * RW) void attn_paged_kernel(AttnPagedArgs 
         vo[i] = row + L::template copy_byte<true>(64 * i, lane);
     }
     const uint32_t base = lds_address(lds);
-    auto stage = [&](const Item& it, const int32_t* table, int tile, uint32_t to) {
+    auto stage = [&](const Pages& pages, int kvh, int j0, int key1, uint32_t to) {
 #pragma unroll
         for (int g = 0; g < groups16; ++g) {
-            const int r0 = 16 * (groups16 * wave + g), j = it.un.key0 + tile * kKeys + r0, last = it.un.key1 - 1 - j;
-            const int p = last >= 0 ? page_at(table, j) : -1;
-            const int64_t off = ((((int64_t)p * a.HK + it.kvh) << a.page_shift) + (j & ((1 << a.page_shift) - 1))) * L::row_bytes;
-            const char* const k = p >= 0 ? static_cast<const char*>(a.k_pages) + off : zero_rows;
-            const char* const v = p >= 0 ? static_cast<const char*>(a.v_pages) + off : zero_rows;
+            const int r0 = 16 * (groups16 * wave + g), j = j0 + r0, last = key1 - 1 - j;
+            int p = pages.p[g];
+            if constexpr (WAVES == 2) p = wave ? pages.p[2 + g] : p;
+            else p = wave == 0 ? p : wave == 1 ? pages.p[1] : wave == 2 ? pages.p[2] : pages.p[3];
+            const int64_t off = ((((int64_t)p * a.HK + kvh) << a.page_shift) + (j & ((1 << a.page_shift) - 1))) * L::row_bytes;
+            const char* const k = copy_base(p >= 0 ? static_cast<const char*>(a.k_pages) + off : zero_rows);
+            const char* const v = copy_base(p >= 0 ? static_cast<const char*>(a.v_pages) + off : zero_rows);
             const uint32_t dst = to + r0 * L::row_bytes;
             if (last >= 15 || p < 0) {
 #pragma unroll
@@ -276,154 +348,153 @@ __global__ __launch_bounds__(64 * KW * RW) void attn_paged_kernel(AttnPagedArgs 
         }
     };
 
-    Item it = item_at(x);
-    const int32_t* table = table_of(it);
     uint32_t to = base;
-    stage(it, table, it.tile, to);
     typename C::At at(base, base + tile_bytes, lane);
-    while (true) {
-        // the lane's row
-        const int r = it.rb * block_rows + 32 * rw + (lane & 31);
-        const bool real = r < it.un.rows;
-        const int rc = min(r, it.un.rows - 1), token = it.un.tok0 + rc / a.per, head = it.kvh * a.per + rc % a.per;
-        const int seq = !PREFIX ? it.u : a.cu ? find_seq(a.cu, a.N, token) : token;
-        const int ctx = a.context[seq];
-        const int seen = ctx < 0 ? 0 : (int)min((int64_t)ctx + (token - seq_first(a, seq)) + 1, (int64_t)it.un.key1);
-        typename C::Q q;
-        C::load_q(static_cast<const char*>(a.q) + ((int64_t)token * a.q_stride + (int64_t)head * D) * L::es, half, a.negate, q);
-        AttnRow<T, D> acc;
-        x += it.count;
-        const bool more = x < xe;
-        Item next;
-        const int32_t* next_table = nullptr;
-        if (more) {
-            next = item_at(x);
-            next_table = table_of(next);
+    const int64_t all = line.tiles[THREADS] * a.HK, per = stretch(a, all);
+    const int64_t xe = min((w + 1) * per, all);
+    for (int64_t x0 = w * per; x0 < xe; x0 = rest) {
+        if (wave == 0) {
+            int64_t next;
+            const int n = find_items<PREFIX>(a, units, block_rows, line, x0, xe, items, next, starts, item_starts);
+            if (lane == 0) { found = n; rest = next; }
         }
-        const int end = it.tile + it.count;
-        for (int tile = it.tile; tile < end; ++tile) {
-            wait_copies();
-            __syncthreads();
-            const uint32_t v = to + tile_bytes;
-            to = 2 * base + 2 * tile_bytes - to;
-            if (tile + 1 < end) stage(it, table, tile + 1, to);
-            else if (more) stage(next, next_table, next.tile, to);
+        __syncthreads();
+        const int n_items = uniform(found);
+        {
+            const Item it = same(items[0]);
+            const int j0 = it.key0 + it.tile * kKeys;
+            stage(pages_of(it.table, j0, it.key1), it.kvh, j0, it.key1, to);
+        }
+        for (int i = 0; i < n_items; ++i) {
+            const Item it = same(items[i]), next = same(items[min(i + 1, n_items - 1)]);
+            const bool more = i + 1 < n_items;
+            Pages now = pages_of(it.table, it.key0 + it.tile * kKeys, it.key1);
+            // the lane's row
+            const int r = it.row0 + 32 * rw + (lane & 31);
+            const bool real = r < it.rows;
+            const int rc = min(r, it.rows - 1), token = it.token0 + rc / a.per, head = it.kvh * a.per + rc % a.per;
+            const int seq = !PREFIX ? it.unit : a.cu ? find_seq(a.cu, a.N, token) : token;
+            const int ctx = a.context[seq];
+            const int seen = ctx < 0 ? 0 : (int)min((int64_t)ctx + (token - seq_first(a, seq)) + 1, (int64_t)it.key1);
+            typename C::Q q;
+            C::load_q(static_cast<const char*>(a.q) + ((int64_t)token * a.q_stride + (int64_t)head * D) * L::es, half, a.negate, q);
+            AttnRow<T, D> acc;
+            const int end = it.tile + it.count;
+            for (int tile = it.tile; tile < end; ++tile) {
+                // the next tile's pages, read while this one's copies are waited for
+                const bool inside = tile + 1 < end;
+                const int key1 = inside ? it.key1 : next.key1, kvh = inside ? it.kvh : next.kvh;
+                const int ahead0 = inside ? it.key0 + (tile + 1) * kKeys : next.key0 + next.tile * kKeys;
+                const Pages ahead = pages_of(inside ? it.table : next.table, ahead0, key1);
+                wait_copies();
+                __syncthreads();
+                const uint32_t v = to + tile_bytes;
+                to = 2 * base + 2 * tile_bytes - to;
+                if (inside || more) stage(ahead, kvh, ahead0, key1, to);
 
-            const int j0 = it.un.key0 + tile * kKeys;
-            // tokens see less than the last of theirs: some rows do not see what others do
-            uint64_t special = 0;
-            if (!PREFIX && it.un.rows > a.per && j0 + kKeys > it.un.key1 - it.un.rows / a.per + 1) {
-                special = take_out_specials<T, D, kKeys, WAVES>(v, special_rows, turn, wave, lane);
-                turn ^= 1;
-            }
-            f32x16_t s[blocks];
+                const int j0 = it.key0 + tile * kKeys;
+                // tokens see less than the last of theirs: some rows do not see what others do
+                uint64_t special = 0;
+                if (!PREFIX && it.rows > a.per && j0 + kKeys > it.key1 - it.rows / a.per + 1) {
+                    special = take_out_specials<T, D, kKeys, WAVES>(v, special_rows, turn, wave, lane);
+                    turn ^= 1;
+                }
+                f32x16_t s[blocks];
 #pragma unroll
-            for (int b = 0; b < blocks; ++b) s[b] = C::scores(KW == 2 ? kw : b, at, q);
-            int pages = 0;   // bit g: keys 16 g .. 16 g + 15 of the tile are in the cache
+                for (int b = 0; b < blocks; ++b) s[b] = C::scores(KW == 2 ? kw : b, at, q);
+                int pages = 0;   // bit g: keys 16 g .. 16 g + 15 of the tile are in the cache
 #pragma unroll
-            for (int g = 0; g < 4; ++g)
-                if (j0 + 16 * g < it.un.key1 && page_at(table, j0 + 16 * g) >= 0) pages |= 1 << g;
-            if (pages != 15 || !__all(seen >= j0 + kKeys)) {
+                for (int g = 0; g < 4; ++g) pages |= (now.p[g] >= 0) << g;
+                if (pages != 15 || !__all(seen >= j0 + kKeys)) {
 #pragma unroll
-                for (int b = 0; b < blocks; ++b)
+                    for (int b = 0; b < blocks; ++b)
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const int k = 32 * (KW == 2 ? kw : b) + key_of(i, half);
-                        s[b][i] = j0 + k < seen && (pages >> (k >> 4) & 1) ? s[b][i] : kNegInf;
+                        for (int i = 0; i < 16; ++i) {
+                            const int k = 32 * (KW == 2 ? kw : b) + key_of(i, half);
+                            s[b][i] = j0 + k < seen && (pages >> (k >> 4) & 1) ? s[b][i] : kNegInf;
+                        }
+                }
+                acc.add(s, a.c, KW == 2 ? kw : 0, at);
+                for (; special; special &= special - 1) {
+                    const int k = __builtin_ctzll(special), j = j0 + k;
+                    if ((KW == 1 || k / 32 == kw) && j < seen) {
+                        const int p = k < 16 ? now.p[0] : k < 32 ? now.p[1] : k < 48 ? now.p[2] : now.p[3];
+                        if (p >= 0)
+                            C::add_specials(static_cast<const char*>(a.v_pages) +
+                                            ((((int64_t)p * a.HK + it.kvh) << a.page_shift) + (j & ((1 << a.page_shift) - 1))) * L::row_bytes,
+                                            half, acc.o);
                     }
-            }
-            acc.add(s, a.c, KW == 2 ? kw : 0, at);
-            for (; special; special &= special - 1) {
-                const int k = __builtin_ctzll(special), j = j0 + k;
-                if ((KW == 1 || k / 32 == kw) && j < seen) {
-                    const int p = page_at(table, j);
-                    if (p >= 0)
-                        C::add_specials(static_cast<const char*>(a.v_pages) +
-                                        ((((int64_t)p * a.HK + it.kvh) << a.page_shift) + (j & ((1 << a.page_shift) - 1))) * L::row_bytes,
-                                        half, acc.o);
                 }
+                at.move(to == base ? (uint32_t)(-2 * tile_bytes) : 2 * tile_bytes);
+                now = ahead;
             }
-            at.move(to == base ? (uint32_t)(-2 * tile_bytes) : 2 * tile_bytes);
-        }
 
-        const bool whole = it.count == it.un.tiles;
-        float l = both_sum(acc.l), m = acc.m;
-        f32x16_t* const o = acc.o;
-        if constexpr (KW == 2) {   // the two waves of a row block: the odd one's part joins the even one's
-            float* const mine = xch + rw * 64 * 18 + lane;
-            if (kw == 1) { mine[16 * 64] = m; mine[17 * 64] = l; }
+            const bool whole = it.count == it.tiles;
+            float l = both_sum(acc.l), m = acc.m;
+            f32x16_t* const o = acc.o;
+            if constexpr (KW == 2) {   // the two waves of a row block: the odd one's part joins the even one's
+                float* const mine = xch + rw * 64 * 18 + lane;
+                if (kw == 1) { mine[16 * 64] = m; mine[17 * 64] = l; }
 #pragma unroll
-            for (int b = 0; b < D / 32; ++b) {
-                if (kw == 1)
+                for (int b = 0; b < D / 32; ++b) {
+                    if (kw == 1)
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) mine[i * 64] = o[b][i];
-                __syncthreads();
-                if (kw == 0) {
-                    const float m1 = mine[16 * 64], l1 = mine[17 * 64], mn = fmaxf(m, m1);
-                    const float e0 = m == kNegInf ? 0.0f : __builtin_amdgcn_exp2f((m - mn) * a.c);
-                    const float e1 = m1 == kNegInf ? 0.0f : __builtin_amdgcn_exp2f((m1 - mn) * a.c);
+                        for (int i = 0; i < 16; ++i) mine[i * 64] = o[b][i];
+                    __syncthreads();
+                    if (kw == 0) {
+                        const float m1 = mine[16 * 64], l1 = mine[17 * 64], mn = fmaxf(m, m1);
+                        const float e0 = m == kNegInf ? 0.0f : __builtin_amdgcn_exp2f((m - mn) * a.c);
+                        const float e1 = m1 == kNegInf ? 0.0f : __builtin_amdgcn_exp2f((m1 - mn) * a.c);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) o[b][i] = o[b][i] * e0 + mine[i * 64] * e1;
-                    if (b == D / 32 - 1) { l = l * e0 + l1 * e1; m = mn; }
-                }
-                __syncthreads();
-            }
-        }
-        if (kw == 0) {
-            if (whole && !a.groups) {
-                const bool store = real && ctx >= 0;
-                const float inv = reciprocal_sum(l);
-                char* row = store ? static_cast<char*>(a.o) + ((int64_t)token * a.HQ + head) * L::row_bytes : nullptr;
-#pragma unroll
-                for (int b = 0; b < D / 32; ++b) o[b] *= inv;
-                C::store(row, half, o);
-                if (a.lse && store && half == 0) a.lse[(int64_t)token * a.HQ + head] = log_sum(m * a.c, l);
-            } else if (real) {
-                const int64_t slot = whole ? 2 * (int64_t)a.workers + (int64_t)it.kvh * all_items + it.items + it.rb : open_slot(w, it.tile > 0);
-                float* s = reinterpret_cast<float*>(slots + slot * slot_bytes);
-                const int row = 32 * rw + (lane & 31);
-                C::store_part(s + row * D, half, o);
-                if (half == 0) {
-                    s[block_rows * D + row] = m == kNegInf ? kNegInf : m * a.c;
-                    s[block_rows * D + block_rows + row] = l;
+                        for (int i = 0; i < 16; ++i) o[b][i] = o[b][i] * e0 + mine[i * 64] * e1;
+                        if (b == D / 32 - 1) { l = l * e0 + l1 * e1; m = mn; }
+                    }
+                    __syncthreads();
                 }
             }
+            if (kw == 0) {
+                if (whole && !a.groups) {
+                    const bool store = real && ctx >= 0;
+                    const float inv = reciprocal_sum(l);
+                    char* row = store ? static_cast<char*>(a.o) + ((int64_t)token * a.HQ + head) * L::row_bytes : nullptr;
+#pragma unroll
+                    for (int b = 0; b < D / 32; ++b) o[b] *= inv;
+                    C::store(row, half, o);
+                    if (a.lse && store && half == 0) a.lse[(int64_t)token * a.HQ + head] = log_sum(m * a.c, l);
+                } else if (real) {
+                    const int64_t slot = whole ? 2 * (int64_t)a.workers + (int64_t)it.kvh * line.items[THREADS] + it.item : open_slot(w, it.tile > 0);
+                    float* s = reinterpret_cast<float*>(slots + slot * slot_bytes);
+                    const int row = 32 * rw + (lane & 31);
+                    C::store_part(s + row * D, half, o);
+                    if (half == 0) {
+                        s[block_rows * D + row] = m == kNegInf ? kNegInf : m * a.c;
+                        s[block_rows * D + block_rows + row] = l;
+                    }
+                }
+            }
+            // the block that it leaves unfinished, for the last kernel
+            const int left = it.tiles - it.count;
+            if (!PREFIX && it.tile == 0 && left > 0 && threadIdx.x == 0)
+                a.open[w] = AttnOpen{it.token0, it.row0, min(block_rows, it.rows - it.row0), it.kvh, 1 + (int)((left + per - 1) / per)};
         }
-        // whoever begins a unit tells the last kernel where it is on the line
-        if (it.kvh == 0 && it.rb == 0 && it.tile == 0 && threadIdx.x == 0) { starts[it.u] = it.tiles; item_starts[it.u] = it.items; }
-        if (!more) break;
-        it = next;
-        table = next_table;
+        __syncthreads();   // before the next items are found
     }
 }
 
-// One wave per (token, query head): its parts joined.  A lane reads the maximum and the sum of one part, then all read
-// the rows.
-template <typename T, int D>
-__global__ __launch_bounds__(256) void attn_join_kernel(AttnPagedArgs a) {
-    constexpr int V = D / 64;
-    const int lane = threadIdx.x & 63;
-    const int64_t id = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    if (id >= a.T * a.HQ) return;
-    const int token = __builtin_amdgcn_readfirstlane((int)(id / a.HQ)), head = __builtin_amdgcn_readfirstlane((int)(id % a.HQ));
-    if (a.cu && token >= a.cu[a.N]) return;
-    const int seq = a.cu ? find_seq(a.cu, a.N, token) : token;
-    if (a.context[seq] < 0) return;
-    const int kvh = head / a.per, hh = head % a.per;
+// Parts of a row, joined by one wave: a lane reads the maximum and the sum of one part, then all read the rows.
+template <int D> struct Joined {
+    static constexpr int V = D / 64;
     float m = kNegInf, l = 0.0f, o[V] = {};
-    auto side = [&](const Unit& un, int u, int units, int rows, const int64_t* starts, const int32_t* items, const char* slots) {
-        if (un.tiles <= 0) return true;
-        const int64_t slot_bytes = (int64_t)rows * (D + 2) * 4, tot = starts[units], per = stretch(a, tot * a.HK);
-        const int r = (token - un.tok0) * a.per + hh, rb = r / rows, row = r % rows;
-        const int64_t x0 = kvh * tot + starts[u] + (int64_t)rb * un.tiles, w0 = x0 / per, w1 = (x0 + un.tiles - 1) / per;
-        if (w0 == w1 && !a.groups) return false;   // written already
-        for (int64_t wa = w0; wa <= w1; wa += 64) {
-            const int n = (int)min((int64_t)64, w1 - wa + 1);
+    // parts k = 0 .. n - 1 of row `row`, in slots of `rows` rows at slots + slot_of(k) * size of a slot
+    template <typename F> __device__ __forceinline__ void add(const char* slots, int rows, int row, int parts, F slot_of) {
+        const int lane = threadIdx.x & 63;
+        const int64_t slot_bytes = (int64_t)rows * (D + 2) * 4;
+        for (int k0 = 0; k0 < parts; k0 += 64) {
+            const int n = min(64, parts - k0);
             int64_t at = 0;
             float m1 = kNegInf, l1 = 0.0f;
             if (lane < n) {
-                const int64_t w = wa + lane;
-                at = (w0 == w1 ? 2 * (int64_t)a.workers + (int64_t)kvh * items[units] + items[u] + rb : open_slot(w, w > w0)) * slot_bytes;
+                at = slot_of(k0 + lane) * slot_bytes;
                 const float* s = reinterpret_cast<const float*>(slots + at);
                 m1 = s[rows * D + row];
                 l1 = s[rows * D + rows + row];
@@ -449,7 +520,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnPagedArgs a) {
                     const int k = min(p + q, n - 1);
                     const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)at, k), hi = __builtin_amdgcn_readlane((uint32_t)(at >> 32), k);
                     const float* s = reinterpret_cast<const float*>(slots + ((int64_t)hi << 32 | lo)) + row * D + V * lane;
-                    f[q] = p + q < n ? __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(e), k)) : 0.0f;
+                    f[q] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(e), k));
 #pragma unroll
                     for (int i = 0; i < V; ++i) y[q][i] = s[i];
                 }
@@ -459,15 +530,64 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnPagedArgs a) {
                     for (int i = 0; i < V; ++i) o[i] += p + q < n ? y[q][i] * f[q] : 0.0f;
             }
         }
-        return true;
-    };
-    if (!side(unit_of<false>(a, seq, a.rows), seq, a.N, a.rows, a.start, a.item, a.slots)) return;
-    if (a.groups && a.group[seq] >= 0)
-        side(unit_of<true>(a, a.group[seq], a.prefix_rows), a.group[seq], a.groups, a.prefix_rows, a.prefix_start, a.prefix_item, a.prefix_slots);
-    const float inv = reciprocal_sum(l);
+    }
+    template <typename T> __device__ __forceinline__ void store(const AttnPagedArgs& a, int token, int head) {
+        const int lane = threadIdx.x & 63;
+        const int64_t id = (int64_t)token * a.HQ + head;
+        const float inv = reciprocal_sum(l);
 #pragma unroll
-    for (int i = 0; i < V; ++i) Elem<T>::store(a.o, id * D + V * lane + i, o[i] * inv);
-    if (a.lse && lane == 0) a.lse[id] = log_sum(m, l);
+        for (int i = 0; i < V; ++i) Elem<T>::store(a.o, id * D + V * lane + i, o[i] * inv);
+        if (a.lse && lane == 0) a.lse[id] = log_sum(m, l);
+    }
+};
+
+// Without prefixes: a workgroup for every block of rows that a stretch has left unfinished, and the rows that see
+// nothing (of sequences without a page's room), which no tile belongs to.
+template <typename T, int D>
+__global__ __launch_bounds__(256) void attn_join_kernel(AttnPagedArgs a) {
+    const int w = blockIdx.x, wave = blockIdx.y * 4 + (threadIdx.x >> 6);
+    if (w < a.workers) {
+        const AttnOpen x = a.open[w];
+        for (int r = wave; x.parts && r < x.rows; r += 4 * gridDim.y) {
+            Joined<D> j;
+            j.add(a.slots, a.rows, r, x.parts, [&](int k) { return open_slot(w + k, k > 0); });
+            const int row = x.row0 + r;
+            j.template store<T>(a, x.token0 + row / a.per, x.kvh * a.per + row % a.per);
+        }
+        return;
+    }
+    // capacity 0: every row
+    const int64_t waves = 4 * (int64_t)gridDim.y, step = waves * (gridDim.x - a.workers);
+    for (int64_t id = (w - a.workers) * waves + wave; id < a.T * a.HQ; id += step) {
+        const int token = (int)(id / a.HQ);
+        if ((a.cu && token >= a.cu[a.N]) || a.context[a.cu ? find_seq(a.cu, a.N, token) : token] < 0) continue;
+        Joined<D>().template store<T>(a, token, (int)(id % a.HQ));
+    }
+}
+
+// With prefixes: one wave per (token, query head); parts of the prefix and of the sequence's own keys.
+template <typename T, int D>
+__global__ __launch_bounds__(256) void attn_join_groups_kernel(AttnPagedArgs a) {
+    const int64_t id = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (id >= a.T * a.HQ) return;
+    const int token = __builtin_amdgcn_readfirstlane((int)(id / a.HQ)), head = __builtin_amdgcn_readfirstlane((int)(id % a.HQ));
+    if (a.cu && token >= uniform_load(a.cu + a.N)) return;
+    const int seq = a.cu ? __builtin_amdgcn_readfirstlane(find_seq(a.cu, a.N, token)) : token;
+    if (uniform_load(a.context + seq) < 0) return;
+    const int kvh = head / a.per, hh = head % a.per, group = uniform_load(a.group + seq);
+    Joined<D> j;
+    auto side = [&](const Unit& un, int u, int units, int rows, const int64_t* starts, const int32_t* items, const char* slots) {
+        if (un.tiles <= 0) return;
+        const int64_t tot = starts[units], start = starts[u], per = stretch(a, tot * a.HK);
+        const int r = (token - un.tok0) * a.per + hh, rb = r / rows;
+        const int64_t x0 = kvh * tot + start + (int64_t)rb * un.tiles, w0 = x0 / per, w1 = (x0 + un.tiles - 1) / per;
+        const int64_t own = 2 * (int64_t)a.workers + (int64_t)kvh * items[units] + items[u] + rb;
+        j.add(slots, rows, r % rows, (int)(w1 - w0 + 1), [&](int k) { return w0 == w1 ? own : open_slot(w0 + k, k > 0); });
+    };
+    if (group >= 0)
+        side(unit_of<true>(a, group, a.prefix_rows), group, a.groups, a.prefix_rows, a.prefix_start, a.prefix_item, a.prefix_slots);
+    side(unit_of<false>(a, seq, a.rows), seq, a.N, a.rows, a.start, a.item, a.slots);
+    j.template store<T>(a, token, head);
 }
 
 template <typename T, int D, bool PREFIX>
@@ -488,7 +608,8 @@ hipError_t launch(const AttnPagedArgs& a, hipStream_t stream) {
     }
     if (e == hipSuccess) e = launch_part<T, D, false>(a, a.rows, stream);
     if (e != hipSuccess) return e;
-    attn_join_kernel<T, D><<<dim3((unsigned)((a.T * a.HQ + 3) / 4)), 256, 0, stream>>>(a);
+    if (a.groups) attn_join_groups_kernel<T, D><<<dim3((unsigned)((a.T * a.HQ + 3) / 4)), 256, 0, stream>>>(a);
+    else attn_join_kernel<T, D><<<dim3((unsigned)(a.workers + (a.capacity == 0 ? 256 : 0)), (unsigned)(a.rows / 16)), 256, 0, stream>>>(a);
     return hipGetLastError();
 }
 
@@ -523,6 +644,7 @@ AttnPagedPlan attn_paged_plan(int64_t T, int32_t N, int32_t HQ, int32_t HK, int 
         p.first = take((size_t)(groups + 1) * 4);
         p.prefix_slots = take(slots(p.prefix_rows, groups));
     }
+    p.open = take((size_t)p.workers * sizeof(AttnOpen));
     p.slots = take(slots(p.rows, N));
     p.total = at;
     return p;
@@ -541,6 +663,7 @@ hipError_t launch_attn_paged(AttnPagedArgs a, const AttnPagedPlan& p, char* ws, 
     a.prefix = reinterpret_cast<int32_t*>(ws + p.prefix);
     a.rep = reinterpret_cast<int32_t*>(ws + p.rep);
     a.first = reinterpret_cast<int32_t*>(ws + p.first);
+    a.open = reinterpret_cast<AttnOpen*>(ws + p.open);
     a.slots = ws + p.slots;
     a.prefix_slots = ws + p.prefix_slots;
     if (io_dtype == 1) return D == 64 ? launch<bf16_t, 64>(a, stream) : launch<bf16_t, 128>(a, stream);

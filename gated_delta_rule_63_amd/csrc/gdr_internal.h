@@ -260,6 +260,11 @@ int64_t attn_prefill_tiles(int64_t T);
 hipError_t launch_attn_prefill(AttnPrefillArgs a, int D, int io_dtype, hipStream_t stream);
 
 // Attention against a paged cache (gdr_attn_paged.hip).
+struct AttnOpen {                // the block of rows that a workgroup has begun and left unfinished
+    int32_t token0, row0, rows, kvh;
+    int32_t parts;               // 0: none
+};
+
 struct AttnPagedArgs {
     const void* q;               // [T, HQ, D] io dtype
     int64_t q_stride;            // elements from one token's row to the next
@@ -287,12 +292,13 @@ struct AttnPagedArgs {
     int32_t *pre, *group;        // [N]: keys read with the group's prefix, the group or -1
     int32_t *prefix, *rep;       // [groups]: keys of the prefix, the sequence whose pages hold them
     int32_t* first;              // [groups + 1]: the groups' first sequences
+    AttnOpen* open;              // [workers]
     char *slots, *prefix_slots;  // parts: [rows, D] fp32, maxima, sums
 };
 
 struct AttnPagedPlan {
     int32_t workers, rows, prefix_rows;
-    size_t start, item, pre, group, prefix_start, prefix_item, prefix, rep, first, slots, prefix_slots, total;
+    size_t start, item, pre, group, prefix_start, prefix_item, prefix, rep, first, open, slots, prefix_slots, total;
 };
 
 AttnPagedPlan attn_paged_plan(int64_t T, int32_t N, int32_t HQ, int32_t HK, int D, int io_bytes, int32_t max_q_len, int32_t groups);
