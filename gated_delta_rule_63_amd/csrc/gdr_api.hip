@@ -723,6 +723,11 @@ gdr_status gdr_attn_decode_paged(const gdr_attn_problem* p, int32_t max_q_len, c
     if (!cu_seqlens && p->total_tokens != p->num_seqs) return GDR_ERROR_INVALID_VALUE;
     if (p->total_tokens > (int64_t)p->num_seqs * max_q_len) return GDR_ERROR_INVALID_VALUE;
     if (p->total_tokens * p->num_q_heads > 0x7FFFFFFF) return GDR_ERROR_NOT_SUPPORTED;
+    {   // tiles of 64 keys are counted in 32 bits, over all sequences and their blocks of 32 rows
+        const int64_t tiles = (((int64_t)pages->max_pages << page_shift(pages->page_size)) + 63) / 64 + 1;
+        const int64_t blocks = ((int64_t)(p->num_q_heads / p->num_kv_heads) * max_q_len + 31) / 32;
+        if (tiles * blocks > 0x7FFFFFFF / (p->num_seqs > 0 ? p->num_seqs : 1)) return GDR_ERROR_NOT_SUPPORTED;
+    }
     if (p->num_seqs == 0 || p->total_tokens == 0) return GDR_SUCCESS;
     if (!(q && o && context_lens) || !aligned16(o) || !rows_ok(p, q, p->num_q_heads, p->q_stride)) return GDR_ERROR_INVALID_VALUE;
     if (num_groups > 0 && !(group_offsets && prefix_lens)) return GDR_ERROR_INVALID_VALUE;

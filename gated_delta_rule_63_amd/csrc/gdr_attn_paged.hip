@@ -37,7 +37,7 @@ __device__ __forceinline__ int keys_of(const AttnPagedArgs& a, int ctx, int toke
 }
 
 __device__ __forceinline__ int64_t stretch(const AttnPagedArgs& a, int64_t tiles) {
-    return max((tiles + a.workers - 1) / a.workers, (int64_t)kMinTiles);
+    return max((tiles + a.workers - 1) >> a.worker_bits, (int64_t)kMinTiles);
 }
 
 // One wave per group: the first sequence that is not padded gives the pages, whole pages are shared.  The wave behind
@@ -100,80 +100,81 @@ __device__ __forceinline__ Unit unit_of(const AttnPagedArgs& a, int u, int block
     return r;
 }
 
-// The line of tiles of one key head: sums before every THREADS-th part of the units, in the LDS.
+// inclusive sum over the lanes of a wave
+template <int CTRL, int ROWS, bool ZERO> __device__ __forceinline__ int dpp_add(int x) {
+    return x + __builtin_amdgcn_update_dpp(0, x, CTRL, ROWS, 0xF, ZERO);
+}
+__device__ __forceinline__ int wave_scan(int x) {
+    x = dpp_add<0x111, 0xF, true>(x);    // row_shr 1, 2, 4, 8: within rows of 16 lanes
+    x = dpp_add<0x112, 0xF, true>(x);
+    x = dpp_add<0x114, 0xF, true>(x);
+    x = dpp_add<0x118, 0xF, true>(x);
+    x = dpp_add<0x142, 0xA, false>(x);   // row 0's total to row 1, row 2's to row 3
+    x = dpp_add<0x143, 0xC, false>(x);   // that of rows 0 and 1 to rows 2 and 3
+    return x;
+}
+__device__ __forceinline__ int lane_value(int x, int lane) { return __builtin_amdgcn_readlane(x, lane); }
+
+// The line of tiles of one key head (below 2^31: the host sees to it): sums before every THREADS-th part of the units,
+// in the LDS.
 template <int THREADS> struct Line {
-    int64_t tiles[THREADS + 1];
+    int tiles[THREADS + 1];
     int items[THREADS + 1];      // row blocks
-    int64_t wave_tiles[THREADS / 64];
-    int wave_items[THREADS / 64];
+    int wave_tiles[THREADS / 64], wave_items[THREADS / 64];
 };
 
+// units: of THREADS units at most, what they are, for find_items
 template <bool PREFIX, int THREADS>
-__device__ __forceinline__ void sum_up(const AttnPagedArgs& a, int units, int block_rows, Line<THREADS>& line) {
+__device__ __forceinline__ void sum_up(const AttnPagedArgs& a, int units, int block_rows, Line<THREADS>& line, Unit* cache) {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int run = (units + THREADS - 1) / THREADS, u0 = min(tid * run, units), u1 = min(u0 + run, units);
-    int64_t t = 0;
-    int n = 0;
+    int t = 0, n = 0;
+    Unit x{};
     for (int u = u0; u < u1; ++u) {
-        const Unit x = unit_of<PREFIX>(a, u, block_rows);
-        t += (int64_t)x.tiles * x.blocks;
+        x = unit_of<PREFIX>(a, u, block_rows);
+        t += x.tiles * x.blocks;
         n += x.blocks;
     }
-    const int64_t mine = t;
-    const int mine_n = n;
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-        const int64_t tt = __shfl_up(t, d);
-        const int nn = __shfl_up(n, d);
-        if (lane >= d) { t += tt; n += nn; }
-    }
-    if (lane == 63) { line.wave_tiles[wave] = t; line.wave_items[wave] = n; }
+    cache[tid] = x;
+    int tiles = wave_scan(t), items = wave_scan(n);
+    if (lane == 63) { line.wave_tiles[wave] = tiles; line.wave_items[wave] = items; }
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < THREADS / 64; ++w)
-        if (w < wave) { t += line.wave_tiles[w]; n += line.wave_items[w]; }
-    line.tiles[tid] = t - mine;
-    line.items[tid] = n - mine_n;
-    if (tid == THREADS - 1) { line.tiles[THREADS] = t; line.items[THREADS] = n; }
+        if (w < wave) { tiles += line.wave_tiles[w]; items += line.wave_items[w]; }
+    line.tiles[tid] = tiles - t;   // before the thread's units
+    line.items[tid] = items - n;
+    if (tid == THREADS - 1) { line.tiles[THREADS] = tiles; line.items[THREADS] = items; }
     __syncthreads();
 }
 
 // the unit that tile y of the line is in, and the tiles and row blocks before it
 template <bool PREFIX, int THREADS>
-__device__ __forceinline__ int find_unit(const AttnPagedArgs& a, int units, int block_rows, const Line<THREADS>& line, int64_t y,
-                                         int64_t& tiles, int& items) {
+__device__ __forceinline__ int find_unit(const AttnPagedArgs& a, int units, int block_rows, const Line<THREADS>& line, int y,
+                                         int& tiles, int& items) {
     const int lane = threadIdx.x & 63, run = (units + THREADS - 1) / THREADS;
     int part = -1;
 #pragma unroll
     for (int i = 0; i < THREADS / 64; ++i) part += __popcll(__ballot(line.tiles[64 * i + lane] <= y));
-    part = __builtin_amdgcn_readfirstlane(part);
-    int64_t t0 = line.tiles[part];
-    int n0 = line.items[part], u = part * run;
+    int t0 = uniform(line.tiles[part]), n0 = uniform(line.items[part]), u = part * run;
     for (int u0 = part * run; run > 1; u0 += 64) {
         Unit x{};
         if (u0 + lane < min((part + 1) * run, units)) x = unit_of<PREFIX>(a, u0 + lane, block_rows);
-        const int64_t mine = (int64_t)x.tiles * x.blocks;
-        int64_t t = mine;
-        int n = x.blocks;
-#pragma unroll
-        for (int d = 1; d < 64; d *= 2) {
-            const int64_t tt = __shfl_up(t, d);
-            const int nn = __shfl_up(n, d);
-            if (lane >= d) { t += tt; n += nn; }
-        }
+        const int mine = x.tiles * x.blocks, t = wave_scan(mine), n = wave_scan(x.blocks);
         const uint64_t here = __ballot(t0 + t - mine <= y && y < t0 + t);
-        const int k = here ? __builtin_ctzll(here) : 63;
-        const int64_t before = t0 + __shfl(t, k) - __shfl(mine, k);
-        const int before_n = n0 + __shfl(n, k) - __shfl(x.blocks, k);
         if (here || u0 + 64 >= (part + 1) * run) {   // the second never without the first
-            t0 = before; n0 = before_n; u = u0 + k;
+            const int k = here ? __builtin_ctzll(here) : 63;
+            t0 += lane_value(t - mine, k);
+            n0 += lane_value(n - x.blocks, k);
+            u = u0 + k;
             break;
         }
-        t0 += __shfl(t, 63); n0 += __shfl(n, 63);
+        t0 += lane_value(t, 63);
+        n0 += lane_value(n, 63);
     }
-    tiles = uniform(t0);
-    items = uniform(n0);
-    return uniform(u);
+    tiles = t0;
+    items = n0;
+    return u;
 }
 
 // Parts of a unit's row block: the slots they are in.  Workgroup w has one for a block that it goes on with and one for a
@@ -195,49 +196,37 @@ constexpr int kItems = 64;     // found at a time
 // The items of the line from x on, up to xe and kItems of them, by one wave: 64 units at a time.  `next` is where the
 // rest begins.
 template <bool PREFIX, int THREADS>
-__device__ __forceinline__ int find_items(const AttnPagedArgs& a, int units, int block_rows, const Line<THREADS>& line, int64_t x,
-                                          int64_t xe, Item* items, int64_t& next, int64_t* starts, int32_t* item_starts) {
+__device__ __forceinline__ int find_items(const AttnPagedArgs& a, int units, int block_rows, const Line<THREADS>& line,
+                                          const Unit* cache, int64_t x, int64_t xe, Item* items, int64_t& next, int64_t* starts,
+                                          int32_t* item_starts) {
     const int lane = threadIdx.x & 63;
-    const int64_t tot = line.tiles[THREADS];
-    const int kvh = (int)(x / tot);
-    const int64_t y = x - kvh * tot, ye = min(tot, xe - kvh * tot);   // one key head's line at a time
-    int64_t t0;
-    int n0;
+    const int tot = uniform(line.tiles[THREADS]);
+    // x / tot: both below 2^53, the quotient a number of heads
+    int kvh = (int)((double)x / (double)tot);
+    if ((int64_t)kvh * tot > x) --kvh;
+    if ((int64_t)(kvh + 1) * tot <= x) ++kvh;
+    const int64_t line0 = (int64_t)kvh * tot;
+    const int y = (int)(x - line0), ye = (int)min((int64_t)tot, xe - line0);   // one key head's line at a time
+    int t0, n0;
     const int u = find_unit<PREFIX>(a, units, block_rows, line, y, t0, n0) + lane;
     Unit un{};
-    if (u < units) un = unit_of<PREFIX>(a, u, block_rows);
-    const int64_t mine = (int64_t)un.tiles * un.blocks;
-    int64_t t = mine;
-    int n = un.blocks;
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-        const int64_t tt = __shfl_up(t, d);
-        const int nn = __shfl_up(n, d);
-        if (lane >= d) { t += tt; n += nn; }
-    }
-    const int64_t behind = t0 + t;             // of the lane's unit
-    t = behind - mine;
-    n = n0 + n - un.blocks;
-    const int64_t a0 = max(t, y), a1 = min(behind, ye);   // the unit's tiles in the stretch
-    const int rb0 = a0 < a1 ? (int)((a0 - t) / un.tiles) : 0, rb1 = a0 < a1 ? (int)((a1 - t - 1) / un.tiles) : -1;
-    int count = rb1 - rb0 + 1, at = count;
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-        const int c = __shfl_up(at, d);
-        if (lane >= d) at += c;
-    }
-    const int all = __shfl(at, 63);
-    at -= count;
+    if (u < units) un = cache ? cache[u] : unit_of<PREFIX>(a, u, block_rows);
+    const int mine = un.tiles * un.blocks;
+    const int behind = t0 + wave_scan(mine), t = behind - mine;   // behind and before the lane's unit
+    const int n = n0 + wave_scan(un.blocks) - un.blocks;
+    const int a0 = max(t, y), a1 = min(behind, ye);               // the unit's tiles in the stretch
+    const int rb0 = a0 < a1 ? (a0 - t) / un.tiles : 0, rb1 = a0 < a1 ? (a1 - t - 1) / un.tiles : -1;
+    const int count = rb1 - rb0 + 1, upto = wave_scan(count), at = upto - count, all = lane_value(upto, 63);
     if (count > 0) {
         int table = u;
         if (PREFIX) table = a.rep[u];
         for (int rb = rb0; rb <= rb1 && at + rb - rb0 < kItems; ++rb) {
-            const int64_t r = t + (int64_t)rb * un.tiles;
+            const int r = t + rb * un.tiles;
             Item it;
             it.token0 = un.tok0; it.row0 = rb * block_rows; it.rows = un.rows;
             it.key0 = un.key0; it.key1 = un.key1; it.table = table;
-            it.tile = (int)(max(r, y) - r);
-            it.count = (int)(min(r + un.tiles, ye) - r) - it.tile;
+            it.tile = max(r, y) - r;
+            it.count = min(r + un.tiles, ye) - r - it.tile;
             it.tiles = un.tiles; it.kvh = kvh; it.item = n + rb;
             it.unit = u;
             items[at + rb - rb0] = it;
@@ -246,15 +235,12 @@ __device__ __forceinline__ int find_items(const AttnPagedArgs& a, int units, int
         if (kvh == 0 && t >= y) { starts[u] = t; item_starts[u] = n; }
     }
     // behind the last unit looked at, or the first item that there was no room for
-    int64_t end = min(ye, (int64_t)__shfl(behind, 63));
+    int end = min(ye, lane_value(behind, 63));
     if (all > kItems) {
-        const bool cut = count > 0 && at <= kItems && at + count > kItems;
-        const uint64_t who = __ballot(cut);
-        const int k = __builtin_ctzll(who);
-        const int64_t from = t + (int64_t)(rb0 + kItems - at) * un.tiles;
-        end = __shfl(from, k);
+        const uint64_t who = __ballot(count > 0 && at <= kItems && upto > kItems);
+        end = lane_value(t + (rb0 + kItems - at) * un.tiles, __builtin_ctzll(who));
     }
-    next = kvh * tot + end;
+    next = line0 + end;
     return min(all, kItems);
 }
 
@@ -293,7 +279,10 @@ __global__ __launch_bounds__(64 * KW * RW, 2) void attn_paged_kernel(AttnPagedAr
     if (threadIdx.x < 4) special_rows[threadIdx.x >> 1][threadIdx.x & 1] = 0;
     int turn = 0;
 
-    sum_up<PREFIX>(a, units, block_rows, line);
+    Unit* cache = reinterpret_cast<Unit*>(lds);   // of the first items; the tiles come over it
+    static_assert(THREADS * sizeof(Unit) <= sizeof(lds), "units in the tiles' place");
+    sum_up<PREFIX>(a, units, block_rows, line, cache);
+    if (units > THREADS) cache = nullptr;
     if (w == 0 && threadIdx.x == 0) { starts[units] = line.tiles[THREADS]; item_starts[units] = line.items[THREADS]; }
     if (!PREFIX && threadIdx.x == 0) a.open[w].parts = 0;
 
@@ -350,14 +339,15 @@ __global__ __launch_bounds__(64 * KW * RW, 2) void attn_paged_kernel(AttnPagedAr
 
     uint32_t to = base;
     typename C::At at(base, base + tile_bytes, lane);
-    const int64_t all = line.tiles[THREADS] * a.HK, per = stretch(a, all);
+    const int64_t all = (int64_t)line.tiles[THREADS] * a.HK, per = stretch(a, all);
     const int64_t xe = min((w + 1) * per, all);
     for (int64_t x0 = w * per; x0 < xe; x0 = rest) {
         if (wave == 0) {
             int64_t next;
-            const int n = find_items<PREFIX>(a, units, block_rows, line, x0, xe, items, next, starts, item_starts);
+            const int n = find_items<PREFIX>(a, units, block_rows, line, cache, x0, xe, items, next, starts, item_starts);
             if (lane == 0) { found = n; rest = next; }
         }
+        cache = nullptr;
         __syncthreads();
         const int n_items = uniform(found);
         {
@@ -482,112 +472,118 @@ __global__ __launch_bounds__(64 * KW * RW, 2) void attn_paged_kernel(AttnPagedAr
 }
 
 // Parts of a row, joined by one wave: a lane reads the maximum and the sum of one part, then all read the rows.
-template <int D> struct Joined {
-    static constexpr int V = D / 64;
+template <typename T, int D, typename F>
+__device__ __forceinline__ void join_row(const AttnPagedArgs& a, int token, int head, int parts, F part_of) {
+    constexpr int V = D / 64;
+    const int lane = threadIdx.x & 63;
     float m = kNegInf, l = 0.0f, o[V] = {};
-    // parts k = 0 .. n - 1 of row `row`, in slots of `rows` rows at slots + slot_of(k) * size of a slot
-    template <typename F> __device__ __forceinline__ void add(const char* slots, int rows, int row, int parts, F slot_of) {
-        const int lane = threadIdx.x & 63;
-        const int64_t slot_bytes = (int64_t)rows * (D + 2) * 4;
-        for (int k0 = 0; k0 < parts; k0 += 64) {
-            const int n = min(64, parts - k0);
-            int64_t at = 0;
-            float m1 = kNegInf, l1 = 0.0f;
-            if (lane < n) {
-                at = slot_of(k0 + lane) * slot_bytes;
-                const float* s = reinterpret_cast<const float*>(slots + at);
-                m1 = s[rows * D + row];
-                l1 = s[rows * D + rows + row];
+    for (int k0 = 0; k0 < parts; k0 += 64) {
+        const int n = min(64, parts - k0);
+        const float* row = nullptr;
+        float m1 = kNegInf, l1 = 0.0f;
+        if (lane < n) {
+            int stats, rows;   // floats from the row to its maximum; rows of the slot
+            row = part_of(k0 + lane, stats, rows);
+            m1 = row[stats];
+            l1 = row[stats + rows];
+        }
+        float mn = m1;
+#pragma unroll
+        for (int d = 1; d < 64; d *= 2) mn = fmaxf(mn, __shfl_xor(mn, d));
+        mn = fmaxf(mn, m);
+        const float base = mn == kNegInf ? 0.0f : mn;
+        const float e = __builtin_amdgcn_exp2f(m1 - base), e0 = __builtin_amdgcn_exp2f(m - base);
+        l1 *= e;
+#pragma unroll
+        for (int d = 1; d < 64; d *= 2) l1 += __shfl_xor(l1, d);
+        m = mn;
+        l = l * e0 + l1;
+#pragma unroll
+        for (int i = 0; i < V; ++i) o[i] *= e0;
+        constexpr int ahead = 8;
+        for (int p = 0; p < n; p += ahead) {
+            float y[ahead][V], f[ahead];
+#pragma unroll
+            for (int q = 0; q < ahead; ++q) {
+                const int k = min(p + q, n - 1);
+                const uint64_t bits = reinterpret_cast<uintptr_t>(row);
+                const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)bits, k), hi = __builtin_amdgcn_readlane((uint32_t)(bits >> 32), k);
+                const float* s = reinterpret_cast<const float*>((uint64_t)hi << 32 | lo) + V * lane;
+                f[q] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(e), k));
+#pragma unroll
+                for (int i = 0; i < V; ++i) y[q][i] = s[i];
             }
-            float mn = m1;
 #pragma unroll
-            for (int d = 1; d < 64; d *= 2) mn = fmaxf(mn, __shfl_xor(mn, d));
-            mn = fmaxf(mn, m);
-            const float base = mn == kNegInf ? 0.0f : mn;
-            const float e = __builtin_amdgcn_exp2f(m1 - base), e0 = __builtin_amdgcn_exp2f(m - base);
-            l1 *= e;
+            for (int q = 0; q < ahead; ++q)
 #pragma unroll
-            for (int d = 1; d < 64; d *= 2) l1 += __shfl_xor(l1, d);
-            m = mn;
-            l = l * e0 + l1;
-#pragma unroll
-            for (int i = 0; i < V; ++i) o[i] *= e0;
-            constexpr int ahead = 8;
-            for (int p = 0; p < n; p += ahead) {
-                float y[ahead][V], f[ahead];
-#pragma unroll
-                for (int q = 0; q < ahead; ++q) {
-                    const int k = min(p + q, n - 1);
-                    const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)at, k), hi = __builtin_amdgcn_readlane((uint32_t)(at >> 32), k);
-                    const float* s = reinterpret_cast<const float*>(slots + ((int64_t)hi << 32 | lo)) + row * D + V * lane;
-                    f[q] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(e), k));
-#pragma unroll
-                    for (int i = 0; i < V; ++i) y[q][i] = s[i];
-                }
-#pragma unroll
-                for (int q = 0; q < ahead; ++q)
-#pragma unroll
-                    for (int i = 0; i < V; ++i) o[i] += p + q < n ? y[q][i] * f[q] : 0.0f;
-            }
+                for (int i = 0; i < V; ++i) o[i] += p + q < n ? y[q][i] * f[q] : 0.0f;
         }
     }
-    template <typename T> __device__ __forceinline__ void store(const AttnPagedArgs& a, int token, int head) {
-        const int lane = threadIdx.x & 63;
-        const int64_t id = (int64_t)token * a.HQ + head;
-        const float inv = reciprocal_sum(l);
+    const int64_t id = (int64_t)token * a.HQ + head;
+    const float inv = reciprocal_sum(l);
 #pragma unroll
-        for (int i = 0; i < V; ++i) Elem<T>::store(a.o, id * D + V * lane + i, o[i] * inv);
-        if (a.lse && lane == 0) a.lse[id] = log_sum(m, l);
-    }
-};
+    for (int i = 0; i < V; ++i) Elem<T>::store(a.o, id * D + V * lane + i, o[i] * inv);
+    if (a.lse && lane == 0) a.lse[id] = log_sum(m, l);
+}
 
-// Without prefixes: a workgroup for every block of rows that a stretch has left unfinished, and the rows that see
-// nothing (of sequences without a page's room), which no tile belongs to.
+template <int D> __device__ __forceinline__ const float* part_row(const char* slots, int64_t slot, int rows, int row, int& stats, int& of) {
+    stats = rows * D + row - row * D;
+    of = rows;
+    return reinterpret_cast<const float*>(slots + slot * ((int64_t)rows * (D + 2) * 4)) + row * D;
+}
+
+// Without prefixes: a wave for every row of the blocks that stretches have left unfinished; and the rows that see nothing
+// although their sequence is not padded (a table without room), which no tile belongs to.
 template <typename T, int D>
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnPagedArgs a) {
-    const int w = blockIdx.x, wave = blockIdx.y * 4 + (threadIdx.x >> 6);
+    const int w = blockIdx.x, wave = blockIdx.y * 4 + uniform((int)threadIdx.x >> 6);
     if (w < a.workers) {
         const AttnOpen x = a.open[w];
         for (int r = wave; x.parts && r < x.rows; r += 4 * gridDim.y) {
-            Joined<D> j;
-            j.add(a.slots, a.rows, r, x.parts, [&](int k) { return open_slot(w + k, k > 0); });
             const int row = x.row0 + r;
-            j.template store<T>(a, x.token0 + row / a.per, x.kvh * a.per + row % a.per);
+            join_row<T, D>(a, x.token0 + row / a.per, x.kvh * a.per + row % a.per, x.parts, [&](int k, int& stats, int& rows) {
+                return part_row<D>(a.slots, open_slot(w + k, k > 0), a.rows, r, stats, rows);
+            });
         }
         return;
     }
-    // capacity 0: every row
     const int64_t waves = 4 * (int64_t)gridDim.y, step = waves * (gridDim.x - a.workers);
     for (int64_t id = (w - a.workers) * waves + wave; id < a.T * a.HQ; id += step) {
         const int token = (int)(id / a.HQ);
         if ((a.cu && token >= a.cu[a.N]) || a.context[a.cu ? find_seq(a.cu, a.N, token) : token] < 0) continue;
-        Joined<D>().template store<T>(a, token, (int)(id % a.HQ));
+        join_row<T, D>(a, token, (int)(id % a.HQ), 0, [](int, int& stats, int& rows) { stats = rows = 0; return (const float*)nullptr; });
     }
 }
 
 // With prefixes: one wave per (token, query head); parts of the prefix and of the sequence's own keys.
 template <typename T, int D>
 __global__ __launch_bounds__(256) void attn_join_groups_kernel(AttnPagedArgs a) {
-    const int64_t id = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    const int64_t id = (int64_t)blockIdx.x * 4 + uniform((int)threadIdx.x >> 6);
     if (id >= a.T * a.HQ) return;
-    const int token = __builtin_amdgcn_readfirstlane((int)(id / a.HQ)), head = __builtin_amdgcn_readfirstlane((int)(id % a.HQ));
+    const int token = uniform((int)(id / a.HQ)), head = uniform((int)(id % a.HQ));
     if (a.cu && token >= uniform_load(a.cu + a.N)) return;
-    const int seq = a.cu ? __builtin_amdgcn_readfirstlane(find_seq(a.cu, a.N, token)) : token;
+    const int seq = a.cu ? uniform(find_seq(a.cu, a.N, token)) : token;
     if (uniform_load(a.context + seq) < 0) return;
     const int kvh = head / a.per, hh = head % a.per, group = uniform_load(a.group + seq);
-    Joined<D> j;
-    auto side = [&](const Unit& un, int u, int units, int rows, const int64_t* starts, const int32_t* items, const char* slots) {
-        if (un.tiles <= 0) return;
-        const int64_t tot = starts[units], start = starts[u], per = stretch(a, tot * a.HK);
+    struct Side { int64_t first, own; int parts, row; };
+    auto side = [&](const Unit& un, int u, int units, int rows, const int64_t* starts, const int32_t* items) {
+        const int64_t tot = starts[units], per = stretch(a, tot * a.HK);
+        const int64_t start = un.tiles > 0 ? starts[u] : 0;
+        const int item = un.tiles > 0 ? items[u] : 0;
         const int r = (token - un.tok0) * a.per + hh, rb = r / rows;
         const int64_t x0 = kvh * tot + start + (int64_t)rb * un.tiles, w0 = x0 / per, w1 = (x0 + un.tiles - 1) / per;
-        const int64_t own = 2 * (int64_t)a.workers + (int64_t)kvh * items[units] + items[u] + rb;
-        j.add(slots, rows, r % rows, (int)(w1 - w0 + 1), [&](int k) { return w0 == w1 ? own : open_slot(w0 + k, k > 0); });
+        return Side{w0, 2 * (int64_t)a.workers + (int64_t)kvh * items[units] + item + rb, un.tiles > 0 ? (int)(w1 - w0 + 1) : 0, r % rows};
     };
-    if (group >= 0)
-        side(unit_of<true>(a, group, a.prefix_rows), group, a.groups, a.prefix_rows, a.prefix_start, a.prefix_item, a.prefix_slots);
-    side(unit_of<false>(a, seq, a.rows), seq, a.N, a.rows, a.start, a.item, a.slots);
-    j.template store<T>(a, token, head);
+    const Side own = side(unit_of<false>(a, seq, a.rows), seq, a.N, a.rows, a.start, a.item);
+    Side pre{0, 0, 0, 0};
+    if (group >= 0) pre = side(unit_of<true>(a, group, a.prefix_rows), group, a.groups, a.prefix_rows, a.prefix_start, a.prefix_item);
+    join_row<T, D>(a, token, head, pre.parts + own.parts, [&](int k, int& stats, int& rows) {
+        const bool p = k < pre.parts;
+        const Side& s = p ? pre : own;
+        const int i = p ? k : k - pre.parts;
+        return part_row<D>(p ? a.prefix_slots : a.slots, s.parts == 1 ? s.own : open_slot(s.first + i, i > 0), p ? a.prefix_rows : a.rows,
+                           s.row, stats, rows);
+    });
 }
 
 template <typename T, int D, bool PREFIX>
@@ -609,7 +605,7 @@ hipError_t launch(const AttnPagedArgs& a, hipStream_t stream) {
     if (e == hipSuccess) e = launch_part<T, D, false>(a, a.rows, stream);
     if (e != hipSuccess) return e;
     if (a.groups) attn_join_groups_kernel<T, D><<<dim3((unsigned)((a.T * a.HQ + 3) / 4)), 256, 0, stream>>>(a);
-    else attn_join_kernel<T, D><<<dim3((unsigned)(a.workers + (a.capacity == 0 ? 256 : 0)), (unsigned)(a.rows / 16)), 256, 0, stream>>>(a);
+    else attn_join_kernel<T, D><<<dim3((unsigned)(a.workers + (a.capacity == 0 ? 256 : 0)), (unsigned)(a.rows / 4)), 256, 0, stream>>>(a);
     return hipGetLastError();
 }
 
@@ -651,7 +647,7 @@ AttnPagedPlan attn_paged_plan(int64_t T, int32_t N, int32_t HQ, int32_t HK, int 
 }
 
 hipError_t launch_attn_paged(AttnPagedArgs a, const AttnPagedPlan& p, char* ws, int D, int io_dtype, hipStream_t stream) {
-    a.workers = p.workers; a.rows = p.rows; a.prefix_rows = p.prefix_rows;
+    a.workers = p.workers; a.worker_bits = p.workers == 512 ? 9 : 8; a.rows = p.rows; a.prefix_rows = p.prefix_rows;
     a.per = a.HQ / a.HK;
     a.capacity = (int64_t)a.max_pages << a.page_shift;
     a.start = reinterpret_cast<int64_t*>(ws + p.start);

@@ -284,7 +284,8 @@ struct AttnPagedArgs {
     bool negate;
     // set by the launcher
     int32_t per;                 // query heads per key head
-    int32_t workers, rows, prefix_rows;   // workgroups; rows of a block of one sequence's, of one group's
+    int32_t workers, worker_bits;         // workgroups, a power of two, and its logarithm
+    int32_t rows, prefix_rows;            // rows of a block of one sequence's, of one group's
     int64_t capacity;            // tokens a row of the table can hold
     // workspace
     int64_t *start, *prefix_start;   // [N + 1], [groups + 1]: tiles before each unit on the line of a key head

@@ -585,7 +585,8 @@ GDR_API gdr_status gdr_attn_prefill_fwd(const gdr_attn_problem* p, const void* q
  *   lse            fp32 [T, HQ] or NULL
  *   workspace      gdr_attn_workspace_size bytes, 256-byte aligned, contents need not be initialised; calls that
  *                  may overlap need one each
- * p->k_stride and p->v_stride are not used.  T * HQ < 2^31.  The result does not depend on what else is in the
+ * p->k_stride and p->v_stride are not used.  T * HQ < 2^31, and N times a table row's tokens below 2^37 over the
+ * blocks of 32 rows that max_q_len tokens of HQ / HKV heads make.  The result does not depend on what else is in the
  * batch by more than the order of fp32 sums.
  */
 GDR_API size_t gdr_attn_workspace_size(const gdr_attn_problem* p, int32_t max_q_len, int32_t num_groups);
