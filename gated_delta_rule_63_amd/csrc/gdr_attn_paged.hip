@@ -2,8 +2,8 @@
 // (gdr_attn_decode_paged).
 //
 // The tokens of one sequence (or, over a shared prefix, of a whole group) times the query heads of one key head
-// are the rows of one product: keys and values are read once for all of them.  The work is a line of tiles of 64
-// keys, (key head, unit, row block, tile) in that order, cut into equal stretches for a fixed number of
+// are the rows of one product: keys and values are read once for all of them.  The work of a key head is a line of
+// tiles of 64 keys, (unit, row block, tile) in that order, cut into equal stretches for a fixed number of
 // workgroups, whatever the lengths are: the host does not know them, and every workgroup sums them up for itself.
 // A stretch may end inside a unit; such a part's maximum, sum and unnormalised output go to the workspace and are
 // joined by the last kernel.
@@ -36,8 +36,9 @@ __device__ __forceinline__ int keys_of(const AttnPagedArgs& a, int ctx, int toke
     return ctx < 0 || tokens <= 0 ? 0 : (int)min((int64_t)ctx + tokens, a.capacity);
 }
 
-__device__ __forceinline__ int64_t stretch(const AttnPagedArgs& a, int64_t tiles) {
-    return max((tiles + a.workers - 1) >> a.worker_bits, (int64_t)kMinTiles);
+// tiles of a stretch, of a line of so many
+__device__ __forceinline__ int stretch(const AttnPagedArgs& a, int tiles) {
+    return max((int)(((int64_t)tiles + a.per_head - 1) / a.per_head), kMinTiles);
 }
 
 // One wave per group: the first sequence that is not padded gives the pages, whole pages are shared.  The wave behind
@@ -187,26 +188,18 @@ struct Item {
     int key0, key1;            // the unit's keys
     int table;                 // row of the page table
     int tile, count, tiles;
-    int kvh;
     int item;                  // row blocks before it on the line of a key head
     int unit;
 };
 constexpr int kItems = 64;     // found at a time
 
-// The items of the line from x on, up to xe and kItems of them, by one wave: 64 units at a time.  `next` is where the
-// rest begins.
+// The items of tiles [y, ye) of key head kvh's line, kItems of them at most, by one wave: 64 units at a time.  `next` is
+// where the rest begins.
 template <bool PREFIX, int THREADS>
 __device__ __forceinline__ int find_items(const AttnPagedArgs& a, int units, int block_rows, const Line<THREADS>& line,
-                                          const Unit* cache, int64_t x, int64_t xe, Item* items, int64_t& next, int64_t* starts,
+                                          const Unit* cache, int kvh, int y, int ye, Item* items, int& next, int32_t* starts,
                                           int32_t* item_starts) {
     const int lane = threadIdx.x & 63;
-    const int tot = uniform(line.tiles[THREADS]);
-    // x / tot: both below 2^53, the quotient a number of heads
-    int kvh = (int)((double)x / (double)tot);
-    if ((int64_t)kvh * tot > x) --kvh;
-    if ((int64_t)(kvh + 1) * tot <= x) ++kvh;
-    const int64_t line0 = (int64_t)kvh * tot;
-    const int y = (int)(x - line0), ye = (int)min((int64_t)tot, xe - line0);   // one key head's line at a time
     int t0, n0;
     const int u = find_unit<PREFIX>(a, units, block_rows, line, y, t0, n0) + lane;
     Unit un{};
@@ -227,7 +220,7 @@ __device__ __forceinline__ int find_items(const AttnPagedArgs& a, int units, int
             it.key0 = un.key0; it.key1 = un.key1; it.table = table;
             it.tile = max(r, y) - r;
             it.count = min(r + un.tiles, ye) - r - it.tile;
-            it.tiles = un.tiles; it.kvh = kvh; it.item = n + rb;
+            it.tiles = un.tiles; it.item = n + rb;
             it.unit = u;
             items[at + rb - rb0] = it;
         }
@@ -240,7 +233,7 @@ __device__ __forceinline__ int find_items(const AttnPagedArgs& a, int units, int
         const uint64_t who = __ballot(count > 0 && at <= kItems && upto > kItems);
         end = lane_value(t + (rb0 + kItems - at) * un.tiles, __builtin_ctzll(who));
     }
-    next = line0 + end;
+    next = end;
     return min(all, kItems);
 }
 
@@ -250,7 +243,7 @@ __device__ __forceinline__ Item same(const Item& it) {
     r.token0 = uniform(it.token0); r.row0 = uniform(it.row0); r.rows = uniform(it.rows);
     r.key0 = uniform(it.key0); r.key1 = uniform(it.key1); r.table = uniform(it.table);
     r.tile = uniform(it.tile); r.count = uniform(it.count); r.tiles = uniform(it.tiles);
-    r.kvh = uniform(it.kvh); r.item = uniform(it.item); r.unit = uniform(it.unit);
+    r.item = uniform(it.item); r.unit = uniform(it.unit);
     return r;
 }
 
@@ -261,21 +254,20 @@ __global__ __launch_bounds__(64 * KW * RW, 2) void attn_paged_kernel(AttnPagedAr
     constexpr int WAVES = KW * RW, THREADS = 64 * WAVES, blocks = 2 / KW, block_rows = 32 * RW;
     constexpr int tile_bytes = kKeys * L::row_bytes;
     __shared__ __align__(1024) char lds[4 * tile_bytes];
-    __shared__ float xch[KW == 2 ? RW * 64 * 18 : 1];
+    __shared__ float xch[RW][2][64];
     __shared__ Line<THREADS> line;
     __shared__ Item items[kItems];
-    __shared__ int64_t rest;
-    __shared__ int found;
+    __shared__ int found, rest;
     __shared__ uint32_t special_rows[2][2];
 
     const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6), half = lane >> 5;
     const int kw = wave % KW, rw = wave / KW;
     const int units = PREFIX ? a.groups : a.N;
     char* const slots = PREFIX ? a.prefix_slots : a.slots;
-    int64_t* const starts = PREFIX ? a.prefix_start : a.start;
+    int32_t* const starts = PREFIX ? a.prefix_start : a.start;
     int32_t* const item_starts = PREFIX ? a.prefix_item : a.item;
     constexpr int64_t slot_bytes = (int64_t)block_rows * (D + 2) * 4;
-    const int w = blockIdx.x;
+    const int w = blockIdx.x, kvh = w / a.per_head;
     if (threadIdx.x < 4) special_rows[threadIdx.x >> 1][threadIdx.x & 1] = 0;
     int turn = 0;
 
@@ -309,7 +301,7 @@ __global__ __launch_bounds__(64 * KW * RW, 2) void attn_paged_kernel(AttnPagedAr
         vo[i] = row + L::template copy_byte<true>(64 * i, lane);
     }
     const uint32_t base = lds_address(lds);
-    auto stage = [&](const Pages& pages, int kvh, int j0, int key1, uint32_t to) {
+    auto stage = [&](const Pages& pages, int j0, int key1, uint32_t to) {
 #pragma unroll
         for (int g = 0; g < groups16; ++g) {
             const int r0 = 16 * (groups16 * wave + g), j = j0 + r0, last = key1 - 1 - j;
@@ -339,12 +331,13 @@ __global__ __launch_bounds__(64 * KW * RW, 2) void attn_paged_kernel(AttnPagedAr
 
     uint32_t to = base;
     typename C::At at(base, base + tile_bytes, lane);
-    const int64_t all = (int64_t)line.tiles[THREADS] * a.HK, per = stretch(a, all);
-    const int64_t xe = min((w + 1) * per, all);
-    for (int64_t x0 = w * per; x0 < xe; x0 = rest) {
+    const int tot = uniform(line.tiles[THREADS]), per = stretch(a, tot), part = w % a.per_head;
+    // (in 64 bits: stretches behind the line's end)
+    const int ye = (int)min(((int64_t)part + 1) * per, (int64_t)tot);
+    for (int y = (int)min((int64_t)part * per, (int64_t)tot); y < ye; y = uniform(rest)) {
         if (wave == 0) {
-            int64_t next;
-            const int n = find_items<PREFIX>(a, units, block_rows, line, cache, x0, xe, items, next, starts, item_starts);
+            int next;
+            const int n = find_items<PREFIX>(a, units, block_rows, line, cache, kvh, y, ye, items, next, starts, item_starts);
             if (lane == 0) { found = n; rest = next; }
         }
         cache = nullptr;
@@ -353,7 +346,7 @@ __global__ __launch_bounds__(64 * KW * RW, 2) void attn_paged_kernel(AttnPagedAr
         {
             const Item it = same(items[0]);
             const int j0 = it.key0 + it.tile * kKeys;
-            stage(pages_of(it.table, j0, it.key1), it.kvh, j0, it.key1, to);
+            stage(pages_of(it.table, j0, it.key1), j0, it.key1, to);
         }
         for (int i = 0; i < n_items; ++i) {
             const Item it = same(items[i]), next = same(items[min(i + 1, n_items - 1)]);
@@ -362,7 +355,7 @@ __global__ __launch_bounds__(64 * KW * RW, 2) void attn_paged_kernel(AttnPagedAr
             // the lane's row
             const int r = it.row0 + 32 * rw + (lane & 31);
             const bool real = r < it.rows;
-            const int rc = min(r, it.rows - 1), token = it.token0 + rc / a.per, head = it.kvh * a.per + rc % a.per;
+            const int rc = min(r, it.rows - 1), token = it.token0 + rc / a.per, head = kvh * a.per + rc % a.per;
             const int seq = !PREFIX ? it.unit : a.cu ? find_seq(a.cu, a.N, token) : token;
             const int ctx = a.context[seq];
             const int seen = ctx < 0 ? 0 : (int)min((int64_t)ctx + (token - seq_first(a, seq)) + 1, (int64_t)it.key1);
@@ -373,14 +366,14 @@ __global__ __launch_bounds__(64 * KW * RW, 2) void attn_paged_kernel(AttnPagedAr
             for (int tile = it.tile; tile < end; ++tile) {
                 // the next tile's pages, read while this one's copies are waited for
                 const bool inside = tile + 1 < end;
-                const int key1 = inside ? it.key1 : next.key1, kvh = inside ? it.kvh : next.kvh;
+                const int key1 = inside ? it.key1 : next.key1;
                 const int ahead0 = inside ? it.key0 + (tile + 1) * kKeys : next.key0 + next.tile * kKeys;
                 const Pages ahead = pages_of(inside ? it.table : next.table, ahead0, key1);
                 wait_copies();
                 __syncthreads();
                 const uint32_t v = to + tile_bytes;
                 to = 2 * base + 2 * tile_bytes - to;
-                if (inside || more) stage(ahead, kvh, ahead0, key1, to);
+                if (inside || more) stage(ahead, ahead0, key1, to);
 
                 const int j0 = it.key0 + tile * kKeys;
                 // tokens see less than the last of theirs: some rows do not see what others do
@@ -411,7 +404,7 @@ __global__ __launch_bounds__(64 * KW * RW, 2) void attn_paged_kernel(AttnPagedAr
                         const int p = k < 16 ? now.p[0] : k < 32 ? now.p[1] : k < 48 ? now.p[2] : now.p[3];
                         if (p >= 0)
                             C::add_specials(static_cast<const char*>(a.v_pages) +
-                                            ((((int64_t)p * a.HK + it.kvh) << a.page_shift) + (j & ((1 << a.page_shift) - 1))) * L::row_bytes,
+                                            ((((int64_t)p * a.HK + kvh) << a.page_shift) + (j & ((1 << a.page_shift) - 1))) * L::row_bytes,
                                             half, acc.o);
                     }
                 }
@@ -423,23 +416,29 @@ __global__ __launch_bounds__(64 * KW * RW, 2) void attn_paged_kernel(AttnPagedAr
             float l = both_sum(acc.l), m = acc.m;
             f32x16_t* const o = acc.o;
             if constexpr (KW == 2) {   // the two waves of a row block: the odd one's part joins the even one's
-                float* const mine = xch + rw * 64 * 18 + lane;
-                if (kw == 1) { mine[16 * 64] = m; mine[17 * 64] = l; }
+                // in the place of the last tile, which the next copies do not touch before the next barrier
+                float* const mine = reinterpret_cast<float*>(lds + (2 * tile_bytes - (to - base))) + rw * (64 * D / 2) + lane;
+                static_assert(RW * 64 * D / 2 * 4 <= 2 * tile_bytes, "outputs in a tile's place");
+                __syncthreads();
+                if (kw == 1) {
+                    xch[rw][0][lane] = m;
+                    xch[rw][1][lane] = l;
 #pragma unroll
-                for (int b = 0; b < D / 32; ++b) {
-                    if (kw == 1)
+                    for (int b = 0; b < D / 32; ++b)
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) mine[i * 64] = o[b][i];
-                    __syncthreads();
-                    if (kw == 0) {
-                        const float m1 = mine[16 * 64], l1 = mine[17 * 64], mn = fmaxf(m, m1);
-                        const float e0 = m == kNegInf ? 0.0f : __builtin_amdgcn_exp2f((m - mn) * a.c);
-                        const float e1 = m1 == kNegInf ? 0.0f : __builtin_amdgcn_exp2f((m1 - mn) * a.c);
+                        for (int i = 0; i < 16; ++i) mine[(16 * b + i) * 64] = o[b][i];
+                }
+                __syncthreads();
+                if (kw == 0) {
+                    const float m1 = xch[rw][0][lane], l1 = xch[rw][1][lane], mn = fmaxf(m, m1);
+                    const float e0 = m == kNegInf ? 0.0f : __builtin_amdgcn_exp2f((m - mn) * a.c);
+                    const float e1 = m1 == kNegInf ? 0.0f : __builtin_amdgcn_exp2f((m1 - mn) * a.c);
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) o[b][i] = o[b][i] * e0 + mine[i * 64] * e1;
-                        if (b == D / 32 - 1) { l = l * e0 + l1 * e1; m = mn; }
-                    }
-                    __syncthreads();
+                    for (int b = 0; b < D / 32; ++b)
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) o[b][i] = o[b][i] * e0 + mine[(16 * b + i) * 64] * e1;
+                    l = l * e0 + l1 * e1;
+                    m = mn;
                 }
             }
             if (kw == 0) {
@@ -452,7 +451,7 @@ __global__ __launch_bounds__(64 * KW * RW, 2) void attn_paged_kernel(AttnPagedAr
                     C::store(row, half, o);
                     if (a.lse && store && half == 0) a.lse[(int64_t)token * a.HQ + head] = log_sum(m * a.c, l);
                 } else if (real) {
-                    const int64_t slot = whole ? 2 * (int64_t)a.workers + (int64_t)it.kvh * line.items[THREADS] + it.item : open_slot(w, it.tile > 0);
+                    const int64_t slot = whole ? 2 * (int64_t)a.workers + (int64_t)kvh * line.items[THREADS] + it.item : open_slot(w, it.tile > 0);
                     float* s = reinterpret_cast<float*>(slots + slot * slot_bytes);
                     const int row = 32 * rw + (lane & 31);
                     C::store_part(s + row * D, half, o);
@@ -465,7 +464,7 @@ __global__ __launch_bounds__(64 * KW * RW, 2) void attn_paged_kernel(AttnPagedAr
             // the block that it leaves unfinished, for the last kernel
             const int left = it.tiles - it.count;
             if (!PREFIX && it.tile == 0 && left > 0 && threadIdx.x == 0)
-                a.open[w] = AttnOpen{it.token0, it.row0, min(block_rows, it.rows - it.row0), it.kvh, 1 + (int)((left + per - 1) / per)};
+                a.open[w] = AttnOpen{it.token0, it.row0, min(block_rows, it.rows - it.row0), kvh, 1 + (left + per - 1) / per};
         }
         __syncthreads();   // before the next items are found
     }
@@ -566,13 +565,13 @@ __global__ __launch_bounds__(256) void attn_join_groups_kernel(AttnPagedArgs a) 
     if (uniform_load(a.context + seq) < 0) return;
     const int kvh = head / a.per, hh = head % a.per, group = uniform_load(a.group + seq);
     struct Side { int64_t first, own; int parts, row; };
-    auto side = [&](const Unit& un, int u, int units, int rows, const int64_t* starts, const int32_t* items) {
-        const int64_t tot = starts[units], per = stretch(a, tot * a.HK);
-        const int64_t start = un.tiles > 0 ? starts[u] : 0;
+    auto side = [&](const Unit& un, int u, int units, int rows, const int32_t* starts, const int32_t* items) {
+        const int per = stretch(a, starts[units]);
+        const int start = un.tiles > 0 ? starts[u] : 0;
         const int item = un.tiles > 0 ? items[u] : 0;
         const int r = (token - un.tok0) * a.per + hh, rb = r / rows;
-        const int64_t x0 = kvh * tot + start + (int64_t)rb * un.tiles, w0 = x0 / per, w1 = (x0 + un.tiles - 1) / per;
-        return Side{w0, 2 * (int64_t)a.workers + (int64_t)kvh * items[units] + item + rb, un.tiles > 0 ? (int)(w1 - w0 + 1) : 0, r % rows};
+        const int x0 = start + rb * un.tiles, w0 = x0 / per, w1 = (x0 + un.tiles - 1) / per;
+        return Side{(int64_t)kvh * a.per_head + w0, 2 * (int64_t)a.workers + (int64_t)kvh * items[units] + item + rb, un.tiles > 0 ? w1 - w0 + 1 : 0, r % rows};
     };
     const Side own = side(unit_of<false>(a, seq, a.rows), seq, a.N, a.rows, a.start, a.item);
     Side pre{0, 0, 0, 0};
@@ -617,23 +616,25 @@ size_t up(size_t x) { return (x + 255) / 256 * 256; }
 AttnPagedPlan attn_paged_plan(int64_t T, int32_t N, int32_t HQ, int32_t HK, int D, int io_bytes, int32_t max_q_len, int32_t groups) {
     AttnPagedPlan p{};
     const int64_t per = HQ / HK;
-    p.workers = D * io_bytes <= 256 ? 512 : 256;   // as many as are resident at once, by their LDS
+    // as many as are resident at once, by their LDS; each has one key head
+    p.per_head = max(1, (D * io_bytes <= 256 ? 512 : 256) / HK);
+    p.workers = p.per_head * HK;
     p.rows = rows_for(per * max_q_len);
     p.prefix_rows = rows_for(per * T);
     auto slots = [&](int rows, int64_t units) {
         // two open parts per workgroup; with prefixes nothing is written straight to the output
-        int64_t n = 2 * p.workers;
+        int64_t n = 2 * (int64_t)p.workers;
         if (groups) n += (units + (T * per + rows - 1) / rows) * HK;
         return up((size_t)n * rows * (D + 2) * 4);
     };
     size_t at = 0;
     auto take = [&](size_t bytes) { const size_t r = at; at += up(bytes); return r; };
-    p.start = take((size_t)(N + 1) * 8);
+    p.start = take((size_t)(N + 1) * 4);
     p.item = take((size_t)(N + 1) * 4);
     if (groups) {
         p.pre = take((size_t)N * 4);
         p.group = take((size_t)N * 4);
-        p.prefix_start = take((size_t)(groups + 1) * 8);
+        p.prefix_start = take((size_t)(groups + 1) * 4);
         p.prefix_item = take((size_t)(groups + 1) * 4);
         p.prefix = take((size_t)groups * 4);
         p.rep = take((size_t)groups * 4);
@@ -647,14 +648,14 @@ AttnPagedPlan attn_paged_plan(int64_t T, int32_t N, int32_t HQ, int32_t HK, int 
 }
 
 hipError_t launch_attn_paged(AttnPagedArgs a, const AttnPagedPlan& p, char* ws, int D, int io_dtype, hipStream_t stream) {
-    a.workers = p.workers; a.worker_bits = p.workers == 512 ? 9 : 8; a.rows = p.rows; a.prefix_rows = p.prefix_rows;
+    a.workers = p.workers; a.per_head = p.per_head; a.rows = p.rows; a.prefix_rows = p.prefix_rows;
     a.per = a.HQ / a.HK;
     a.capacity = (int64_t)a.max_pages << a.page_shift;
-    a.start = reinterpret_cast<int64_t*>(ws + p.start);
+    a.start = reinterpret_cast<int32_t*>(ws + p.start);
     a.item = reinterpret_cast<int32_t*>(ws + p.item);
     a.pre = reinterpret_cast<int32_t*>(ws + p.pre);
     a.group = reinterpret_cast<int32_t*>(ws + p.group);
-    a.prefix_start = reinterpret_cast<int64_t*>(ws + p.prefix_start);
+    a.prefix_start = reinterpret_cast<int32_t*>(ws + p.prefix_start);
     a.prefix_item = reinterpret_cast<int32_t*>(ws + p.prefix_item);
     a.prefix = reinterpret_cast<int32_t*>(ws + p.prefix);
     a.rep = reinterpret_cast<int32_t*>(ws + p.rep);

@@ -284,11 +284,11 @@ struct AttnPagedArgs {
     bool negate;
     // set by the launcher
     int32_t per;                 // query heads per key head
-    int32_t workers, worker_bits;         // workgroups, a power of two, and its logarithm
+    int32_t workers, per_head;            // workgroups, those of a key head
     int32_t rows, prefix_rows;            // rows of a block of one sequence's, of one group's
     int64_t capacity;            // tokens a row of the table can hold
     // workspace
-    int64_t *start, *prefix_start;   // [N + 1], [groups + 1]: tiles before each unit on the line of a key head
+    int32_t *start, *prefix_start;   // [N + 1], [groups + 1]: tiles before each unit on the line of a key head
     int32_t *item, *prefix_item;     // row blocks before each unit
     int32_t *pre, *group;        // [N]: keys read with the group's prefix, the group or -1
     int32_t *prefix, *rep;       // [groups]: keys of the prefix, the sequence whose pages hold them
@@ -298,7 +298,7 @@ struct AttnPagedArgs {
 };
 
 struct AttnPagedPlan {
-    int32_t workers, rows, prefix_rows;
+    int32_t workers, per_head, rows, prefix_rows;
     size_t start, item, pre, group, prefix_start, prefix_item, prefix, rep, first, open, slots, prefix_slots, total;
 };
 
