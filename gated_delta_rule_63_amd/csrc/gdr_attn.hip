@@ -1,9 +1,10 @@
 // Causal attention over packed prompts (gdr_attn_prefill_fwd).
 //
-// A workgroup owns 128 consecutive tokens of the packed batch and one query head: four waves of 32 query rows.
-// Tiles of 64 keys and values go through the LDS once for all four.  The tokens are cut at fixed borders, not at
-// those of the sequences: a tile may hold several sequences' rows, each row sees the tokens from its sequence's
-// start to itself, and 128 one-token sequences are one workgroup's work.
+// A workgroup owns 32 RW consecutive tokens of the packed batch and one query head: RW row blocks of 32 query rows, each
+// a wave's, or two waves' (KW = 2) that take the two halves of every tile's keys and join their parts at the end.
+// Tiles of 64 keys and values go through the LDS once for all of them, copied a tile ahead.  The tokens are cut at
+// fixed borders, not at those of the sequences: a tile may hold several sequences' rows, each row sees the tokens
+// from its sequence's start to itself, and 128 one-token sequences are one workgroup's work.
 #include <hip/hip_runtime.h>
 
 #include "gdr_attn_device.h"
@@ -11,16 +12,16 @@
 namespace gdr {
 namespace {
 
-constexpr int kRows = 128;
-
-template <typename T, int D>
-__global__ __launch_bounds__(256, 2) void attn_prefill_kernel(AttnPrefillArgs a) {
+template <typename T, int D, int KW, int RW>
+__global__ __launch_bounds__(64 * KW * RW, 2) void attn_prefill_kernel(AttnPrefillArgs a) {
     using L = AttnTile<T, D>;
     using C = AttnCore<T, D>;
-    constexpr int kKeys = L::row_bytes == 512 ? 32 : 64, blocks = kKeys / 32;   // two tiles of K and V fit twice into a CU's LDS
+    constexpr int WAVES = KW * RW, kRows = 32 * RW;
+    constexpr int kKeys = L::row_bytes == 512 && KW == 1 ? 32 : 64, blocks = kKeys / 32 / KW;   // (two workgroups' tiles fit into a CU's LDS)
     constexpr int tile_bytes = kKeys * L::row_bytes;
     __shared__ __align__(1024) char lds[4 * tile_bytes];
     __shared__ uint32_t special_rows[2][2];
+    __shared__ float xch[RW][2][64];
     if (threadIdx.x < 4) special_rows[threadIdx.x >> 1][threadIdx.x & 1] = 0;
     int turn = 0;
 
@@ -39,13 +40,13 @@ __global__ __launch_bounds__(256, 2) void attn_prefill_kernel(AttnPrefillArgs a)
     const int end = a.cu ? a.cu[a.N] : (int)a.T;
     const int t0 = tile * kRows;
     if (t0 >= end) return;
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), half = lane >> 5;
+    const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6), half = lane >> 5, kw = wave % KW, rw = wave / KW;
     const int kvh = head / (a.HQ / a.HK);
-    const int t = t0 + 32 * wave + (lane & 31);
+    const int t = t0 + 32 * rw + (lane & 31);
     const int tc = min(t, end - 1);
     const int start = a.cu ? a.cu[find_seq(a.cu, a.N, tc)] : 0;
     const int lo = a.cu ? a.cu[find_seq(a.cu, a.N, t0)] : 0;
-    const int wlo = __builtin_amdgcn_readfirstlane(start), wfirst = t0 + 32 * wave;
+    const int wlo = __builtin_amdgcn_readfirstlane(start), wfirst = t0 + 32 * rw;
     const int wlate = __builtin_amdgcn_readlane(start, 31);
     const int latest = a.cu ? a.cu[find_seq(a.cu, a.N, min(t0 + kRows, end) - 1)] : 0;
     const int hi = min(t0 + kRows, end), whi = min(wfirst + 32, end);
@@ -57,7 +58,7 @@ __global__ __launch_bounds__(256, 2) void attn_prefill_kernel(AttnPrefillArgs a)
     const char* const vb = static_cast<const char*>(a.v) + (int64_t)kvh * D * L::es;
 
     // the lane's places in a tile's copies; rows behind the last token stand for it (no row sees them)
-    constexpr int per = L::template per<kKeys, 4>();
+    constexpr int per = L::template per<kKeys, WAVES>();
     const uint32_t ks = (uint32_t)a.k_stride * L::es, vs = (uint32_t)a.v_stride * L::es;
     uint32_t ko[per], vo[per];
     auto places = [&](int last) {
@@ -89,30 +90,36 @@ __global__ __launch_bounds__(256, 2) void attn_prefill_kernel(AttnPrefillArgs a)
         if (j0 + kKeys < hi) stage(j0 + kKeys, to);
         uint64_t special = 0;
         if (j0 + kKeys - 1 > t0 || j0 < latest) {
-            special = take_out_specials<T, D, kKeys, 4>(2 * base + 3 * tile_bytes - to, special_rows, turn, wave, lane);
+            special = take_out_specials<T, D, kKeys, WAVES>(2 * base + 3 * tile_bytes - to, special_rows, turn, wave, lane);
             turn ^= 1;
         }
         if (j0 < whi && j0 + kKeys > wlo) {
             f32x16_t s[blocks];
 #pragma unroll
-            for (int b = 0; b < blocks; ++b) s[b] = C::scores(b, at, q);
+            for (int b = 0; b < blocks; ++b) s[b] = C::scores(blocks * kw + b, at, q);
             auto seen = [&](int j) { return j >= start && j <= t; };
             if (j0 + kKeys - 1 > wfirst || j0 < wlate)
 #pragma unroll
                 for (int b = 0; b < blocks; ++b)
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) s[b][i] = seen(j0 + 32 * b + key_of(i, half)) ? s[b][i] : kNegInf;
-            r.add(s, a.c, 0, at);
+                    for (int i = 0; i < 16; ++i) s[b][i] = seen(j0 + 32 * (blocks * kw + b) + key_of(i, half)) ? s[b][i] : kNegInf;
+            r.add(s, a.c, blocks * kw, at);
             for (; special; special &= special - 1) {
-                const int j = j0 + __builtin_ctzll(special);
-                if (seen(j) && j < end) C::add_specials(vb + (int64_t)j * a.v_stride * L::es, half, r.o);
+                const int k = __builtin_ctzll(special), j = j0 + k;
+                if ((KW == 1 || k / 32 == kw) && seen(j) && j < end) C::add_specials(vb + (int64_t)j * a.v_stride * L::es, half, r.o);
             }
         }
         const uint32_t by = to - base == 0 ? (uint32_t)(-2 * tile_bytes) : 2 * tile_bytes;
         at.move(by);
         to -= by;
     }
-    const float l = both_sum(r.l), inv = reciprocal_sum(l);
+    float l = both_sum(r.l);
+    if constexpr (KW == 2) {
+        static_assert(RW * 64 * D / 2 * 4 <= 4 * tile_bytes, "outputs in the tiles' place");
+        join_waves<D>(r.o, r.m, l, a.c, reinterpret_cast<float*>(lds) + rw * (64 * D / 2) + lane, &xch[rw][0][lane], kw);
+        if (kw == 1) return;
+    }
+    const float inv = reciprocal_sum(l);
     char* row = t < end ? static_cast<char*>(a.o) + ((int64_t)t * a.HQ + head) * L::row_bytes : nullptr;
 #pragma unroll
     for (int b = 0; b < D / 32; ++b) r.o[b] *= inv;
@@ -120,18 +127,25 @@ __global__ __launch_bounds__(256, 2) void attn_prefill_kernel(AttnPrefillArgs a)
     if (a.lse && t < end && half == 0) a.lse[(int64_t)t * a.HQ + head] = log_sum(r.m * a.c, l);
 }
 
+template <typename T, int D, int KW, int RW>
+hipError_t start(AttnPrefillArgs a, hipStream_t stream) {
+    a.tiles = (int)((a.T + 32 * RW - 1) / (32 * RW));
+    attn_prefill_kernel<T, D, KW, RW><<<dim3((unsigned)(a.tiles * a.HQ)), 64 * KW * RW, 0, stream>>>(a);
+    return hipGetLastError();
+}
+
 template <typename T, int D>
 hipError_t launch(const AttnPrefillArgs& a, hipStream_t stream) {
-    attn_prefill_kernel<T, D><<<dim3((unsigned)(a.tiles * a.HQ)), 256, 0, stream>>>(a);
-    return hipGetLastError();
+    const int64_t wide = (a.T + 127) / 128 * a.HQ;
+    if (wide >= 512) return start<T, D, 1, 4>(a, stream);
+    return start<T, D, 2, 1>(a, stream);
 }
 
 }  // namespace
 
-int64_t attn_prefill_tiles(int64_t T) { return (T + kRows - 1) / kRows; }
+int64_t attn_prefill_tiles(int64_t T) { return (T + 31) / 32; }
 
 hipError_t launch_attn_prefill(AttnPrefillArgs a, int D, int io_dtype, hipStream_t stream) {
-    a.tiles = (int)attn_prefill_tiles(a.T);
     if (io_dtype == 1) return D == 64 ? launch<bf16_t, 64>(a, stream) : launch<bf16_t, 128>(a, stream);
     return D == 64 ? launch<float, 64>(a, stream) : launch<float, 128>(a, stream);
 }

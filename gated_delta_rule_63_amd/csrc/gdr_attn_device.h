@@ -322,6 +322,33 @@ template <typename T, int D> struct AttnRow {
     }
 };
 
+// The parts of two waves with the same rows and different keys: the odd one's (kw == 1) joins the even one's.  All waves
+// of the workgroup call it; `mine`: a float per lane and output register at stride 64, `stats`: two, for each pair.
+template <int D>
+__device__ __forceinline__ void join_waves(f32x16_t* o, float& m, float& l, float c, float* mine, float* stats, int kw) {
+    __syncthreads();
+    if (kw == 1) {
+        stats[0] = m;
+        stats[64] = l;
+#pragma unroll
+        for (int b = 0; b < D / 32; ++b)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) mine[(16 * b + i) * 64] = o[b][i];
+    }
+    __syncthreads();
+    if (kw == 0) {
+        const float m1 = stats[0], l1 = stats[64], mn = fmaxf(m, m1);
+        const float e0 = m == kNegInf ? 0.0f : __builtin_amdgcn_exp2f((m - mn) * c);
+        const float e1 = m1 == kNegInf ? 0.0f : __builtin_amdgcn_exp2f((m1 - mn) * c);
+#pragma unroll
+        for (int b = 0; b < D / 32; ++b)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[b][i] = o[b][i] * e0 + mine[(16 * b + i) * 64] * e1;
+        l = l * e0 + l1 * e1;
+        m = mn;
+    }
+}
+
 // Values that are not finite, in a tile of which some row does not see some key: 0 * inf must not reach that row.
 // Before the tile is used they become 0 in the LDS; the rows that see them then add them as they are.  `rows` holds
 // a bit per key, in two turns: the turn after the next barrier is cleared behind this one's.

@@ -7,8 +7,7 @@
 // workgroups, whatever the lengths are: the host does not know them, and every workgroup sums them up for itself.
 // A stretch may end inside a unit; such a part's maximum, sum and unnormalised output go to the workspace and are
 // joined by the last kernel.
-//   attn_groups_kernel  (with prefixes) each group's pages and length, each sequence's group
-//   attn_paged_kernel   the groups' prefixes, then what is each sequence's own
+//   attn_paged_kernel   the groups' prefixes (with prefixes), then what is each sequence's own
 //   attn_join_kernel    parts -> outputs
 #include <hip/hip_runtime.h>
 
@@ -41,40 +40,41 @@ __device__ __forceinline__ int stretch(const AttnPagedArgs& a, int tiles) {
     return max((int)(((int64_t)tiles + a.per_head - 1) / a.per_head), kMinTiles);
 }
 
-// One wave per group: the first sequence that is not padded gives the pages, whole pages are shared.  The wave behind
-// the last group takes the sequences of none.
-__global__ __launch_bounds__(256) void attn_groups_kernel(AttnPagedArgs a) {
-    const int lane = threadIdx.x & 63, g = blockIdx.x * 4 + (threadIdx.x >> 6);
-    if (g > a.groups) return;
-    auto offset = [&](int i) { return max(0, min(a.group_offsets[i], a.N)); };
-    if (g == a.groups) {
-        const int s = offset(0), e = offset(a.groups);
-        for (int n = lane; n < a.N; n += 64)
+// Group g's sequences [s, e), the first of them that is not padded (its pages are the group's; -1: none) and the keys in
+// whole pages of the prefix.
+struct Group { int s, e, rep, prefix; };
+__device__ __forceinline__ int group_offset(const AttnPagedArgs& a, int i) { return max(0, min(a.group_offsets[i], a.N)); }
+__device__ __forceinline__ Group group_of(const AttnPagedArgs& a, int g) {
+    Group r;
+    r.s = group_offset(a, g);
+    r.e = max(r.s, group_offset(a, g + 1));
+    r.rep = -1;
+    for (int n = r.s; n < r.e && r.rep < 0; ++n)
+        if (keys_of(a, a.context[n], a.cu ? a.cu[n + 1] - a.cu[n] : 1) > 0) r.rep = n;
+    const int64_t len = r.rep < 0 ? 0 : min((int64_t)max(0, a.prefix_lens[g]), a.capacity);
+    r.prefix = (int)(len >> a.page_shift << a.page_shift);
+    return r;
+}
+
+// Each sequence's group and the keys that it reads with it, for the kernels behind this one: workgroup by workgroup.
+__device__ __forceinline__ void tell_groups(const AttnPagedArgs& a) {
+    for (int g = blockIdx.x; g < a.groups; g += gridDim.x) {
+        const Group x = group_of(a, g);
+        for (int n = x.s + threadIdx.x; n < x.e; n += blockDim.x) { a.pre[n] = x.prefix; a.group[n] = g; }
+        if (threadIdx.x == 0) { a.prefix[g] = x.prefix; a.first[g] = x.s; }
+    }
+    if (blockIdx.x == 0) {   // the sequences of none
+        const int s = group_offset(a, 0), e = group_offset(a, a.groups);
+        if (threadIdx.x == 0) a.first[a.groups] = e;
+        for (int n = threadIdx.x; n < a.N; n += blockDim.x)
             if (n < s || n >= e) { a.pre[n] = 0; a.group[n] = -1; }
-        return;
-    }
-    const int s = offset(g), e = max(s, offset(g + 1));
-    int rep = -1;
-    for (int n0 = s; n0 < e && rep < 0; n0 += 64) {
-        const int n = n0 + lane;
-        const bool live = n < e && keys_of(a, a.context[n], a.cu ? a.cu[n + 1] - a.cu[n] : 1) > 0;
-        const uint64_t some = __ballot(live);
-        if (some) rep = n0 + __builtin_ctzll(some);
-    }
-    const int64_t len = rep < 0 ? 0 : min((int64_t)max(0, a.prefix_lens[g]), a.capacity);
-    const int pre = (int)(len >> a.page_shift << a.page_shift);
-    for (int n = s + lane; n < e; n += 64) { a.pre[n] = pre; a.group[n] = g; }
-    if (lane == 0) {
-        a.rep[g] = rep;
-        a.prefix[g] = pre;
-        a.first[g] = s;
-        if (g == a.groups - 1) a.first[a.groups] = e;
     }
 }
 
 struct Unit {
     int tok0, rows;      // first token, tokens * heads per key head
     int key0, key1;      // keys
+    int table;           // row of the page table
     int tiles, blocks;   // tiles of keys, blocks of rows; both 0 if there are no keys
 };
 
@@ -82,11 +82,12 @@ template <bool PREFIX>
 __device__ __forceinline__ Unit unit_of(const AttnPagedArgs& a, int u, int block_rows) {
     Unit r;
     if (PREFIX) {
-        const int s = a.first[u], e = a.first[u + 1];
+        const Group g = group_of(a, u);
         r.key0 = 0;
-        r.key1 = a.prefix[u];
-        r.tok0 = seq_first(a, s);
-        r.rows = (seq_first(a, e) - r.tok0) * a.per;
+        r.key1 = g.prefix;
+        r.tok0 = seq_first(a, g.s);
+        r.rows = (seq_first(a, g.e) - r.tok0) * a.per;
+        r.table = g.rep;
     } else {
         const int ctx = a.context[u];
         r.key0 = a.groups ? a.pre[u] : 0;
@@ -94,6 +95,7 @@ __device__ __forceinline__ Unit unit_of(const AttnPagedArgs& a, int u, int block
         const int tokens = seq_first(a, u + 1) - r.tok0;
         r.rows = tokens * a.per;
         r.key1 = keys_of(a, ctx, tokens);
+        r.table = u;
     }
     const bool some = r.key1 > r.key0 && r.rows > 0;
     r.tiles = some ? (r.key1 - r.key0 + kKeys - 1) / kKeys : 0;
@@ -211,13 +213,11 @@ __device__ __forceinline__ int find_items(const AttnPagedArgs& a, int units, int
     const int rb0 = a0 < a1 ? (a0 - t) / un.tiles : 0, rb1 = a0 < a1 ? (a1 - t - 1) / un.tiles : -1;
     const int count = rb1 - rb0 + 1, upto = wave_scan(count), at = upto - count, all = lane_value(upto, 63);
     if (count > 0) {
-        int table = u;
-        if (PREFIX) table = a.rep[u];
         for (int rb = rb0; rb <= rb1 && at + rb - rb0 < kItems; ++rb) {
             const int r = t + rb * un.tiles;
             Item it;
             it.token0 = un.tok0; it.row0 = rb * block_rows; it.rows = un.rows;
-            it.key0 = un.key0; it.key1 = un.key1; it.table = table;
+            it.key0 = un.key0; it.key1 = un.key1; it.table = un.table;
             it.tile = max(r, y) - r;
             it.count = min(r + un.tiles, ye) - r - it.tile;
             it.tiles = un.tiles; it.item = n + rb;
@@ -277,6 +277,7 @@ __global__ __launch_bounds__(64 * KW * RW, 2) void attn_paged_kernel(AttnPagedAr
     if (units > THREADS) cache = nullptr;
     if (w == 0 && threadIdx.x == 0) { starts[units] = line.tiles[THREADS]; item_starts[units] = line.items[THREADS]; }
     if (!PREFIX && threadIdx.x == 0) a.open[w].parts = 0;
+    if (PREFIX) tell_groups(a);
 
     // pages of a tile's four runs of 16 keys; -1: none
     struct Pages { int p[4]; };
@@ -417,29 +418,9 @@ __global__ __launch_bounds__(64 * KW * RW, 2) void attn_paged_kernel(AttnPagedAr
             f32x16_t* const o = acc.o;
             if constexpr (KW == 2) {   // the two waves of a row block: the odd one's part joins the even one's
                 // in the place of the last tile, which the next copies do not touch before the next barrier
-                float* const mine = reinterpret_cast<float*>(lds + (2 * tile_bytes - (to - base))) + rw * (64 * D / 2) + lane;
                 static_assert(RW * 64 * D / 2 * 4 <= 2 * tile_bytes, "outputs in a tile's place");
-                __syncthreads();
-                if (kw == 1) {
-                    xch[rw][0][lane] = m;
-                    xch[rw][1][lane] = l;
-#pragma unroll
-                    for (int b = 0; b < D / 32; ++b)
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) mine[(16 * b + i) * 64] = o[b][i];
-                }
-                __syncthreads();
-                if (kw == 0) {
-                    const float m1 = xch[rw][0][lane], l1 = xch[rw][1][lane], mn = fmaxf(m, m1);
-                    const float e0 = m == kNegInf ? 0.0f : __builtin_amdgcn_exp2f((m - mn) * a.c);
-                    const float e1 = m1 == kNegInf ? 0.0f : __builtin_amdgcn_exp2f((m1 - mn) * a.c);
-#pragma unroll
-                    for (int b = 0; b < D / 32; ++b)
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) o[b][i] = o[b][i] * e0 + mine[(16 * b + i) * 64] * e1;
-                    l = l * e0 + l1 * e1;
-                    m = mn;
-                }
+                float* const place = reinterpret_cast<float*>(lds + (2 * tile_bytes - (to - base))) + rw * (64 * D / 2);
+                join_waves<D>(o, m, l, a.c, place + lane, &xch[rw][0][lane], kw);
             }
             if (kw == 0) {
                 if (whole && !a.groups) {
@@ -575,7 +556,12 @@ __global__ __launch_bounds__(256) void attn_join_groups_kernel(AttnPagedArgs a) 
     };
     const Side own = side(unit_of<false>(a, seq, a.rows), seq, a.N, a.rows, a.start, a.item);
     Side pre{0, 0, 0, 0};
-    if (group >= 0) pre = side(unit_of<true>(a, group, a.prefix_rows), group, a.groups, a.prefix_rows, a.prefix_start, a.prefix_item);
+    if (group >= 0) {
+        Unit un{};
+        un.tok0 = seq_first(a, a.first[group]);
+        un.tiles = (a.prefix[group] + kKeys - 1) / kKeys;
+        pre = side(un, group, a.groups, a.prefix_rows, a.prefix_start, a.prefix_item);
+    }
     join_row<T, D>(a, token, head, pre.parts + own.parts, [&](int k, int& stats, int& rows) {
         const bool p = k < pre.parts;
         const Side& s = p ? pre : own;
@@ -597,10 +583,7 @@ hipError_t launch_part(const AttnPagedArgs& a, int rows, hipStream_t stream) {
 template <typename T, int D>
 hipError_t launch(const AttnPagedArgs& a, hipStream_t stream) {
     hipError_t e = hipSuccess;
-    if (a.groups) {
-        attn_groups_kernel<<<dim3((unsigned)(a.groups / 4 + 1)), 256, 0, stream>>>(a);
-        if ((e = hipGetLastError()) == hipSuccess) e = launch_part<T, D, true>(a, a.prefix_rows, stream);
-    }
+    if (a.groups) e = launch_part<T, D, true>(a, a.prefix_rows, stream);
     if (e == hipSuccess) e = launch_part<T, D, false>(a, a.rows, stream);
     if (e != hipSuccess) return e;
     if (a.groups) attn_join_groups_kernel<T, D><<<dim3((unsigned)((a.T * a.HQ + 3) / 4)), 256, 0, stream>>>(a);
@@ -620,7 +603,7 @@ AttnPagedPlan attn_paged_plan(int64_t T, int32_t N, int32_t HQ, int32_t HK, int 
     p.per_head = max(1, (D * io_bytes <= 256 ? 512 : 256) / HK);
     p.workers = p.per_head * HK;
     p.rows = rows_for(per * max_q_len);
-    p.prefix_rows = rows_for(per * T);
+    p.prefix_rows = groups ? rows_for((per * T + groups - 1) / groups) : 0;   // of a group of average size
     auto slots = [&](int rows, int64_t units) {
         // two open parts per workgroup; with prefixes nothing is written straight to the output
         int64_t n = 2 * (int64_t)p.workers;
@@ -637,7 +620,6 @@ AttnPagedPlan attn_paged_plan(int64_t T, int32_t N, int32_t HQ, int32_t HK, int 
         p.prefix_start = take((size_t)(groups + 1) * 4);
         p.prefix_item = take((size_t)(groups + 1) * 4);
         p.prefix = take((size_t)groups * 4);
-        p.rep = take((size_t)groups * 4);
         p.first = take((size_t)(groups + 1) * 4);
         p.prefix_slots = take(slots(p.prefix_rows, groups));
     }
@@ -658,7 +640,6 @@ hipError_t launch_attn_paged(AttnPagedArgs a, const AttnPagedPlan& p, char* ws, 
     a.prefix_start = reinterpret_cast<int32_t*>(ws + p.prefix_start);
     a.prefix_item = reinterpret_cast<int32_t*>(ws + p.prefix_item);
     a.prefix = reinterpret_cast<int32_t*>(ws + p.prefix);
-    a.rep = reinterpret_cast<int32_t*>(ws + p.rep);
     a.first = reinterpret_cast<int32_t*>(ws + p.first);
     a.open = reinterpret_cast<AttnOpen*>(ws + p.open);
     a.slots = ws + p.slots;

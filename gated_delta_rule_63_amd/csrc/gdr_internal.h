@@ -291,7 +291,7 @@ struct AttnPagedArgs {
     int32_t *start, *prefix_start;   // [N + 1], [groups + 1]: tiles before each unit on the line of a key head
     int32_t *item, *prefix_item;     // row blocks before each unit
     int32_t *pre, *group;        // [N]: keys read with the group's prefix, the group or -1
-    int32_t *prefix, *rep;       // [groups]: keys of the prefix, the sequence whose pages hold them
+    int32_t* prefix;             // [groups]: keys of the prefix
     int32_t* first;              // [groups + 1]: the groups' first sequences
     AttnOpen* open;              // [workers]
     char *slots, *prefix_slots;  // parts: [rows, D] fp32, maxima, sums
@@ -299,7 +299,7 @@ struct AttnPagedArgs {
 
 struct AttnPagedPlan {
     int32_t workers, per_head, rows, prefix_rows;
-    size_t start, item, pre, group, prefix_start, prefix_item, prefix, rep, first, open, slots, prefix_slots, total;
+    size_t start, item, pre, group, prefix_start, prefix_item, prefix, first, open, slots, prefix_slots, total;
 };
 
 AttnPagedPlan attn_paged_plan(int64_t T, int32_t N, int32_t HQ, int32_t HK, int D, int io_bytes, int32_t max_q_len, int32_t groups);
