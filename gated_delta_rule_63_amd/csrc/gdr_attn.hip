@@ -2,15 +2,18 @@
 //
 // A workgroup owns 32 RW consecutive tokens of the packed batch and one query head: RW row blocks of 32 query rows, each
 // a wave's, or two waves' (KW = 2) that take the two halves of every tile's keys and join their parts at the end.
-// Tiles of 64 keys and values go through the LDS once for all of them, copied a tile ahead.  The tokens are cut at
-// fixed borders, not at those of the sequences: a tile may hold several sequences' rows, each row sees the tokens
-// from its sequence's start to itself, and 128 one-token sequences are one workgroup's work.
+// Tiles of 64 keys and values go through the LDS once for all of them, copied a tile ahead.  Up to 64 sequences are cut
+// into rows each for itself.  More are cut at fixed borders of the packed batch: a workgroup's rows may be several
+// sequences', each row sees the tokens from its sequence's start to itself, and 128 one-token sequences are one
+// workgroup's work.
 #include <hip/hip_runtime.h>
 
 #include "gdr_attn_device.h"
 
 namespace gdr {
 namespace {
+
+constexpr int kSorted = 64;   // sequences, at most, whose tiles are sorted by cost
 
 template <typename T, int D, int KW, int RW>
 __global__ __launch_bounds__(64 * KW * RW, 2) void attn_prefill_kernel(AttnPrefillArgs a) {
@@ -25,31 +28,50 @@ __global__ __launch_bounds__(64 * KW * RW, 2) void attn_prefill_kernel(AttnPrefi
     if (threadIdx.x < 4) special_rows[threadIdx.x >> 1][threadIdx.x & 1] = 0;
     int turn = 0;
 
-    int tile, head;
+    int rank, head;
     {
         const int b = blockIdx.x;
         if (a.HQ % 8 == 0) {  // workgroups go round the eight XCDs: each keeps to its own heads' keys and values
             const int per = a.HQ / 8, x = b & 7, i = b >> 3;
-            tile = a.tiles - 1 - i / per;
+            rank = i / per;
             head = x * per + i % per;
         } else {
-            tile = a.tiles - 1 - b / a.HQ;
+            rank = b / a.HQ;
             head = b % a.HQ;
         }
     }
-    const int end = a.cu ? a.cu[a.N] : (int)a.T;
-    const int t0 = tile * kRows;
-    if (t0 >= end) return;
     const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6), half = lane >> 5, kw = wave % KW, rw = wave / KW;
-    const int kvh = head / (a.HQ / a.HK);
-    const int t = t0 + 32 * rw + (lane & 31);
-    const int tc = min(t, end - 1);
-    const int start = a.cu ? a.cu[find_seq(a.cu, a.N, tc)] : 0;
-    const int lo = a.cu ? a.cu[find_seq(a.cu, a.N, t0)] : 0;
-    const int wlo = __builtin_amdgcn_readfirstlane(start), wfirst = t0 + 32 * rw;
-    const int wlate = __builtin_amdgcn_readlane(start, 31);
-    const int latest = a.cu ? a.cu[find_seq(a.cu, a.N, min(t0 + kRows, end) - 1)] : 0;
-    const int hi = min(t0 + kRows, end), whi = min(wfirst + 32, end);
+    const int end = a.cu ? uniform(a.cu[a.N]) : (int)a.T;
+    // rows [t0, stop); `lo`: the first key that any of them sees; the lane's token t sees [start, t]
+    int t0, stop, lo, start, latest;
+    if (a.N <= kSorted) {
+        // tiles are cut at the sequences' borders, the longest sequence first and its last tile first: what is begun last
+        // is short, and neighbours share their keys and values in the L2
+        const int first = lane < a.N && a.cu ? a.cu[lane] : 0, len = lane < a.N ? (a.cu ? a.cu[lane + 1] - first : (int)a.T) : 0;
+        const int tiles = (len + kRows - 1) / kRows;
+        int before = 0;   // tiles of the sequences ahead of the lane's
+        for (int j = 0; j < a.N; ++j) {
+            const int other = lane_value(len, j);
+            before += other > len || (other == len && j < lane) ? (other + kRows - 1) / kRows : 0;
+        }
+        const uint64_t here = __ballot(before <= rank && rank < before + tiles);
+        if (!here) return;
+        const int n = __builtin_ctzll(here), p = lane_value(before + tiles - 1, n) - rank;
+        lo = start = latest = lane_value(first, n);
+        t0 = lo + p * kRows;
+        stop = min(t0 + kRows, lo + lane_value(len, n));
+    } else {
+        // at fixed borders, the last first
+        t0 = (a.tiles - 1 - rank) * kRows;
+        if (t0 >= end) return;
+        stop = min(t0 + kRows, end);
+        lo = uniform(a.cu[find_seq(a.cu, a.N, t0)]);
+        latest = uniform(a.cu[find_seq(a.cu, a.N, stop - 1)]);
+        start = a.cu[find_seq(a.cu, a.N, min(t0 + 32 * rw + (lane & 31), stop - 1))];
+    }
+    const int t = t0 + 32 * rw + (lane & 31), tc = min(t, stop - 1), kvh = head / (a.HQ / a.HK);
+    const int wlo = uniform(start), wfirst = t0 + 32 * rw, wlate = lane_value(start, 31);
+    const int hi = stop, whi = min(wfirst + 32, stop);
 
     typename C::Q q;
     C::load_q(static_cast<const char*>(a.q) + ((int64_t)tc * a.q_stride + (int64_t)head * D) * L::es, half, a.negate, q);
@@ -106,7 +128,7 @@ __global__ __launch_bounds__(64 * KW * RW, 2) void attn_prefill_kernel(AttnPrefi
             r.add(s, a.c, blocks * kw, at);
             for (; special; special &= special - 1) {
                 const int k = __builtin_ctzll(special), j = j0 + k;
-                if ((KW == 1 || k / 32 == kw) && seen(j) && j < end) C::add_specials(vb + (int64_t)j * a.v_stride * L::es, half, r.o);
+                if ((KW == 1 || k / 32 == kw) && seen(j) && j < stop) C::add_specials(vb + (int64_t)j * a.v_stride * L::es, half, r.o);
             }
         }
         const uint32_t by = to - base == 0 ? (uint32_t)(-2 * tile_bytes) : 2 * tile_bytes;
@@ -120,16 +142,16 @@ __global__ __launch_bounds__(64 * KW * RW, 2) void attn_prefill_kernel(AttnPrefi
         if (kw == 1) return;
     }
     const float inv = reciprocal_sum(l);
-    char* row = t < end ? static_cast<char*>(a.o) + ((int64_t)t * a.HQ + head) * L::row_bytes : nullptr;
+    char* row = t < stop ? static_cast<char*>(a.o) + ((int64_t)t * a.HQ + head) * L::row_bytes : nullptr;
 #pragma unroll
     for (int b = 0; b < D / 32; ++b) r.o[b] *= inv;
     C::store(row, half, r.o);
-    if (a.lse && t < end && half == 0) a.lse[(int64_t)t * a.HQ + head] = log_sum(r.m * a.c, l);
+    if (a.lse && t < stop && half == 0) a.lse[(int64_t)t * a.HQ + head] = log_sum(r.m * a.c, l);
 }
 
 template <typename T, int D, int KW, int RW>
 hipError_t start(AttnPrefillArgs a, hipStream_t stream) {
-    a.tiles = (int)((a.T + 32 * RW - 1) / (32 * RW));
+    a.tiles = (int)((a.T + 32 * RW - 1) / (32 * RW)) + (a.N <= kSorted ? a.N - 1 : 0);
     attn_prefill_kernel<T, D, KW, RW><<<dim3((unsigned)(a.tiles * a.HQ)), 64 * KW * RW, 0, stream>>>(a);
     return hipGetLastError();
 }
@@ -143,7 +165,7 @@ hipError_t launch(const AttnPrefillArgs& a, hipStream_t stream) {
 
 }  // namespace
 
-int64_t attn_prefill_tiles(int64_t T) { return (T + 31) / 32; }
+int64_t attn_prefill_tiles(int64_t T) { return (T + 31) / 32 + kSorted; }
 
 hipError_t launch_attn_prefill(AttnPrefillArgs a, int D, int io_dtype, hipStream_t stream) {
     if (io_dtype == 1) return D == 64 ? launch<bf16_t, 64>(a, stream) : launch<bf16_t, 128>(a, stream);

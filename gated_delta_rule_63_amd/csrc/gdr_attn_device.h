@@ -61,6 +61,30 @@ __device__ __forceinline__ void copy_to_lds(const char* base, uint32_t off, uint
 }
 __device__ __forceinline__ void wait_copies() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
+// inclusive sum over the lanes of a wave
+template <int CTRL, int ROWS, bool ZERO> __device__ __forceinline__ int dpp_add(int x) {
+    return x + __builtin_amdgcn_update_dpp(0, x, CTRL, ROWS, 0xF, ZERO);
+}
+__device__ __forceinline__ int wave_scan(int x) {
+    x = dpp_add<0x111, 0xF, true>(x);    // row_shr 1, 2, 4, 8: within rows of 16 lanes
+    x = dpp_add<0x112, 0xF, true>(x);
+    x = dpp_add<0x114, 0xF, true>(x);
+    x = dpp_add<0x118, 0xF, true>(x);
+    x = dpp_add<0x142, 0xA, false>(x);   // row 0's total to row 1, row 2's to row 3
+    x = dpp_add<0x143, 0xC, false>(x);   // that of rows 0 and 1 to rows 2 and 3
+    return x;
+}
+__device__ __forceinline__ int lane_value(int x, int lane) { return __builtin_amdgcn_readlane(x, lane); }
+__device__ __forceinline__ int wave_max(int x) {   // x >= 0
+    x = max(x, __builtin_amdgcn_update_dpp(0, x, 0x111, 0xF, 0xF, true));
+    x = max(x, __builtin_amdgcn_update_dpp(0, x, 0x112, 0xF, 0xF, true));
+    x = max(x, __builtin_amdgcn_update_dpp(0, x, 0x114, 0xF, 0xF, true));
+    x = max(x, __builtin_amdgcn_update_dpp(0, x, 0x118, 0xF, 0xF, true));
+    x = max(x, __builtin_amdgcn_update_dpp(0, x, 0x142, 0xA, 0xF, false));
+    x = max(x, __builtin_amdgcn_update_dpp(0, x, 0x143, 0xC, 0xF, false));
+    return lane_value(x, 63);
+}
+
 // sequence of a token below cu[N]: the last n with cu[n] <= t (so an empty sequence is never found)
 __device__ __forceinline__ int find_seq(const int32_t* cu, int N, int t) {
     int lo = 0, hi = N;

@@ -103,21 +103,6 @@ __device__ __forceinline__ Unit unit_of(const AttnPagedArgs& a, int u, int block
     return r;
 }
 
-// inclusive sum over the lanes of a wave
-template <int CTRL, int ROWS, bool ZERO> __device__ __forceinline__ int dpp_add(int x) {
-    return x + __builtin_amdgcn_update_dpp(0, x, CTRL, ROWS, 0xF, ZERO);
-}
-__device__ __forceinline__ int wave_scan(int x) {
-    x = dpp_add<0x111, 0xF, true>(x);    // row_shr 1, 2, 4, 8: within rows of 16 lanes
-    x = dpp_add<0x112, 0xF, true>(x);
-    x = dpp_add<0x114, 0xF, true>(x);
-    x = dpp_add<0x118, 0xF, true>(x);
-    x = dpp_add<0x142, 0xA, false>(x);   // row 0's total to row 1, row 2's to row 3
-    x = dpp_add<0x143, 0xC, false>(x);   // that of rows 0 and 1 to rows 2 and 3
-    return x;
-}
-__device__ __forceinline__ int lane_value(int x, int lane) { return __builtin_amdgcn_readlane(x, lane); }
-
 // The line of tiles of one key head (below 2^31: the host sees to it): sums before every THREADS-th part of the units,
 // in the LDS.
 template <int THREADS> struct Line {
