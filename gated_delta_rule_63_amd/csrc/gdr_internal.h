@@ -237,10 +237,9 @@ struct RopeArgs {
     void *q_out, *k_out;         // k_out may be NULL
     int64_t T;
     int32_t N, HQ, HK;
-    int32_t per;                 // set by the launcher: tokens per workgroup
 };
 
-hipError_t launch_rope_append(RopeArgs a, int D, int io_dtype, hipStream_t stream);
+hipError_t launch_rope_append(const RopeArgs& a, int D, int io_dtype, hipStream_t stream);
 
 // Attention over packed prompts (gdr_attn.hip).  Strides in elements from one token's row to the next.
 struct AttnPrefillArgs {
