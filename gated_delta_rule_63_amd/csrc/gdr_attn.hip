@@ -1,8 +1,8 @@
 // Causal attention over packed prompts (gdr_attn_prefill_fwd).
 //
 // A workgroup owns 32 RW consecutive tokens of the packed batch and one query head: RW row blocks of 32 query rows, each
-// a wave's, or two waves' (KW = 2) that take the two halves of every tile's keys and join their parts at the end.
-// Tiles of 64 keys and values go through the LDS once for all of them, copied a tile ahead.  Up to 64 sequences are cut
+// a wave's, or KW waves' that share every tile's keys and join their parts at the end.
+// Tiles of 32 to 128 keys and values go through the LDS once for all of them, copied a tile ahead.  Up to 64 sequences are cut
 // into rows each for itself.  More are cut at fixed borders of the packed batch: a workgroup's rows may be several
 // sequences', each row sees the tokens from its sequence's start to itself, and 128 one-token sequences are one
 // workgroup's work.
@@ -20,12 +20,12 @@ __global__ __launch_bounds__(64 * KW * RW, 2) void attn_prefill_kernel(AttnPrefi
     using L = AttnTile<T, D>;
     using C = AttnCore<T, D>;
     constexpr int WAVES = KW * RW, kRows = 32 * RW;
-    constexpr int kKeys = L::row_bytes == 512 && KW == 1 ? 32 : 64, blocks = kKeys / 32 / KW;   // (two workgroups' tiles fit into a CU's LDS)
+    constexpr int kKeys = KW == 4 ? 128 : L::row_bytes == 512 && KW == 1 ? 32 : 64, blocks = kKeys / 32 / KW;
     constexpr int tile_bytes = kKeys * L::row_bytes;
     __shared__ __align__(1024) char lds[4 * tile_bytes];
-    __shared__ uint32_t special_rows[2][2];
-    __shared__ float xch[RW][2][64];
-    if (threadIdx.x < 4) special_rows[threadIdx.x >> 1][threadIdx.x & 1] = 0;
+    __shared__ uint32_t special_rows[2][kKeys / 32];
+    __shared__ float xch[RW * KW][64];
+    if (threadIdx.x < kKeys / 16) special_rows[threadIdx.x / (kKeys / 32)][threadIdx.x % (kKeys / 32)] = 0;
     int turn = 0;
 
     int rank, head;
@@ -110,10 +110,10 @@ __global__ __launch_bounds__(64 * KW * RW, 2) void attn_prefill_kernel(AttnPrefi
         wait_copies();
         __syncthreads();
         if (j0 + kKeys < hi) stage(j0 + kKeys, to);
-        uint64_t special = 0;
-        if (j0 + kKeys - 1 > t0 || j0 < latest) {
-            special = take_out_specials<T, D, kKeys, WAVES>(2 * base + 3 * tile_bytes - to, special_rows, turn, wave, lane);
+        const bool uneven = j0 + kKeys - 1 > t0 || j0 < latest;
+        if (uneven) {
             turn ^= 1;
+            take_out_specials<T, D, kKeys, WAVES>(2 * base + 3 * tile_bytes - to, special_rows, turn, wave, lane);
         }
         if (j0 < whi && j0 + kKeys > wlo) {
             f32x16_t s[blocks];
@@ -126,20 +126,22 @@ __global__ __launch_bounds__(64 * KW * RW, 2) void attn_prefill_kernel(AttnPrefi
 #pragma unroll
                     for (int i = 0; i < 16; ++i) s[b][i] = seen(j0 + 32 * (blocks * kw + b) + key_of(i, half)) ? s[b][i] : kNegInf;
             r.add(s, a.c, blocks * kw, at);
-            for (; special; special &= special - 1) {
-                const int k = __builtin_ctzll(special), j = j0 + k;
-                if ((KW == 1 || k / 32 == kw) && seen(j) && j < stop) C::add_specials(vb + (int64_t)j * a.v_stride * L::es, half, r.o);
-            }
+            if (uneven)
+                for (int b = 0; b < blocks; ++b)
+                    for (uint32_t left = uniform((int)special_rows[turn][blocks * kw + b]); left; left &= left - 1) {
+                        const int j = j0 + 32 * (blocks * kw + b) + __builtin_ctz(left);
+                        if (seen(j) && j < stop) C::add_specials(vb + (int64_t)j * a.v_stride * L::es, half, r.o);
+                    }
         }
         const uint32_t by = to - base == 0 ? (uint32_t)(-2 * tile_bytes) : 2 * tile_bytes;
         at.move(by);
         to -= by;
     }
     float l = both_sum(r.l);
-    if constexpr (KW == 2) {
-        static_assert(RW * 64 * D / 2 * 4 <= 4 * tile_bytes, "outputs in the tiles' place");
-        join_waves<D>(r.o, r.m, l, a.c, reinterpret_cast<float*>(lds) + rw * (64 * D / 2) + lane, &xch[rw][0][lane], kw);
-        if (kw == 1) return;
+    if constexpr (KW > 1) {
+        static_assert(RW * KW * 64 * D <= 4 * tile_bytes, "outputs in the tiles' place");
+        join_waves<D, KW>(r.o, r.m, l, a.c, reinterpret_cast<float*>(lds) + rw * (KW * 64 * D / 4), xch[rw * KW], kw, lane);
+        if (kw > 0) return;
     }
     const float inv = reciprocal_sum(l);
     char* row = t < stop ? static_cast<char*>(a.o) + ((int64_t)t * a.HQ + head) * L::row_bytes : nullptr;
@@ -158,9 +160,17 @@ hipError_t start(AttnPrefillArgs a, hipStream_t stream) {
 
 template <typename T, int D>
 hipError_t launch(const AttnPrefillArgs& a, hipStream_t stream) {
+    // `wide`: workgroups of 128 rows.  From 640 on they fill the card, and rows that share a tile's reads count most: 32
+    // heads, D = 128, bf16, 2000 tokens 55 us (64 rows 56), 4000 148 (173); 16 heads, D = 64, 6000 tokens 116 (116),
+    // 16000 563 (646); fp32, 8 heads, D = 128, 12000 tokens 1244 (1277).  Below, 64 rows by two waves each: 32 heads, D =
+    // 128, 1000 tokens 24 us (128 rows 28), fp32 6000 tokens 400 (612).  As long as 32 rows by four waves are about one
+    // round of the card, that: 16 heads, D = 64, 1000 tokens 13 us (64 rows 15), twice as many 27 (26); 8 heads, D = 128,
+    // 1000 tokens 20 (21), 2000 38 (36); fp32, D = 64, 3001 tokens 70 (89).
     const int64_t wide = (a.T + 127) / 128 * a.HQ;
-    if (wide >= 512) return start<T, D, 1, 4>(a, stream);
-    return start<T, D, 2, 1>(a, stream);
+    constexpr int es = Elem<T>::bytes, few = es == 4 ? 256 : D == 64 ? 128 : 64;
+    if constexpr (D * es <= 256)
+        if (wide <= few) return start<T, D, 4, 1>(a, stream);
+    return wide < 640 ? start<T, D, 2, 2>(a, stream) : start<T, D, 1, 4>(a, stream);
 }
 
 }  // namespace

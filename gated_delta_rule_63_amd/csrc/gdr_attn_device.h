@@ -346,38 +346,44 @@ template <typename T, int D> struct AttnRow {
     }
 };
 
-// The parts of two waves with the same rows and different keys: the odd one's (kw == 1) joins the even one's.  All waves
-// of the workgroup call it; `mine`: a float per lane and output register at stride 64, `stats`: two, for each pair.
-template <int D>
-__device__ __forceinline__ void join_waves(f32x16_t* o, float& m, float& l, float c, float* mine, float* stats, int kw) {
-    __syncthreads();
-    if (kw == 1) {
-        stats[0] = m;
-        stats[64] = l;
+// The parts of the KW waves with the same rows and different keys, joined in that with kw == 0: the upper half of the
+// waves hands its parts to the lower half until one is left.  All waves of the workgroup call it.  place: KW / 2 times
+// 64 lanes' outputs, stats: as many times two floats a lane, of the waves with the same rows.
+template <int D, int KW>
+__device__ __forceinline__ void join_waves(f32x16_t* o, float& m, float& l, float c, float* place, float* stats, int kw, int lane) {
 #pragma unroll
-        for (int b = 0; b < D / 32; ++b)
+    for (int n = KW / 2; n > 0; n /= 2) {
+        float* const mine = place + (kw % n) * (64 * D / 2) + lane;
+        float* const st = stats + (kw % n) * 128 + lane;
+        __syncthreads();
+        if (kw >= n && kw < 2 * n) {
+            st[0] = m;
+            st[64] = l;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) mine[(16 * b + i) * 64] = o[b][i];
-    }
-    __syncthreads();
-    if (kw == 0) {
-        const float m1 = stats[0], l1 = stats[64], mn = fmaxf(m, m1);
-        const float e0 = m == kNegInf ? 0.0f : __builtin_amdgcn_exp2f((m - mn) * c);
-        const float e1 = m1 == kNegInf ? 0.0f : __builtin_amdgcn_exp2f((m1 - mn) * c);
+            for (int b = 0; b < D / 32; ++b)
 #pragma unroll
-        for (int b = 0; b < D / 32; ++b)
+                for (int i = 0; i < 16; ++i) mine[(16 * b + i) * 64] = o[b][i];
+        }
+        __syncthreads();
+        if (kw < n) {
+            const float m1 = st[0], l1 = st[64], mn = fmaxf(m, m1);
+            const float e0 = m == kNegInf ? 0.0f : __builtin_amdgcn_exp2f((m - mn) * c);
+            const float e1 = m1 == kNegInf ? 0.0f : __builtin_amdgcn_exp2f((m1 - mn) * c);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) o[b][i] = o[b][i] * e0 + mine[(16 * b + i) * 64] * e1;
-        l = l * e0 + l1 * e1;
-        m = mn;
+            for (int b = 0; b < D / 32; ++b)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[b][i] = o[b][i] * e0 + mine[(16 * b + i) * 64] * e1;
+            l = l * e0 + l1 * e1;
+            m = mn;
+        }
     }
 }
 
 // Values that are not finite, in a tile of which some row does not see some key: 0 * inf must not reach that row.
-// Before the tile is used they become 0 in the LDS; the rows that see them then add them as they are.  `rows` holds
-// a bit per key, in two turns: the turn after the next barrier is cleared behind this one's.
+// Before the tile is used they become 0 in the LDS; the rows that see them then add them as they are.  rows[turn] holds
+// a bit per key, in two turns: the other one is cleared here, behind the barrier that ends its use.
 template <typename T, int D, int KEYS, int WAVES>
-__device__ __forceinline__ uint64_t take_out_specials(uint32_t v, uint32_t (*rows)[2], int turn, int wave, int lane) {
+__device__ __forceinline__ void take_out_specials(uint32_t v, uint32_t (*rows)[KEYS / 32], int turn, int wave, int lane) {
     using L = AttnTile<T, D>;
     typedef __attribute__((address_space(3))) uint4 lds_u4;
     constexpr int per = L::template per<KEYS, WAVES>();
@@ -395,9 +401,7 @@ __device__ __forceinline__ uint64_t take_out_specials(uint32_t v, uint32_t (*row
         }
     }
     __syncthreads();
-    if (threadIdx.x < 2) rows[turn ^ 1][threadIdx.x] = 0;
-    const uint32_t lo = __builtin_amdgcn_readfirstlane(rows[turn][0]), hi = __builtin_amdgcn_readfirstlane(rows[turn][1]);
-    return (uint64_t)hi << 32 | lo;
+    if (threadIdx.x < KEYS / 32) rows[turn ^ 1][threadIdx.x] = 0;
 }
 
 // 1 / l; 0 for a row that saw nothing; a NaN stays one

@@ -243,7 +243,7 @@ __global__ __launch_bounds__(64 * KW * RW, 2) void attn_paged_kernel(AttnPagedAr
     __shared__ Line<THREADS> line;
     __shared__ Item items[kItems];
     __shared__ int found, rest;
-    __shared__ uint32_t special_rows[2][2];
+    __shared__ uint32_t special_rows[2][kKeys / 32];
 
     const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6), half = lane >> 5;
     const int kw = wave % KW, rw = wave / KW;
@@ -363,10 +363,10 @@ __global__ __launch_bounds__(64 * KW * RW, 2) void attn_paged_kernel(AttnPagedAr
 
                 const int j0 = it.key0 + tile * kKeys;
                 // tokens see less than the last of theirs: some rows do not see what others do
-                uint64_t special = 0;
-                if (!PREFIX && it.rows > a.per && j0 + kKeys > it.key1 - it.rows / a.per + 1) {
-                    special = take_out_specials<T, D, kKeys, WAVES>(v, special_rows, turn, wave, lane);
+                const bool uneven = !PREFIX && it.rows > a.per && j0 + kKeys > it.key1 - it.rows / a.per + 1;
+                if (uneven) {
                     turn ^= 1;
+                    take_out_specials<T, D, kKeys, WAVES>(v, special_rows, turn, wave, lane);
                 }
                 f32x16_t s[blocks];
 #pragma unroll
@@ -384,16 +384,16 @@ __global__ __launch_bounds__(64 * KW * RW, 2) void attn_paged_kernel(AttnPagedAr
                         }
                 }
                 acc.add(s, a.c, KW == 2 ? kw : 0, at);
-                for (; special; special &= special - 1) {
-                    const int k = __builtin_ctzll(special), j = j0 + k;
-                    if ((KW == 1 || k / 32 == kw) && j < seen) {
-                        const int p = k < 16 ? now.p[0] : k < 32 ? now.p[1] : k < 48 ? now.p[2] : now.p[3];
-                        if (p >= 0)
-                            C::add_specials(static_cast<const char*>(a.v_pages) +
-                                            ((((int64_t)p * a.HK + kvh) << a.page_shift) + (j & ((1 << a.page_shift) - 1))) * L::row_bytes,
-                                            half, acc.o);
-                    }
-                }
+                if (uneven)
+                    for (int b = 0; b < blocks; ++b)
+                        for (uint32_t left = uniform((int)special_rows[turn][blocks * kw + b]); left; left &= left - 1) {
+                            const int k = 32 * (blocks * kw + b) + __builtin_ctz(left), j = j0 + k;
+                            const int p = k < 16 ? now.p[0] : k < 32 ? now.p[1] : k < 48 ? now.p[2] : now.p[3];
+                            if (j < seen && p >= 0)
+                                C::add_specials(static_cast<const char*>(a.v_pages) +
+                                                ((((int64_t)p * a.HK + kvh) << a.page_shift) + (j & ((1 << a.page_shift) - 1))) * L::row_bytes,
+                                                half, acc.o);
+                        }
                 at.move(to == base ? (uint32_t)(-2 * tile_bytes) : 2 * tile_bytes);
                 now = ahead;
             }
@@ -401,11 +401,11 @@ __global__ __launch_bounds__(64 * KW * RW, 2) void attn_paged_kernel(AttnPagedAr
             const bool whole = it.count == it.tiles;
             float l = both_sum(acc.l), m = acc.m;
             f32x16_t* const o = acc.o;
-            if constexpr (KW == 2) {   // the two waves of a row block: the odd one's part joins the even one's
+            if constexpr (KW == 2) {   // the two waves of a row block
                 // in the place of the last tile, which the next copies do not touch before the next barrier
                 static_assert(RW * 64 * D / 2 * 4 <= 2 * tile_bytes, "outputs in a tile's place");
                 float* const place = reinterpret_cast<float*>(lds + (2 * tile_bytes - (to - base))) + rw * (64 * D / 2);
-                join_waves<D>(o, m, l, a.c, place + lane, &xch[rw][0][lane], kw);
+                join_waves<D, KW>(o, m, l, a.c, place, &xch[rw][0][0], kw, lane);
             }
             if (kw == 0) {
                 if (whole && !a.groups) {
