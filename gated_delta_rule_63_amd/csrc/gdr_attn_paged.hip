@@ -436,123 +436,124 @@ __global__ __launch_bounds__(64 * KW * RW, 2) void attn_paged_kernel(AttnPagedAr
     }
 }
 
-// Parts of a row, joined by one wave: a lane reads the maximum and the sum of one part, then all read the rows.
-template <typename T, int D, typename F>
+// A part of a row: its output in the slot and, `stats` and `stats + rows` floats behind, its maximum and its sum.
+struct Part { const float* row; int stats, rows; };
+template <int D> __device__ __forceinline__ Part part_at(const char* slots, int64_t slot, int rows, int row) {
+    return {reinterpret_cast<const float*>(slots + slot * ((int64_t)rows * (D + 2) * 4)) + row * D, rows * D + row - row * D, rows};
+}
+
+// Parts of a row, joined by LANES = 32 or 64 lanes: a lane reads the maximum and the sum of one part, then each half of
+// the wave reads the rows, all of them or every second one.
+template <typename T, int D, int LANES, typename F>
 __device__ __forceinline__ void join_row(const AttnPagedArgs& a, int token, int head, int parts, F part_of) {
-    constexpr int V = D / 64;
-    const int lane = threadIdx.x & 63;
-    float m = kNegInf, l = 0.0f, o[V] = {};
-    for (int k0 = 0; k0 < parts; k0 += 64) {
-        const int n = min(64, parts - k0);
-        const float* row = nullptr;
+    constexpr int V = D / 32, turns = LANES / 32;
+    typedef float vec_t __attribute__((ext_vector_type(V)));
+    const int part = threadIdx.x & (LANES - 1), lane = threadIdx.x & 31, turn = part >> 5;
+    float m = kNegInf, l = 0.0f;
+    vec_t o = {};
+    for (int k0 = 0; k0 < parts; k0 += LANES) {
+        const int n = min(LANES, parts - k0);
         float m1 = kNegInf, l1 = 0.0f;
-        if (lane < n) {
-            int stats, rows;   // floats from the row to its maximum; rows of the slot
-            row = part_of(k0 + lane, stats, rows);
-            m1 = row[stats];
-            l1 = row[stats + rows];
+        if (part < n) {
+            const Part p = part_of(k0 + part);
+            m1 = p.row[p.stats];
+            l1 = p.row[p.stats + p.rows];
         }
         float mn = m1;
 #pragma unroll
-        for (int d = 1; d < 64; d *= 2) mn = fmaxf(mn, __shfl_xor(mn, d));
+        for (int d = 1; d < LANES; d *= 2) mn = fmaxf(mn, __shfl_xor(mn, d));
         mn = fmaxf(mn, m);
         const float base = mn == kNegInf ? 0.0f : mn;
         const float e = __builtin_amdgcn_exp2f(m1 - base), e0 = __builtin_amdgcn_exp2f(m - base);
         l1 *= e;
 #pragma unroll
-        for (int d = 1; d < 64; d *= 2) l1 += __shfl_xor(l1, d);
+        for (int d = 1; d < LANES; d *= 2) l1 += __shfl_xor(l1, d);
         m = mn;
         l = l * e0 + l1;
-#pragma unroll
-        for (int i = 0; i < V; ++i) o[i] *= e0;
+        o *= e0;
         constexpr int ahead = 8;
-        for (int p = 0; p < n; p += ahead) {
-            float y[ahead][V], f[ahead];
+        for (int p = 0; p < n; p += ahead * turns) {
+            vec_t y[ahead];
+            float f[ahead];
 #pragma unroll
             for (int q = 0; q < ahead; ++q) {
-                const int k = min(p + q, n - 1);
-                const uint64_t bits = reinterpret_cast<uintptr_t>(row);
-                const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)bits, k), hi = __builtin_amdgcn_readlane((uint32_t)(bits >> 32), k);
-                const float* s = reinterpret_cast<const float*>((uint64_t)hi << 32 | lo) + V * lane;
-                f[q] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(e), k));
-#pragma unroll
-                for (int i = 0; i < V; ++i) y[q][i] = s[i];
+                const int k = p + turns * q + turn, kk = min(k, n - 1);
+                f[q] = __shfl(e, kk, LANES);
+                y[q] = reinterpret_cast<const vec_t*>(part_of(k0 + kk).row)[lane];
             }
 #pragma unroll
             for (int q = 0; q < ahead; ++q)
-#pragma unroll
-                for (int i = 0; i < V; ++i) o[i] += p + q < n ? y[q][i] * f[q] : 0.0f;
+                if (p + turns * q + turn < n) o += y[q] * f[q];   // (a value may be infinite: not by a weight of 0)
         }
     }
+    if constexpr (turns == 2)
+#pragma unroll
+        for (int i = 0; i < V; ++i) o[i] += __shfl_xor(o[i], 32);
+    if (turn > 0) return;
     const int64_t id = (int64_t)token * a.HQ + head;
     const float inv = reciprocal_sum(l);
+    if constexpr (Elem<T>::bytes == 4) {
+        reinterpret_cast<vec_t*>(static_cast<float*>(a.o) + id * D)[lane] = o * inv;
+    } else {
+        uint32_t* to = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.o) + id * D) + lane * (V / 2);
 #pragma unroll
-    for (int i = 0; i < V; ++i) Elem<T>::store(a.o, id * D + V * lane + i, o[i] * inv);
+        for (int i = 0; i < V / 2; ++i) to[i] = pack_bf16x2(o[2 * i] * inv, o[2 * i + 1] * inv);
+    }
     if (a.lse && lane == 0) a.lse[id] = log_sum(m, l);
 }
 
-template <int D> __device__ __forceinline__ const float* part_row(const char* slots, int64_t slot, int rows, int row, int& stats, int& of) {
-    stats = rows * D + row - row * D;
-    of = rows;
-    return reinterpret_cast<const float*>(slots + slot * ((int64_t)rows * (D + 2) * 4)) + row * D;
-}
-
-// Without prefixes: a wave for every row of the blocks that stretches have left unfinished; and the rows that see nothing
-// although their sequence is not padded (a table without room), which no tile belongs to.
-template <typename T, int D>
+// Without prefixes: LANES lanes for every row of the blocks that stretches have left unfinished; and the rows that see
+// nothing although their sequence is not padded (a table without room), which no tile belongs to.
+template <typename T, int D, int LANES>
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnPagedArgs a) {
-    const int w = blockIdx.x, wave = blockIdx.y * 4 + uniform((int)threadIdx.x >> 6);
+    constexpr int rows = 256 / LANES;
+    const int w = blockIdx.x, mine = blockIdx.y * rows + threadIdx.x / LANES;
     if (w < a.workers) {
         const AttnOpen x = a.open[w];
-        for (int r = wave; x.parts && r < x.rows; r += 4 * gridDim.y) {
-            const int row = x.row0 + r;
-            join_row<T, D>(a, x.token0 + row / a.per, x.kvh * a.per + row % a.per, x.parts, [&](int k, int& stats, int& rows) {
-                return part_row<D>(a.slots, open_slot(w + k, k > 0), a.rows, r, stats, rows);
-            });
-        }
+        const int r = mine;
+        if (r >= x.rows || x.parts == 0) return;
+        const int row = x.row0 + r;
+        join_row<T, D, LANES>(a, x.token0 + row / a.per, x.kvh * a.per + row % a.per, x.parts,
+                       [&](int k) { return part_at<D>(a.slots, open_slot(w + k, k > 0), a.rows, r); });
         return;
     }
-    const int64_t waves = 4 * (int64_t)gridDim.y, step = waves * (gridDim.x - a.workers);
-    for (int64_t id = (w - a.workers) * waves + wave; id < a.T * a.HQ; id += step) {
+    const int64_t all = rows * (int64_t)gridDim.y, step = all * (gridDim.x - a.workers);
+    for (int64_t id = (w - a.workers) * all + mine; id < a.T * a.HQ; id += step) {
         const int token = (int)(id / a.HQ);
         if ((a.cu && token >= a.cu[a.N]) || a.context[a.cu ? find_seq(a.cu, a.N, token) : token] < 0) continue;
-        join_row<T, D>(a, token, (int)(id % a.HQ), 0, [](int, int& stats, int& rows) { stats = rows = 0; return (const float*)nullptr; });
+        join_row<T, D, LANES>(a, token, (int)(id % a.HQ), 0, [](int) { return Part{}; });
     }
 }
 
 // With prefixes: one wave per (token, query head); parts of the prefix and of the sequence's own keys.
 template <typename T, int D>
 __global__ __launch_bounds__(256) void attn_join_groups_kernel(AttnPagedArgs a) {
-    const int64_t id = (int64_t)blockIdx.x * 4 + uniform((int)threadIdx.x >> 6);
+    const int64_t id = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
     if (id >= a.T * a.HQ) return;
-    const int token = uniform((int)(id / a.HQ)), head = uniform((int)(id % a.HQ));
-    if (a.cu && token >= uniform_load(a.cu + a.N)) return;
-    const int seq = a.cu ? uniform(find_seq(a.cu, a.N, token)) : token;
-    if (uniform_load(a.context + seq) < 0) return;
-    const int kvh = head / a.per, hh = head % a.per, group = uniform_load(a.group + seq);
+    const int token = (int)(id / a.HQ), head = (int)(id % a.HQ);
+    if (a.cu && token >= a.cu[a.N]) return;
+    const int seq = a.cu ? find_seq(a.cu, a.N, token) : token;
+    // all that depends on the sequence, then all that depends on its group (what an empty unit has not been told is not used)
+    const Unit un = unit_of<false>(a, seq, a.rows);
+    const int ctx = a.context[seq], group = a.group[seq], own_start = a.start[seq], own_item = a.item[seq];
+    const int own_tiles = a.start[a.N], own_items = a.item[a.N], pre_tiles = a.prefix_start[a.groups], pre_items = a.prefix_item[a.groups];
+    const int g = max(group, 0), pre_keys = a.prefix[g], pre_tok0 = seq_first(a, a.first[g]), pre_start = a.prefix_start[g], pre_item = a.prefix_item[g];
+    if (ctx < 0) return;
+    const int kvh = head / a.per, hh = head % a.per;
     struct Side { int64_t first, own; int parts, row; };
-    auto side = [&](const Unit& un, int u, int units, int rows, const int32_t* starts, const int32_t* items) {
-        const int per = stretch(a, starts[units]);
-        const int start = un.tiles > 0 ? starts[u] : 0;
-        const int item = un.tiles > 0 ? items[u] : 0;
-        const int r = (token - un.tok0) * a.per + hh, rb = r / rows;
-        const int x0 = start + rb * un.tiles, w0 = x0 / per, w1 = (x0 + un.tiles - 1) / per;
-        return Side{(int64_t)kvh * a.per_head + w0, 2 * (int64_t)a.workers + (int64_t)kvh * items[units] + item + rb, un.tiles > 0 ? w1 - w0 + 1 : 0, r % rows};
+    auto side = [&](int tok0, int tiles, int rows, int start, int item, int all_tiles, int all_items) {
+        const int per = stretch(a, all_tiles), r = (token - tok0) * a.per + hh, rb = r / rows;
+        const int x0 = start + rb * tiles, w0 = x0 / per, w1 = (x0 + tiles - 1) / per;
+        return Side{(int64_t)kvh * a.per_head + w0, 2 * (int64_t)a.workers + (int64_t)kvh * all_items + item + rb, w1 - w0 + 1, r % rows};
     };
-    const Side own = side(unit_of<false>(a, seq, a.rows), seq, a.N, a.rows, a.start, a.item);
-    Side pre{0, 0, 0, 0};
-    if (group >= 0) {
-        Unit un{};
-        un.tok0 = seq_first(a, a.first[group]);
-        un.tiles = (a.prefix[group] + kKeys - 1) / kKeys;
-        pre = side(un, group, a.groups, a.prefix_rows, a.prefix_start, a.prefix_item);
-    }
-    join_row<T, D>(a, token, head, pre.parts + own.parts, [&](int k, int& stats, int& rows) {
+    const Side own = un.tiles > 0 ? side(un.tok0, un.tiles, a.rows, own_start, own_item, own_tiles, own_items) : Side{0, 0, 0, 0};
+    const Side pre = group >= 0 && pre_keys > 0
+        ? side(pre_tok0, (pre_keys + kKeys - 1) / kKeys, a.prefix_rows, pre_start, pre_item, pre_tiles, pre_items) : Side{0, 0, 0, 0};
+    join_row<T, D, 64>(a, token, head, pre.parts + own.parts, [&](int k) {
         const bool p = k < pre.parts;
-        const Side& s = p ? pre : own;
+        const Side s = p ? pre : own;
         const int i = p ? k : k - pre.parts;
-        return part_row<D>(p ? a.prefix_slots : a.slots, s.parts == 1 ? s.own : open_slot(s.first + i, i > 0), p ? a.prefix_rows : a.rows,
-                           s.row, stats, rows);
+        return part_at<D>(p ? a.prefix_slots : a.slots, s.parts == 1 ? s.own : open_slot(s.first + i, i > 0), p ? a.prefix_rows : a.rows, s.row);
     });
 }
 
@@ -571,8 +572,15 @@ hipError_t launch(const AttnPagedArgs& a, hipStream_t stream) {
     if (a.groups) e = launch_part<T, D, true>(a, a.prefix_rows, stream);
     if (e == hipSuccess) e = launch_part<T, D, false>(a, a.rows, stream);
     if (e != hipSuccess) return e;
-    if (a.groups) attn_join_groups_kernel<T, D><<<dim3((unsigned)((a.T * a.HQ + 3) / 4)), 256, 0, stream>>>(a);
-    else attn_join_kernel<T, D><<<dim3((unsigned)(a.workers + (a.capacity == 0 ? 256 : 0)), (unsigned)(a.rows / 4)), 256, 0, stream>>>(a);
+    if (a.groups) {
+        attn_join_groups_kernel<T, D><<<dim3((unsigned)((a.T * a.HQ + 3) / 4)), 256, 0, stream>>>(a);
+    } else {
+        // few rows are likely to have many parts (one sequence of 4097 tokens, 33 parts: 6.0 us with a wave per row, 7.4 with
+        // half a one), many rows few (64 sequences of 1..12 tokens, 2 or 3 parts of 48 rows: 12.4 and 9.3)
+        const unsigned across = (unsigned)(a.workers + (a.capacity == 0 ? 256 : 0));
+        if (a.rows == 32) attn_join_kernel<T, D, 64><<<dim3(across, 8), 256, 0, stream>>>(a);
+        else attn_join_kernel<T, D, 32><<<dim3(across, (unsigned)(a.rows / 8)), 256, 0, stream>>>(a);
+    }
     return hipGetLastError();
 }
 
