@@ -823,6 +823,10 @@ def _token_rows(t, name: str, heads, dim, dtype, device: int):
     return t.data_ptr(), st if shape[0] > 1 else heads * dim
 
 
+def _dense(shape, dtype, device: int) -> torch.Tensor:
+    return torch.empty_strided(shape, (shape[1] * shape[2], shape[2], 1), dtype=dtype, device=device)
+
+
 def _attn_problem(q, k, num_seqs: int, scale, kv_heads: int):
     """(problem with q's stride, device, io dtype, q's address)"""
     if q.dim() != 3:
@@ -898,9 +902,9 @@ def gdr_rope_append_paged(q, k, v=None, inv_freq=None, k_pages=None, v_pages=Non
         r = Rotary(_arg(inv_freq, "inv_freq", inv_freq.shape, f32, dev), pos, 2 * half, axes, 1 if interleaved else 0)
     with _On(dev, stream) as raw:
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=dtype, device=q.device)
+            q_out = _dense(q.shape, dtype, dev)
         if k_out is None and (output_k or k_pages is None):
-            k_out = torch.empty(k.shape, dtype=dtype, device=q.device)
+            k_out = _dense(k.shape, dtype, dev)
         st = lib().gdr_rope_append_paged(ctypes.byref(p), ctypes.byref(r), pq, pk, pv,
                                          _arg(cu_seqlens, "cu_seqlens", (N + 1,), i32, dev),
                                          _arg(context_lens, "context_lens", (N,), i32, dev), pages,
@@ -926,7 +930,7 @@ def gdr_attn_prefill_fwd(q, k, v, cu_seqlens=None, scale=None, o=None, lse=None,
     want_lse = output_lse or lse is not None
     with _On(dev, stream) as raw:
         if o is None:
-            o = torch.empty(q.shape, dtype=dtype, device=q.device)
+            o = _dense(q.shape, dtype, dev)
         if want_lse and lse is None:
             lse = _rows(T, q.shape[1], torch.float32, dev)
         st = lib().gdr_attn_prefill_fwd(ctypes.byref(p), pq, pk, pv, _arg(cu_seqlens, "cu_seqlens", (N + 1,), torch.int32, dev),
@@ -971,7 +975,7 @@ def gdr_attn_decode_paged(q, k_pages, v_pages, page_table, context_lens, cu_seql
     want_lse = output_lse or lse is not None
     with _On(dev, stream) as raw:
         if o is None:
-            o = torch.empty(q.shape, dtype=dtype, device=q.device)
+            o = _dense(q.shape, dtype, dev)
         if want_lse and lse is None:
             lse = _rows(T, HQ, torch.float32, dev)
         ref = ctypes.byref(p)
