@@ -590,7 +590,7 @@ gdr_status check_attn(const gdr_attn_problem* p) {
     if (p->total_tokens < 0 || p->num_seqs < 0) return GDR_ERROR_INVALID_VALUE;
     if (p->num_q_heads <= 0 || p->num_kv_heads <= 0 || p->num_q_heads % p->num_kv_heads != 0) return GDR_ERROR_INVALID_VALUE;
     if (!dtype_ok(p->io_dtype) || p->head_dim <= 0) return GDR_ERROR_INVALID_VALUE;
-    if (!(p->scale >= -3.0e38f && p->scale <= 3.0e38f)) return GDR_ERROR_INVALID_VALUE;  // NaN fails too
+    if (!(p->scale >= -0x1p127f && p->scale <= 0x1p127f)) return GDR_ERROR_INVALID_VALUE;  // NaN fails too
     if (p->num_seqs == 0 && p->total_tokens > 0) return GDR_ERROR_INVALID_VALUE;
     if (!head_dim_ok(p->head_dim)) return GDR_ERROR_NOT_SUPPORTED;
     if (p->num_seqs > 65535 || p->num_q_heads > 65535 || p->total_tokens > 0x7FFFFFFF - 1023) return GDR_ERROR_NOT_SUPPORTED;
@@ -626,6 +626,11 @@ gdr_status check_pages(const gdr_attn_problem* p, const gdr_kv_pages* c) {
     // positions in the cache are 32-bit
     if (((int64_t)c->max_pages << page_shift(c->page_size)) > 0x7FFFFFFF) return GDR_ERROR_NOT_SUPPORTED;
     return GDR_SUCCESS;
+}
+
+int64_t pages_bytes(const gdr_attn_problem* p, const gdr_kv_pages* c) {
+    const __int128 n = (__int128)((int64_t)c->num_pages * p->num_kv_heads) * ((int64_t)p->head_dim * elem_bytes(p->io_dtype) * c->page_size);
+    return n < (int64_t)1 << 62 ? (int64_t)n : (int64_t)1 << 62;
 }
 
 // |scale| log2(e); a zero scale as the smallest normal number, so that a masked score times it stays -inf
@@ -667,6 +672,16 @@ gdr_status gdr_rope_append_paged(const gdr_attn_problem* p, const gdr_rotary* r,
             if (!itself && ranges_meet(out[i], out_size[i], in[j], size[j])) return GDR_ERROR_INVALID_VALUE;
         }
     if (ranges_meet(q_out, out_size[0], k_out, out_size[1])) return GDR_ERROR_INVALID_VALUE;
+    if (pages) {   // the cache is written, while others of its workgroups still read
+        const int64_t cache = pages_bytes(p, pages);
+        if (ranges_meet(pages->k, cache, pages->v, cache)) return GDR_ERROR_INVALID_VALUE;
+        for (void* c : {pages->k, pages->v}) {
+            for (int i = 0; i < 2; ++i)
+                if (ranges_meet(c, cache, out[i], out_size[i])) return GDR_ERROR_INVALID_VALUE;
+            for (int i = 0; i < 3; ++i)
+                if (ranges_meet(c, cache, in[i], size[i])) return GDR_ERROR_INVALID_VALUE;
+        }
+    }
     if ((st = check_device()) != GDR_SUCCESS) return st;
     gdr::RopeArgs a{};
     a.q = q; a.k = k; a.v = v;
@@ -693,7 +708,15 @@ gdr_status gdr_attn_prefill_fwd(const gdr_attn_problem* p, const void* q, const 
     if (!rows_ok(p, q, p->num_q_heads, p->q_stride) || !rows_ok(p, k, p->num_kv_heads, p->k_stride) ||
         !rows_ok(p, v, p->num_kv_heads, p->v_stride))
         return GDR_ERROR_INVALID_VALUE;
-    if (gdr::attn_prefill_tiles(p->total_tokens) * p->num_q_heads > 0x7FFFFFFF) return GDR_ERROR_NOT_SUPPORTED;  // grid
+    if (gdr::attn_prefill_tiles(p->total_tokens) * p->num_q_heads >= 1 << 24) return GDR_ERROR_NOT_SUPPORTED;  // 2^32 threads
+    const int64_t T = p->total_tokens, o_bytes = T * p->num_q_heads * p->head_dim * elem_bytes(p->io_dtype);
+    const int64_t lse_bytes = T * p->num_q_heads * (int64_t)sizeof(float);
+    const void* in[3] = {q, k, v};
+    const int64_t size[3] = {rows_bytes(p, p->num_q_heads, p->q_stride), rows_bytes(p, p->num_kv_heads, p->k_stride),
+                             rows_bytes(p, p->num_kv_heads, p->v_stride)};
+    for (int i = 0; i < 3; ++i)
+        if (ranges_meet(o, o_bytes, in[i], size[i]) || ranges_meet(lse, lse_bytes, in[i], size[i])) return GDR_ERROR_INVALID_VALUE;
+    if (ranges_meet(lse, lse_bytes, o, o_bytes)) return GDR_ERROR_INVALID_VALUE;
     if ((st = check_device()) != GDR_SUCCESS) return st;
     gdr::AttnPrefillArgs a{};
     a.q = q; a.k = k; a.v = v;
@@ -735,6 +758,17 @@ gdr_status gdr_attn_decode_paged(const gdr_attn_problem* p, int32_t max_q_len, c
                                                        p->head_dim, elem_bytes(p->io_dtype), max_q_len, num_groups);
     if (!workspace || workspace_bytes < pl.total) return GDR_ERROR_INVALID_VALUE;
     if (reinterpret_cast<uintptr_t>(workspace) % 256 != 0) return GDR_ERROR_INVALID_VALUE;
+    // what is written may meet neither what is read nor one another
+    const int64_t rows = p->total_tokens * p->num_q_heads, cache = pages_bytes(p, pages);
+    void* out[3] = {o, lse, workspace};
+    const int64_t out_size[3] = {rows * p->head_dim * elem_bytes(p->io_dtype), rows * (int64_t)sizeof(float), (int64_t)pl.total};
+    for (int i = 0; i < 3; ++i) {
+        if (ranges_meet(out[i], out_size[i], q, rows_bytes(p, p->num_q_heads, p->q_stride)) ||
+            ranges_meet(out[i], out_size[i], pages->k, cache) || ranges_meet(out[i], out_size[i], pages->v, cache))
+            return GDR_ERROR_INVALID_VALUE;
+        for (int j = 0; j < i; ++j)
+            if (ranges_meet(out[i], out_size[i], out[j], out_size[j])) return GDR_ERROR_INVALID_VALUE;
+    }
     if ((st = check_device()) != GDR_SUCCESS) return st;
     gdr::AttnPagedArgs a{};
     a.q = q; a.q_stride = p->q_stride; a.cu = cu_seqlens; a.context = context_lens;

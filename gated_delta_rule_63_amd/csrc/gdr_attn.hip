@@ -175,7 +175,8 @@ hipError_t launch(const AttnPrefillArgs& a, hipStream_t stream) {
 
 }  // namespace
 
-int64_t attn_prefill_tiles(int64_t T) { return (T + 31) / 32 + kSorted; }
+// of a large batch
+int64_t attn_prefill_tiles(int64_t T) { return (T + 127) / 128 + kSorted; }
 
 hipError_t launch_attn_prefill(AttnPrefillArgs a, int D, int io_dtype, hipStream_t stream) {
     if (io_dtype == 1) return D == 64 ? launch<bf16_t, 64>(a, stream) : launch<bf16_t, 128>(a, stream);

@@ -17,6 +17,7 @@ namespace gdr {
 namespace {
 
 constexpr int kKeys = 64;       // keys per tile
+constexpr int kJoinGroups = 1 << 16;   // workgroups that join with prefixes, at most
 constexpr int kMinTiles = 2;    // tiles of a workgroup's stretch at least: below, parts cost more than they save
 
 // what stands for a page outside the cache: finite rows that nobody sees
@@ -304,12 +305,14 @@ __global__ __launch_bounds__(64 * KW * RW, 2) void attn_paged_kernel(AttnPagedAr
                     copy_to_lds(k, ko[i], dst + 1024 * i);
                     copy_to_lds(v, vo[i], dst + tile_bytes + 1024 * i);
                 }
-            } else {   // rows behind the last key stand for it
+            } else {   // behind the last key, which nobody sees: that key again, and zeros for values (0 * inf)
+                typedef __attribute__((address_space(3))) f32x4_t lds_f4;
 #pragma unroll
                 for (int i = 0; i < copies; ++i) {
-                    const uint32_t over = max(L::copy_row(64 * i, lane) - last, 0) * L::row_bytes;
-                    copy_to_lds(k, ko[i] - over, dst + 1024 * i);
-                    copy_to_lds(v, vo[i] - over, dst + tile_bytes + 1024 * i);
+                    const int over = max(L::copy_row(64 * i, lane) - last, 0);
+                    copy_to_lds(k, ko[i] - over * L::row_bytes, dst + 1024 * i);
+                    if (over > 0) *(lds_f4*)(uintptr_t)(dst + tile_bytes + 1024 * i + 16 * lane) = f32x4_t{};
+                    else copy_to_lds(v, vo[i], dst + tile_bytes + 1024 * i);
                 }
             }
         }
@@ -528,33 +531,34 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnPagedArgs a) {
 // With prefixes: one wave per (token, query head); parts of the prefix and of the sequence's own keys.
 template <typename T, int D>
 __global__ __launch_bounds__(256) void attn_join_groups_kernel(AttnPagedArgs a) {
-    const int64_t id = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    if (id >= a.T * a.HQ) return;
-    const int token = (int)(id / a.HQ), head = (int)(id % a.HQ);
-    if (a.cu && token >= a.cu[a.N]) return;
-    const int seq = a.cu ? find_seq(a.cu, a.N, token) : token;
-    // all that depends on the sequence, then all that depends on its group (what an empty unit has not been told is not used)
-    const Unit un = unit_of<false>(a, seq, a.rows);
-    const int ctx = a.context[seq], group = a.group[seq], own_start = a.start[seq], own_item = a.item[seq];
-    const int own_tiles = a.start[a.N], own_items = a.item[a.N], pre_tiles = a.prefix_start[a.groups], pre_items = a.prefix_item[a.groups];
-    const int g = max(group, 0), pre_keys = a.prefix[g], pre_tok0 = seq_first(a, a.first[g]), pre_start = a.prefix_start[g], pre_item = a.prefix_item[g];
-    if (ctx < 0) return;
-    const int kvh = head / a.per, hh = head % a.per;
-    struct Side { int64_t first, own; int parts, row; };
-    auto side = [&](int tok0, int tiles, int rows, int start, int item, int all_tiles, int all_items) {
-        const int per = stretch(a, all_tiles), r = (token - tok0) * a.per + hh, rb = r / rows;
-        const int x0 = start + rb * tiles, w0 = x0 / per, w1 = (x0 + tiles - 1) / per;
-        return Side{(int64_t)kvh * a.per_head + w0, 2 * (int64_t)a.workers + (int64_t)kvh * all_items + item + rb, w1 - w0 + 1, r % rows};
-    };
-    const Side own = un.tiles > 0 ? side(un.tok0, un.tiles, a.rows, own_start, own_item, own_tiles, own_items) : Side{0, 0, 0, 0};
-    const Side pre = group >= 0 && pre_keys > 0
-        ? side(pre_tok0, (pre_keys + kKeys - 1) / kKeys, a.prefix_rows, pre_start, pre_item, pre_tiles, pre_items) : Side{0, 0, 0, 0};
-    join_row<T, D, 64>(a, token, head, pre.parts + own.parts, [&](int k) {
-        const bool p = k < pre.parts;
-        const Side s = p ? pre : own;
-        const int i = p ? k : k - pre.parts;
-        return part_at<D>(p ? a.prefix_slots : a.slots, s.parts == 1 ? s.own : open_slot(s.first + i, i > 0), p ? a.prefix_rows : a.rows, s.row);
-    });
+    // (a launch has fewer than 2^32 threads)
+    for (int64_t id = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); id < a.T * a.HQ; id += 4 * (int64_t)gridDim.x) {
+        const int token = (int)(id / a.HQ), head = (int)(id % a.HQ);
+        if (a.cu && token >= a.cu[a.N]) return;
+        const int seq = a.cu ? find_seq(a.cu, a.N, token) : token;
+        // all that depends on the sequence, then all that depends on its group (what an empty unit has not been told is not used)
+        const Unit un = unit_of<false>(a, seq, a.rows);
+        const int ctx = a.context[seq], group = a.group[seq], own_start = a.start[seq], own_item = a.item[seq];
+        const int own_tiles = a.start[a.N], own_items = a.item[a.N], pre_tiles = a.prefix_start[a.groups], pre_items = a.prefix_item[a.groups];
+        const int g = max(group, 0), pre_keys = a.prefix[g], pre_tok0 = seq_first(a, a.first[g]), pre_start = a.prefix_start[g], pre_item = a.prefix_item[g];
+        if (ctx < 0) continue;
+        const int kvh = head / a.per, hh = head % a.per;
+        struct Side { int64_t first, own; int parts, row; };
+        auto side = [&](int tok0, int tiles, int rows, int start, int item, int all_tiles, int all_items) {
+            const int per = stretch(a, all_tiles), r = (token - tok0) * a.per + hh, rb = r / rows;
+            const int x0 = start + rb * tiles, w0 = x0 / per, w1 = (x0 + tiles - 1) / per;
+            return Side{(int64_t)kvh * a.per_head + w0, 2 * (int64_t)a.workers + (int64_t)kvh * all_items + item + rb, w1 - w0 + 1, r % rows};
+        };
+        const Side own = un.tiles > 0 ? side(un.tok0, un.tiles, a.rows, own_start, own_item, own_tiles, own_items) : Side{0, 0, 0, 0};
+        const Side pre = group >= 0 && pre_keys > 0
+            ? side(pre_tok0, (pre_keys + kKeys - 1) / kKeys, a.prefix_rows, pre_start, pre_item, pre_tiles, pre_items) : Side{0, 0, 0, 0};
+        join_row<T, D, 64>(a, token, head, pre.parts + own.parts, [&](int k) {
+            const bool p = k < pre.parts;
+            const Side s = p ? pre : own;
+            const int i = p ? k : k - pre.parts;
+            return part_at<D>(p ? a.prefix_slots : a.slots, s.parts == 1 ? s.own : open_slot(s.first + i, i > 0), p ? a.prefix_rows : a.rows, s.row);
+        });
+    }
 }
 
 template <typename T, int D, bool PREFIX>
@@ -573,7 +577,7 @@ hipError_t launch(const AttnPagedArgs& a, hipStream_t stream) {
     if (e == hipSuccess) e = launch_part<T, D, false>(a, a.rows, stream);
     if (e != hipSuccess) return e;
     if (a.groups) {
-        attn_join_groups_kernel<T, D><<<dim3((unsigned)((a.T * a.HQ + 3) / 4)), 256, 0, stream>>>(a);
+        attn_join_groups_kernel<T, D><<<dim3((unsigned)min((a.T * a.HQ + 3) / 4, (int64_t)kJoinGroups)), 256, 0, stream>>>(a);
     } else {
         // few rows are likely to have many parts (one sequence of 4097 tokens, 33 parts: 6.0 us with a wave per row, 7.4 with
         // half a one), many rows few (64 sequences of 1..12 tokens, 2 or 3 parts of 48 rows: 12.4 and 9.3)

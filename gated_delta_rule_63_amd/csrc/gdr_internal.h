@@ -235,6 +235,7 @@ struct RopeArgs {
     const int32_t* table;        // [N, max_pages]
     int32_t num_pages, max_pages, page_shift;
     void *q_out, *k_out;         // k_out may be NULL
+    int64_t first;               // token of a launch
     int64_t T;
     int32_t N, HQ, HK;
 };

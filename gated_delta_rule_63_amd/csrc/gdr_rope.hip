@@ -11,6 +11,7 @@
 namespace gdr {
 namespace {
 
+constexpr int64_t kTokens = 1 << 22;   // of a launch, at most: it has fewer than 2^32 threads
 constexpr int kLarge = 4096;    // tokens of a batch whose rows no cache will hold until they are read again
 
 // NT: rows of a large batch are read and written past the caches.
@@ -29,7 +30,7 @@ template <typename T, int D, int MODE, bool NT>  // MODE 0: pairs (i, i + R/2) i
 __global__ __launch_bounds__(512) void rope_append_kernel(RopeArgs a) {
     constexpr int es = Elem<T>::bytes, V = 16 / es, units = MODE == 2 ? D / 2 : D / V / 2;
     __shared__ float cj[D / 2], sj[D / 2];
-    const int64_t t = blockIdx.x;
+    const int64_t t = a.first + blockIdx.x;
     const int half = a.rotary / 2;
     int n = 0, first = 0;
     if (a.cu) {
@@ -53,7 +54,7 @@ __global__ __launch_bounds__(512) void rope_append_kernel(RopeArgs a) {
         if (a.positions) {
             for (int x = 0; x < a.axes; ++x) theta += (double)a.positions[x * a.T + t] * (double)a.freq[x * half + p];
         } else {
-            theta = (double)(int)place * (double)a.freq[p];
+            theta = (double)place * (double)a.freq[p];
         }
         // whole turns off, 2 pi in two parts
         const double turns = rint(theta * 0.15915494309189535);
@@ -140,7 +141,7 @@ __global__ __launch_bounds__(512) void rope_append_kernel(RopeArgs a) {
 template <typename T, int D, bool NT>
 hipError_t launch(const RopeArgs& a, hipStream_t stream) {
     constexpr int V = 16 / Elem<T>::bytes;
-    const dim3 grid((unsigned)a.T);
+    const dim3 grid((unsigned)min(a.T - a.first, kTokens));
     // a thread per piece of the token where that is at most eight waves
     const int64_t pieces = (int64_t)(a.HQ + 2 * a.HK) * (D / V / 2);
     const int threads = (int)min((int64_t)512, (pieces + 63) / 64 * 64);
@@ -152,7 +153,10 @@ hipError_t launch(const RopeArgs& a, hipStream_t stream) {
 
 template <typename T, int D>
 hipError_t launch(const RopeArgs& a, hipStream_t stream) {
-    return a.T >= kLarge ? launch<T, D, true>(a, stream) : launch<T, D, false>(a, stream);
+    hipError_t e = hipSuccess;
+    for (RopeArgs part = a; part.first < a.T && e == hipSuccess; part.first += kTokens)
+        e = a.T >= kLarge ? launch<T, D, true>(part, stream) : launch<T, D, false>(part, stream);
+    return e;
 }
 
 }  // namespace

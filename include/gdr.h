@@ -509,7 +509,7 @@ typedef struct gdr_attn_problem {
     int32_t num_q_heads;    /* HQ <= 65535, a multiple of HKV                                */
     int32_t num_kv_heads;   /* HKV                                                           */
     int32_t head_dim;       /* D in {64, 128}                                                */
-    float scale;            /* finite; 1/sqrt(D) in the usual setting                        */
+    float scale;            /* at most 2^127 in size; 1/sqrt(D) in the usual setting         */
     int64_t q_stride;       /* elements from one token's row to the next, >= HQ D            */
     int64_t k_stride;       /* >= HKV D                                                      */
     int64_t v_stride;       /* >= HKV D                                                      */
@@ -554,7 +554,7 @@ typedef struct gdr_rotary {
  *   q, q_out       NULL together: only k and v.  q_out may be q where q is dense
  *   k_out          [T, HKV, D] rotated keys for gdr_attn_prefill_fwd, or NULL (with a cache).  May be k where k
  *                  is dense
- * Two tokens of one call never share a row of the cache as long as the sequences' pages are their own.
+ * No other output overlaps an input or another output, the cache included.  Two tokens of one call never share a row of the cache as long as the sequences' pages are their own.
  */
 GDR_API gdr_status gdr_rope_append_paged(const gdr_attn_problem* p, const gdr_rotary* rotary,
                                  const void* q, const void* k, const void* v,
@@ -566,6 +566,7 @@ GDR_API gdr_status gdr_rope_append_paged(const gdr_attn_problem* p, const gdr_ro
  *
  *   cu_seqlens     int32 [N+1]; may be NULL only when N == 1 (one sequence of T tokens)
  *   lse            fp32 [T, HQ] or NULL
+ * o and lse overlap neither an input nor each other.  (T / 128 + 64) HQ < 2^24.
  */
 GDR_API gdr_status gdr_attn_prefill_fwd(const gdr_attn_problem* p, const void* q, const void* k, const void* v,
                                 const int32_t* cu_seqlens, void* o, float* lse, void* hip_stream);
@@ -585,7 +586,7 @@ GDR_API gdr_status gdr_attn_prefill_fwd(const gdr_attn_problem* p, const void* q
  *   lse            fp32 [T, HQ] or NULL
  *   workspace      gdr_attn_workspace_size bytes, 256-byte aligned, contents need not be initialised; calls that
  *                  may overlap need one each
- * p->k_stride and p->v_stride are not used.  T * HQ < 2^31, and N times a table row's tokens below 2^37 over the
+ * o, lse and workspace overlap neither q nor the cache nor one another.  p->k_stride and p->v_stride are not used.  T * HQ < 2^31, and N times a table row's tokens below 2^37 over the
  * blocks of 32 rows that max_q_len tokens of HQ / HKV heads make.  The result does not depend on what else is in the
  * batch by more than the order of fp32 sums.
  */

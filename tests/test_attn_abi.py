@@ -47,7 +47,7 @@ def _decode(p, ql=12, q=PTR, cu=PTR, ctx=PTR, pages="some", G=0, off=None, pre=N
 
 
 BAD = [(_ap(T=-1), 1), (_ap(N=-1), 1), (_ap(HQ=0), 1), (_ap(HK=0), 1), (_ap(HQ=9), 1), (_ap(D=0), 1), (_ap(io=2), 1),
-       (_ap(scale=float("nan")), 1), (_ap(scale=float("inf")), 1), (_ap(N=0), 1), (_ap(D=96, q=768, k=192, v=192), 2),
+       (_ap(scale=float("nan")), 1), (_ap(scale=float("inf")), 1), (_ap(scale=2.5e38), 1), (_ap(scale=-1.8e38), 1), (_ap(N=0), 1), (_ap(D=96, q=768, k=192, v=192), 2),
        (_ap(D=32), 2), (_ap(N=65536), 2), (_ap(HQ=65538), 2), (_ap(T=(1 << 31) - 1), 2)]
 
 
@@ -97,6 +97,39 @@ def test_append_outputs_over_inputs():
     assert _append(dense, qo=at(k)) == 1 and _append(dense, qo=at(v + 512)) == 1
     assert _append(dense, ko=at(q)) == 1 and _append(dense, ko=at(k + 16)) == 1 and _append(dense, ko=at(v)) == 1
     assert _append(dense, ko=at(FAR["qo"].value + 1024)) == 1
+
+
+def test_append_over_the_cache():
+    at = lambda x: ctypes.c_void_p(x)  # noqa: E731
+    k, n = 6 << 32, 8 * 2 * 16 * 64 * 2
+    far = lambda **kw: _append(pages=_kp(**dict(dict(k=at(k), v=at(k + n)), **kw)))  # noqa: E731
+    assert far(v=at(k)) == 1 and far(v=at(k + n - 16)) == 1
+    for name in ("q", "k", "v", "qo", "ko"):
+        for c in ("k", "v"):
+            assert far(**{c: FAR[name]}) == 1 and far(**{c: at(FAR[name].value - n + 16)}) == 1, (name, c)
+
+
+def test_outputs_of_attention_over_inputs():
+    at = lambda x: ctypes.c_void_p(x << 32)  # noqa: E731
+    L, p = gdr.lib(), _ap(T=20)
+
+    def prefill(**kw):
+        a = dict(dict(q=at(1), k=at(2), v=at(3), o=at(4), lse=at(5)), **kw)
+        return L.gdr_attn_prefill_fwd(_ref(p), a["q"], a["k"], a["v"], PTR, a["o"], a["lse"], None)
+
+    def decode(**kw):
+        a = dict(dict(q=at(1), k=at(2), v=at(3), o=at(4), lse=at(5), ws=at(6)), **kw)
+        return L.gdr_attn_decode_paged(_ref(p), 12, a["q"], PTR, PTR, _ref(_kp(k=a["k"], v=a["v"])), 0, None, None, a["o"], a["lse"],
+                                       a["ws"], 1 << 30, None)
+
+    for call, outs in ((prefill, ("o", "lse")), (decode, ("o", "lse", "ws"))):
+        for i, name in enumerate(outs):
+            for other in ("q", "k", "v") + outs[:i]:
+                assert call(**{name: at(9), other: at(9)}) == 1, (name, other)
+
+
+def test_largest_launches():
+    assert _prefill(_ap(T=1 << 30, HQ=8, q=512)) == 2 and _prefill(_ap(T=1 << 24, HQ=128, q=8192), o=ctypes.c_void_p(1 << 45)) == 2
 
 
 @pytest.mark.parametrize("call", [lambda c: _append(pages=c), lambda c: _decode(_ap(T=20), pages=c)])

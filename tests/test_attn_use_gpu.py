@@ -355,6 +355,58 @@ def test_every_size_of_row_blocks(T, HQ, HK, D, io):
         check_attention(o[:, h:h + 1], None, ref, io, np.arange(T - 5), f"head {h}")
 
 
+def test_appending_more_tokens_than_a_launch_takes():
+    T = (1 << 23) + 1000
+    q, k = torch.empty(T, 1, 64, dtype=torch.bfloat16, device="cuda"), torch.empty(T, 1, 64, dtype=torch.bfloat16, device="cuda")
+    at = torch.tensor([0, 1, (1 << 22) - 1, 1 << 22, (1 << 23) - 1, 1 << 23, T - 1], device="cuda")
+    x, w = normal(np.random.default_rng(74), (len(at), 2, 64), "bf16")
+    q[at], k[at] = x[:, :1], x[:, 1:]
+    for half in (1, 32):     # one pair takes the kernel for any number of channels
+        qo, ko = gdr.gdr_rope_append_paged(q, k, inv_freq=to_dev(_freq(1, half)))
+        theta = attn.angles(to_host(at)[None], _freq(1, half))
+        _rotated_close(f64(qo[at]), w[:, :1], theta, False, "bf16", "q")
+        _rotated_close(f64(ko[at]), w[:, 1:], theta, False, "bf16", "k")
+
+
+def test_joining_more_rows_than_a_launch_has_waves():
+    N = 20000
+    d = _decode_inputs(75, "f32", 64, 16, 1, [1] * N, [20 + n % 3 for n in range(N)], 16, groups=[(N, 16)])
+    o, lse = _decode_call(d, output_lse=True)
+    rows = np.unique(np.concatenate([[0, N // 2, N - 1], np.random.default_rng(75).integers(0, N, 500)]))
+    for n in rows:
+        ref = attn.decode(d["qw"][n:n + 1], [0, 1], d["ctx"][n:n + 1], d["kw"], d["vw"], d["table"][n:n + 1], 1 / 8)
+        check_attention(f64(o[n:n + 1]), f64(lse[n:n + 1]), ref, "f32", np.arange(1), f"sequence {n}")
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("q_len", [1, 3])
+def test_infinities_that_are_seen(q_len, D, io):
+    """An infinite value of the last key that a row sees: that channel is infinite, the others are as ever; so with one in
+    a prefix."""
+    lens = [1, 2, 15, 16, 17, 33, 63, 64, 65, 100, 127, 128, 129]
+    cu = np.concatenate([[0], np.cumsum([q_len] * len(lens))])
+    for groups in (None, [(len(lens), 0)], [(5, 48)]):
+        ctx = [max(x, 48) if groups and groups[0][1] else x for x in lens]
+        d = _decode_inputs(76, io, D, 4, 2, [q_len] * len(lens), ctx, 16, groups=groups)
+        for n, c in enumerate(ctx):
+            last = c + q_len - 1
+            page = int(d["table"][n][last // 16])
+            d["v"][page, 1, last % 16, 5], d["vw"][page, 1, last % 16, 5] = float("inf"), 0.0
+        if groups and groups[0][1]:
+            page = int(d["table"][0][2])
+            d["v"][page, 0, 15, 7], d["vw"][page, 0, 15, 7] = -float("inf"), 0.0
+        o = f64(_decode_call(d))
+        want = np.zeros(o.shape)
+        want[cu[1:] - 1, 2:, 5] = np.inf
+        if groups and groups[0][1]:
+            want[: cu[5], :2, 7] = -np.inf
+        assert np.array_equal(np.where(np.isinf(want), want, 0), np.where(np.isfinite(o), 0, o))
+        ref = attn.decode(d["qw"], d["cu"], d["ctx"], d["kw"], d["vw"], d["table"], 1 / np.sqrt(D))
+        fine = np.where(np.isinf(want), ref["o"], o)
+        check_attention(fine, None, ref, io, np.arange(len(o)))
+
+
 def test_nothing_to_do():
     z = lambda *s: torch.zeros(*s, device="cuda")  # noqa: E731
     i = lambda *s: torch.zeros(*s, dtype=torch.int32, device="cuda")  # noqa: E731
