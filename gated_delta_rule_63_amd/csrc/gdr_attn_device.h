@@ -103,8 +103,11 @@ template <typename T, int D> struct AttnTile {
     static constexpr int es = Elem<T>::bytes;
     static constexpr int row_bytes = D * es;
     static constexpr int chunks = row_bytes / 16;
-    __device__ __forceinline__ static int swz_k(int row) { return row & 7; }
-    __device__ __forceinline__ static int swz_v(int row) { return es == 2 ? (row & 3) << 1 : 0; }
+    // so many rows' reads of one chunk meet all places of 256 bytes
+    __device__ __forceinline__ static int swz_k(int row) { return chunks >= 16 ? row & 15 : (row >> 1) & 7; }
+    // step s of a lane's reads of a key row (chunk 2 s + half) is at register s % regs, 32 regs bytes on for each turn
+    static constexpr int regs = chunks >= 16 ? 8 : 4;
+    __device__ __forceinline__ static int swz_v(int row) { return es == 2 ? (row & 3) << (chunks >= 16 ? 2 : 1) : 0; }
     // instruction i of a wave's copies fills the places 64 (per * wave + i) ..; the lane's row and byte in the row
     template <int ROWS, int WAVES> static constexpr int per() { return ROWS * chunks / 64 / WAVES; }
     __device__ __forceinline__ static int copy_row(int first, int lane) { return (first + lane) / chunks; }
@@ -138,22 +141,21 @@ template <int D> struct AttnCore<bf16_t, D> {
             q[s] = __builtin_bit_cast(bf16x8_t, w);
         }
     }
-    // Addresses of the lane's reads in a tile.  Steps s and s + 4 are 128 bytes apart under every swizzle, and so are
-    // the channel blocks b and b + 2: four and two registers, the rest is in the instructions' offsets.
+    // Addresses of the lane's reads in a tile: the rest is in the instructions' offsets
     struct At {
-        uint32_t k[4], v[2];
+        uint32_t k[L::regs], v[D / 32];
         __device__ __forceinline__ void move(uint32_t by) {
 #pragma unroll
-            for (int s = 0; s < 4; ++s) hide_int(k[s] += by);
+            for (int s = 0; s < L::regs; ++s) hide_int(k[s] += by);
 #pragma unroll
-            for (int b = 0; b < 2; ++b) hide_int(v[b] += by);
+            for (int b = 0; b < D / 32; ++b) hide_int(v[b] += by);
         }
         __device__ __forceinline__ At(uint32_t k0, uint32_t v0, int lane) {
             const int row = lane & 31, half = lane >> 5, grp = lane >> 4, r = (lane >> 2) & 3;
 #pragma unroll
-            for (int s = 0; s < 4; ++s) k[s] = k0 + row * L::row_bytes + 16 * ((2 * s + half) ^ L::swz_k(row));
+            for (int s = 0; s < L::regs; ++s) k[s] = k0 + row * L::row_bytes + 16 * ((2 * s + half) ^ L::swz_k(row));
 #pragma unroll
-            for (int b = 0; b < 2; ++b)
+            for (int b = 0; b < D / 32; ++b)
                 v[b] = v0 + (4 * (grp >> 1) + r) * L::row_bytes + 16 * ((4 * b + 2 * (grp & 1) + ((lane & 3) >> 1)) ^ L::swz_v(r)) +
                        8 * (lane & 1);
         }
@@ -163,7 +165,7 @@ template <int D> struct AttnCore<bf16_t, D> {
         f32x16_t acc = {};
 #pragma unroll
         for (int s = 0; s < steps; ++s) {
-            const bf16x8_t a = *(lds_v8*)(uintptr_t)(at.k[s & 3] + (128 * (s >> 2) + 32 * block * L::row_bytes));
+            const bf16x8_t a = *(lds_v8*)(uintptr_t)(at.k[s % L::regs] + (32 * L::regs * (s / L::regs) + 32 * block * L::row_bytes));
             acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, q[s], acc, 0, 0, 0);
         }
         return acc;
@@ -172,9 +174,9 @@ template <int D> struct AttnCore<bf16_t, D> {
     __device__ __forceinline__ static bf16x8_t values(int block, int t, int b, const At& at) {
         typedef short v4i16 __attribute__((ext_vector_type(4)));
         typedef __attribute__((address_space(3))) v4i16 lds_v4i16;
-        const uint32_t off = 128 * (b >> 1) + (32 * block + 16 * t) * L::row_bytes;
-        const v4i16 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(uintptr_t)(at.v[b & 1] + off));
-        const v4i16 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(uintptr_t)(at.v[b & 1] + (off + 8 * L::row_bytes)));
+        const uint32_t off = (32 * block + 16 * t) * L::row_bytes;
+        const v4i16 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(uintptr_t)(at.v[b] + off));
+        const v4i16 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(uintptr_t)(at.v[b] + (off + 8 * L::row_bytes)));
         return __builtin_bit_cast(bf16x8_t, s16x8_t{x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]});
     }
     // o += V^T p, with the weights rounded to bf16; their sum takes them as they are, for the sake of lse
@@ -251,16 +253,16 @@ template <int D> struct AttnCore<float, D> {
     static constexpr int nb = D / 32;
     typedef float vec_t __attribute__((ext_vector_type(nb)));
     struct At {
-        uint32_t k[4], v;
+        uint32_t k[L::regs], v;
         __device__ __forceinline__ void move(uint32_t by) {
 #pragma unroll
-            for (int s = 0; s < 4; ++s) hide_int(k[s] += by);
+            for (int s = 0; s < L::regs; ++s) hide_int(k[s] += by);
             hide_int(v += by);
         }
         __device__ __forceinline__ At(uint32_t k0, uint32_t v0, int lane) {
             const int row = lane & 31, half = lane >> 5;
 #pragma unroll
-            for (int s = 0; s < 4; ++s) k[s] = k0 + row * L::row_bytes + 16 * ((2 * s + half) ^ L::swz_k(row));
+            for (int s = 0; s < L::regs; ++s) k[s] = k0 + row * L::row_bytes + 16 * ((2 * s + half) ^ L::swz_k(row));
             v = v0 + 4 * half * L::row_bytes + 4 * nb * row;
         }
     };
@@ -269,7 +271,7 @@ template <int D> struct AttnCore<float, D> {
         f32x16_t acc = {};
 #pragma unroll
         for (int s = 0; s < steps; ++s) {
-            const f32x4_t a = *(lds_v4*)(uintptr_t)(at.k[s & 3] + (128 * (s >> 2) + 32 * block * L::row_bytes));
+            const f32x4_t a = *(lds_v4*)(uintptr_t)(at.k[s % L::regs] + (32 * L::regs * (s / L::regs) + 32 * block * L::row_bytes));
 #pragma unroll
             for (int e = 0; e < 4; ++e) acc = __builtin_amdgcn_mfma_f32_32x32x2f32(a[e], q[s][e], acc, 0, 0, 0);
         }
