@@ -4,6 +4,11 @@
 // and reduced to turns in 64 bits: at position 10^6 a 32-bit product would already be off by 0.03 radians.
 // A workgroup takes one token and all its heads, forms each pair's cosine and sine once into the LDS, and then only
 // moves data: two 16-byte pieces per thread, the pair's halves, so that a row may be rotated in place.
+//
+// HBM bounds it: 32768 bf16 tokens of 32 + 8 + 8 heads of 128 channels, 403 MB read and 470 written, take 144 us (6.0
+// TB/s; a large copy reaches 4.95).  With 8, 4 and 2 tokens per workgroup it was 163, 158 and 147: the angles of one token
+// are formed while others' rows move.  256 tokens take 5 us, the launch and one chain of dependent loads (sequence,
+// context, page).
 #include <hip/hip_runtime.h>
 
 #include "gdr_attn_device.h"
@@ -12,7 +17,9 @@ namespace gdr {
 namespace {
 
 constexpr int64_t kTokens = 1 << 22;   // of a launch, at most: it has fewer than 2^32 threads
-constexpr int kLarge = 4096;    // tokens of a batch whose rows no cache will hold until they are read again
+// Bytes moved, past what the last cache holds, from which on rows are read and written past the caches: 872 MB 154 us
+// through them and 146 past them, 436 MB 79 and 74; 218 MB 36 and 39, 215 MB of fp32 40 and 47.
+constexpr int64_t kLarge = (int64_t)1 << 28;
 
 // NT: rows of a large batch are read and written past the caches.
 template <bool NT> __device__ __forceinline__ u32x4_t read16(const char* p, int c) {
@@ -154,8 +161,9 @@ hipError_t launch(const RopeArgs& a, hipStream_t stream) {
 template <typename T, int D>
 hipError_t launch(const RopeArgs& a, hipStream_t stream) {
     hipError_t e = hipSuccess;
+    const bool large = a.T * (2 * a.HQ + 5 * a.HK) * D * Elem<T>::bytes >= kLarge;
     for (RopeArgs part = a; part.first < a.T && e == hipSuccess; part.first += kTokens)
-        e = a.T >= kLarge ? launch<T, D, true>(part, stream) : launch<T, D, false>(part, stream);
+        e = large ? launch<T, D, true>(part, stream) : launch<T, D, false>(part, stream);
     return e;
 }
 

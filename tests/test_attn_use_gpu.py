@@ -368,6 +368,31 @@ def test_appending_more_tokens_than_a_launch_takes():
         _rotated_close(f64(ko[at]), w[:, 1:], theta, False, "bf16", "k")
 
 
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_appending_past_the_caches(io, interleaved):
+    """A batch that no cache holds, stored as one call and as two of half the tokens."""
+    r = np.random.default_rng(77)
+    T, HQ, HK, D, page = 16000 if io == "bf16" else 8000, 16, 8, 128, 16
+    (q, _), (k, _), (v, _) = normal(r, (T, HQ, D), io), normal(r, (T, HK, D), io), normal(r, (T, HK, D), io)
+    need = T // page + 1
+    table, freq = r.permutation(need).astype(np.int32)[None], to_dev(_freq(1, D // 2))
+    got = []
+    for parts in (1, 2):
+        kp, vp = torch.zeros(need, HK, page, D, dtype=TORCH[io], device="cuda"), torch.zeros(need, HK, page, D, dtype=TORCH[io], device="cuda")
+        outs = []
+        for i in range(parts):
+            a, n = i * T // parts, T // parts
+            outs.append(gdr.gdr_rope_append_paged(q[a:a + n], k[a:a + n], v[a:a + n], freq, k_pages=kp, v_pages=vp, page_table=to_dev(table),
+                                                  cu_seqlens=to_dev(np.array([0, n], np.int32)), context_lens=to_dev(np.array([a], np.int32)),
+                                                  interleaved=interleaved))
+        got.append([kp, vp] + [torch.cat(x) for x in zip(*outs)])
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+    some = [0, 1, T // 2, T - 1]
+    _rotated_close(f64(got[0][2][some]), f64(q[some]), attn.angles(np.array([some]), _freq(1, D // 2)), interleaved, io, "q")
+
+
 def test_joining_more_rows_than_a_launch_has_waves():
     N = 20000
     d = _decode_inputs(75, "f32", 64, 16, 1, [1] * N, [20 + n % 3 for n in range(N)], 16, groups=[(N, 16)])
