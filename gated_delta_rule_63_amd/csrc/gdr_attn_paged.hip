@@ -9,6 +9,14 @@
 // joined by the last kernel.
 //   attn_paged_kernel   the groups' prefixes (with prefixes), then what is each sequence's own
 //   attn_join_kernel    parts -> outputs
+//
+// Long caches are bound by HBM: 64 sequences of up to 8191 tokens, 8 key heads of 128 bf16 channels, 976 MB, take 177 us
+// (5.5 TB/s) and their join 5; 1..12 tokens each against up to 4095, 554 MB, 124 + 9.  Short ones are bound by latency:
+// one sequence of 4097 tokens (17 MB) takes 11.6 + 5.3 us, a chain of dependent loads (lengths, page, tile) and two tiles;
+// stretches of at least two or four tiles took as long or 1.5 us longer.  With a prefix of 16384 tokens for 64 sequences
+// its parts are a third of the traffic: 33 us (18% of the matrix unit's cycles), then 25 for up to 512 own tokens each and
+// 10 to join.  In fp32 a product takes eight times as many of these cycles as in bf16, and 4 rows fill an eighth of a
+// block: 32 x 8 beams over 1000 tokens with up to 127 of their own 24 + 28 + 8 us.
 #include <hip/hip_runtime.h>
 
 #include "gdr_attn_device.h"
@@ -17,8 +25,7 @@ namespace gdr {
 namespace {
 
 constexpr int kKeys = 64;       // keys per tile
-constexpr int kJoinGroups = 1 << 16;   // workgroups that join with prefixes, at most
-constexpr int kMinTiles = 2;    // tiles of a workgroup's stretch at least: below, parts cost more than they save
+constexpr int kJoinGroups = 1 << 16;   // workgroups that join with prefixes, at most (a launch has fewer than 2^32 threads)
 
 // what stands for a page outside the cache: finite rows that nobody sees
 __device__ __align__(256) const char zero_rows[16 * 512] = {};
@@ -38,7 +45,7 @@ __device__ __forceinline__ int keys_of(const AttnPagedArgs& a, int ctx, int toke
 
 // tiles of a stretch, of a line of so many
 __device__ __forceinline__ int stretch(const AttnPagedArgs& a, int tiles) {
-    return max((int)(((int64_t)tiles + a.per_head - 1) / a.per_head), kMinTiles);
+    return max((int)(((int64_t)tiles + a.per_head - 1) / a.per_head), 1);
 }
 
 // Group g's sequences [s, e), the first of them that is not padded (its pages are the group's; -1: none) and the keys in
@@ -531,7 +538,6 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnPagedArgs a) {
 // With prefixes: one wave per (token, query head); parts of the prefix and of the sequence's own keys.
 template <typename T, int D>
 __global__ __launch_bounds__(256) void attn_join_groups_kernel(AttnPagedArgs a) {
-    // (a launch has fewer than 2^32 threads)
     for (int64_t id = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); id < a.T * a.HQ; id += 4 * (int64_t)gridDim.x) {
         const int token = (int)(id / a.HQ), head = (int)(id % a.HQ);
         if (a.cu && token >= a.cu[a.N]) return;
