@@ -818,7 +818,7 @@ def _token_rows(t, name: str, heads, dim, dtype, device: int):
     if t.get_device() != device:
         raise ValueError(f"{name} is on {t.device}, expected cuda:{device}")
     st, sh, sd = t.stride()
-    if sd != 1 or (sh != dim and heads > 1):
+    if shape[0] > 0 and (sd != 1 or (sh != dim and heads > 1)):   # (no tokens: any strides)
         raise ValueError(f"{name}: a token's heads must be contiguous")
     return t.data_ptr(), st if shape[0] > 1 else heads * dim
 

@@ -441,6 +441,8 @@ def test_nothing_to_do():
     assert gdr.gdr_attn_decode_paged(z(0, 2, 64), kp, vp, i(3, 4), i(3), cu_seqlens=i(4)).shape == (0, 2, 64)
     q, k = gdr.gdr_rope_append_paged(z(0, 2, 64), z(0, 1, 64), z(0, 1, 64), z(32), k_pages=kp, v_pages=vp, page_table=i(0, 4), context_lens=i(0))
     assert q.shape == (0, 2, 64) and k.shape == (0, 1, 64)
+    odd = torch.zeros(4, 64, 2, device="cuda").transpose(1, 2)[:0]      # strides of a tensor without tokens mean nothing
+    assert gdr.gdr_attn_prefill_fwd(odd, odd, odd, cu_seqlens=i(4)).shape == (0, 2, 64)
     # all padded; a table without columns: rows see nothing
     o = gdr.gdr_attn_decode_paged(torch.ones(3, 2, 64, device="cuda"), kp, vp, i(3, 4), i(3) - 1, o=z(3, 2, 64) + 7)
     assert bool((o == 7).all())
