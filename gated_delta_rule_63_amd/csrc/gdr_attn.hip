@@ -21,14 +21,19 @@ namespace {
 
 constexpr int kSorted = 64;   // sequences, at most, whose tiles are sorted by cost
 
-template <typename T, int D, int KW, int RW>
+// keys of a tile
+template <typename T, int D, int KW> constexpr int tile_keys() { return KW == 4 ? 128 : D * Elem<T>::bytes == 512 && KW == 1 ? 32 : 64; }
+
+// ONE: the LDS holds one tile only, so that two workgroups fit a CU; the next keys are on their way during the softmax and the
+// products with the values, the next values during the products with the keys.
+template <typename T, int D, int KW, int RW, bool ONE>
 __global__ __launch_bounds__(64 * KW * RW, 2) void attn_prefill_kernel(AttnPrefillArgs a) {
     using L = AttnTile<T, D>;
     using C = AttnCore<T, D>;
     constexpr int WAVES = KW * RW, kRows = 32 * RW;
-    constexpr int kKeys = KW == 4 ? 128 : L::row_bytes == 512 && KW == 1 ? 32 : 64, blocks = kKeys / 32 / KW;
+    constexpr int kKeys = tile_keys<T, D, KW>(), blocks = kKeys / 32 / KW;
     constexpr int tile_bytes = kKeys * L::row_bytes;
-    __shared__ __align__(1024) char lds[4 * tile_bytes];
+    __shared__ __align__(1024) char lds[(ONE ? 2 : 4) * tile_bytes];
     __shared__ uint32_t special_rows[2][kKeys / 32];
     __shared__ float xch[RW * KW][64];
     if (threadIdx.x < kKeys / 16) special_rows[threadIdx.x / (kKeys / 32)][threadIdx.x % (kKeys / 32)] = 0;
@@ -98,34 +103,48 @@ __global__ __launch_bounds__(64 * KW * RW, 2) void attn_prefill_kernel(AttnPrefi
             vo[i] = row * vs + L::template copy_byte<true>(first, lane);
         }
     };
-    auto stage = [&](int j0, uint32_t to) {
+    auto stage_keys = [&](int j0, uint32_t to) {
         if (j0 + kKeys > end) places(end - 1 - j0);
         const char* const k0 = copy_base(kb + (int64_t)j0 * a.k_stride * L::es);
+#pragma unroll
+        for (int i = 0; i < per; ++i) copy_to_lds(k0, ko[i], to + 1024 * (per * wave + i));
+    };
+    auto stage_values = [&](int j0, uint32_t to) {
         const char* const v0 = copy_base(vb + (int64_t)j0 * a.v_stride * L::es);
 #pragma unroll
-        for (int i = 0; i < per; ++i) {
-            copy_to_lds(k0, ko[i], to + 1024 * (per * wave + i));
-            copy_to_lds(v0, vo[i], to + tile_bytes + 1024 * (per * wave + i));
-        }
+        for (int i = 0; i < per; ++i) copy_to_lds(v0, vo[i], to + tile_bytes + 1024 * (per * wave + i));
     };
+    auto stage = [&](int j0, uint32_t to) { stage_keys(j0, to); stage_values(j0, to); };
     const uint32_t base = lds_address(lds);
     places(kKeys - 1);
     stage(lo, base);
     typename C::At at(base, base + tile_bytes, lane);
     uint32_t to = base + 2 * tile_bytes;
     for (int j0 = lo; j0 < hi; j0 += kKeys) {
+        const bool next = j0 + kKeys < hi, here = j0 < whi && j0 + kKeys > wlo;
+        f32x16_t s[blocks];
+        if constexpr (ONE) {
+            wait_copies<per>();   // the values' are behind the keys'
+            __syncthreads();
+            if (here)
+#pragma unroll
+                for (int b = 0; b < blocks; ++b) s[b] = C::scores(blocks * kw + b, at, q);
+        }
         wait_copies();
         __syncthreads();
-        if (j0 + kKeys < hi) stage(j0 + kKeys, to);
+        if (next) {
+            if constexpr (ONE) stage_keys(j0 + kKeys, base);
+            else stage(j0 + kKeys, to);
+        }
         const bool uneven = j0 + kKeys - 1 > t0 || j0 < latest;
         if (uneven) {
             turn ^= 1;
-            take_out_specials<T, D, kKeys, WAVES>(2 * base + 3 * tile_bytes - to, special_rows, turn, wave, lane);
+            take_out_specials<T, D, kKeys, WAVES>(ONE ? base + tile_bytes : 2 * base + 3 * tile_bytes - to, special_rows, turn, wave, lane);
         }
-        if (j0 < whi && j0 + kKeys > wlo) {
-            f32x16_t s[blocks];
+        if (here) {
+            if constexpr (!ONE)
 #pragma unroll
-            for (int b = 0; b < blocks; ++b) s[b] = C::scores(blocks * kw + b, at, q);
+                for (int b = 0; b < blocks; ++b) s[b] = C::scores(blocks * kw + b, at, q);
             auto seen = [&](int j) { return j >= start && j <= t; };
             if (j0 + kKeys - 1 > wfirst || j0 < wlate)
 #pragma unroll
@@ -140,13 +159,18 @@ __global__ __launch_bounds__(64 * KW * RW, 2) void attn_prefill_kernel(AttnPrefi
                         if (seen(j) && j < stop) C::add_specials(vb + (int64_t)j * a.v_stride * L::es, half, r.o);
                     }
         }
-        const uint32_t by = to - base == 0 ? (uint32_t)(-2 * tile_bytes) : 2 * tile_bytes;
-        at.move(by);
-        to -= by;
+        if constexpr (ONE) {
+            __syncthreads();
+            if (next) stage_values(j0 + kKeys, base);
+        } else {
+            const uint32_t by = to - base == 0 ? (uint32_t)(-2 * tile_bytes) : 2 * tile_bytes;
+            at.move(by);
+            to -= by;
+        }
     }
     float l = both_sum(r.l);
     if constexpr (KW > 1) {
-        static_assert(RW * KW * 64 * D <= 4 * tile_bytes, "outputs in the tiles' place");
+        static_assert(RW * KW * 64 * D <= (ONE ? 2 : 4) * tile_bytes, "outputs in the tiles' place");
         join_waves<D, KW>(r.o, r.m, l, a.c, reinterpret_cast<float*>(lds) + rw * (KW * 64 * D / 4), xch[rw * KW], kw, lane);
         if (kw > 0) return;
     }
@@ -161,8 +185,18 @@ __global__ __launch_bounds__(64 * KW * RW, 2) void attn_prefill_kernel(AttnPrefi
 template <typename T, int D, int KW, int RW>
 hipError_t start(AttnPrefillArgs a, hipStream_t stream) {
     a.tiles = (int)((a.T + 32 * RW - 1) / (32 * RW)) + (a.N <= kSorted ? a.N - 1 : 0);
-    attn_prefill_kernel<T, D, KW, RW><<<dim3((unsigned)(a.tiles * a.HQ)), 64 * KW * RW, 0, stream>>>(a);
-    return hipGetLastError();
+    const int n = a.tiles * a.HQ;
+    const auto run = [&](auto* kernel) {
+        kernel<<<dim3((unsigned)n), 64 * KW * RW, 0, stream>>>(a);
+        return hipGetLastError();
+    };
+    // Where two tiles leave room for one workgroup on a CU: with one tile each from nearly two rounds of the card on (fp32, 8
+    // heads, D = 64, 3001 tokens 55 us, with two tiles 74; 2500 tokens 43 and 55; D = 128, 6000 tokens 343 and 385), and in
+    // less than one (bf16, 8 heads, D = 128, 1000 tokens 17 and 19.5).  In between two workgroups meet on some CUs while
+    // others are idle (fp32, D = 64, 1500 tokens 30 and 27; D = 128, 3000 tokens 166 and 136).
+    if constexpr (4 * tile_keys<T, D, KW>() * D * Elem<T>::bytes > 80 * 1024)
+        if (n <= 256 || n > 448) return run(attn_prefill_kernel<T, D, KW, RW, true>);
+    return run(attn_prefill_kernel<T, D, KW, RW, false>);
 }
 
 template <typename T, int D>
@@ -174,7 +208,7 @@ hipError_t launch(const AttnPrefillArgs& a, hipStream_t stream) {
     // round of the card, that: 16 heads, D = 64, 1000 tokens 13 us (64 rows 15), twice as many 27 (26); 8 heads, D = 128,
     // 1000 tokens 20 (21), 2000 38 (36); fp32, D = 64, 3001 tokens 70 (89).
     const int64_t wide = (a.T + 127) / 128 * a.HQ;
-    constexpr int es = Elem<T>::bytes, few = es == 4 ? 256 : D == 64 ? 128 : 64;
+    constexpr int es = Elem<T>::bytes, few = es == 4 ? 256 : 128;
     if constexpr (D * es <= 256)
         if (wide <= few) return start<T, D, 4, 1>(a, stream);
     return wide < 640 ? start<T, D, 2, 2>(a, stream) : start<T, D, 1, 4>(a, stream);
