@@ -204,13 +204,15 @@ hipError_t launch(const AttnPrefillArgs& a, hipStream_t stream) {
     // `wide`: workgroups of 128 rows.  From 640 on they fill the card, and rows that share a tile's reads count most: 32
     // heads, D = 128, bf16, 2000 tokens 55 us (64 rows 56), 4000 148 (173); 16 heads, D = 64, 6000 tokens 116 (116),
     // 16000 563 (646); fp32, 8 heads, D = 128, 12000 tokens 1244 (1277).  Below, 64 rows by two waves each: 32 heads, D =
-    // 128, 1000 tokens 24 us (128 rows 28), fp32 6000 tokens 400 (612).  As long as 32 rows by four waves are about one
-    // round of the card, that: 16 heads, D = 64, 1000 tokens 13 us (64 rows 15), twice as many 27 (26); 8 heads, D = 128,
-    // 1000 tokens 20 (21), 2000 38 (36); fp32, D = 64, 3001 tokens 70 (89).
+    // 128, 1000 tokens 24 us (128 rows 28), fp32 6000 tokens 400 (612).  Small batches of sequences that are long enough
+    // for four waves to share their keys take 32 rows by four waves: 16 heads, D = 64, 1000 tokens 13 us (64 rows 15), twice as
+    // many 27 (26); 16 heads, D = 128, 1000 tokens 19 (21), in 4 sequences 14 (14), in 8 18 (12); 8 heads, 3000 tokens 44
+    // (54) but 32 heads, 700 tokens 23 (19); fp32, 8 heads, D = 64, 3 sequences of 600 tokens 14 (20), 8 of 1000 18 (16), 16 of
+    // 3000 30 (28), 3 of 3001 55 (89).
     const int64_t wide = (a.T + 127) / 128 * a.HQ;
-    constexpr int es = Elem<T>::bytes, few = es == 4 ? 256 : 128;
+    constexpr int es = Elem<T>::bytes, few = es == 4 ? 256 : 128, tokens = es == 4 ? 192 : 256;
     if constexpr (D * es <= 256)
-        if (wide <= few) return start<T, D, 4, 1>(a, stream);
+        if (wide <= few && a.T >= (int64_t)tokens * a.N) return start<T, D, 4, 1>(a, stream);
     return wide < 640 ? start<T, D, 2, 2>(a, stream) : start<T, D, 1, 4>(a, stream);
 }
 
