@@ -731,7 +731,7 @@ size_t gdr_attn_workspace_size(const gdr_attn_problem* p, int32_t max_q_len, int
     if (check_attn(p) != GDR_SUCCESS || max_q_len < 1 || max_q_len > 12) return 0;
     if (num_groups < 0 || num_groups > 65535 || p->num_seqs == 0 || p->total_tokens == 0) return 0;
     return gdr::attn_paged_plan(p->total_tokens, p->num_seqs, p->num_q_heads, p->num_kv_heads, p->head_dim,
-                                elem_bytes(p->io_dtype), max_q_len, num_groups).total;
+                                max_q_len, num_groups).total;
 }
 
 gdr_status gdr_attn_decode_paged(const gdr_attn_problem* p, int32_t max_q_len, const void* q, const int32_t* cu_seqlens,
@@ -755,7 +755,7 @@ gdr_status gdr_attn_decode_paged(const gdr_attn_problem* p, int32_t max_q_len, c
     if (!(q && o && context_lens) || !aligned16(o) || !rows_ok(p, q, p->num_q_heads, p->q_stride)) return GDR_ERROR_INVALID_VALUE;
     if (num_groups > 0 && !(group_offsets && prefix_lens)) return GDR_ERROR_INVALID_VALUE;
     const gdr::AttnPagedPlan pl = gdr::attn_paged_plan(p->total_tokens, p->num_seqs, p->num_q_heads, p->num_kv_heads,
-                                                       p->head_dim, elem_bytes(p->io_dtype), max_q_len, num_groups);
+                                                       p->head_dim, max_q_len, num_groups);
     if (!workspace || workspace_bytes < pl.total) return GDR_ERROR_INVALID_VALUE;
     if (reinterpret_cast<uintptr_t>(workspace) % 256 != 0) return GDR_ERROR_INVALID_VALUE;
     // what is written may meet neither what is read nor one another

@@ -19,6 +19,8 @@
 // block: 32 x 8 beams over 1000 tokens with up to 127 of their own 24 + 28 + 8 us.
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "gdr_attn_device.h"
 
 namespace gdr {
@@ -246,7 +248,11 @@ __global__ __launch_bounds__(64 * KW * RW, 2) void attn_paged_kernel(AttnPagedAr
     using C = AttnCore<T, D>;
     constexpr int WAVES = KW * RW, THREADS = 64 * WAVES, blocks = 2 / KW, block_rows = 32 * RW;
     constexpr int tile_bytes = kKeys * L::row_bytes;
-    __shared__ __align__(1024) char lds[4 * tile_bytes];
+    // Two tiles of fp32 rows of 128 channels would leave room for one workgroup on a CU.  With one, the next keys are on their way
+    // during the softmax and the products with the values, the next values during the products with the keys (64 sequences of
+    // up to 8191 tokens 360 us, with two tiles 631).
+    constexpr bool ONE = L::row_bytes == 512;
+    __shared__ __align__(1024) char lds[(ONE ? 2 : 4) * tile_bytes];
     __shared__ float xch[RW][2][64];
     __shared__ Line<THREADS> line;
     __shared__ Item items[kItems];
@@ -295,7 +301,7 @@ __global__ __launch_bounds__(64 * KW * RW, 2) void attn_paged_kernel(AttnPagedAr
         vo[i] = row + L::template copy_byte<true>(64 * i, lane);
     }
     const uint32_t base = lds_address(lds);
-    auto stage = [&](const Pages& pages, int j0, int key1, uint32_t to) {
+    auto stage_part = [&](const Pages& pages, int j0, int key1, uint32_t to, auto keys, auto values) {
 #pragma unroll
         for (int g = 0; g < groups16; ++g) {
             const int r0 = 16 * (groups16 * wave + g), j = j0 + r0, last = key1 - 1 - j;
@@ -309,21 +315,26 @@ __global__ __launch_bounds__(64 * KW * RW, 2) void attn_paged_kernel(AttnPagedAr
             if (last >= 15 || p < 0) {
 #pragma unroll
                 for (int i = 0; i < copies; ++i) {
-                    copy_to_lds(k, ko[i], dst + 1024 * i);
-                    copy_to_lds(v, vo[i], dst + tile_bytes + 1024 * i);
+                    if constexpr (keys.value) copy_to_lds(k, ko[i], dst + 1024 * i);
+                    if constexpr (values.value) copy_to_lds(v, vo[i], dst + tile_bytes + 1024 * i);
                 }
             } else {   // behind the last key, which nobody sees: that key again, and zeros for values (0 * inf)
                 typedef __attribute__((address_space(3))) f32x4_t lds_f4;
 #pragma unroll
                 for (int i = 0; i < copies; ++i) {
                     const int over = max(L::copy_row(64 * i, lane) - last, 0);
-                    copy_to_lds(k, ko[i] - over * L::row_bytes, dst + 1024 * i);
-                    if (over > 0) *(lds_f4*)(uintptr_t)(dst + tile_bytes + 1024 * i + 16 * lane) = f32x4_t{};
-                    else copy_to_lds(v, vo[i], dst + tile_bytes + 1024 * i);
+                    if constexpr (keys.value) copy_to_lds(k, ko[i] - over * L::row_bytes, dst + 1024 * i);
+                    if constexpr (values.value) {
+                        if (over > 0) *(lds_f4*)(uintptr_t)(dst + tile_bytes + 1024 * i + 16 * lane) = f32x4_t{};
+                        else copy_to_lds(v, vo[i], dst + tile_bytes + 1024 * i);
+                    }
                 }
             }
         }
     };
+    constexpr std::true_type yes{};
+    constexpr std::false_type no{};
+    auto stage = [&](const Pages& pages, int j0, int key1, uint32_t to) { stage_part(pages, j0, key1, to, yes, yes); };
 
     uint32_t to = base;
     typename C::At at(base, base + tile_bytes, lane);
@@ -339,7 +350,7 @@ __global__ __launch_bounds__(64 * KW * RW, 2) void attn_paged_kernel(AttnPagedAr
         cache = nullptr;
         __syncthreads();
         const int n_items = uniform(found);
-        {
+        if constexpr (!ONE) {
             const Item it = same(items[0]);
             const int j0 = it.key0 + it.tile * kKeys;
             stage(pages_of(it.table, j0, it.key1), j0, it.key1, to);
@@ -348,6 +359,11 @@ __global__ __launch_bounds__(64 * KW * RW, 2) void attn_paged_kernel(AttnPagedAr
             const Item it = same(items[i]), next = same(items[min(i + 1, n_items - 1)]);
             const bool more = i + 1 < n_items;
             Pages now = pages_of(it.table, it.key0 + it.tile * kKeys, it.key1);
+            if constexpr (ONE) {
+                const int j0 = it.key0 + it.tile * kKeys;
+                stage_part(now, j0, it.key1, to, yes, no);
+                stage_part(now, j0, it.key1, to, no, yes);
+            }
             // the lane's row
             const int r = it.row0 + 32 * rw + (lane & 31);
             const bool real = r < it.rows;
@@ -365,11 +381,24 @@ __global__ __launch_bounds__(64 * KW * RW, 2) void attn_paged_kernel(AttnPagedAr
                 const int key1 = inside ? it.key1 : next.key1;
                 const int ahead0 = inside ? it.key0 + (tile + 1) * kKeys : next.key0 + next.tile * kKeys;
                 const Pages ahead = pages_of(inside ? it.table : next.table, ahead0, key1);
+                f32x16_t s[blocks];
+                if constexpr (ONE) {
+                    // the values' copies are the last ones (fewer of them where rows behind the last key take zeros)
+                    if (it.key0 + (tile + 1) * kKeys <= it.key1) wait_copies<copies * groups16>();
+                    else wait_copies();
+                    __syncthreads();
+#pragma unroll
+                    for (int b = 0; b < blocks; ++b) s[b] = C::scores(KW == 2 ? kw : b, at, q);
+                }
                 wait_copies();
                 __syncthreads();
                 const uint32_t v = to + tile_bytes;
-                to = 2 * base + 2 * tile_bytes - to;
-                if (inside || more) stage(ahead, ahead0, key1, to);
+                if constexpr (ONE) {
+                    if (inside) stage_part(ahead, ahead0, key1, to, yes, no);
+                } else {
+                    to = 2 * base + 2 * tile_bytes - to;
+                    if (inside || more) stage(ahead, ahead0, key1, to);
+                }
 
                 const int j0 = it.key0 + tile * kKeys;
                 // tokens see less than the last of theirs: some rows do not see what others do
@@ -378,9 +407,9 @@ __global__ __launch_bounds__(64 * KW * RW, 2) void attn_paged_kernel(AttnPagedAr
                     turn ^= 1;
                     take_out_specials<T, D, kKeys, WAVES>(v, special_rows, turn, wave, lane);
                 }
-                f32x16_t s[blocks];
+                if constexpr (!ONE)
 #pragma unroll
-                for (int b = 0; b < blocks; ++b) s[b] = C::scores(KW == 2 ? kw : b, at, q);
+                    for (int b = 0; b < blocks; ++b) s[b] = C::scores(KW == 2 ? kw : b, at, q);
                 int pages = 0;   // bit g: keys 16 g .. 16 g + 15 of the tile are in the cache
 #pragma unroll
                 for (int g = 0; g < 4; ++g) pages |= (now.p[g] >= 0) << g;
@@ -404,7 +433,12 @@ __global__ __launch_bounds__(64 * KW * RW, 2) void attn_paged_kernel(AttnPagedAr
                                                 ((((int64_t)p * a.HK + kvh) << a.page_shift) + (j & ((1 << a.page_shift) - 1))) * L::row_bytes,
                                                 half, acc.o);
                         }
-                at.move(to == base ? (uint32_t)(-2 * tile_bytes) : 2 * tile_bytes);
+                if constexpr (ONE) {
+                    __syncthreads();
+                    if (inside) stage_part(ahead, ahead0, key1, to, no, yes);
+                } else {
+                    at.move(to == base ? (uint32_t)(-2 * tile_bytes) : 2 * tile_bytes);
+                }
                 now = ahead;
             }
 
@@ -414,7 +448,7 @@ __global__ __launch_bounds__(64 * KW * RW, 2) void attn_paged_kernel(AttnPagedAr
             if constexpr (KW == 2) {   // the two waves of a row block
                 // in the place of the last tile, which the next copies do not touch before the next barrier
                 static_assert(RW * 64 * D / 2 * 4 <= 2 * tile_bytes, "outputs in a tile's place");
-                float* const place = reinterpret_cast<float*>(lds + (2 * tile_bytes - (to - base))) + rw * (64 * D / 2);
+                float* const place = reinterpret_cast<float*>(lds + (ONE ? 0 : 2 * tile_bytes - (to - base))) + rw * (64 * D / 2);
                 join_waves<D, KW>(o, m, l, a.c, place, &xch[rw][0][0], kw, lane);
             }
             if (kw == 0) {
@@ -439,6 +473,7 @@ __global__ __launch_bounds__(64 * KW * RW, 2) void attn_paged_kernel(AttnPagedAr
             }
             // the block that it leaves unfinished, for the last kernel
             const int left = it.tiles - it.count;
+            if constexpr (ONE) __syncthreads();   // the next item's copies come over the parts
             if (!PREFIX && it.tile == 0 && left > 0 && threadIdx.x == 0)
                 a.open[w] = AttnOpen{it.token0, it.row0, min(block_rows, it.rows - it.row0), kvh, 1 + (left + per - 1) / per};
         }
@@ -599,11 +634,11 @@ size_t up(size_t x) { return (x + 255) / 256 * 256; }
 
 }  // namespace
 
-AttnPagedPlan attn_paged_plan(int64_t T, int32_t N, int32_t HQ, int32_t HK, int D, int io_bytes, int32_t max_q_len, int32_t groups) {
+AttnPagedPlan attn_paged_plan(int64_t T, int32_t N, int32_t HQ, int32_t HK, int D, int32_t max_q_len, int32_t groups) {
     AttnPagedPlan p{};
     const int64_t per = HQ / HK;
     // as many as are resident at once, by their LDS; each has one key head
-    p.per_head = max(1, (D * io_bytes <= 256 ? 512 : 256) / HK);
+    p.per_head = max(1, 512 / HK);
     p.workers = p.per_head * HK;
     p.rows = rows_for(per * max_q_len);
     p.prefix_rows = groups ? rows_for((per * T + groups - 1) / groups) : 0;   // of a group of average size

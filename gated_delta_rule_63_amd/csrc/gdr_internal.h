@@ -302,7 +302,7 @@ struct AttnPagedPlan {
     size_t start, item, pre, group, prefix_start, prefix_item, prefix, first, open, slots, prefix_slots, total;
 };
 
-AttnPagedPlan attn_paged_plan(int64_t T, int32_t N, int32_t HQ, int32_t HK, int D, int io_bytes, int32_t max_q_len, int32_t groups);
+AttnPagedPlan attn_paged_plan(int64_t T, int32_t N, int32_t HQ, int32_t HK, int D, int32_t max_q_len, int32_t groups);
 hipError_t launch_attn_paged(AttnPagedArgs a, const AttnPagedPlan& p, char* ws, int D, int io_dtype, hipStream_t stream);
 
 }  // namespace gdr
