@@ -8,10 +8,10 @@
 // workgroup's work.
 //
 // The matrix unit and the clock bound the large ones: 16384 tokens of 32 heads of 128 channels, bf16, run 2199 GFLOP in
-// 2.05 ms, 1073 TFLOP/s (a product of 8192 x 8192 x 8192 by the library 1159), with the matrix unit busy 55%, vector
-// instructions 49% and the LDS 41% of the cycles at about 1.8 GHz.  8 ragged prompts of 32768 tokens 1.40 ms, 974 TFLOP/s.
-// fp32 of 64 channels, 3001 tokens of 8 heads: 69 us, 61 of the 154 TFLOP/s of such a product, in one round of 768
-// workgroups of which the longest decide.
+// 2.03 ms, 1086 TFLOP/s (a product of 8192 x 8192 x 8192 by the library 1159), with the matrix unit busy 55%, vector
+// instructions 49% and the LDS 41% of the cycles at about 1.75 GHz.  8 ragged prompts of 32768 tokens 1.36 ms, 1001
+// TFLOP/s.  fp32 of 64 channels, 3 prompts of 3001 tokens, 8 heads: 51 us, 83 of the 154 TFLOP/s of such a product, the matrix
+// unit busy 51%; the longest row blocks decide.
 #include <hip/hip_runtime.h>
 
 #include "gdr_attn_device.h"
