@@ -339,10 +339,9 @@ def test_many_heads(HQ, HK):
 
 @pytest.mark.parametrize("io", ["bf16", "f32"])
 @pytest.mark.parametrize("D", [64, 128])
-@pytest.mark.parametrize("T,HQ,HK", [(700, 4, 2), (1500, 16, 4), (1400, 64, 8)])
+@pytest.mark.parametrize("T,HQ,HK", [(700, 4, 2), (1500, 16, 4), (1400, 64, 8), (1000, 8, 8), (1300, 24, 8), (2000, 16, 4)])
 def test_every_size_of_row_blocks(T, HQ, HK, D, io):
-    """The three ways to cut a batch into workgroups: some rows of each against the oracle, the rest against the rows of
-    another cut (a batch of one head)."""
+    """The three ways to cut a batch into workgroups, with one tile in the LDS or two: the first and the last head."""
     r = np.random.default_rng(T + D)
     (q, qw), (k, kw), (v, vw) = normal(r, (T, HQ, D), io), normal(r, (T, HK, D), io), normal(r, (T, HK, D), io)
     cu = np.array([0, T // 3, T // 3, T - 5], np.int32)
