@@ -570,10 +570,11 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnPagedArgs a) {
     }
 }
 
-// With prefixes: one wave per (token, query head); parts of the prefix and of the sequence's own keys.
-template <typename T, int D>
+// With prefixes: LANES lanes per (token, query head); parts of the prefix and of the sequence's own keys.
+template <typename T, int D, int LANES>
 __global__ __launch_bounds__(256) void attn_join_groups_kernel(AttnPagedArgs a) {
-    for (int64_t id = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); id < a.T * a.HQ; id += 4 * (int64_t)gridDim.x) {
+    constexpr int rows = 256 / LANES;
+    for (int64_t id = (int64_t)blockIdx.x * rows + threadIdx.x / LANES; id < a.T * a.HQ; id += rows * (int64_t)gridDim.x) {
         const int token = (int)(id / a.HQ), head = (int)(id % a.HQ);
         if (a.cu && token >= a.cu[a.N]) return;
         const int seq = a.cu ? find_seq(a.cu, a.N, token) : token;
@@ -593,7 +594,7 @@ __global__ __launch_bounds__(256) void attn_join_groups_kernel(AttnPagedArgs a) 
         const Side own = un.tiles > 0 ? side(un.tok0, un.tiles, a.rows, own_start, own_item, own_tiles, own_items) : Side{0, 0, 0, 0};
         const Side pre = group >= 0 && pre_keys > 0
             ? side(pre_tok0, (pre_keys + kKeys - 1) / kKeys, a.prefix_rows, pre_start, pre_item, pre_tiles, pre_items) : Side{0, 0, 0, 0};
-        join_row<T, D, 64>(a, token, head, pre.parts + own.parts, [&](int k) {
+        join_row<T, D, LANES>(a, token, head, pre.parts + own.parts, [&](int k) {
             const bool p = k < pre.parts;
             const Side s = p ? pre : own;
             const int i = p ? k : k - pre.parts;
@@ -618,7 +619,10 @@ hipError_t launch(const AttnPagedArgs& a, hipStream_t stream) {
     if (e == hipSuccess) e = launch_part<T, D, false>(a, a.rows, stream);
     if (e != hipSuccess) return e;
     if (a.groups) {
-        attn_join_groups_kernel<T, D><<<dim3((unsigned)min((a.T * a.HQ + 3) / 4, (int64_t)kJoinGroups)), 256, 0, stream>>>(a);
+        // half a wave for each of many rows: 64 heads, 182 sequences of up to 5 tokens 69 us for all kernels (with a wave 95), 32 x 8
+        // fp32 beams of 16 heads 56 (57); a wave for few: 64 tokens, 32 heads, 33 parts 65 (67)
+        if (a.T * a.HQ < 4096) attn_join_groups_kernel<T, D, 64><<<dim3((unsigned)((a.T * a.HQ + 3) / 4)), 256, 0, stream>>>(a);
+        else attn_join_groups_kernel<T, D, 32><<<dim3((unsigned)min((a.T * a.HQ + 7) / 8, (int64_t)kJoinGroups)), 256, 0, stream>>>(a);
     } else {
         // few rows are likely to have many parts (one sequence of 4097 tokens, 33 parts: 6.0 us with a wave per row, 7.4 with
         // half a one), many rows few (64 sequences of 1..12 tokens, 2 or 3 parts of 48 rows: 12.4 and 9.3)
