@@ -16,7 +16,7 @@
 // stretches of at least two or four tiles took as long or 1.5 us longer.  With a prefix of 16384 tokens for 64 sequences
 // its parts are a third of the traffic: 33 us (18% of the matrix unit's cycles), then 25 for up to 512 own tokens each and
 // 10 to join.  In fp32 a product takes eight times as many of these cycles as in bf16, and 4 rows fill an eighth of a
-// block: 32 x 8 beams over 1000 tokens with up to 127 of their own 24 + 28 + 8 us.
+// block: 32 x 8 beams over 1000 tokens with up to 127 of their own 24 + 28 + 6 us.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
