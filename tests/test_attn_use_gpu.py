@@ -393,8 +393,9 @@ def test_appending_past_the_caches(io, interleaved):
 
 
 def test_joining_more_rows_than_a_launch_has_waves():
+    """640000 rows with a prefix: their kernel's launch has half a wave for 524288."""
     N = 20000
-    d = _decode_inputs(75, "f32", 64, 16, 1, [1] * N, [20 + n % 3 for n in range(N)], 16, groups=[(N, 16)])
+    d = _decode_inputs(75, "f32", 64, 32, 1, [1] * N, [20 + n % 3 for n in range(N)], 16, groups=[(N, 16)])
     o, lse = _decode_call(d, output_lse=True)
     rows = np.unique(np.concatenate([[0, N // 2, N - 1], np.random.default_rng(75).integers(0, N, 500)]))
     for n in rows:
