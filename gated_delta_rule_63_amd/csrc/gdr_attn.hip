@@ -194,9 +194,11 @@ hipError_t start(AttnPrefillArgs a, hipStream_t stream) {
     // heads, D = 64, 3001 tokens 55 us, with two tiles 74; 2500 tokens 43 and 55; D = 128, 6000 tokens 343 and 385), and in
     // less than one (bf16, 8 heads, D = 128, 1000 tokens 17 and 19.5).  In between two workgroups meet on some CUs while
     // others are idle (fp32, D = 64, 1500 tokens 30 and 27; D = 128, 3000 tokens 166 and 136).
-    if constexpr (4 * tile_keys<T, D, KW>() * D * Elem<T>::bytes > 80 * 1024)
-        if (n <= 256 || n > 448) return run(attn_prefill_kernel<T, D, KW, RW, true>);
-    return run(attn_prefill_kernel<T, D, KW, RW, false>);
+    // Two of D = 128 in fp32 and 128 keys do not fit at all.
+    constexpr int two = 4 * tile_keys<T, D, KW>() * D * Elem<T>::bytes;
+    if constexpr (two > 80 * 1024)
+        if (two > 160 * 1024 || n <= 256 || n > 448) return run(attn_prefill_kernel<T, D, KW, RW, true>);
+    if constexpr (two <= 160 * 1024) return run(attn_prefill_kernel<T, D, KW, RW, false>);
 }
 
 template <typename T, int D>
@@ -208,11 +210,10 @@ hipError_t launch(const AttnPrefillArgs& a, hipStream_t stream) {
     // for four waves to share their keys take 32 rows by four waves: 16 heads, D = 64, 1000 tokens 13 us (64 rows 15), twice as
     // many 27 (26); 16 heads, D = 128, 1000 tokens 19 (21), in 4 sequences 14 (14), in 8 18 (12); 8 heads, 3000 tokens 44
     // (54) but 32 heads, 700 tokens 23 (19); fp32, 8 heads, D = 64, 3 sequences of 600 tokens 14 (20), 8 of 1000 18 (16), 16 of
-    // 3000 30 (28), 3 of 3001 55 (89).
+    // 3000 30 (28), 3 of 3001 55 (89); D = 128, one head, 1 of 1669 78 (121), 8 heads, 3 of 1500 49 (69), 3 of 4000 204 (213).
     const int64_t wide = (a.T + 127) / 128 * a.HQ;
     constexpr int es = Elem<T>::bytes, few = es == 4 ? 256 : 128, tokens = es == 4 ? 192 : 256;
-    if constexpr (D * es <= 256)
-        if (wide <= few && a.T >= (int64_t)tokens * a.N) return start<T, D, 4, 1>(a, stream);
+    if (wide <= few && a.T >= (int64_t)tokens * a.N) return start<T, D, 4, 1>(a, stream);
     return wide < 640 ? start<T, D, 2, 2>(a, stream) : start<T, D, 1, 4>(a, stream);
 }
 
