@@ -341,7 +341,7 @@ __global__ __launch_bounds__(64 * KW * RW, 2) void attn_paged_kernel(AttnPagedAr
     const int tot = uniform(line.tiles[THREADS]), per = stretch(a, tot), part = w % a.per_head;
     // (in 64 bits: stretches behind the line's end)
     const int ye = (int)min(((int64_t)part + 1) * per, (int64_t)tot);
-    for (int y = (int)min((int64_t)part * per, (int64_t)tot); y < ye; y = uniform(rest)) {
+    for (int y = (int)min((int64_t)part * per, (int64_t)tot), y_next; y < ye; y = y_next) {
         if (wave == 0) {
             int next;
             const int n = find_items<PREFIX>(a, units, block_rows, line, cache, kvh, y, ye, items, next, starts, item_starts);
@@ -349,7 +349,9 @@ __global__ __launch_bounds__(64 * KW * RW, 2) void attn_paged_kernel(AttnPagedAr
         }
         cache = nullptr;
         __syncthreads();
+        // into registers before the barrier below: behind it the first wave goes on and writes them again
         const int n_items = uniform(found);
+        y_next = uniform(rest);
         if constexpr (!ONE) {
             const Item it = same(items[0]);
             const int j0 = it.key0 + it.tile * kKeys;

@@ -1,0 +1,82 @@
+"""Full attention of serving at the edges of its kernels' bookkeeping, against the fp64 oracle (tolerances: _attn.py)."""
+import numpy as np
+import pytest
+import torch
+
+from _attn import TORCH, check_attention, normal
+from _dev import f64, to_dev
+from gated_delta_rule_63_amd import gdr
+from oracle import attn
+
+pytestmark = pytest.mark.gpu
+
+
+def _repeated(seed, io, D, HQ, HK, lens, ctx, pages=12, page=16, groups=None):
+    """Inputs of a paged step whose sequences name the same few pages many times (groups: [(sequences, pages)] whose first
+    pages are the same)."""
+    r = np.random.default_rng(seed)
+    cu = np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
+    ctx = np.asarray(ctx, np.int32)
+    most = -(-int((ctx + np.asarray(lens)).max()) // page)
+    table = r.integers(0, pages, (len(lens), most)).astype(np.int32)
+    d = dict(cu=cu, ctx=ctx, table=table, io=io, D=D, HQ=HQ, HK=HK, page=page, lens=list(lens), args={})
+    if groups is not None:
+        offsets = np.concatenate([[0], np.cumsum([n for n, _ in groups])]).astype(np.int32)
+        for g, (_, shared) in enumerate(groups):
+            table[offsets[g]: offsets[g + 1], :shared] = table[offsets[g], :shared]
+        d["args"] = dict(group_offsets=to_dev(offsets), prefix_lens=to_dev(np.array([p * page for _, p in groups], np.int32)))
+    d["q"], d["qw"] = normal(r, (int(cu[-1]), HQ, D), io, 2.0)
+    (d["k"], d["kw"]), (d["v"], d["vw"]) = normal(r, (pages, HK, page, D), io), normal(r, (pages, HK, page, D), io)
+    return d
+
+
+def _run(d, **kw):
+    T = int(d["cu"][-1])
+    o = torch.full((T, d["HQ"], d["D"]), 7.0, dtype=TORCH[d["io"]], device="cuda")
+    lse = torch.full((T, d["HQ"]), 7.0, device="cuda")
+    gdr.gdr_attn_decode_paged(d["q"], d["k"], d["v"], to_dev(d["table"]), to_dev(d["ctx"]), cu_seqlens=to_dev(d["cu"]),
+                              max_q_len=max(d["lens"]), o=o, lse=lse, **d["args"], **kw)
+    torch.cuda.synchronize()
+    return f64(o), f64(lse)
+
+
+def _check_key_heads(d, heads, what=""):
+    """every row of the query heads of some key heads"""
+    o, lse = _run(d)
+    per = d["HQ"] // d["HK"]
+    live = np.repeat(d["ctx"] >= 0, d["lens"])
+    for h in heads:
+        of = slice(h * per, (h + 1) * per)
+        ref = attn.decode(d["qw"][:, of], d["cu"], d["ctx"], d["kw"][:, h:h + 1], d["vw"][:, h:h + 1], d["table"], 1 / np.sqrt(d["D"]))
+        check_attention(o[:, of], lse[:, of], ref, d["io"], np.nonzero(live)[0], f"{what} key head {h}")
+    assert (o[~live] == 7.0).all() and (lse[~live] == 7.0).all()
+
+
+# ---------------------------------------------------------------------------
+# A workgroup finds 64 sequences, or row blocks, of its stretch at a time.
+@pytest.mark.parametrize("io,D,per,q_len", [("bf16", 64, 1, 1), ("bf16", 128, 1, 3), ("f32", 64, 2, 2), ("f32", 128, 1, 1), ("bf16", 64, 5, 12),
+                                            ("f32", 128, 4, 12), ("bf16", 128, 12, 12)])
+@pytest.mark.parametrize("shared", [False, True])
+def test_stretches_of_many_sequences(shared, io, D, per, q_len):
+    """A workgroup per key head, each with the whole line of 200 sequences: some padded, some without tokens, one of several
+    tiles; with groups, 90 prefixes on a line of their own."""
+    HK, n = 520, 200
+    r = np.random.default_rng(per + D)
+    lens = r.integers(0 if q_len > 1 else 1, q_len + 1, n)
+    ctx = np.where(r.random(n) < 0.2, -1, r.integers(16, 60, n))
+    ctx[37], lens[37] = 700, q_len
+    d = _repeated([per, D], io, D, per * HK, HK, lens.tolist(), ctx, groups=[(2, i % 2) for i in range(90)] if shared else None)
+    _check_key_heads(d, [0, 7, HK - 1])
+
+
+@pytest.mark.parametrize("io,D", [("bf16", 64), ("f32", 128)])
+@pytest.mark.parametrize("at", [0, 60, 149])
+def test_one_long_context_beside_many_short_ones(at, io, D):
+    """Eight workgroups per key head: the long sequence's tiles make stretches that hold all of the short ones, before it
+    and behind it."""
+    HK, n = 64, 150
+    r = np.random.default_rng(at)
+    ctx = np.where(r.random(n) < 0.3, -1, r.integers(0, 50, n))
+    ctx[at] = 64 * 80 * 8
+    d = _repeated([at, D], io, D, HK, HK, [1] * n, ctx)
+    _check_key_heads(d, [0, 31, HK - 1])
