@@ -174,6 +174,7 @@ __global__ __launch_bounds__(64 * KW * RW, 2) void attn_prefill_kernel(AttnPrefi
         join_waves<D, KW>(r.o, r.m, l, a.c, reinterpret_cast<float*>(lds) + rw * (KW * 64 * D / 4), xch[rw * KW], kw, lane);
         if (kw > 0) return;
     }
+    if (l == 0.0f) l = no_sum();   // a row sees itself at least
     const float inv = reciprocal_sum(l);
     char* row = t < stop ? static_cast<char*>(a.o) + ((int64_t)t * a.HQ + head) * L::row_bytes : nullptr;
 #pragma unroll

@@ -407,6 +407,9 @@ __device__ __forceinline__ void take_out_specials(uint32_t v, uint32_t (*rows)[K
     if (threadIdx.x < KEYS / 32) rows[turn ^ 1][threadIdx.x] = 0;
 }
 
+// Weights without a sum: those of a row that saw nothing, whose output is 0 and lse -inf, or of one that saw scores of -inf
+// only, whose softmax is 0 / 0.  The caller knows which, and says so by a sum that is a NaN.
+__device__ __forceinline__ float no_sum() { return __builtin_nanf(""); }
 // 1 / l; 0 for a row that saw nothing; a NaN stays one
 __device__ __forceinline__ float reciprocal_sum(float l) { return l == 0.0f ? 0.0f : 1.0f / l; }
 __device__ __forceinline__ float log_sum(float base, float l) {

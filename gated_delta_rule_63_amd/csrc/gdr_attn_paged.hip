@@ -175,6 +175,9 @@ __device__ __forceinline__ int find_unit(const AttnPagedArgs& a, int units, int 
     return u;
 }
 
+// The maximum of a part that saw scores of -inf only: above that of one that saw nothing, below all that have a sum.
+constexpr float kLost = -__FLT_MAX__;
+
 // Parts of a unit's row block: the slots they are in.  Workgroup w has one for a block that it goes on with and one for a
 // block that it leaves unfinished; where outputs are joined anyway, a block that it holds whole has one of its own.
 __device__ __forceinline__ int64_t open_slot(int64_t w, bool continued) { return 2 * w + (continued ? 0 : 1); }
@@ -454,8 +457,23 @@ __global__ __launch_bounds__(64 * KW * RW, 2) void attn_paged_kernel(AttnPagedAr
                 join_waves<D, KW>(o, m, l, a.c, place, &xch[rw][0][0], kw, lane);
             }
             if (kw == 0) {
+                // No weight at all: nothing that is in the cache, or scores of -inf only.  Looked up for those rows alone, so that the
+                // loop over the tiles carries nothing for it.
+                bool lost = false;
+                if (__any(real && l == 0.0f)) {
+                    const Item x = same(items[i]);
+                    const int left = l == 0.0f ? seen : 0;
+                    for (int tile = x.tile; tile < x.tile + x.count; ++tile) {
+                        const int j0 = x.key0 + tile * kKeys;
+                        if (!__any(left > j0)) break;
+                        const Pages p = pages_of(x.table, j0, x.key1);
+#pragma unroll
+                        for (int g = 0; g < 4; ++g) lost |= p.p[g] >= 0 && left - j0 > 16 * g;
+                    }
+                }
                 if (whole && !a.groups) {
                     const bool store = real && ctx >= 0;
+                    if (lost) l = no_sum();
                     const float inv = reciprocal_sum(l);
                     char* row = store ? static_cast<char*>(a.o) + ((int64_t)token * a.HQ + head) * L::row_bytes : nullptr;
 #pragma unroll
@@ -468,7 +486,7 @@ __global__ __launch_bounds__(64 * KW * RW, 2) void attn_paged_kernel(AttnPagedAr
                     const int row = 32 * rw + (lane & 31);
                     C::store_part(s + row * D, half, o);
                     if (half == 0) {
-                        s[block_rows * D + row] = m == kNegInf ? kNegInf : m * a.c;
+                        s[block_rows * D + row] = lost ? kLost : m == kNegInf ? kNegInf : m * a.c;
                         s[block_rows * D + block_rows + row] = l;
                     }
                 }
@@ -537,6 +555,7 @@ __device__ __forceinline__ void join_row(const AttnPagedArgs& a, int token, int 
 #pragma unroll
         for (int i = 0; i < V; ++i) o[i] += __shfl_xor(o[i], 32);
     if (turn > 0) return;
+    if (l == 0.0f && m > kNegInf) l = no_sum();
     const int64_t id = (int64_t)token * a.HQ + head;
     const float inv = reciprocal_sum(l);
     if constexpr (Elem<T>::bytes == 4) {

@@ -493,8 +493,9 @@ GDR_API gdr_status gdr_beam_reorder(int32_t batch, int32_t beams, const int32_t*
  *     o[t,h] = sum_j p_j v[j,h']       p = softmax over the visible j of  scale q[t,h] . k[j,h']
  *     lse[t,h] = log sum_j e^(scale q[t,h] . k[j,h'])
  *
- * A row that sees nothing has o = 0 and lse = -inf.  What a row does not see has no part in it: infinities and NaN
- * in the keys and values of other sequences, of later tokens and of the cache's unused rows included.
+ * A row that sees nothing has o = 0 and lse = -inf; one that sees keys, but scores of -inf only (a key that is infinite),
+ * has NaN in both.  What a row does not see has no part in it: infinities and NaN in the keys and values of other
+ * sequences, of later tokens and of the cache's unused rows included.
  * Scores, the softmax and the sums are held in fp32; with bf16 I/O the weights p are rounded to bf16 (relative to
  * the row's running maximum) for the product with v, whose products are exact and summed in fp32.
  *

@@ -7,6 +7,7 @@ from _attn import TORCH, check_attention, normal
 from _dev import f64, to_dev
 from gated_delta_rule_63_amd import gdr
 from oracle import attn
+from test_attn_gpu import _decode_call, _decode_inputs
 
 pytestmark = pytest.mark.gpu
 
@@ -80,3 +81,70 @@ def test_one_long_context_beside_many_short_ones(at, io, D):
     ctx[at] = 64 * 80 * 8
     d = _repeated([at, D], io, D, HK, HK, [1] * n, ctx)
     _check_key_heads(d, [0, 31, HK - 1])
+
+
+# ---------------------------------------------------------------------------
+# A row that sees nothing has o = 0 and lse = -inf; one that sees scores of -inf only has neither.  Every query's channel 2
+# is -1 here, so that a key with an infinity there scores -inf.
+def _finite_sizes(ref, clean):
+    """the tolerance's sums come from the keys that are finite"""
+    return {**ref, "size": clean["size"]}
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("HQ,HK,lens,heads", [(4, 2, [5, 70, 1, 300], 0), (1, 1, [700], 0), (32, 8, [40] * 70 + [300], 3)])
+def test_prompts_with_scores_of_minus_infinity(HQ, HK, lens, heads, D, io):
+    """The first keys of each sequence, one to 200 of them, in one key head."""
+    r = np.random.default_rng(D + len(lens))
+    cu = np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
+    (q, qw), (k, kw), (v, vw) = (normal(r, (int(cu[-1]), h, D), io) for h in (HQ, HK, HK))
+    q[:, :, 2], qw[:, :, 2] = -1.0, -1.0
+    k[:, heads, 2], kw[:, heads, 2] = 0.0, 0.0
+    per = HQ // HK
+    some = slice(heads * per, (heads + 1) * per) if len(lens) > 60 else slice(0, HQ)    # of many sequences: the head itself
+    of = lambda x, y, z: (x[:, some], y[:, some.start // per: some.stop // per], z[:, some.start // per: some.stop // per])  # noqa: E731
+    clean = attn.prefill(*of(qw, kw, vw), cu, 1 / np.sqrt(D))
+    for n, L in enumerate(lens):
+        bad = slice(int(cu[n]), int(cu[n]) + min(L, (1, 3, 70, 200)[n % 4]))
+        k[bad, heads, 2], kw[bad, heads, 2] = float("inf"), np.inf
+    o, lse = gdr.gdr_attn_prefill_fwd(q, k, v, cu_seqlens=to_dev(cu), output_lse=True)
+    with np.errstate(invalid="ignore"):
+        ref = attn.prefill(*of(qw, kw, vw), cu, 1 / np.sqrt(D))
+    assert np.isnan(ref["o"]).any() and np.isnan(ref["lse"]).any() and not np.isnan(ref["o"]).all()
+    check_attention(f64(o)[:, some], f64(lse)[:, some], _finite_sizes(ref, clean), io, np.arange(int(cu[-1])))
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("HQ", [2, 8, 24])
+@pytest.mark.parametrize("shared", [False, True])
+def test_steps_with_scores_of_minus_infinity(shared, HQ, D, io):
+    lens = [1, 1, 2, 12, 12, 1, 3, 1, 2, 1, 3]
+    ctx = [210, 699, 699, 210, 200, 300, 0, 0, 80, -1, 30]
+    #      the prefix of two groups is all such keys, the prefix of a third is none
+    groups = [(3, 210), (2, 200), (1, 300), (0, 0)] if shared else None
+    d = _decode_inputs([HQ, D], io, D, HQ, 2, lens, ctx, 16, groups=groups)
+    d["q"][:, :, 2], d["qw"][:, :, 2] = -1.0, -1.0
+    d["k"][:, 0, :, 2], d["kw"][:, 0, :, 2] = 0.0, 0.0
+    table, num = d["table"], d["kw"].shape[0]
+    if not shared:
+        table[8, :] = -1            # sees nothing
+        table[2, 5] = table[7, 0] = -1
+        table[10, 0] = num          # its first page is none, the others' keys are all such
+    clean = attn.decode(d["qw"], d["cu"], d["ctx"], d["kw"], d["vw"], table, 1 / np.sqrt(D))
+    #        whole contexts, all but the last keys, the first ones, the last ones
+    spans = {0: (0, 211), 1: (0, 700), 2: (0, 400), 3: (0, 222), 4: (0, 200), 5: (288, 301), 6: (0, 2), 10: (16, 33)}
+    for n, (a, b) in spans.items():
+        for j in range(a, b):
+            p = attn.place(table, num, 16, n, j)
+            if p is not None:
+                d["k"][p[0], 0, p[1], 2], d["kw"][p[0], 0, p[1], 2] = float("inf"), np.inf
+    o, lse = _decode_call(d, output_lse=True)
+    with np.errstate(invalid="ignore"):
+        ref = attn.decode(d["qw"], d["cu"], d["ctx"], d["kw"], d["vw"], table, 1 / np.sqrt(D))
+    live = np.nonzero(np.repeat(np.asarray(ctx) >= 0, lens))[0]
+    assert np.isnan(ref["o"][live, 0, 0]).sum() > 10 and not np.isnan(ref["o"][live, HQ - 1]).any()
+    if not shared:
+        assert (ref["o"][d["cu"][8]: d["cu"][9]] == 0).all()
+    check_attention(f64(o), f64(lse), _finite_sizes(ref, clean), io, live)
