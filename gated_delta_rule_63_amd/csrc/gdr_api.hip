@@ -746,6 +746,8 @@ gdr_status gdr_attn_decode_paged(const gdr_attn_problem* p, int32_t max_q_len, c
     if (!cu_seqlens && p->total_tokens != p->num_seqs) return GDR_ERROR_INVALID_VALUE;
     if (p->total_tokens > (int64_t)p->num_seqs * max_q_len) return GDR_ERROR_INVALID_VALUE;
     if (p->total_tokens * p->num_q_heads > 0x7FFFFFFF) return GDR_ERROR_NOT_SUPPORTED;
+    // the ends of a row's last tile and of the tile behind it are formed in 32 bits
+    if (((int64_t)pages->max_pages << page_shift(pages->page_size)) > 0x7FFFFFFF - 127) return GDR_ERROR_NOT_SUPPORTED;
     {   // tiles of 64 keys are counted in 32 bits, over all sequences and their blocks of 32 rows
         const int64_t tiles = (((int64_t)pages->max_pages << page_shift(pages->page_size)) + 63) / 64 + 1;
         const int64_t blocks = ((int64_t)(p->num_q_heads / p->num_kv_heads) * max_q_len + 31) / 32;

@@ -528,7 +528,7 @@ typedef struct gdr_kv_pages {
     const int32_t* table;   /* [N, max_pages]                                                */
     int32_t num_pages;      /* >= 1                                                          */
     int32_t page_size;      /* a power of two, 16..65536                                     */
-    int32_t max_pages;      /* >= 0                                                          */
+    int32_t max_pages;      /* >= 0; max_pages * page_size < 2^31, in attention <= 2^31 - 128 */
 } gdr_kv_pages;
 
 /*

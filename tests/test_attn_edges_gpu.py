@@ -148,3 +148,26 @@ def test_steps_with_scores_of_minus_infinity(shared, HQ, D, io):
     if not shared:
         assert (ref["o"][d["cu"][8]: d["cu"][9]] == 0).all()
     check_attention(f64(o), f64(lse), _finite_sizes(ref, clean), io, live)
+
+
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("shared", [False, True])
+def test_the_longest_table_row(shared):
+    """2^31 - 128 keys, of which the table names the same few pages over and over; with a prefix, own tiles that begin in the
+    middle of 64 keys.  Equal scores and values: o is the value, lse the logarithm of the keys.  A lane adds up 2^20 weights of
+    1 and a workgroup 2^22, exactly; the join adds up at most 514 such sums, each time off by 2^-24 of the total at most.
+    Weights times values have eight more bits: an accumulator takes 2^21 keys, and the i-th addition rounds a sum that is i
+    2^-21 of the last one by 2^-24, together 2^20 2^-24; then the join, the division and the output's rounding."""
+    D, page, most = 64, 16, (1 << 27) - 8
+    k = torch.randn(4, 1, page, D, device="cuda").bfloat16()
+    value = torch.randn(D, device="cuda").bfloat16()
+    v = value.expand(4, 1, page, D).contiguous()
+    table = torch.randint(0, 4, (1, most), dtype=torch.int32, device="cuda")
+    ctx = torch.tensor([most * page - 1], dtype=torch.int32, device="cuda")
+    q = torch.zeros(1, 2, D, dtype=torch.bfloat16, device="cuda")
+    args = dict(group_offsets=to_dev(np.array([0, 1], np.int32)), prefix_lens=to_dev(np.array([48], np.int32))) if shared else {}
+    o, lse = gdr.gdr_attn_decode_paged(q, k, v, table, ctx, output_lse=True, **args)
+    assert (np.abs(f64(o) - f64(value)) <= np.abs(f64(value)) * (2.0 ** -4 + 520 * 2.0 ** -24 + 2.0 ** -8)).all()
+    assert np.abs(f64(lse) - np.log(2.0 ** 31 - 128)).max() < 514 * 2.0 ** -24 + 100 * 2.0 ** -24
+    with pytest.raises(gdr.GdrError):      # one page more
+        gdr.gdr_attn_decode_paged(q, k, v, torch.zeros(1, most + 1, dtype=torch.int32, device="cuda"), ctx)
