@@ -633,10 +633,11 @@ int64_t pages_bytes(const gdr_attn_problem* p, const gdr_kv_pages* c) {
     return n < (int64_t)1 << 62 ? (int64_t)n : (int64_t)1 << 62;
 }
 
-// |scale| log2(e); a zero scale as the smallest normal number, so that a masked score times it stays -inf
+// |scale| log2(e); a zero scale as the smallest number, so that a masked score times it stays -inf: times a score of 2^127 it is
+// 2^-22.  (The kernels keep fp32 denormals.)
 float score_factor(float scale) {
     const float c = (scale < 0 ? -scale : scale) * 1.4426950408889634f;
-    return c < 1.17549435e-38f ? 1.17549435e-38f : c;
+    return c > 0 ? c : 0x1p-149f;
 }
 
 }  // namespace

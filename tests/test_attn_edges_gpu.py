@@ -171,3 +171,25 @@ def test_the_longest_table_row(shared):
     assert np.abs(f64(lse) - np.log(2.0 ** 31 - 128)).max() < 514 * 2.0 ** -24 + 100 * 2.0 ** -24
     with pytest.raises(gdr.GdrError):      # one page more
         gdr.gdr_attn_decode_paged(q, k, v, torch.zeros(1, most + 1, dtype=torch.int32, device="cuda"), ctx)
+
+
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("scale", [0.0, -0.0, 1e-39, -3e-39, 2e-42, 3e-45])
+def test_scales_near_zero_of_large_scores(scale, io):
+    """q . k of 10^37: no scale below the smallest normal number may be taken for a larger one.  (A scale's conversion to base
+    2 is off by half of 2^-149: times scores below 2^127 that is 2^-23, of the 64 u for such things.)"""
+    r = np.random.default_rng(91)
+    HQ, HK, D, lens = 4, 2, 64, [150, 3, 70]
+    cu = np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
+    (q, qw), (k, kw), (v, vw) = (normal(r, (int(cu[-1]), h, D), io, x) for h, x in ((HQ, 1e18), (HK, 1e18), (HK, 1.0)))
+    assert np.abs(np.einsum("thd,thd->th", qw[:, ::2], kw)).max() > 5e36
+    scale = np.float32(scale).item()
+    o, lse = gdr.gdr_attn_prefill_fwd(q, k, v, cu_seqlens=to_dev(cu), scale=scale, output_lse=True)
+    check_attention(f64(o), f64(lse), attn.prefill(qw, kw, vw, cu, scale), io, np.arange(int(cu[-1])))
+    d = _decode_inputs(92, io, D, HQ, HK, [2, 1, 3], [300, 30, 77], 16, sharp=1e18)
+    d["k"].mul_(1e18)
+    d["kw"] = f64(d["k"])
+    o, lse = _decode_call(d, scale=scale, output_lse=True)
+    ref = attn.decode(d["qw"], d["cu"], d["ctx"], d["kw"], d["vw"], d["table"], scale)
+    check_attention(f64(o), f64(lse), ref, io, np.arange(6))
