@@ -341,7 +341,15 @@ template <typename T, int D> struct AttnRow {
 #pragma unroll
             for (int b = 0; b < D / 32; ++b) o[b] *= alpha;
         }
-        const float base = m == kNegInf ? 0.0f : m * c;
+        float base = m == kNegInf ? 0.0f : m * c;
+        // Rounding m c moves all weights of the row by one factor of up to 2^(2^-24 m c).  Where that could leave fp32, or m c
+        // itself does, the scores are taken relative to m before the scale.
+        if (__any(__builtin_fabsf(base) > 0x1p24f)) {
+            const float m0 = m == kNegInf ? 0.0f : m;
+#pragma unroll
+            for (int i = 0; i < 16 * NB; ++i) s[i >> 4][i & 15] -= m0;
+            base = 0.0f;
+        }
 #pragma unroll
         for (int i = 0; i < 16 * NB; ++i) s[i >> 4][i & 15] = __builtin_amdgcn_exp2f(fmaf(s[i >> 4][i & 15], c, -base));
 #pragma unroll

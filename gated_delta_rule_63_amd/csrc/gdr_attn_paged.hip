@@ -486,7 +486,7 @@ __global__ __launch_bounds__(64 * KW * RW, 2) void attn_paged_kernel(AttnPagedAr
                     const int row = 32 * rw + (lane & 31);
                     C::store_part(s + row * D, half, o);
                     if (half == 0) {
-                        s[block_rows * D + row] = lost ? kLost : m == kNegInf ? kNegInf : m * a.c;
+                        s[block_rows * D + row] = lost ? kLost : m;
                         s[block_rows * D + block_rows + row] = l;
                     }
                 }
@@ -529,7 +529,7 @@ __device__ __forceinline__ void join_row(const AttnPagedArgs& a, int token, int 
         for (int d = 1; d < LANES; d *= 2) mn = fmaxf(mn, __shfl_xor(mn, d));
         mn = fmaxf(mn, m);
         const float base = mn == kNegInf ? 0.0f : mn;
-        const float e = __builtin_amdgcn_exp2f(m1 - base), e0 = __builtin_amdgcn_exp2f(m - base);
+        const float e = __builtin_amdgcn_exp2f((m1 - base) * a.c), e0 = __builtin_amdgcn_exp2f((m - base) * a.c);
         l1 *= e;
 #pragma unroll
         for (int d = 1; d < LANES; d *= 2) l1 += __shfl_xor(l1, d);
@@ -565,7 +565,7 @@ __device__ __forceinline__ void join_row(const AttnPagedArgs& a, int token, int 
 #pragma unroll
         for (int i = 0; i < V / 2; ++i) to[i] = pack_bf16x2(o[2 * i] * inv, o[2 * i + 1] * inv);
     }
-    if (a.lse && lane == 0) a.lse[id] = log_sum(m, l);
+    if (a.lse && lane == 0) a.lse[id] = log_sum(m * a.c, l);
 }
 
 // Without prefixes: LANES lanes for every row of the blocks that stretches have left unfinished; and the rows that see

@@ -493,10 +493,11 @@ GDR_API gdr_status gdr_beam_reorder(int32_t batch, int32_t beams, const int32_t*
  *     o[t,h] = sum_j p_j v[j,h']       p = softmax over the visible j of  scale q[t,h] . k[j,h']
  *     lse[t,h] = log sum_j e^(scale q[t,h] . k[j,h'])
  *
- * A row that sees nothing has o = 0 and lse = -inf; one that sees keys, but scores of -inf only (a key that is infinite),
+ * A row that sees nothing has o = 0 and lse = -inf; one that sees keys, but scores of -inf only,
  * has NaN in both.  What a row does not see has no part in it: infinities and NaN in the keys and values of other
  * sequences, of later tokens and of the cache's unused rows included.
- * Scores, the softmax and the sums are held in fp32; with bf16 I/O the weights p are rounded to bf16 (relative to
+ * q . k, the softmax and the sums (of up to 2^8 |v_j| a key, divided by that of the weights at the end) are held in fp32, and
+ * one that is past fp32 is an infinity; with bf16 I/O the weights p are rounded to bf16 (relative to
  * the row's running maximum) for the product with v, whose products are exact and summed in fp32.
  *
  * Layouts: q, o [T, HQ, D], k, v [T, HKV, D] io_dtype.  q, k and v may be views of wider rows (a fused projection's):

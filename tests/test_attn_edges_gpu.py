@@ -3,7 +3,7 @@ import numpy as np
 import pytest
 import torch
 
-from _attn import TORCH, check_attention, normal
+from _attn import HALF, TORCH, check_attention, normal
 from _dev import f64, to_dev
 from gated_delta_rule_63_amd import gdr
 from oracle import attn
@@ -193,3 +193,63 @@ def test_scales_near_zero_of_large_scores(scale, io):
     o, lse = _decode_call(d, scale=scale, output_lse=True)
     ref = attn.decode(d["qw"], d["cu"], d["ctx"], d["kw"], d["vw"], d["table"], scale)
     check_attention(f64(o), f64(lse), ref, io, np.arange(6))
+
+
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_the_largest_scale(sign, D, io):
+    """Scores are a key's first channel times +-2^127: the largest has a weight of 1 and the others none, also where they are
+    past fp32 (3 and -3) and lse is infinite."""
+    r = np.random.default_rng(101)
+    scale, HQ, HK = sign * 2.0 ** 127, 4, 2
+    lens = [330, 40, 700]
+    cu = np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
+    T = int(cu[-1])
+    x = np.full(T, -3.0)
+    for n, a in enumerate((150, 0, 400)):                  # from there on growing; one of 3 at the very end
+        x[cu[n] + a:cu[n + 1]] = np.array([-0.5, -0.25, 0.0, 0.25, 0.5, 0.625, 0.75, 1.0])[np.arange(lens[n] - a) * 8 // (lens[n] - a)]
+    first = np.array([np.argmax(x[cu[n]:cu[n] + i + 1]) + cu[n] for n in range(3) for i in range(lens[n])])
+    ties = np.array([int((x[cu[n]:cu[n] + i + 1] == x[f]).sum()) for (n, i), f in zip([(n, i) for n in range(3) for i in range(lens[n])], first)])
+    q, k = np.zeros((T, HQ, D)), np.zeros((T, HK, D))
+    q[:, :, 0], k[:, :, 0] = 1.0, sign * x[:, None]
+    k[T - 1, :, 0] = sign * 3.0
+    q, k = to_dev(q.astype(np.float32)).to(TORCH[io]), to_dev(k.astype(np.float32)).to(TORCH[io])
+    v, vw = normal(r, (T, HK, D), io)
+    top = x[first]
+    want = np.stack([vw[f:f + c].mean(0) for f, c in zip(first, ties)])[:, np.arange(HQ) // (HQ // HK)]
+    lse_want = np.where(top == -3.0, -np.inf, top * 2.0 ** 127)
+    want[T - 1], lse_want[T - 1] = vw[T - 1][np.arange(HQ) // (HQ // HK)], np.inf
+    most = np.abs(vw).max()
+
+    def check(o, lse, rows, what):
+        # c values and the division: (c + 2) u of the largest; lse: the two constants, three products and the sum, 6 u, and the
+        # logarithm of up to 100 keys
+        past = np.isinf(lse_want[rows])
+        assert (lse[past] == lse_want[rows][past][:, None]).all() and past.any() and not past.all(), what
+        allowed = (ties[rows][:, None, None] + 2) * 2.0 ** -24 * most + HALF[io] * np.abs(want[rows])
+        assert (np.abs(o - want[rows]) <= allowed).all(), what
+        lse, fine = lse[~past], lse_want[rows][~past][:, None]
+        assert (np.abs(lse - fine) <= 6 * 2.0 ** -24 * np.abs(fine) + 5).all(), what
+
+    o, lse = gdr.gdr_attn_prefill_fwd(q, k, v, cu_seqlens=to_dev(cu), scale=scale, output_lse=True)
+    check(f64(o), f64(lse), np.arange(T), "prompts")
+    # the same from a cache: four tokens of each of several lengths
+    page = 16
+    table = np.zeros((8, 48), np.int32)
+    ends = [(0, 100), (0, 152), (0, 330), (1, 4), (1, 40), (2, 390), (2, 405), (2, 700)]
+    pages = []
+    for s, (n, e) in enumerate(ends):
+        for i in range(-(-e // page)):
+            table[s, i] = len(pages)
+            pages.append((cu[n] + i * page + np.arange(page)).clip(0, T - 1))
+    at = to_dev(np.stack(pages)).long()
+    kp, vp = k[at].transpose(1, 2).contiguous(), v[at].transpose(1, 2).contiguous()
+    rows = np.concatenate([cu[n] + np.arange(e - 4, e) for n, e in ends])
+    ctx = np.array([e - 4 for _, e in ends], np.int32)
+    for groups in (None, ([0, 1, 2, 3], [96, 144, 160]), ([0, 6, 7, 8], [0, 400, 688])):
+        args = {} if groups is None else dict(zip(("group_offsets", "prefix_lens"), (to_dev(np.array(x, np.int32)) for x in groups)))
+        o, lse = gdr.gdr_attn_decode_paged(q[to_dev(rows).long()].contiguous(), kp, vp, to_dev(table), to_dev(ctx),
+                                           cu_seqlens=to_dev(np.arange(0, 33, 4, dtype=np.int32)), max_q_len=4, scale=scale, output_lse=True, **args)
+        check(f64(o), f64(lse), rows, f"steps {groups}")
