@@ -57,7 +57,7 @@ __device__ __forceinline__ const char* copy_base(const char* p) {
 __device__ __forceinline__ void copy_to_lds(const char* base, uint32_t off, uint32_t lds) {
     lds = (uint32_t)uniform((int)lds);
     asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
-                 : : "v"(off), "s"(base), "s"(lds) : "memory");
+                 : : "v"(off), "s"(base), "s"(lds) : "memory", "m0");
 }
 // until at most LEFT of the wave's copies, the last ones, are on their way
 template <int LEFT = 0> __device__ __forceinline__ void wait_copies() { asm volatile("s_waitcnt vmcnt(%0)" : : "n"(LEFT) : "memory"); }
