@@ -253,3 +253,30 @@ def test_the_largest_scale(sign, D, io):
         o, lse = gdr.gdr_attn_decode_paged(q[to_dev(rows).long()].contiguous(), kp, vp, to_dev(table), to_dev(ctx),
                                            cu_seqlens=to_dev(np.arange(0, 33, 4, dtype=np.int32)), max_q_len=4, scale=scale, output_lse=True, **args)
         check(f64(o), f64(lse), rows, f"steps {groups}")
+
+
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n,mean,HQ,HK", [(70, 300, 1, 1), (65, 205, 2, 1), (65, 205, 1, 1), (100, 30, 16, 4), (90, 30, 24, 8), (70, 45, 32, 8), (100, 40, 64, 8), (80, 20, 80, 10),
+                                          (65, 200, 40, 5)])
+def test_many_ragged_prompts(n, mean, HQ, HK, D, io):
+    """More sequences than are cut at their own borders: workgroups of 32, 64 and 128 rows (one or two heads of long prompts, few
+    heads, many heads) that hold several sequences, some without tokens; the first, an inner and the last head."""
+    r = np.random.default_rng([n, HQ])
+    lens = np.where(r.random(n) < 0.1, 0, r.integers(1, 2 * mean, n))
+    lens[n // 2] = 5 * mean
+    lens[-1] = 3
+    if HQ < 3:                                             # long ones for all
+        lens = np.maximum(lens, 200) if mean > 205 else r.integers(195, 216, n)
+    cu = np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
+    end, T = int(cu[-1]), int(cu[-1]) + 5
+    (q, qw), (k, kw), (v, vw) = (normal(r, (T, h, D), io, x) for h, x in ((HQ, 2.0), (HK, 1.0), (HK, 1.0)))
+    o = torch.full((T, HQ, D), 7.0, dtype=TORCH[io], device="cuda")
+    lse = torch.full((T, HQ), 7.0, device="cuda")
+    gdr.gdr_attn_prefill_fwd(q, k, v, cu_seqlens=to_dev(cu), o=o, lse=lse)
+    assert bool((o[end:] == 7.0).all()) and bool((lse[end:] == 7.0).all())
+    o, lse = f64(o), f64(lse)
+    for h in sorted({0, HQ // 2 - HQ // 7, HQ - 1}):
+        ref = attn.prefill(qw[:end, h:h + 1], kw[:end, h * HK // HQ][:, None], vw[:end, h * HK // HQ][:, None], cu, 1 / np.sqrt(D))
+        check_attention(o[:end, h:h + 1], lse[:end, h:h + 1], ref, io, np.arange(end), f"head {h}")
