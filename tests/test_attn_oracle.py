@@ -63,3 +63,36 @@ def test_what_is_not_there_is_not_seen():
     one = attn.prefill(np.ones((16, 1, 8)), k[2, 0][:, None], k[2, 0][:, None], [0, 16], 1.0)
     assert np.allclose(d["o"][0], one["o"][15]) and d["keys"][0] == 16
     assert (d["o"][1] == 0).all() and np.isneginf(d["lse"][1]).all()
+
+
+def test_one_key_takes_all():
+    """Scores far apart: the largest one's value, in a prompt and from a cache, and its score as lse."""
+    r = np.random.default_rng(5)
+    v = r.normal(size=(9, 2, 4))
+    k = np.zeros((9, 2, 4))
+    k[:, 0, 0], k[:, 1, 1] = r.permutation(9) * 1000.0, r.permutation(9) * 1000.0
+    q = np.ones((9, 4, 4))
+    got = attn.prefill(q, k, v, [0, 4, 9], 1.0)
+    for t in range(9):
+        for h in range(4):
+            seen = np.arange(0 if t < 4 else 4, t + 1)
+            j = seen[np.argmax(k[seen, h // 2].sum(-1))]
+            assert np.allclose(got["o"][t, h], v[j, h // 2]) and np.isclose(got["lse"][t, h], k[j, h // 2].sum())
+    pages = lambda x: np.concatenate([x, np.zeros((7, 2, 4))])[None].transpose(0, 2, 1, 3)  # noqa: E731
+    d = attn.decode(q[4:], [0, 5], [4], pages(k), pages(v), np.array([[0]]), 1.0)
+    assert np.allclose(d["o"][4, 3], v[np.argmax(k[:, 1, 1]), 1])
+
+
+@pytest.mark.parametrize("n", range(1, 40))
+def test_decode_is_the_end_of_a_prompt_wherever_it_begins(n):
+    r = np.random.default_rng(n)
+    q, k, v = r.normal(size=(40, 2, 4)), r.normal(size=(40, 1, 4)), r.normal(size=(40, 1, 4))
+    whole = attn.prefill(q, k, v, [0, 40], 0.4)
+    table = r.permutation(3)[None]
+    kp, vp = np.full((3, 1, 16, 4), np.nan), np.full((3, 1, 16, 4), np.nan)
+    for t in range(40):
+        p, row = attn.place(table, 3, 16, 0, t)
+        kp[p, :, row], vp[p, :, row] = k[t], v[t]
+    d = attn.decode(q[n:], [0, 40 - n], [n], kp, vp, table, 0.4)
+    assert np.allclose(d["o"], whole["o"][n:], atol=1e-14) and np.allclose(d["lse"], whole["lse"][n:], atol=1e-14)
+    assert np.array_equal(d["keys"], whole["keys"][n:])
