@@ -7,11 +7,11 @@
 // sequences', each row sees the tokens from its sequence's start to itself, and 128 one-token sequences are one
 // workgroup's work.
 //
-// The matrix unit and the clock bound the large ones: 16384 tokens of 32 heads of 128 channels, bf16, run 2199 GFLOP in
-// 2.03 ms, 1086 TFLOP/s (a product of 8192 x 8192 x 8192 by the library 1159), with the matrix unit busy 55%, vector
-// instructions 49% and the LDS 41% of the cycles at about 1.75 GHz.  8 ragged prompts of 32768 tokens 1.36 ms, 1001
-// TFLOP/s.  fp32 of 64 channels, 3 prompts of 3001 tokens, 8 heads: 51 us, 83 of the 154 TFLOP/s of such a product, the matrix
-// unit busy 51%; the longest row blocks decide.
+// 16384 tokens of 32 heads of 128 channels, bf16, run 2199 GFLOP in 2.08 ms, 1059 TFLOP/s (a product of 8192 x 8192 x 8192 by
+// the library 1139), with the matrix unit busy 55%, vector instructions 50% and the LDS 42% of the cycles at about 1.75 GHz: the
+// softmax and the products take turns in a wave, and two waves to a SIMD hide a part of it.  8 ragged prompts, 32768 tokens
+// together, 1.40 ms, 975 TFLOP/s (1.31 to 1.46 on other cards).  fp32 of 64 channels, 3 prompts, 3001 tokens together, 8 heads:
+// 52 us, 81 of the 153 TFLOP/s of such a product, the matrix unit busy 49%; the longest row blocks decide.
 #include <hip/hip_runtime.h>
 
 #include "gdr_attn_device.h"
@@ -57,8 +57,8 @@ __global__ __launch_bounds__(64 * KW * RW, 2) void attn_prefill_kernel(AttnPrefi
     int t0, stop, lo, start, latest;
     if (a.N <= kSorted) {
         // tiles are cut at the sequences' borders, the longest sequence first and its last tile first: what is begun last
-        // is short, and neighbours share their keys and values in the L2 (3 prompts, 3001 fp32 tokens: 81 us, at fixed
-        // borders 107)
+        // is short, and neighbours share their keys and values in the L2 (3 prompts, 3001 fp32 tokens together: 81 us, at
+        // fixed borders 107)
         const int first = lane < a.N && a.cu ? a.cu[lane] : 0, len = lane < a.N ? (a.cu ? a.cu[lane + 1] - first : (int)a.T) : 0;
         const int tiles = (len + kRows - 1) / kRows;
         int before = 0;   // tiles of the sequences ahead of the lane's
@@ -192,9 +192,9 @@ hipError_t start(AttnPrefillArgs a, hipStream_t stream) {
         return hipGetLastError();
     };
     // Where two tiles leave room for one workgroup on a CU: with one tile each from nearly two rounds of the card on (fp32, 8
-    // heads, D = 64, 3001 tokens 55 us, with two tiles 74; 2500 tokens 43 and 55; D = 128, 6000 tokens 343 and 385), and in
-    // less than one (bf16, 8 heads, D = 128, 1000 tokens 17 and 19.5).  In between two workgroups meet on some CUs while
-    // others are idle (fp32, D = 64, 1500 tokens 30 and 27; D = 128, 3000 tokens 166 and 136).
+    // heads, 3 ragged prompts, tokens together: D = 64, 3001 tokens 53 us, with two tiles 69; 2500 tokens 46 and 57; D = 128,
+    // 6000 tokens 345 and 392), and in less than one (bf16, 8 heads, D = 128, one prompt of 1000 tokens 17.5 and 19.8).  In
+    // between two workgroups meet on some CUs while others are idle (fp32, D = 64, 1500 tokens of 3 prompts 31 and 28).
     // Two of D = 128 in fp32 and 128 keys do not fit at all.
     constexpr int two = 4 * tile_keys<T, D, KW>() * D * Elem<T>::bytes;
     if constexpr (two > 80 * 1024)
@@ -204,14 +204,16 @@ hipError_t start(AttnPrefillArgs a, hipStream_t stream) {
 
 template <typename T, int D>
 hipError_t launch(const AttnPrefillArgs& a, hipStream_t stream) {
-    // `wide`: workgroups of 128 rows.  From 640 on they fill the card, and rows that share a tile's reads count most: 32
-    // heads, D = 128, bf16, 2000 tokens 55 us (64 rows 56), 4000 148 (173); 16 heads, D = 64, 6000 tokens 116 (116),
-    // 16000 563 (646); fp32, 8 heads, D = 128, 12000 tokens 1244 (1277).  Below, 64 rows by two waves each: 32 heads, D =
-    // 128, 1000 tokens 24 us (128 rows 28), fp32 6000 tokens 400 (612).  Small batches of sequences that are long enough
-    // for four waves to share their keys take 32 rows by four waves: 16 heads, D = 64, 1000 tokens 13 us (64 rows 15), twice as
-    // many 27 (26); 16 heads, D = 128, 1000 tokens 19 (21), in 4 sequences 14 (14), in 8 18 (12); 8 heads, 3000 tokens 44
-    // (54) but 32 heads, 700 tokens 23 (19); fp32, 8 heads, D = 64, 3 sequences of 600 tokens 14 (20), 8 of 1000 18 (16), 16 of
-    // 3000 30 (28), 3 of 3001 55 (89); D = 128, one head, 1 of 1669 78 (121), 8 heads, 3 of 1500 49 (69), 3 of 4000 204 (213).
+    // `wide`: workgroups of 128 rows.  From 640 on they fill the card, and rows that share a tile's reads count most.  One prompt,
+    // bf16: 32 heads, D = 128, 2000 tokens 53 us (56 in workgroups of 64 rows, by two waves each, which the rule takes: 512), 4000
+    // 155 (180); 16 heads, D = 64, 6000 tokens 112 (118), 16000 580 (672).  Below, 64 rows: 32 heads, D = 128, 1000 tokens 25 us
+    // (128 rows 28); 3 ragged prompts, fp32, 8 heads, D = 128, 6000 tokens together 350 (605), but 12000 1133 (1242, which the
+    // rule takes).
+    // Small batches of sequences that are long enough for four waves to share their keys take 32 rows by four waves (in brackets:
+    // 64 rows).  bf16, 16 heads, one prompt: D = 64, 1000 tokens 13 us (16), 2000 27 (27); D = 128, 1000 tokens 19 (22), as 4
+    // ragged prompts 14 (14), as 8 18 (12); 8 heads, one prompt of 3000 tokens 43 (54), yet 32 heads, 700 tokens 24 (20).
+    // fp32, 8 heads, ragged prompts, tokens together: D = 64, 3 of 600 14 (19), 8 of 1000 18 (16), 16 of 3000 29 (27), 3 of 3001
+    // 54 (89); D = 128, 3 of 1500 48 (69), 3 of 4000 204 (215); one head, one prompt of 1669 78 (121).
     const int64_t wide = (a.T + 127) / 128 * a.HQ;
     constexpr int es = Elem<T>::bytes, few = es == 4 ? 256 : 128, tokens = es == 4 ? 192 : 256;
     if (wide <= few && a.T >= (int64_t)tokens * a.N) return start<T, D, 4, 1>(a, stream);

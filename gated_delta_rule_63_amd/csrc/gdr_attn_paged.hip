@@ -10,13 +10,15 @@
 //   attn_paged_kernel   the groups' prefixes (with prefixes), then what is each sequence's own
 //   attn_join_kernel    parts -> outputs
 //
-// Long caches are bound by HBM: 64 sequences of up to 8191 tokens, 8 key heads of 128 bf16 channels, 976 MB, take 177 us
-// (5.5 TB/s) and their join 5; 1..12 tokens each against up to 4095, 554 MB, 124 + 9.  Short ones are bound by latency:
-// one sequence of 4097 tokens (17 MB) takes 11.6 + 5.3 us, a chain of dependent loads (lengths, page, tile) and two tiles;
+// Long caches are bound by HBM: 64 sequences of up to 8191 tokens, 8 key heads of 128 bf16 channels, 976 MB, take 175 us
+// (5.6 TB/s) and their join 5; 1..12 tokens each against up to 4095, 554 MB, 124 + 9.  Short ones are bound by latency:
+// one sequence of 4097 tokens (17 MB) takes 12.0 + 5.2 us, a chain of dependent loads (lengths, page, tile) and two tiles;
 // stretches of at least two or four tiles took as long or 1.5 us longer.  With a prefix of 16384 tokens for 64 sequences
-// its parts are a third of the traffic: 33 us (18% of the matrix unit's cycles), then 25 for up to 512 own tokens each and
-// 10 to join.  In fp32 a product takes eight times as many of these cycles as in bf16, and 4 rows fill an eighth of a
-// block: 32 x 8 beams over 1000 tokens with up to 127 of their own 24 + 28 + 6 us.
+// its parts are a third of the traffic: 33 us (17% of the matrix unit's cycles), then 25 for up to 512 own tokens each and
+// 10 to join.  32 x 8 fp32 beams over 1000 tokens with up to 127 of their own: 24 + 28 + 6 us, the matrix unit busy 22% and
+// 15%; 4 rows fill an eighth of a block, whose products are a chain of their own in each wave, behind the start and the first
+// tile.  fp32 rows of 128 channels in blocks of 64 and 128 (q_len 12: 64 sequences against up to 4095 tokens 344 us of a
+// floor of 224) keep 18 and 16 registers in scratch memory; no other kernel does.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>

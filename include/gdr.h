@@ -493,12 +493,12 @@ GDR_API gdr_status gdr_beam_reorder(int32_t batch, int32_t beams, const int32_t*
  *     o[t,h] = sum_j p_j v[j,h']       p = softmax over the visible j of  scale q[t,h] . k[j,h']
  *     lse[t,h] = log sum_j e^(scale q[t,h] . k[j,h'])
  *
- * A row that sees nothing has o = 0 and lse = -inf; one that sees keys, but scores of -inf only,
- * has NaN in both.  What a row does not see has no part in it: infinities and NaN in the keys and values of other
- * sequences, of later tokens and of the cache's unused rows included.
+ * A row that sees nothing has o = 0 and lse = -inf; one that sees keys, but scores of -inf only, has NaN in both.  An
+ * infinite value whose weight is 0 in fp32 gives an infinity or NaN.  What a row does not see has no part in it: infinities
+ * and NaN in the keys and values of other sequences, of later tokens and of the cache's unused rows included.
  * q . k, the softmax and the sums (of up to 2^8 |v_j| a key, divided by that of the weights at the end) are held in fp32, and
- * one that is past fp32 is an infinity; with bf16 I/O the weights p are rounded to bf16 (relative to
- * the row's running maximum) for the product with v, whose products are exact and summed in fp32.
+ * one that is past fp32 is an infinity; with bf16 I/O the weights p are rounded to bf16 (relative to the row's running
+ * maximum) for the product with v, whose products are exact and summed in fp32.
  *
  * Layouts: q, o [T, HQ, D], k, v [T, HKV, D] io_dtype.  q, k and v may be views of wider rows (a fused projection's):
  * a token's heads are contiguous, tokens q_stride, k_stride, v_stride elements (at most 2^22) apart.  Outputs are dense.  Every
@@ -577,7 +577,7 @@ GDR_API gdr_status gdr_attn_prefill_fwd(const gdr_attn_problem* p, const void* q
  * gdr_attn_decode_paged -- 1..12 tokens of each sequence against the cache, which holds them already
  * (gdr_rope_append_paged): token i of sequence n sees the tokens 0 .. context_lens[n] + i.
  *
- *   max_q_len, cu_seqlens   as in gdr_decode_paged
+ *   max_q_len, cu_seqlens   as in gdr_decode_paged; T <= N max_q_len, rows behind the last sequence included
  *   context_lens   int32 [N]; negative: a padded sequence, skipped, its o and lse rows untouched
  *   num_groups     0, or the number of groups of consecutive sequences that share a prefix: group g is the sequences
  *                  group_offsets[g] .. group_offsets[g+1]-1 (int32 [num_groups+1], non-decreasing from 0; sequences
