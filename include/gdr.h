@@ -588,6 +588,8 @@ GDR_API gdr_status gdr_attn_prefill_fwd(const gdr_attn_problem* p, const void* q
  *   lse            fp32 [T, HQ] or NULL
  *   workspace      gdr_attn_workspace_size bytes, 256-byte aligned, contents need not be initialised; calls that
  *                  may overlap need one each
+ * Several sequences may name the same pages: a longer piece of a prompt behind tokens that are in the cache, once it is stored
+ * itself, is so many sequences of up to 12 tokens with the same table row, and a group of them shares what was there before.
  * o, lse and workspace overlap neither q nor the cache nor one another.  p->k_stride and p->v_stride are not used.  T * HQ < 2^31, and N times a table row's tokens below 2^37 over the
  * blocks of 32 rows that max_q_len tokens of HQ / HKV heads make.  The result does not depend on what else is in the
  * batch by more than the order of fp32 sums.

@@ -280,3 +280,34 @@ def test_many_ragged_prompts(n, mean, HQ, HK, D, io):
     for h in sorted({0, HQ // 2 - HQ // 7, HQ - 1}):
         ref = attn.prefill(qw[:end, h:h + 1], kw[:end, h * HK // HQ][:, None], vw[:end, h * HK // HQ][:, None], cu, 1 / np.sqrt(D))
         check_attention(o[:end, h:h + 1], lse[:end, h:h + 1], ref, io, np.arange(end), f"head {h}")
+
+
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("shared", [False, True])
+def test_a_prompt_in_pieces(shared, io):
+    """Tokens of a prompt behind others of it that are in the cache: stored first, then attended to as sequences of up to 12
+    tokens with the same table row, whose common tokens are a prefix.  The last piece's rows are those of the whole prompt."""
+    r = np.random.default_rng(111)
+    HQ, HK, D, page, lens = 8, 2, 64, 16, [150, 40, 230]
+    cut = [70, 33, 128]                                    # tokens of the first piece
+    cu = np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
+    (q, qw), (k, kw), (v, vw) = (normal(r, (int(cu[-1]), h, D), io) for h in (HQ, HK, HK))
+    table = r.permutation(45).reshape(3, 15).astype(np.int32)
+    kp = torch.full((45, HK, page, D), float("nan"), dtype=TORCH[io], device="cuda")
+    vp = kp.clone()
+    for part in (0, 1):
+        rows = np.concatenate([cu[n] + (np.arange(cut[n]) if part == 0 else np.arange(cut[n], lens[n])) for n in range(3)])
+        at, have = to_dev(rows).long(), [0, 0, 0] if part == 0 else cut
+        many = np.concatenate([[0], np.cumsum([cut[n] if part == 0 else lens[n] - cut[n] for n in range(3)])]).astype(np.int32)
+        gdr.gdr_rope_append_paged(q[at], k[at], v[at], k_pages=kp, v_pages=vp, page_table=to_dev(table), cu_seqlens=to_dev(many),
+                                  context_lens=to_dev(np.array(have, np.int32)))
+    ctx = [c for n in range(3) for c in range(cut[n], lens[n], 12)]
+    of = [n for n in range(3) for _ in range(cut[n], lens[n], 12)]
+    steps = np.concatenate([[0], np.cumsum([min(12, lens[n] - c) for c, n in zip(ctx, of)])]).astype(np.int32)
+    offsets = np.searchsorted(of, np.arange(4)).astype(np.int32)
+    args = dict(group_offsets=to_dev(offsets), prefix_lens=to_dev(np.array(cut, np.int32))) if shared else {}
+    o, lse = gdr.gdr_attn_decode_paged(q[at], kp, vp, to_dev(table[of]), to_dev(np.array(ctx, np.int32)), cu_seqlens=to_dev(steps),
+                                       max_q_len=12, output_lse=True, **args)
+    ref = attn.prefill(qw, kw, vw, cu, 1 / np.sqrt(D))
+    check_attention(f64(o), f64(lse), {x: ref[x][rows] for x in ref}, io, np.arange(len(rows)))
